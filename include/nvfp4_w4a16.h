@@ -58,7 +58,8 @@ typedef enum {
     NVFP4_ERR_WORKSPACE = 4,         /* workspace missing or smaller than the query says */
     NVFP4_ERR_CUDA = 5,              /* a CUDA runtime call failed (message has the CUDA error) */
     NVFP4_ERR_TIMEOUT = 6,           /* device status: a pipeline wait exceeded its limit */
-    NVFP4_ERR_BAD_WEIGHT = 7         /* device status: repacked header magic/shape mismatch */
+    NVFP4_ERR_BAD_WEIGHT = 7,        /* device status: repacked header magic/shape mismatch */
+    NVFP4_ERR_BAD_INDEX = 8          /* device status: a length, page, slot or position out of range */
 } nvfp4_status;
 
 /* Version of this ABI (bumped on any incompatible change). */
@@ -419,6 +420,123 @@ nvfp4_status nvfp4_w4a16_moe_grouped_noalloc(const void* X, const float* router_
                                              int64_t T, int E, int topk, int64_t H, int64_t I,
                                              void* out, int32_t* topk_idx_out, float* topk_weight_out,
                                              int32_t* perm_out, int32_t* offsets_out, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Between the linears: norm, rotary positions, key-value cache, attention   */
+/* ------------------------------------------------------------------------ */
+
+/* Output of the norm: the activation type, or E4M3 codes with FP32 scales. */
+typedef enum { NVFP4_OUT_16 = 0, NVFP4_OUT_E4M3 = 1 } nvfp4_out_type;
+
+/*
+ * Root-mean-square norm of rows, with the residual's addition before it:
+ *     r = RN(X + residual)  (residual == NULL: r = X)
+ *     y = r * rsqrt(mean(r^2) + eps) * weight
+ * and Y = RN(y), or, with out_type NVFP4_OUT_E4M3, per row (group = 0) or per
+ * `group` columns s = max(max|y| / 448, 2^-100) and Y = E4M3(y / s), nearest even.
+ * A NaN keeps its code and leaves the scale alone; an infinity makes its group's
+ * values read back as NaN.
+ *  X, residual   device BF16 (FP16 with f16 = 1) [T, H], rows x_stride /
+ *                residual_stride elements apart.
+ *  weight        device [H], the same type.
+ *  Y             device [T, H], dense: 16-bit, or uint8 E4M3 codes.  Must not
+ *                overlap the inputs.
+ *  scales        device FP32 [T, H / group] ([T, 1] with group 0); E4M3 only.
+ *  residual_out  device [T, H], dense, with residual only: receives r.  It may be
+ *                residual or X where that is dense (element for element in place).
+ *  group         0, 16, 32, 64, 128 or 256, dividing H (0 for 16-bit output).
+ * H in [1, 2^24], any width, stride and alignment; rows whose width, strides and
+ * pointers are multiples of 16 bytes run on vector loads.  T == 0 launches nothing.
+ */
+nvfp4_status nvfp4_rms_norm(const void* X, int64_t x_stride, const void* residual, int64_t residual_stride,
+                            const void* weight, int64_t T, int64_t H, float eps, int out_type, int64_t group,
+                            int f16, void* Y, float* scales, void* residual_out, void* stream);
+
+/* How a cache holds keys and values. */
+typedef enum { NVFP4_CACHE_16 = 0, NVFP4_CACHE_E4M3 = 1 } nvfp4_cache_type;
+
+/*
+ * A paged key-value cache (a host struct, read during the call).  The key of
+ * token `at` of page p and head h is the head_dim elements at
+ *     k + p * page_stride + h * head_stride + at * token_stride
+ * and the value likewise at v: NVFP4_CACHE_16 in the activation type of the
+ * call, NVFP4_CACHE_E4M3 as codes whose values are code * scale, with the scales
+ * dense FP32 [num_pages, heads, page_size] (at least 2^-100, as the write makes
+ * them).  Rows start on 16-byte boundaries (pointers and byte strides multiples
+ * of 16); head_dim is a multiple of 16 up to 256.
+ */
+typedef struct {
+    void *k, *v;
+    float *k_scale, *v_scale;                            /* NULL for NVFP4_CACHE_16 */
+    int64_t num_pages, page_size, heads, head_dim;
+    int64_t page_stride, head_stride, token_stride;      /* elements */
+    int64_t type;                                        /* nvfp4_cache_type */
+} nvfp4_kv_cache;
+
+/*
+ * Rotate T tokens' queries and keys, and store keys and values in the cache.
+ * Frequency i < rot/2 belongs to the axis whose section holds it (axis a has
+ * sections[a] of them, in order); with that axis's position p = positions[a*T + t],
+ * c = table[p*rot + i] and s = table[p*rot + rot/2 + i],
+ *     (x1, x2) -> (x1 c - x2 s, x2 c + x1 s)
+ * for x1, x2 = x[i], x[i + rot/2], or x[2i], x[2i+1] with interleaved = 1; elements
+ * from rot on pass through.  FP32, products and sums rounded separately.
+ *  q, k, v       device BF16 (FP16 with f16 = 1): [T, Hq, D], and [T, heads, D] with
+ *                the cache's heads and head_dim D; strides in elements, multiples of 8.
+ *  sections      host int32 [axes]; NULL: one axis.  axes is 1 to 4.
+ *  table         device FP32 [table_rows, rot], 16-byte aligned.
+ *  slots         device int64 [T]: page * page_size + token, negative: not stored.
+ *                No two tokens may share a slot.
+ *  q_out         device [T, Hq, D], dense, RN of the rotated q (q itself if dense).
+ * The cache gets RN(k), RN(v), or per token and head s = max(amax / 448, 2^-100)
+ * and E4M3(x / s) of the FP32 values (NaN and infinities as in nvfp4_rms_norm).
+ * A position outside the table leaves its elements as they are, a slot outside
+ * the cache is not written; both record NVFP4_ERR_BAD_INDEX in the status word.
+ */
+nvfp4_status nvfp4_rope_cache_write(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                                    const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                                    const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                                    int64_t T, int64_t Hq, const int64_t* positions, int axes,
+                                    const int32_t* sections, const float* table, int64_t table_rows, int64_t rot,
+                                    int interleaved, int f16, const int64_t* slots,
+                                    const nvfp4_kv_cache* cache, void* q_out, void* stream);
+
+/*
+ * Read cached rows back: k_out, v_out [T, heads, D] dense, 16-byte aligned, of
+ * the slots (negative: zeros; outside the cache: zeros and NVFP4_ERR_BAD_INDEX
+ * in the status word), RN(code * scale) from an E4M3 cache.
+ */
+nvfp4_status nvfp4_kv_cache_read(const nvfp4_kv_cache* cache, const int64_t* slots, int64_t T, int f16,
+                                 void* k_out, void* v_out, void* stream);
+
+/*
+ * Attention of one new token per sequence over the cache.  For head h of
+ * sequence b, with n = lengths[b], on key head h / (Hq / heads):
+ *     z_j = softmax_scale * q . k_j,  max(0, n - window) <= j < n  (window 0: all),
+ *     out = sum_j exp(z_j) v_j / sum_j exp(z_j),  lse = log sum_j exp(z_j).
+ * n == 0: out = 0, lse = -infinity.
+ *  q             device BF16 (FP16 with f16 = 1) [B, Hq, D]; 16-byte aligned rows.
+ *  block_table   device int32 [B, table_width], rows table_stride apart: the page
+ *                of tokens [i * page_size, (i + 1) * page_size).  Entries past a
+ *                sequence's length are not read.
+ *  lengths       device int32 [B].
+ *  out           device [B, Hq, D], dense, 16-byte aligned.
+ *  lse           device FP32 [B, Hq] or NULL.
+ *  workspace     device, >= nvfp4_paged_attention_workspace(...) bytes, 256-byte
+ *                aligned.  Contents on entry do not matter.
+ * The lengths stay on the device: the same launch serves any of them, so a
+ * captured graph may be replayed as the sequences grow.  A length outside
+ * [0, table_width * page_size] is clamped and a page outside the cache read as
+ * page 0; both record NVFP4_ERR_BAD_INDEX in the status word.  Repeated calls
+ * on the same inputs give the same bits.
+ */
+size_t nvfp4_paged_attention_workspace(int64_t B, int64_t Hq, int64_t heads, int64_t head_dim);
+nvfp4_status nvfp4_paged_attention(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                                   const nvfp4_kv_cache* cache, const int32_t* block_table,
+                                   int64_t table_stride, int64_t table_width, const int32_t* lengths,
+                                   int64_t B, int64_t Hq, float softmax_scale, int64_t window, int f16,
+                                   void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                   void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,526 @@
+"""The operators between a decoder layer's linears against the 64-bit oracle:
+norm, rotary positions with the cache write, cache read, paged attention.
+
+Tolerances.  u is the unit roundoff of a 16-bit type (BF16 2^-8, FP16 2^-11; FP16
+has an absolute 2^-25 below its normals).  A 16-bit output computed in 32 bits is
+within u |ref| of the 64-bit value, plus the 32-bit error (at most 2^-13 relative
+here: sums of up to 2^11 terms per thread).  Attention also rounds each softmax
+weight to the 16-bit type that meets the values in the MMA (BF16 for a BF16
+cache, else FP16), which moves the output by at most u_p sum_j p_j |v_j|; scores in 32
+bits move it by their error, at most 2^-12 relative to that sum for the
+magnitudes here.  Caches and the rotation are defined step by step in 32 bits, so
+their codes, scales and 16-bit values are equal bit for bit.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import w4a16_nvfp4_weight_gb300 as nv
+from oracle import layer
+from tests import gpu_util as gu
+
+pytestmark = pytest.mark.gpu
+E4M3 = torch.float8_e4m3fn
+DT = {"bf16": torch.bfloat16, "f16": torch.float16}
+U = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11}
+TINY = {"bf16": 2.0 ** -133, "f16": 2.0 ** -25}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib(lib):
+    torch.cuda.init()
+    yield
+    gu.check_device_status()
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _randn(g, shape, act="bf16", std=1.0):
+    return (torch.randn(shape, generator=g, device="cuda") * std).to(DT[act])
+
+
+def _np(t):
+    return t.detach().cpu().double().numpy()
+
+
+def _close16(got, ref, act, rel=2.0 ** -13):
+    got = _np(got)
+    fine = np.isfinite(ref)
+    assert np.array_equal(np.isnan(got), np.isnan(ref))
+    assert np.array_equal(got[~fine & ~np.isnan(ref)], ref[~fine & ~np.isnan(ref)])
+    err = np.abs(got - ref)[fine]
+    assert np.all(err <= (U[act] + rel) * np.abs(ref[fine]) + TINY[act]), err.max()
+
+
+# ------------------------------------------------------------------- norm ---
+
+NORM_SHAPES = [(1, 1), (3, 7), (5, 16), (2, 64), (9, 128), (33, 720), (4, 1000), (7, 2064), (1, 4096), (300, 4096),
+               (3, 5120), (2, 8192), (1300, 256), (2, 16384), (3, 40000), (2, 40008)]
+
+
+@pytest.mark.parametrize("T,H", NORM_SHAPES)
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+@pytest.mark.parametrize("res", [False, True])
+def test_norm(T, H, act, res):
+    g = _gen(T * 131 + H)
+    x, w, r = _randn(g, (T, H), act), _randn(g, (H,), act), _randn(g, (T, H), act, 3.0)
+    if res:
+        y, added = nv.rms_norm(x, w, eps=1e-5, residual=r)
+        want = (x.float() + r.float()).to(DT[act])
+        assert torch.equal(added, want)
+        x = want
+    else:
+        y = nv.rms_norm(x, w, eps=1e-5)
+    _close16(y, layer.rms_norm(_np(x), _np(w), 1e-5), act)
+
+
+@pytest.mark.parametrize("T,H,group", [(1, 16, 16), (5, 64, 0), (3, 720, 16), (33, 2064, 0), (4, 4096, 128),
+                                       (300, 4096, 0), (7, 5120, 256), (2, 8192, 32), (9, 1024, 64), (2, 33024, 128),
+                                       (3, 7, 0), (2, 40008, 0), (700, 128, 64)])
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+def test_norm_e4m3(T, H, group, act):
+    g = _gen(T + H + group)
+    x, w, r = _randn(g, (T, H), act), _randn(g, (H,), act), _randn(g, (T, H), act)
+    codes, scales, added = nv.rms_norm_e4m3(x, w, group=group, residual=r)
+    n = group or H
+    assert codes.dtype == E4M3 and scales.shape == (T, H // n)
+    ref = layer.rms_norm(_np(added), _np(w), 1e-6).reshape(T, H // n, n)
+    s = np.maximum(np.abs(ref).max(-1) / 448, 2.0 ** -100)
+    got_s = _np(scales)
+    assert np.all(np.abs(got_s - s) <= 2.0 ** -13 * s)
+    # a code is a nearest one: within half a step of y / s, allowing the 32-bit error of y / s
+    q = ref / got_s[..., None]
+    c = _np(codes.float()).reshape(q.shape)
+    _, e = np.frexp(q)
+    step = np.exp2(np.maximum(e.astype(float) - 4, -9.0))
+    assert np.all(np.abs(c - q) <= step / 2 * (1 + 2.0 ** -8) + 2.0 ** -13 * np.abs(q))
+    plain, added2 = nv.rms_norm(x, w, residual=r)
+    assert torch.equal(added, added2)
+
+
+def test_norm_strides_offsets_and_in_place():
+    g = _gen(5)
+    w = _randn(g, (512,))
+    wide = _randn(g, (40, 1600))
+    for start in (0, 8, 3):                               # aligned and odd starts, row stride above H
+        x = wide[:, start:start + 512]
+        _close16(nv.rms_norm(x, w), layer.rms_norm(_np(x), _np(w), 1e-6), "bf16")
+        r = wide[:, 1024 + start:1536 + start]
+        y, a = nv.rms_norm(x, w, residual=r)
+        assert torch.equal(a, (x.float() + r.float()).to(torch.bfloat16))
+        _close16(y, layer.rms_norm(_np(a), _np(w), 1e-6), "bf16")
+    odd = _randn(g, (17, 1601))[:, :512]                  # odd row stride
+    _close16(nv.rms_norm(odd, w), layer.rms_norm(_np(odd), _np(w), 1e-6), "bf16")
+    once = _randn(g, (1, 512))                            # one row for all: stride 0
+    assert torch.equal(nv.rms_norm(once.expand(6, 512), w), nv.rms_norm(once.repeat(6, 1), w))
+    for H in (512, 509):
+        x, r = _randn(g, (64, H)), _randn(g, (64, H))
+        y, a = nv.rms_norm(x, w[:H].contiguous(), residual=r)
+        r2, x2 = r.clone(), x.clone()
+        y2, a2 = nv.rms_norm(x, w[:H].contiguous(), residual=r2, residual_out=r2)
+        assert a2 is r2 and torch.equal(r2, a) and torch.equal(y2, y)
+        y3, _ = nv.rms_norm(x2, w[:H].contiguous(), residual=r, residual_out=x2)
+        assert torch.equal(x2, a) and torch.equal(y3, y)
+
+
+def test_norm_special_values():
+    w = torch.ones(256, dtype=torch.bfloat16, device="cuda")
+    x = torch.zeros(5, 256, dtype=torch.bfloat16, device="cuda")
+    x[1] = 1e-30
+    x[2, 7] = float("nan")
+    x[3, 9] = float("inf")
+    x[4] = 2.0 ** 55
+    y = nv.rms_norm(x, w)
+    assert torch.all(y[0] == 0) and torch.all(y[2].isnan())
+    assert y[3, 9].isnan() and torch.all(y[3, :9] == 0)
+    assert torch.all(y[4] == 1)                           # 256 squares of 2^110 sum inside 32 bits
+    c, s = nv.rms_norm_e4m3(x, w, group=64)
+    assert torch.all(s[0] == 2.0 ** -100) and torch.all(c[0].float() == 0)
+    assert torch.all(c[2].float().isnan())
+    assert torch.all(c[4].float() == 448) and nv.rms_norm(x[:0], w).shape == (0, 256)
+
+
+# ----------------------------------------------------- cache write and read ---
+
+def _make_cache(pages, heads, page, D, act, kind, fill=float("nan"), layout="hnd"):
+    dt = E4M3 if kind == "e4m3" else DT[act]
+
+    def full(shape):
+        if kind == "e4m3":
+            return torch.full(shape, 0x7F, dtype=torch.uint8, device="cuda").view(E4M3)
+        return torch.full(shape, fill, dtype=dt, device="cuda")
+    if layout == "hnd":
+        k, v = full((pages, heads, page, D)), full((pages, heads, page, D))
+    elif layout == "nhd":
+        k, v = (full((pages, page, heads, D)).transpose(1, 2) for _ in range(2))
+    else:                                                 # one pool, keys and values of a page side by side, rows padded
+        pool = full((pages, 2, heads, page, D + 16))
+        k, v = pool[:, 0, :, :, :D], pool[:, 1, :, :, :D]
+    c = dict(k_cache=k, v_cache=v)
+    if kind == "e4m3":
+        c.update({n: torch.full((pages, heads, page), float("nan"), device="cuda") for n in ("k_scale", "v_scale")})
+    return c
+
+
+def _cached_values(c, which, slots, page):
+    """[T, heads, D] float64 of cached rows, read with torch."""
+    p, a = slots // page, slots % page
+    x = c[which + "_cache"]
+    if x.dtype == E4M3:
+        x = x.view(torch.uint8)[p, :, a].view(E4M3).double() * c[which + "_scale"][p, :, a].double()[..., None]
+    else:
+        x = x[p, :, a].double()
+    return x.cpu().numpy()
+
+
+ROPE_CASES = [
+    # T, Hq, Hkv, D, rot, page, axes/sections, interleaved, act, kind, layout
+    (1, 32, 8, 128, 128, 16, None, False, "bf16", "16", "hnd"),
+    (16, 32, 8, 128, 128, 16, None, False, "bf16", "e4m3", "hnd"),
+    (7, 4, 4, 64, 64, 1, None, True, "f16", "e4m3", "nhd"),
+    (33, 5, 1, 80, 80, 24, [20, 10, 10], False, "bf16", "16", "pool"),
+    (50, 6, 2, 256, 128, 64, [13, 21, 30], False, "f16", "16", "hnd"),
+    (19, 8, 2, 96, 34, 8, [5, 0, 12], False, "bf16", "e4m3", "pool"),
+    (19, 8, 2, 112, 38, 8, [19], True, "bf16", "e4m3", "nhd"),
+    (300, 40, 8, 128, 128, 64, [16, 24, 24], False, "bf16", "16", "hnd"),
+    (300, 12, 3, 192, 192, 32, [24, 24, 24, 24], True, "f16", "e4m3", "hnd"),
+    (5, 2, 1, 16, 2, 4, None, False, "bf16", "e4m3", "hnd"),
+    (5, 0, 1, 48, 0, 4, None, False, "bf16", "16", "hnd"),
+    (2000, 16, 4, 128, 64, 16, None, False, "bf16", "e4m3", "nhd"),
+]
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D,rot,page,sections,inter,act,kind,layout", ROPE_CASES)
+def test_rope_cache_write_and_read(T, Hq, Hkv, D, rot, page, sections, inter, act, kind, layout):
+    g, r = _gen(T + D), np.random.default_rng(T * 7 + D)
+    qkv = _randn(g, (T, Hq + 2 * Hkv, D), act)
+    q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+    rows, axes = 500, len(sections) if sections else 1
+    table = nv.rope_table(rows, rot)
+    positions = torch.from_numpy(r.integers(0, rows, (axes, T)))
+    pages = -(-T // page) + 2
+    slots = torch.from_numpy(r.permutation(pages * page)[:T]).cuda()
+    if T > 4:
+        slots[3] = -1
+    c = _make_cache(pages, Hkv, page, D, act, kind, layout=layout)
+    before = {n: t.clone() for n, t in c.items()}
+    pos = positions.cuda() if sections else positions[0].cuda()
+    out = nv.rope_cache_write(q, k, v, pos, table, slots=slots, sections=sections, interleaved=inter, **c)
+    gu.check_device_status()
+    tn = table.cpu().numpy()
+    turn = lambda x: layer.rope(x.float().cpu().numpy(), positions.numpy(), tn, sections, inter)  # noqa: E731
+    assert torch.equal(out.cpu(), torch.from_numpy(turn(q)).to(DT[act]))
+    held = (slots >= 0).cpu().numpy()
+    read = nv.cache_read(slots=slots, dtype=DT[act], **c)
+    for which, x, back in (("k", turn(k), read[0]), ("v", v.float().cpu().numpy(), read[1])):
+        if kind == "e4m3":
+            codes, s = layer.quantise(x)
+            want = codes * s[..., None].astype(np.float64)
+            p, a = slots // page, slots % page
+            assert np.array_equal(c[which + "_scale"][p, :, a].cpu().numpy()[held], s[held])
+        else:
+            want = torch.from_numpy(x).to(DT[act]).double().numpy()
+        got = _cached_values(c, which, slots, page)
+        assert np.array_equal(got[held], want[held])
+        back16 = torch.from_numpy(want.astype(np.float32)).to(DT[act])
+        back16[~torch.from_numpy(held)] = 0
+        assert torch.equal(back.cpu(), back16)
+    # nothing else was written
+    free = torch.ones(pages * page, dtype=torch.bool, device="cuda")
+    free[slots[slots >= 0]] = False
+    other = free.nonzero()[:, 0]
+    for n, t in c.items():
+        a, b = ((u.view(torch.uint8) if u.dtype == E4M3 else u)[other // page, :, other % page] for u in (t, before[n]))
+        assert torch.equal(torch.nan_to_num(a.float(), nan=-5.0), torch.nan_to_num(b.float(), nan=-5.0))
+
+
+def test_rope_in_place_and_separate_tensors():
+    g = _gen(9)
+    q, k, v = _randn(g, (40, 8, 128)), _randn(g, (40, 2, 128)), _randn(g, (40, 2, 128))
+    table, slots = nv.rope_table(64, 128), torch.arange(40, device="cuda")
+    pos = slots.clone()
+    for inter in (False, True):
+        a, b = (_make_cache(3, 2, 16, 128, "bf16", "16") for _ in range(2))
+        want = nv.rope_cache_write(q, k, v, pos, table, slots=slots, interleaved=inter, **a)
+        q2 = q.clone()
+        got = nv.rope_cache_write(q2, k, v, pos, table, slots=slots, interleaved=inter, q_out=q2, **b)
+        assert got is q2 and torch.equal(want, got)
+        for n in a:
+            assert torch.equal(a[n].view(torch.int16), b[n].view(torch.int16))
+
+
+def test_rope_out_of_range_is_reported_not_followed():
+    g = _gen(10)
+    q, k, v = _randn(g, (4, 2, 64)), _randn(g, (4, 1, 64)), _randn(g, (4, 1, 64))
+    table = nv.rope_table(10, 64)
+    c = _make_cache(2, 1, 4, 64, "bf16", "16", fill=0.0)
+    slots = torch.tensor([0, 8, 1 << 40, 2], device="cuda")
+    pos = torch.tensor([3, 4, 5, 6], device="cuda")
+    nv.rope_cache_write(q, k, v, pos, table, slots=slots, **c)
+    assert nv.device_status() == 8
+    assert torch.equal(c["v_cache"][0, 0, 0], v[0, 0]) and torch.equal(c["v_cache"][0, 0, 2], v[3, 0])
+    assert torch.all(c["v_cache"][1] == 0)
+    out = nv.rope_cache_write(q, k, v, torch.tensor([10, -1, 1 << 50, 0], device="cuda"), table,
+                              slots=torch.arange(4, device="cuda"), **c)
+    assert nv.device_status() == 8 and torch.equal(out, q)      # unrotated; position 0 rotates by nothing
+    kk, vv = nv.cache_read(slots=torch.tensor([8, 0], device="cuda"), **c)
+    assert nv.device_status() == 8 and torch.all(kk[0] == 0) and torch.equal(vv[1], v[0])
+
+
+def test_cache_write_special_values():
+    x = torch.zeros(4, 1, 64, dtype=torch.bfloat16, device="cuda")
+    x[1, 0, 5] = float("nan")
+    x[1, 0, 6] = 2.0
+    x[2, 0, 3] = float("inf")
+    x[3] = 1e-38
+    c = _make_cache(1, 1, 4, 64, "bf16", "e4m3")
+    slots = torch.arange(4, device="cuda")
+    nv.rope_cache_write(x, x, x, slots, nv.rope_table(4, 0), slots=slots, **c)
+    k, _ = nv.cache_read(slots=slots, dtype=torch.bfloat16, **c)
+    assert torch.all(k[0] == 0) and torch.all(k[3] == 0)
+    assert k[1, 0, 5].isnan() and k[1, 0, 6] == 2 and k[1].isnan().sum() == 1
+    assert torch.all(k[2].isnan())
+    gu.check_device_status()
+
+
+# -------------------------------------------------------------- attention ---
+
+def _attention_case(lengths, Hq, Hkv, D, page, act, kind, seed, layout="hnd", std=1.0, extra=3, width=None):
+    """A cache whose unused rows hold NaN and a table whose unused entries are -1."""
+    g, r = _gen(seed), np.random.default_rng(seed)
+    B, n = len(lengths), np.array(lengths)
+    per = -(-n // page)
+    pages = int(per.sum()) + extra
+    c = _make_cache(pages, Hkv, page, D, act, kind, layout=layout)
+    order = r.permutation(pages)
+    table = np.full((B, width or max(1, per.max())), -1, dtype=np.int32)
+    at, rows = 0, []
+    for b in range(B):
+        table[b, :per[b]] = order[at:at + per[b]]
+        at += per[b]
+        t = np.arange(n[b])
+        rows.append(table[b, t // page].astype(np.int64) * page + t % page)
+    slots = torch.from_numpy(np.concatenate(rows)).cuda() if n.sum() else torch.empty(0, dtype=torch.int64, device="cuda")
+    T = slots.numel()
+    k, v = _randn(g, (T, Hkv, D), act, std), _randn(g, (T, Hkv, D), act)
+    if kind == "e4m3":                                    # rows of very different sizes
+        v = (v.float() * torch.exp2(torch.randint(-12, 3, (T, Hkv, 1), generator=g, device="cuda").float())).to(DT[act])
+    nv.rope_cache_write(k, k, v, slots, nv.rope_table(1, 0), slots=slots, **c)
+    q = _randn(g, (B, Hq, D), act)
+    return c, q, torch.from_numpy(table).cuda(), torch.from_numpy(n.astype(np.int32)).cuda(), slots
+
+
+def _check_attention(c, q, table, lengths, slots, page, act, kind, window=0, scale=None, **kw):
+    out, lse = nv.paged_attention(q, block_table=table, lengths=lengths, window=window, softmax_scale=scale,
+                                  return_lse=True, **c, **kw)
+    gu.check_device_status()
+    k, v = _cached_values(c, "k", slots, page), _cached_values(c, "v", slots, page)
+    u_p = U["bf16"] if kind == "16" and act == "bf16" else U["f16"]
+    at = 0
+    got, got_lse, qn = _np(out), _np(lse), _np(q)
+    for b, n in enumerate(lengths.tolist()):
+        first = max(0, n - window) if window else 0
+        kk, vv = k[at + first:at + n], v[at + first:at + n]
+        at += n
+        ref, ref_lse, mag = layer.attend(qn[b], kk, vv, q.shape[2] ** -0.5 if scale is None else scale)
+        if n == 0:
+            assert np.all(got[b] == 0) and np.all(got_lse[b] == -np.inf)
+            continue
+        top = np.abs(vv).max() if vv.size else 0.0
+        bound = U[act] * np.abs(ref) + TINY[act] + (u_p + 2.0 ** -11) * mag + 2.0 ** -25 * n * top
+        err = np.abs(got[b] - ref)
+        assert np.all(err <= bound), (b, n, (err / bound).max())
+        assert np.all(np.abs(got_lse[b] - ref_lse) <= 2.0 ** -17 * (1 + np.abs(ref_lse))), (b, n)
+    return out, lse
+
+
+ATTN_CASES = [
+    # lengths, Hq, Hkv, D, page, act, kind, layout, window
+    ([1], 1, 1, 64, 16, "bf16", "16", "hnd", 0),
+    ([1, 2, 15, 16, 17, 31, 33, 0, 64], 32, 8, 128, 16, "bf16", "16", "hnd", 0),
+    ([0, 0, 5], 8, 1, 128, 8, "f16", "16", "nhd", 0),
+    ([0], 8, 8, 128, 8, "bf16", "e4m3", "hnd", 0),
+    ([1000], 32, 8, 128, 16, "bf16", "16", "hnd", 0),
+    ([1000, 3], 32, 8, 128, 1, "f16", "e4m3", "nhd", 0),
+    ([777, 130, 1], 5, 1, 80, 24, "bf16", "16", "pool", 0),
+    ([777, 130, 1], 5, 1, 80, 24, "bf16", "e4m3", "pool", 0),
+    ([300, 41], 12, 1, 128, 32, "f16", "16", "hnd", 0),
+    ([300, 41], 16, 1, 128, 32, "bf16", "e4m3", "hnd", 0),
+    ([257, 90], 20, 1, 128, 64, "bf16", "16", "hnd", 0),      # more heads a key head than one MMA row block
+    ([257, 90], 40, 1, 64, 64, "bf16", "e4m3", "hnd", 0),
+    ([400, 7], 8, 2, 256, 16, "bf16", "16", "hnd", 0),
+    ([400, 7], 32, 2, 256, 16, "bf16", "e4m3", "nhd", 0),
+    ([100, 7], 4, 2, 192, 16, "f16", "16", "hnd", 0),
+    ([100, 7], 4, 2, 16, 16, "bf16", "16", "hnd", 0),
+    ([100, 7], 4, 2, 16, 16, "f16", "e4m3", "hnd", 0),
+    ([100, 7], 4, 2, 48, 40, "bf16", "e4m3", "hnd", 0),
+    ([500, 100, 17, 16, 0, 33], 8, 2, 128, 16, "bf16", "16", "hnd", 17),
+    ([500, 100, 17, 16, 0, 33], 8, 2, 64, 24, "f16", "e4m3", "hnd", 100),
+    ([3000, 1], 8, 2, 128, 16, "bf16", "16", "hnd", 1),
+    ([9000, 33, 4000], 16, 2, 128, 128, "bf16", "16", "hnd", 0),
+    ([9000, 33, 4000], 16, 2, 128, 128, "bf16", "e4m3", "hnd", 0),
+    ([9000, 33, 4000], 16, 16, 64, 128, "f16", "16", "hnd", 0),
+    (list(range(0, 300)), 4, 2, 64, 16, "bf16", "16", "hnd", 0),
+    ([20] * 700, 8, 4, 64, 16, "bf16", "e4m3", "hnd", 0),
+]
+
+
+@pytest.mark.parametrize("lengths,Hq,Hkv,D,page,act,kind,layout,window", ATTN_CASES)
+def test_paged_attention(lengths, Hq, Hkv, D, page, act, kind, layout, window):
+    case = _attention_case(lengths, Hq, Hkv, D, page, act, kind, len(lengths) * 31 + D + Hq, layout)
+    out, lse = _check_attention(*case, page, act, kind, window)
+    again, lse2 = nv.paged_attention(case[1], block_table=case[2], lengths=case[3], window=window, return_lse=True,
+                                     **case[0])
+    assert torch.equal(out.view(torch.int16), again.view(torch.int16))
+    assert torch.equal(lse.view(torch.int32), lse2.view(torch.int32))
+
+
+@pytest.mark.parametrize("kind", ["16", "e4m3"])
+@pytest.mark.parametrize("scale", [0.0, -0.1, 2.0])
+def test_paged_attention_scales_and_peaked_rows(kind, scale):
+    """Negative and zero scales, and scores whose largest comes at any token."""
+    case = _attention_case([2000, 65, 16], 8, 2, 128, 16, "bf16", kind, 77, std=2.0)
+    _check_attention(*case, 16, "bf16", kind, scale=scale)
+
+
+@pytest.mark.parametrize("kind", ["16", "e4m3"])
+def test_paged_attention_strided_query_and_large_queries(kind):
+    case = list(_attention_case([120, 3], 8, 2, 128, 16, "bf16", kind, 78))
+    wide = _randn(_gen(79), (2, 12, 128), std=1e4)
+    case[1] = wide[:, 2:10]                               # scores in the thousands: one token takes it all
+    _check_attention(*case, 16, "bf16", kind, scale=1e-4)
+    assert torch.equal(nv.paged_attention(case[1], block_table=case[2], lengths=case[3], **case[0]),
+                       nv.paged_attention(case[1].contiguous(), block_table=case[2], lengths=case[3], **case[0]))
+
+
+def test_paged_attention_nan_and_infinity_in_held_tokens():
+    c, q, table, lengths, slots = _attention_case([40, 40], 4, 2, 64, 16, "bf16", "16", 80)
+    c["k_cache"][int(table[0, 1]), 0, 3, 5] = float("nan")
+    c["v_cache"][int(table[1, 0]), 1, 2, 7] = float("inf")
+    out = nv.paged_attention(q, block_table=table, lengths=lengths, **c)
+    assert torch.all(out[0, :2].isnan()) and torch.all(out[0, 2:].isfinite())
+    assert torch.all(out[1, 2:, 7] == float("inf")) and torch.all(out[1, :2].isfinite())
+
+
+def test_paged_attention_bad_lengths_and_pages_are_reported():
+    c, q, table, lengths, slots = _attention_case([40, 40], 4, 2, 64, 16, "bf16", "16", 81)
+    good = nv.paged_attention(q, block_table=table, lengths=lengths, **c)
+    gu.check_device_status()
+    bad = table.clone()
+    bad[1, 2] = 1 << 30
+    out = nv.paged_attention(q, block_table=bad, lengths=lengths, **c)
+    assert nv.device_status() == 8 and torch.equal(out[0], good[0])
+    out = nv.paged_attention(q, block_table=table, lengths=torch.tensor([40, -7], dtype=torch.int32, device="cuda"), **c)
+    assert nv.device_status() == 8 and torch.equal(out[0], good[0]) and torch.all(out[1] == 0)
+    nv.paged_attention(q, block_table=table, lengths=torch.tensor([40, 1 << 30], dtype=torch.int32, device="cuda"), **c)
+    assert nv.device_status() == 8
+
+
+def test_paged_attention_shared_pages_and_drafted_tokens():
+    """Two rows with one table and lengths one apart: each attends to its own tokens."""
+    c, q, table, lengths, slots = _attention_case([100], 8, 2, 128, 16, "bf16", "16", 82)
+    both = nv.paged_attention(q.repeat(2, 1, 1), block_table=table.repeat(2, 1),
+                              lengths=torch.tensor([99, 100], dtype=torch.int32, device="cuda"), **c)
+    assert torch.equal(both[1:], nv.paged_attention(q, block_table=table, lengths=lengths, **c))
+    assert not torch.equal(both[0], both[1])
+
+
+def test_cache_rows_past_four_gigabytes():
+    """A pool whose rows lie past 2^32 bytes from its start."""
+    pages, Hkv, page, D = 90000, 2, 128, 128              # 5.9 GB a tensor
+    k = torch.empty((pages, Hkv, page, D), dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    c, q, table, lengths, slots = _attention_case([500, 200], 8, Hkv, D, page, "bf16", "16", 83)
+    small = nv.paged_attention(q, block_table=table, lengths=lengths, **c)
+    high = torch.where(table >= 0, pages - 1 - table, table)
+    rows = nv.cache_read(slots=slots, **c)
+    far = (pages - 1 - slots // page) * page + slots % page
+    nv.rope_cache_write(rows[0], rows[0], rows[1], slots, nv.rope_table(1, 0), k, v, far)
+    assert torch.equal(nv.paged_attention(q, k, v, high, lengths), small)
+    back = nv.cache_read(k, v, far)
+    assert torch.equal(back[0], rows[0]) and torch.equal(back[1], rows[1])
+    gu.check_device_status()
+
+
+def test_side_stream_and_graph_replay_as_sequences_grow():
+    c, q, table, lengths, slots = _attention_case([200, 64], 8, 2, 128, 16, "bf16", "e4m3", 84)
+    want = {}
+    for n in ((200, 64), (17, 1), (0, 63)):
+        lengths.copy_(torch.tensor(n, dtype=torch.int32))
+        want[n] = nv.paged_attention(q, block_table=table, lengths=lengths, **c)
+    size = nv.paged_attention_workspace_size(2, 8, 2, 128)
+    ws = torch.full((max(size, 1),), 0xFF, dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(q)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        nv.paged_attention(q, block_table=table, lengths=lengths, out=out, workspace=ws, **c)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            nv.paged_attention(q, block_table=table, lengths=lengths, out=out, workspace=ws, **c)
+        for n, w in want.items():
+            lengths.copy_(torch.tensor(n, dtype=torch.int32))
+            out.fill_(3.0)
+            g.replay()
+            s.synchronize()
+            assert torch.equal(out, w)
+    torch.cuda.current_stream().wait_stream(s)
+
+
+def test_refusals():
+    g = _gen(90)
+    x, w = _randn(g, (4, 64)), _randn(g, (64,))
+    c = _make_cache(4, 2, 16, 64, "bf16", "16")
+    e = _make_cache(4, 2, 16, 64, "bf16", "e4m3")
+    q, kv = _randn(g, (3, 8, 64)), _randn(g, (3, 2, 64))
+    slots, table = torch.arange(3, device="cuda"), nv.rope_table(8, 64)
+    bt, n = torch.zeros((3, 2), dtype=torch.int32, device="cuda"), torch.ones(3, dtype=torch.int32, device="cuda")
+
+    def refused(status, fn, *a, **kw):
+        with pytest.raises(nv.Nvfp4Error) as err:
+            fn(*a, **kw)
+        assert err.value.status == status, err.value
+
+    refused(1, nv.rms_norm, x.float(), w)
+    refused(1, nv.rms_norm, x, w.half())
+    refused(2, nv.rms_norm, x, w[:32])
+    refused(1, nv.rms_norm, x.cpu(), w)
+    refused(1, nv.rms_norm, x.t(), w[:4])
+    refused(1, nv.rms_norm, x, w, eps=float("nan"))
+    refused(1, nv.rms_norm, x, w, residual_out=x)
+    refused(2, nv.rms_norm_e4m3, x, w, group=24)
+    refused(2, nv.rms_norm_e4m3, x, w, group=8)
+    refused(2, nv.rms_norm_e4m3, x, w, group=-16)
+    write = lambda q=q, k=kv, v=kv, pos=slots, tab=table, slots=slots, cc=c, **kw: nv.rope_cache_write(  # noqa: E731
+        q, k, v, pos, tab, slots=slots, **cc, **kw)
+    refused(1, write, q=q.half())
+    refused(2, write, k=kv[:2])
+    refused(2, write, q=_randn(g, (3, 8, 32)))
+    refused(1, write, slots=slots.int())
+    refused(2, write, tab=nv.rope_table(8, 80))
+    refused(2, write, pos=torch.zeros((3, 3), dtype=torch.int64, device="cuda"), sections=[8, 8, 8])
+    refused(2, write, pos=torch.zeros((5, 3), dtype=torch.int64, device="cuda"), sections=[8, 8, 8, 4, 4])
+    refused(1, write, pos=torch.zeros((2, 3), dtype=torch.int64, device="cuda"), sections=[40, -8])
+    refused(1, write, cc=dict(e, k_scale=None))
+    refused(1, write, cc=dict(c, k_scale=e["k_scale"], v_scale=e["v_scale"]))
+    refused(1, write, cc=dict(c, v_cache=c["v_cache"].transpose(1, 2).contiguous().transpose(1, 2)))
+    refused(3, write, q=_randn(g, (3, 8, 65))[:, :, 1:])
+    attend = lambda q=q, bt=bt, n=n, cc=c, **kw: nv.paged_attention(q, block_table=bt, lengths=n, **cc, **kw)  # noqa: E731
+    refused(2, attend, q=_randn(g, (3, 7, 64)))
+    refused(1, attend, n=n.long())
+    refused(2, attend, n=n[:2])
+    refused(1, attend, window=-1)
+    refused(1, attend, softmax_scale=float("inf"))
+    refused(1, attend, bt=bt.t().contiguous().t())
+    refused(2, attend, cc=_make_cache(4, 2, 16, 24, "bf16", "16"), q=_randn(g, (3, 8, 24)))
+    if nv.paged_attention_workspace_size(3, 8, 2, 64):
+        refused(4, attend, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    refused(1, nv.cache_read, slots=slots, **e)
+    refused(1, nv.cache_read, slots=slots, dtype=torch.float16, **c)
+    assert attend(q=q[:0], bt=bt[:0], n=n[:0]).shape == (0, 8, 64)
+    assert write(q=q[:0], k=kv[:0], v=kv[:0], pos=slots[:0], slots=slots[:0]).shape == (0, 8, 64)
+    assert nv.cache_read(slots=slots[:0], **c)[0].shape == (0, 2, 64)
+    gu.check_device_status()

@@ -10,6 +10,9 @@ in the library's CUDA kernels; there is no Python or CPU fallback.
     y = gemm(x_bf16, w, pre_quant_scale=s)    # AWQ checkpoints
     y = gemm(x_fp16, w)                       # FP16 activations: FP16 weights and output
 
+and, between the linears (layer_ops): rms_norm, rms_norm_e4m3, rope_cache_write,
+cache_read and paged_attention.
+
 The activation dtype (torch.bfloat16 or torch.float16) selects the entry
 point (nvfp4_w4a16_gemm or nvfp4_w4a16_gemm_f16, and likewise for the MoE
 layer and the dequant).
@@ -21,11 +24,15 @@ import torch
 
 from . import _lib
 from ._lib import Nvfp4Error
+from .layer_ops import (cache_read, paged_attention, paged_attention_workspace_size, rms_norm, rms_norm_e4m3,
+                        rope_cache_write, rope_table)
 
 __all__ = ["Nvfp4Error", "NVFP4Weight", "repack", "repack_size", "swizzled_scales_size", "dequant", "gemm",
            "gemm_workspace_size", "gemm_plan", "moe_grouped", "moe_plan", "moe_route", "moe_workspace_size",
            "moe_finalize_pre_quant_scale",
            "mlp", "mlp_workspace_size",
+           "rms_norm", "rms_norm_e4m3", "rope_table", "rope_cache_write", "cache_read",
+           "paged_attention", "paged_attention_workspace_size",
            "device_status",
            "abi_version"]
 

@@ -15,6 +15,17 @@ c_size = ctypes.c_size_t
 c_vp = ctypes.c_void_p
 c_float = ctypes.c_float
 
+
+
+class KVCache(ctypes.Structure):
+    """nvfp4_kv_cache of the header."""
+    _fields_ = [("k", c_vp), ("v", c_vp), ("k_scale", c_vp), ("v_scale", c_vp),
+                ("num_pages", c_i64), ("page_size", c_i64), ("heads", c_i64), ("head_dim", c_i64),
+                ("page_stride", c_i64), ("head_stride", c_i64), ("token_stride", c_i64), ("type", c_i64)]
+
+
+c_cache = ctypes.POINTER(KVCache)
+
 # name -> (restype, argtypes), mirroring include/nvfp4_w4a16.h
 SIGNATURES = {
     "nvfp4_abi_version": (c_int, []),
@@ -47,12 +58,20 @@ SIGNATURES = {
     "nvfp4_w4a16_moe_noalloc_scratch_bytes": (c_size, []),
     "nvfp4_w4a16_moe_grouped_noalloc": (c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_int, c_int, c_i64,
                                                 c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "nvfp4_rms_norm": (c_int, [c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_i64, c_float, c_int, c_i64, c_int, c_vp, c_vp,
+                               c_vp, c_vp]),
+    "nvfp4_rope_cache_write": (c_int, [c_vp, c_i64, c_i64, c_vp, c_i64, c_i64, c_vp, c_i64, c_i64, c_i64, c_i64, c_vp,
+                                       c_int, c_vp, c_vp, c_i64, c_i64, c_int, c_int, c_vp, c_cache, c_vp, c_vp]),
+    "nvfp4_kv_cache_read": (c_int, [c_cache, c_vp, c_i64, c_int, c_vp, c_vp, c_vp]),
+    "nvfp4_paged_attention_workspace": (c_size, [c_i64, c_i64, c_i64, c_i64]),
+    "nvfp4_paged_attention": (c_int, [c_vp, c_i64, c_i64, c_cache, c_vp, c_i64, c_i64, c_vp, c_i64, c_i64, c_float,
+                                      c_i64, c_int, c_vp, c_vp, c_vp, c_size, c_vp]),
 }
 
 STATUS_NAMES = {
     0: "NVFP4_OK", 1: "NVFP4_ERR_INVALID_ARG", 2: "NVFP4_ERR_UNSUPPORTED_SHAPE",
     3: "NVFP4_ERR_ALIGNMENT", 4: "NVFP4_ERR_WORKSPACE", 5: "NVFP4_ERR_CUDA",
-    6: "NVFP4_ERR_TIMEOUT", 7: "NVFP4_ERR_BAD_WEIGHT",
+    6: "NVFP4_ERR_TIMEOUT", 7: "NVFP4_ERR_BAD_WEIGHT", 8: "NVFP4_ERR_BAD_INDEX",
 }
 
 

@@ -1,0 +1,286 @@
+// Rotary positions with the write into a paged key-value cache, and the read of
+// cached rows.
+//
+// Rotation: frequency i of R/2 belongs to the position axis whose section holds
+// it; with (c, s) = (table[p, i], table[p, R/2 + i]) of that axis's position p,
+//     (x1, x2) -> (x1 c - x2 s, x2 c + x1 s)
+// for the pair (x[i], x[i + R/2]), or (x[2i], x[2i+1]) when interleaved; elements
+// from R on pass through.  The products and their sum are separate 32-bit
+// roundings (no fused multiply-add), so that a key is the same bits, and gets
+// the same 8-bit code, in whatever kernel it is computed.
+// Write: keys (rotated) and values rounded once, to the activation type or to
+// E4M3 with s = max(amax / 448, 2^-100) per token and head.
+#include <algorithm>
+
+#include "common.cuh"
+#include "kv_cache.cuh"
+#include "numeric.cuh"
+#include "ptx.cuh"
+
+namespace nvfp4 {
+
+nvfp4_status check_cache(const char* fn, const nvfp4_kv_cache* c, CacheView* view) {
+    if (!c) return fail(NVFP4_ERR_INVALID_ARG, "%s: null cache", fn);
+    if (c->type != NVFP4_CACHE_16 && c->type != NVFP4_CACHE_E4M3)
+        return fail(NVFP4_ERR_INVALID_ARG, "%s: cache type %lld must be NVFP4_CACHE_16 or NVFP4_CACHE_E4M3", fn, (long long)c->type);
+    const bool e4m3 = c->type == NVFP4_CACHE_E4M3;
+    const int64_t es = e4m3 ? 1 : 2;
+    if (c->num_pages <= 0 || c->num_pages > INT32_MAX || c->page_size <= 0 || c->page_size > (1 << 20) || c->heads <= 0 || c->heads > 4096)
+        return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s: cache of %lld pages of %lld tokens, %lld heads (limits 2^31-1, 2^20, 4096)", fn,
+                    (long long)c->num_pages, (long long)c->page_size, (long long)c->heads);
+    if (c->head_dim <= 0 || c->head_dim % 16 != 0 || c->head_dim > kMaxHeadDim)
+        return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s: head_dim=%lld must be a multiple of 16 up to %d", fn, (long long)c->head_dim, kMaxHeadDim);
+    if (!c->k || !c->v || (e4m3 && (!c->k_scale || !c->v_scale)))
+        return fail(NVFP4_ERR_INVALID_ARG, "%s: null cache pointer", fn);
+    if (c->page_stride <= 0 || c->head_stride <= 0 || c->token_stride < c->head_dim)
+        return fail(NVFP4_ERR_INVALID_ARG, "%s: cache strides (%lld, %lld, %lld) must be positive and hold a row", fn,
+                    (long long)c->page_stride, (long long)c->head_stride, (long long)c->token_stride);
+    if (c->page_stride * es % 16 || c->head_stride * es % 16 || c->token_stride * es % 16 || !aligned(c->k, 16) || !aligned(c->v, 16))
+        return fail(NVFP4_ERR_ALIGNMENT, "%s: cache rows must start on 16-byte boundaries", fn);
+    if (e4m3 && (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)))
+        return fail(NVFP4_ERR_ALIGNMENT, "%s: cache scales must be 4-byte aligned", fn);
+    view->k = (uint8_t*)c->k; view->v = (uint8_t*)c->v;
+    view->k_scale = e4m3 ? c->k_scale : nullptr; view->v_scale = e4m3 ? c->v_scale : nullptr;
+    view->num_pages = c->num_pages; view->num_slots = c->num_pages * c->page_size;
+    view->page_bytes = c->page_stride * es; view->head_bytes = c->head_stride * es; view->token_bytes = c->token_stride * es;
+    view->page_size = (int)c->page_size; view->heads = (int)c->heads; view->D = (int)c->head_dim;
+    view->e4m3 = e4m3;
+    return NVFP4_OK;
+}
+
+namespace {
+
+constexpr int kMaxAxes = 4;
+
+struct RopeParams {
+    const uint16_t *q, *k, *v;
+    int64_t q_token, q_head, k_token, k_head, v_token, v_head;   // strides, elements
+    const int64_t* positions;      // [axes, T]
+    const float* table;            // [rows, rot]: cosines, then sines
+    const int64_t* slots;
+    uint16_t* q_out;               // [T, Hq, D]
+    int64_t T, rows;
+    int Hq, Hkv, D, rot, axes;
+    int end[kMaxAxes];             // frequencies [end[a-1], end[a]) belong to axis a
+    int* status;
+    CacheView cache;
+};
+
+// The position of frequency f's axis, or -1 (recorded) outside the table.
+__device__ __forceinline__ int64_t axis_position(const RopeParams& p, int64_t t, int f) {
+    int a = 0;
+    while (a + 1 < p.axes && f >= p.end[a]) ++a;
+    const int64_t pos = p.positions[a * p.T + t];
+    if ((uint64_t)pos < (uint64_t)p.rows) return pos;
+    record_status(p.status, NVFP4_ERR_BAD_INDEX);
+    return -1;
+}
+
+// A warp takes one head of one token, a lane every 32nd element.
+template <bool F16, bool INTER>
+__global__ void __launch_bounds__(256) rope_write_any_kernel(RopeParams p) {
+    const int lane = threadIdx.x & 31;
+    const int heads = p.Hq + 2 * p.Hkv;
+    const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
+    const int half = p.rot / 2;
+    for (int64_t w = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); w < p.T * heads; w += warps) {
+        const int64_t t = w / heads;
+        int h = (int)(w % heads);
+        const int kind = h < p.Hq ? 0 : h < p.Hq + p.Hkv ? 1 : 2;       // query, key, value
+        h -= kind == 0 ? 0 : kind == 1 ? p.Hq : p.Hq + p.Hkv;
+        const int64_t slot = p.slots[t];
+        if (kind > 0 && slot < 0) continue;
+        if (kind > 0 && slot >= p.cache.num_slots) {
+            if (lane == 0) record_status(p.status, NVFP4_ERR_BAD_INDEX);
+            continue;
+        }
+        const uint16_t* x = kind == 0 ? p.q + t * p.q_token + h * p.q_head
+                          : kind == 1 ? p.k + t * p.k_token + h * p.k_head : p.v + t * p.v_token + h * p.v_head;
+        float y[kMaxHeadDim / 32];
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < kMaxHeadDim / 32; ++i) {
+            const int d = lane + 32 * i;
+            y[i] = 0.f;
+            if (d >= p.D) continue;
+            float v = act_to_f32<F16>(x[d]);
+            if (kind < 2 && d < p.rot) {
+                const int f = INTER ? d / 2 : d % half;
+                const bool first = INTER ? d % 2 == 0 : d < half;
+                const float other = act_to_f32<F16>(x[INTER ? d ^ 1 : first ? d + half : d - half]);
+                const int64_t pos = axis_position(p, t, f);
+                const float c = pos < 0 ? 1.f : p.table[pos * p.rot + f], s = pos < 0 ? 0.f : p.table[pos * p.rot + half + f];
+                v = first ? __fsub_rn(__fmul_rn(v, c), __fmul_rn(other, s)) : __fadd_rn(__fmul_rn(v, c), __fmul_rn(other, s));
+            }
+            y[i] = v;
+            amax = fmaxf(amax, fabsf(v));
+        }
+        __syncwarp();                                  // q_out may be q: no store before every lane has read its pair
+        if (kind == 0) {
+#pragma unroll
+            for (int i = 0; i < kMaxHeadDim / 32; ++i)
+                if (lane + 32 * i < p.D) p.q_out[(t * p.Hq + h) * p.D + lane + 32 * i] = f32_to_act_bits<F16>(y[i]);
+            continue;
+        }
+        const int64_t page = slot / p.cache.page_size;
+        const int at = (int)(slot % p.cache.page_size);
+        uint8_t* row = (kind == 1 ? p.cache.k : p.cache.v) + p.cache.row(page, h, at);
+        if (!p.cache.e4m3) {
+#pragma unroll
+            for (int i = 0; i < kMaxHeadDim / 32; ++i)
+                if (lane + 32 * i < p.D) ((uint16_t*)row)[lane + 32 * i] = f32_to_act_bits<F16>(y[i]);
+            continue;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const float s = e4m3_scale(amax);
+        if (lane == 0) (kind == 1 ? p.cache.k_scale : p.cache.v_scale)[p.cache.scale_at(page, h, at)] = s;
+#pragma unroll
+        for (int i = 0; i < kMaxHeadDim / 32; ++i)
+            if (lane + 32 * i < p.D) row[lane + 32 * i] = (uint8_t)f32_to_e4m3x2(__fdiv_rn(y[i], s), 0.f);
+    }
+}
+
+struct ReadParams {
+    CacheView cache;
+    const int64_t* slots;
+    uint16_t *k_out, *v_out;       // [T, heads, D]
+    int64_t T;
+    int* status;
+};
+
+// A thread takes 16 elements of one row.
+template <bool F16, bool E4M3>
+__global__ void __launch_bounds__(256) cache_read_kernel(ReadParams p) {
+    const int per = p.cache.D / 16;
+    const int64_t total = p.T * p.cache.heads * per;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t row = i / per;
+        const int c = (int)(i % per);
+        const int64_t t = row / p.cache.heads;
+        const int h = (int)(row % p.cache.heads);
+        const int64_t slot = p.slots[t];
+        const bool held = slot >= 0 && slot < p.cache.num_slots;
+        if (slot >= p.cache.num_slots) record_status(p.status, NVFP4_ERR_BAD_INDEX);
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+            uint4 out[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+            if (held) {
+                const int64_t page = slot / p.cache.page_size;
+                const int at = (int)(slot % p.cache.page_size);
+                const uint8_t* src = (kv == 0 ? p.cache.k : p.cache.v) + p.cache.row(page, h, at) + c * (E4M3 ? 16 : 32);
+                if (!E4M3) {
+                    out[0] = ((const uint4*)src)[0];
+                    out[1] = ((const uint4*)src)[1];
+                } else {
+                    const float s = (kv == 0 ? p.cache.k_scale : p.cache.v_scale)[p.cache.scale_at(page, h, at)];
+                    const uint4 w = *(const uint4*)src;
+                    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+                    uint32_t* o = (uint32_t*)out;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 a = act2_to_f32<true>(e4m3x2_to_f16x2((uint16_t)in[j]));
+                        const float2 b = act2_to_f32<true>(e4m3x2_to_f16x2((uint16_t)(in[j] >> 16)));
+                        o[2 * j] = f32_to_act2<F16>(a.x * s, a.y * s);
+                        o[2 * j + 1] = f32_to_act2<F16>(b.x * s, b.y * s);
+                    }
+                }
+            }
+            uint4* dst = (uint4*)((kv == 0 ? p.k_out : p.v_out) + row * p.cache.D + c * 16);
+            dst[0] = out[0];
+            dst[1] = out[1];
+        }
+    }
+}
+
+bool no_device(int** status) {
+    *status = device_status_ptr();
+    return *status == nullptr;
+}
+
+}  // namespace
+}  // namespace nvfp4
+
+using namespace nvfp4;
+
+extern "C" nvfp4_status nvfp4_rope_cache_write(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                                               const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                                               const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                                               int64_t T, int64_t Hq, const int64_t* positions, int axes,
+                                               const int32_t* sections, const float* table, int64_t table_rows, int64_t rot,
+                                               int interleaved, int f16, const int64_t* slots,
+                                               const nvfp4_kv_cache* cache, void* q_out, void* stream) {
+    const char* fn = "nvfp4_rope_cache_write";
+    RopeParams p{};
+    if (nvfp4_status st = check_cache(fn, cache, &p.cache)) return st;
+    if (T < 0 || Hq < 0) return fail(NVFP4_ERR_INVALID_ARG, "%s: negative size T=%lld Hq=%lld", fn, (long long)T, (long long)Hq);
+    if (T > INT32_MAX || Hq > 65536) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s: T=%lld or Hq=%lld too large", fn, (long long)T, (long long)Hq);
+    if ((f16 != 0 && f16 != 1) || (interleaved != 0 && interleaved != 1))
+        return fail(NVFP4_ERR_INVALID_ARG, "%s: f16=%d and interleaved=%d must be 0 or 1", fn, f16, interleaved);
+    const int64_t D = p.cache.D;
+    if (rot < 0 || rot % 2 != 0 || rot > D) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s: rot=%lld must be even and at most head_dim=%lld", fn, (long long)rot, (long long)D);
+    if (axes < 1 || axes > kMaxAxes) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s: axes=%d must be 1 to %d", fn, axes, kMaxAxes);
+    if (axes > 1 && !sections) return fail(NVFP4_ERR_INVALID_ARG, "%s: %d axes need their sections", fn, axes);
+    int64_t sum = 0;
+    for (int a = 0; a < axes; ++a) {
+        const int64_t n = sections ? sections[a] : rot / 2;
+        if (n < 0) return fail(NVFP4_ERR_INVALID_ARG, "%s: negative section", fn);
+        sum += n;
+        p.end[a] = (int)std::min<int64_t>(sum, kMaxHeadDim);
+    }
+    if (sum != rot / 2) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s: the sections sum to %lld, not to rot/2=%lld", fn, (long long)sum, (long long)(rot / 2));
+    if (T == 0) return NVFP4_OK;
+    if ((Hq > 0 && (!q || !q_out)) || !k || !v || !positions || !slots || (rot > 0 && !table))
+        return fail(NVFP4_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (rot > 0 && table_rows <= 0) return fail(NVFP4_ERR_INVALID_ARG, "%s: table_rows=%lld must be positive", fn, (long long)table_rows);
+    const int64_t strides[] = {q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride, v_head_stride};
+    for (int64_t s : strides) {
+        if (s < 0) return fail(NVFP4_ERR_INVALID_ARG, "%s: negative stride", fn);
+        if (s % 8) return fail(NVFP4_ERR_ALIGNMENT, "%s: strides must be multiples of 8 elements", fn);
+    }
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(table, 16) || !aligned(positions, 8) || !aligned(slots, 8))
+        return fail(NVFP4_ERR_ALIGNMENT, "%s: q, k, v, q_out and table must be 16-byte aligned, positions and slots 8-byte", fn);
+    if (no_device(&p.status)) return fail(NVFP4_ERR_CUDA, "%s: no CUDA device", fn);
+    p.q = (const uint16_t*)q; p.k = (const uint16_t*)k; p.v = (const uint16_t*)v;
+    p.q_token = q_token_stride; p.q_head = q_head_stride; p.k_token = k_token_stride; p.k_head = k_head_stride;
+    p.v_token = v_token_stride; p.v_head = v_head_stride;
+    p.positions = positions; p.table = table; p.slots = slots; p.q_out = (uint16_t*)q_out;
+    p.T = T; p.rows = table_rows; p.Hq = (int)Hq; p.Hkv = p.cache.heads; p.D = (int)D; p.rot = (int)rot; p.axes = axes;
+    cudaStream_t s = (cudaStream_t)stream;
+    const int64_t warps = T * (Hq + 2 * p.Hkv);
+    const int grid = (int)std::min<int64_t>(ceil_div(warps, 8), (int64_t)sm_count() * 8);
+    if (f16) {
+        if (interleaved) rope_write_any_kernel<true, true><<<grid, 256, 0, s>>>(p);
+        else rope_write_any_kernel<true, false><<<grid, 256, 0, s>>>(p);
+    } else {
+        if (interleaved) rope_write_any_kernel<false, true><<<grid, 256, 0, s>>>(p);
+        else rope_write_any_kernel<false, false><<<grid, 256, 0, s>>>(p);
+    }
+    return check_cuda(cudaGetLastError(), fn);
+}
+
+extern "C" nvfp4_status nvfp4_kv_cache_read(const nvfp4_kv_cache* cache, const int64_t* slots, int64_t T, int f16,
+                                            void* k_out, void* v_out, void* stream) {
+    const char* fn = "nvfp4_kv_cache_read";
+    ReadParams p{};
+    if (nvfp4_status st = check_cache(fn, cache, &p.cache)) return st;
+    if (T < 0) return fail(NVFP4_ERR_INVALID_ARG, "%s: negative size T=%lld", fn, (long long)T);
+    if (f16 != 0 && f16 != 1) return fail(NVFP4_ERR_INVALID_ARG, "%s: f16=%d must be 0 or 1", fn, f16);
+    if (T > INT32_MAX) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s: T=%lld too large", fn, (long long)T);
+    if (T == 0) return NVFP4_OK;
+    if (!slots || !k_out || !v_out) return fail(NVFP4_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (!aligned(slots, 8) || !aligned(k_out, 16) || !aligned(v_out, 16))
+        return fail(NVFP4_ERR_ALIGNMENT, "%s: slots must be 8-byte aligned, k_out and v_out 16-byte", fn);
+    if (no_device(&p.status)) return fail(NVFP4_ERR_CUDA, "%s: no CUDA device", fn);
+    p.slots = slots; p.k_out = (uint16_t*)k_out; p.v_out = (uint16_t*)v_out; p.T = T;
+    cudaStream_t s = (cudaStream_t)stream;
+    const int64_t threads = T * p.cache.heads * (p.cache.D / 16);
+    const int grid = (int)std::min<int64_t>(ceil_div(threads, 256), (int64_t)sm_count() * 16);
+    if (p.cache.e4m3) {
+        if (f16) cache_read_kernel<true, true><<<grid, 256, 0, s>>>(p);
+        else cache_read_kernel<false, true><<<grid, 256, 0, s>>>(p);
+    } else {
+        cache_read_kernel<false, false><<<grid, 256, 0, s>>>(p);        // a copy: the type does not matter
+    }
+    return check_cuda(cudaGetLastError(), fn);
+}
