@@ -5,6 +5,8 @@ implementation to fall back to.
 """
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 from . import build_lib
@@ -106,6 +108,27 @@ def load(build_if_missing=False):
         fn.argtypes = args
     _handle = h
     return h
+
+
+_binding = None
+
+
+def load_binding():
+    """The compiled Python entry points of layer_ops (built with the library)."""
+    global _binding
+    if _binding is None:
+        load()
+        name = "_nvfp4_binding"
+        if not os.path.exists(build_lib.BINDING):
+            raise RuntimeError(
+                f"Python module not built ({build_lib.BINDING} missing); run "
+                "`python -c 'import __graft_entry__ as g; g.build()'` first")
+        loader = importlib.machinery.ExtensionFileLoader(name, build_lib.BINDING)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_file_location(name, build_lib.BINDING, loader=loader))
+        loader.exec_module(module)
+        module.set_error_type(Nvfp4Error)
+        _binding = module
+    return _binding
 
 
 def check(status):
