@@ -27,75 +27,221 @@ struct NormParams {
 };
 
 template <bool MAX>
-__device__ __forceinline__ float warp_reduce(float v) {
+__device__ __forceinline__ float join(float a, float b) { return MAX ? fmaxf(a, b) : a + b; }
+
+// Reduction over groups of `lanes` neighbouring lanes (a power of two).
+template <bool MAX>
+__device__ __forceinline__ float lane_reduce(float v, int lanes = 32) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float u = __shfl_xor_sync(0xffffffffu, v, o);
-        v = MAX ? fmaxf(v, u) : v + u;
-    }
+    for (int o = 16; o > 0; o >>= 1)
+        if (o < lanes) v = join<MAX>(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
 }
 
-// Reduction over the block; every thread gets the result.
+// Reduction over the threads of a row; every thread gets the result.  `sm` holds
+// a float a warp and is used once.
 template <bool MAX>
-__device__ float block_reduce(float v, float* sm) {
-    v = warp_reduce<MAX>(v);
-    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    __syncthreads();                                   // the last use of sm is over
-    if ((threadIdx.x & 31) == 0) sm[warp] = v;
+__device__ __forceinline__ float row_reduce(float v, float* sm) {
+    v = lane_reduce<MAX>(v);
+    const int warps = blockDim.x >> 5;
+    if (warps == 1) return v;
+    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
     __syncthreads();
     v = (threadIdx.x & 31) < warps ? sm[threadIdx.x & 31] : 0.f;     // sums and magnitudes: 0 is neutral
-    return warp_reduce<MAX>(v);
+    return lane_reduce<MAX>(v);
+}
+
+// Rows of 16-byte pieces: a row's threads keep it in registers, V pieces of 8
+// elements each, so that it is read once.
+// Bound by memory: 2 or 3 passes' worth of bytes a row (x, residual in; r, y
+// out), all loads issued before the first use, and the weights' (from L2) before
+// the one barrier of the sum.
+template <bool F16, bool E4M3, int V>
+__global__ void __launch_bounds__(1024) norm_rows_kernel(const NormParams p) {
+    __shared__ float sm[2][32];
+    pdl_wait_previous();
+    pdl_launch_dependents();
+    const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    if (t >= p.T) return;                              // whole warps: several rows a block have a warp each
+    const int pieces = (int)(p.H / 8);
+    uint4 r[V], w[V];
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = i * blockDim.x + threadIdx.x;
+        r[i] = c < pieces ? ldg_once(p.x + t * p.x_stride + c * 8) : make_uint4(0, 0, 0, 0);
+    }
+    if (p.residual) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = i * blockDim.x + threadIdx.x;
+            w[i] = c < pieces ? ldg_once(p.residual + t * p.res_stride + c * 8) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = i * blockDim.x + threadIdx.x;
+            uint32_t* a = &r[i].x;
+            const uint32_t* b = &w[i].x;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 u = act2_to_f32<F16>(a[j]), v = act2_to_f32<F16>(b[j]);
+                a[j] = f32_to_act2<F16>(u.x + v.x, u.y + v.y);
+            }
+            if (c < pieces) *(uint4*)(p.residual_out + t * p.H + c * 8) = r[i];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = i * blockDim.x + threadIdx.x;
+        w[i] = c < pieces ? *(const uint4*)(p.weight + c * 8) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const uint32_t* a = &r[i].x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 u = act2_to_f32<F16>(a[j]);
+            sum += u.x * u.x + u.y * u.y;
+        }
+    }
+    const float rstd = rsqrtf(row_reduce<false>(sum, sm[0]) / (float)p.H + p.eps);
+    if constexpr (!E4M3) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = i * blockDim.x + threadIdx.x;
+            uint32_t* a = &r[i].x;
+            const uint32_t* b = &w[i].x;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 u = act2_to_f32<F16>(a[j]), v = act2_to_f32<F16>(b[j]);
+                a[j] = f32_to_act2<F16>(u.x * rstd * v.x, u.y * rstd * v.y);
+            }
+            if (c < pieces) *(uint4*)((uint16_t*)p.y + t * p.H + c * 8) = r[i];
+        }
+    } else {
+        const bool by_row = p.group == p.H;
+        const int lanes = by_row ? 32 : (int)(p.group / 8);       // threads of one scale
+        float amax[V], top = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const uint32_t *a = &r[i].x, *b = &w[i].x;
+            amax[i] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 u = act2_to_f32<F16>(a[j]), v = act2_to_f32<F16>(b[j]);
+                amax[i] = fmaxf(amax[i], fmaxf(fabsf(u.x * rstd * v.x), fabsf(u.y * rstd * v.y)));
+            }
+            top = fmaxf(top, amax[i]);
+        }
+        if (by_row) top = row_reduce<true>(top, sm[1]);
+        const int64_t groups = p.H / p.group;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = i * blockDim.x + threadIdx.x;
+            const float s = e4m3_scale(by_row ? top : lane_reduce<true>(amax[i], lanes)), inv = __frcp_rn(s);
+            if (c >= pieces) continue;
+            if (by_row ? c == 0 : threadIdx.x % lanes == 0) p.scales[t * groups + (by_row ? 0 : c / lanes)] = s;
+            const uint32_t *a = &r[i].x, *b = &w[i].x;
+            uint32_t o[2];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 u = act2_to_f32<F16>(a[j]), v = act2_to_f32<F16>(b[j]);
+                const uint32_t two = f32_to_e4m3x2(e4m3_quotient(u.x * rstd * v.x, s, inv), e4m3_quotient(u.y * rstd * v.y, s, inv));
+                o[j >> 1] = j & 1 ? o[j >> 1] | two << 16 : two;
+            }
+            *(uint2*)((uint8_t*)p.y + t * p.H + c * 8) = make_uint2(o[0], o[1]);
+        }
+    }
 }
 
 // Any width, stride and alignment: a block walks a row element by element, and
 // reads it again (from L1/L2) for the output.
 template <bool F16>
-__global__ void __launch_bounds__(256) norm_any_kernel(NormParams p) {
-    __shared__ float sm[32];
-    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
-        const uint16_t* x = p.x + t * p.x_stride;
-        const uint16_t* r = x;
-        float sum = 0.f;
-        for (int64_t i = threadIdx.x; i < p.H; i += blockDim.x) {
-            float v = act_to_f32<F16>(x[i]);
-            if (p.residual) {
-                const uint16_t b = f32_to_act_bits<F16>(v + act_to_f32<F16>(p.residual[t * p.res_stride + i]));
-                p.residual_out[t * p.H + i] = b;
-                v = act_to_f32<F16>(b);
-            }
-            sum += v * v;
+__global__ void __launch_bounds__(256) norm_any_kernel(const NormParams p) {
+    __shared__ float sm[2][8];
+    pdl_wait_previous();
+    pdl_launch_dependents();
+    const int64_t t = blockIdx.x;
+    const uint16_t* x = p.x + t * p.x_stride;
+    const uint16_t* r = x;
+    float sum = 0.f;
+    for (int64_t i = threadIdx.x; i < p.H; i += blockDim.x) {
+        float v = act_to_f32<F16>(x[i]);
+        if (p.residual) {
+            const uint16_t b = f32_to_act_bits<F16>(v + act_to_f32<F16>(p.residual[t * p.res_stride + i]));
+            p.residual_out[t * p.H + i] = b;
+            v = act_to_f32<F16>(b);
         }
-        if (p.residual) r = p.residual_out + t * p.H;
-        sum = block_reduce<false>(sum, sm);            // its barriers make the block's r visible, too
-        const float rstd = rsqrtf(sum / (float)p.H + p.eps);
-        if (!p.scales) {
-            uint16_t* y = (uint16_t*)p.y + t * p.H;
-            for (int64_t i = threadIdx.x; i < p.H; i += blockDim.x)
-                y[i] = f32_to_act_bits<F16>(act_to_f32<F16>(r[i]) * rstd * act_to_f32<F16>(p.weight[i]));
-            continue;
-        }
-        uint8_t* y = (uint8_t*)p.y + t * p.H;
-        const int64_t groups = p.H / p.group;
-        for (int64_t g = 0; g < groups; ++g) {
-            const int64_t end = (g + 1) * p.group;
-            float amax = 0.f;
-            for (int64_t i = g * p.group + threadIdx.x; i < end; i += blockDim.x)
-                amax = fmaxf(amax, fabsf(act_to_f32<F16>(r[i]) * rstd * act_to_f32<F16>(p.weight[i])));
-            const float s = e4m3_scale(block_reduce<true>(amax, sm));
-            if (threadIdx.x == 0) p.scales[t * groups + g] = s;
-            for (int64_t i = g * p.group + threadIdx.x; i < end; i += blockDim.x)
-                y[i] = (uint8_t)f32_to_e4m3x2(
-                    __fdiv_rn(act_to_f32<F16>(r[i]) * rstd * act_to_f32<F16>(p.weight[i]), s), 0.f);
-        }
+        sum += v * v;
+    }
+    if (p.residual) r = p.residual_out + t * p.H;
+    sum = row_reduce<false>(sum, sm[0]);               // its barrier makes the block's r visible, too
+    const float rstd = rsqrtf(sum / (float)p.H + p.eps);
+    auto value = [&](int64_t i) { return act_to_f32<F16>(r[i]) * rstd * act_to_f32<F16>(p.weight[i]); };
+    if (!p.scales) {
+        uint16_t* y = (uint16_t*)p.y + t * p.H;
+        for (int64_t i = threadIdx.x; i < p.H; i += blockDim.x) y[i] = f32_to_act_bits<F16>(value(i));
+        return;
+    }
+    uint8_t* y = (uint8_t*)p.y + t * p.H;
+    if (p.group == p.H) {
+        float amax = 0.f;
+        for (int64_t i = threadIdx.x; i < p.H; i += blockDim.x) amax = fmaxf(amax, fabsf(value(i)));
+        const float s = e4m3_scale(row_reduce<true>(amax, sm[1])), inv = __frcp_rn(s);
+        if (threadIdx.x == 0) p.scales[t] = s;
+        for (int64_t i = threadIdx.x; i < p.H; i += blockDim.x) y[i] = (uint8_t)f32_to_e4m3x2(e4m3_quotient(value(i), s, inv), 0.f);
+        return;
+    }
+    const int64_t groups = p.H / p.group;              // a warp takes a group at a time
+    const int lane = threadIdx.x & 31;
+    for (int64_t g = threadIdx.x >> 5; g < groups; g += blockDim.x >> 5) {
+        float amax = 0.f;
+        for (int64_t i = g * p.group + lane; i < (g + 1) * p.group; i += 32) amax = fmaxf(amax, fabsf(value(i)));
+        const float s = e4m3_scale(lane_reduce<true>(amax)), inv = __frcp_rn(s);
+        if (lane == 0) p.scales[t * groups + g] = s;
+        for (int64_t i = g * p.group + lane; i < (g + 1) * p.group; i += 32)
+            y[i] = (uint8_t)f32_to_e4m3x2(e4m3_quotient(value(i), s, inv), 0.f);
     }
 }
 
-nvfp4_status launch_norm(const NormParams& p, bool f16, cudaStream_t s) {
-    const int grid = (int)std::min<int64_t>(p.T, (int64_t)sm_count() * 8);
-    if (f16) norm_any_kernel<true><<<grid, 256, 0, s>>>(p);
-    else norm_any_kernel<false><<<grid, 256, 0, s>>>(p);
-    return check_cuda(cudaGetLastError(), "nvfp4_rms_norm");
+template <bool F16>
+const void* rows_kernel(bool e4m3, int V) {
+    switch (V) {
+        case 1: return e4m3 ? (const void*)norm_rows_kernel<F16, true, 1> : (const void*)norm_rows_kernel<F16, false, 1>;
+        case 2: return e4m3 ? (const void*)norm_rows_kernel<F16, true, 2> : (const void*)norm_rows_kernel<F16, false, 2>;
+        default: return e4m3 ? (const void*)norm_rows_kernel<F16, true, 4> : (const void*)norm_rows_kernel<F16, false, 4>;
+    }
+}
+
+nvfp4_status launch_norm(const NormParams& p, bool f16, cudaStream_t stream) {
+    const char* fn = "nvfp4_rms_norm";
+    const bool e4m3 = p.scales != nullptr;
+    const int64_t pieces = p.H / 8;
+    const bool rows = p.H % 8 == 0 && pieces <= 4096 && p.x_stride % 8 == 0 && p.res_stride % 8 == 0 && aligned(p.x, 16) &&
+                      aligned(p.residual, 16) && aligned(p.weight, 16) && aligned(p.residual_out, 16) && aligned(p.y, e4m3 ? 8 : 16);
+    const void* kernel = f16 ? (const void*)norm_any_kernel<true> : (const void*)norm_any_kernel<false>;
+    dim3 block(256);
+    if (rows) {
+        // Rows that fill the GPU take four pieces a thread (enough loads in flight
+        // with few threads to join); few rows take as many threads as they have
+        // pieces, for the shortest way through one row.
+        int V = p.T > sm_count() * 2 ? 4 : 1;
+        while (pieces > 1024 * V) V *= 2;
+        block = dim3((unsigned)round_up(ceil_div(pieces, V), 32));
+        if (block.x == 32) block.y = p.T > sm_count() * 2 ? 8 : 1;    // a warp a row
+        kernel = f16 ? rows_kernel<true>(e4m3, V) : rows_kernel<false>(e4m3, V);
+    }
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ceil_div(p.T, block.y));
+    cfg.blockDim = block;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    void* args[] = {const_cast<NormParams*>(&p)};
+    return check_cuda(cudaLaunchKernelExC(&cfg, kernel, args), fn);
 }
 
 }  // namespace
@@ -108,6 +254,7 @@ extern "C" nvfp4_status nvfp4_rms_norm(const void* X, int64_t x_stride, const vo
                                        int f16, void* Y, float* scales, void* residual_out, void* stream) {
     const char* fn = "nvfp4_rms_norm";
     if (T < 0) return fail(NVFP4_ERR_INVALID_ARG, "%s: negative size T=%lld", fn, (long long)T);
+    if (T > INT32_MAX) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s: T=%lld too large", fn, (long long)T);
     if (H <= 0 || H > (1 << 24)) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s: H=%lld must be in [1, 2^24]", fn, (long long)H);
     if (f16 != 0 && f16 != 1) return fail(NVFP4_ERR_INVALID_ARG, "%s: f16=%d must be 0 or 1", fn, f16);
     if (out_type != NVFP4_OUT_16 && out_type != NVFP4_OUT_E4M3)
