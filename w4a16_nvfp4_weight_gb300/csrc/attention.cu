@@ -32,6 +32,7 @@
 // below 2^-28 of it lose bits).  The scale of a value row is multiplied into its weight,
 // whose running maximum is taken over z + log2(scale), so that it fits FP16.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "common.cuh"
@@ -57,7 +58,7 @@ struct AttnParams {
     float* parts;                  // workspace: partial results of blocks, then of warps
     int* joins;                    // workspace: [blocks][2], unit and last block of a unit that starts here and goes on
     int B, Hq, G, chunks, units;   // chunks: head groups of one key head; units = heads * chunks a sequence
-    int width, page_shift;         // page_shift: log2(page_size), or -1
+    int width;
     int window;                    // 0: none
     float scale_log2;              // softmax_scale * log2(e)
     int* status;
@@ -313,7 +314,7 @@ attend_kernel(const AttnParams p) {
             const int t = f.step * kStep + (lane & 15);
             page = -1;
             if (t >= f.lo && t < f.n) {
-                const int i = p.page_shift >= 0 ? t >> p.page_shift : t / p.cache.page_size;
+                const int i = p.cache.page_shift >= 0 ? t >> p.cache.page_shift : t / p.cache.page_size;
                 at = t - i * p.cache.page_size;
                 page = p.block_table[f.b * p.table_stride + i];
                 if ((uint32_t)page >= (uint32_t)p.cache.num_pages) {
@@ -710,8 +711,16 @@ nvfp4_status launch_attention(AttnParams p, void* workspace, cudaStream_t stream
     p.joins = (int*)workspace;
     p.parts = (float*)((uint8_t*)workspace + round_up((int64_t)ctas * 8, 256));
     auto kernel = attend_kernel<F16, E4M3, DP, NT>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+    static std::atomic<uint64_t> opted_in{0};                   // devices whose instance has its shared memory limit raised
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return check_cuda(e, fn);
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(opted_in.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+        if (e != cudaSuccess) return check_cuda(e, fn);
+        opted_in.fetch_or(bit, std::memory_order_relaxed);
+    }
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -789,9 +798,6 @@ extern "C" nvfp4_status nvfp4_paged_attention(const void* q, int64_t q_row_strid
     p.units = p.cache.heads * p.chunks;
     p.window = (int)std::min<int64_t>(window, INT32_MAX);
     p.scale_log2 = softmax_scale * 1.44269504088896341f;
-    p.page_shift = -1;
-    for (int s = 0; s <= 20; ++s)
-        if (p.cache.page_size == 1 << s) p.page_shift = s;
     cudaStream_t s = (cudaStream_t)stream;
     if (p.cache.e4m3) return f16 ? launch_shape<true, true>(p, DP, NT, workspace, s) : launch_shape<false, true>(p, DP, NT, workspace, s);
     return f16 ? launch_shape<true, false>(p, DP, NT, workspace, s) : launch_shape<false, false>(p, DP, NT, workspace, s);

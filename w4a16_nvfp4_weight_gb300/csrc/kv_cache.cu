@@ -44,6 +44,9 @@ nvfp4_status check_cache(const char* fn, const nvfp4_kv_cache* c, CacheView* vie
     view->num_pages = c->num_pages; view->num_slots = c->num_pages * c->page_size;
     view->page_bytes = c->page_stride * es; view->head_bytes = c->head_stride * es; view->token_bytes = c->token_stride * es;
     view->page_size = (int)c->page_size; view->heads = (int)c->heads; view->D = (int)c->head_dim;
+    view->page_shift = -1;
+    for (int i = 0; i <= 20; ++i)
+        if (view->page_size == 1 << i) view->page_shift = i;
     view->e4m3 = e4m3;
     return NVFP4_OK;
 }
@@ -76,9 +79,11 @@ __device__ __forceinline__ int64_t axis_position(const RopeParams& p, int64_t t,
     return -1;
 }
 
-// A warp takes one head of one token, a lane every 32nd element.
+// Any rot: a warp takes one head of one token, a lane every 32nd element.
 template <bool F16, bool INTER>
-__global__ void __launch_bounds__(256) rope_write_any_kernel(RopeParams p) {
+__global__ void __launch_bounds__(256) rope_write_any_kernel(const RopeParams p) {
+    pdl_wait_previous();
+    pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
     const int heads = p.Hq + 2 * p.Hkv;
     const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
@@ -122,8 +127,9 @@ __global__ void __launch_bounds__(256) rope_write_any_kernel(RopeParams p) {
                 if (lane + 32 * i < p.D) p.q_out[(t * p.Hq + h) * p.D + lane + 32 * i] = f32_to_act_bits<F16>(y[i]);
             continue;
         }
-        const int64_t page = slot / p.cache.page_size;
-        const int at = (int)(slot % p.cache.page_size);
+        int64_t page;
+        int at;
+        p.cache.split(slot, &page, &at);
         uint8_t* row = (kind == 1 ? p.cache.k : p.cache.v) + p.cache.row(page, h, at);
         if (!p.cache.e4m3) {
 #pragma unroll
@@ -133,12 +139,203 @@ __global__ void __launch_bounds__(256) rope_write_any_kernel(RopeParams p) {
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const float s = e4m3_scale(amax);
+        const float s = e4m3_scale(amax), inv = __frcp_rn(s);
         if (lane == 0) (kind == 1 ? p.cache.k_scale : p.cache.v_scale)[p.cache.scale_at(page, h, at)] = s;
 #pragma unroll
         for (int i = 0; i < kMaxHeadDim / 32; ++i)
-            if (lane + 32 * i < p.D) row[lane + 32 * i] = (uint8_t)f32_to_e4m3x2(__fdiv_rn(y[i], s), 0.f);
+            if (lane + 32 * i < p.D) row[lane + 32 * i] = (uint8_t)f32_to_e4m3x2(e4m3_quotient(y[i], s, inv), 0.f);
     }
+}
+
+// Cosines and sines of the eight elements of piece c (INTER: of its four pairs).
+template <bool INTER>
+__device__ __forceinline__ void turn_of(const RopeParams& p, int64_t t, int c, float cs[8], float sn[8]) {
+    constexpr int N = INTER ? 4 : 8;
+    const int half = p.rot / 2, f0 = INTER ? c * 4 : c * 8 >= half ? c * 8 - half : c * 8;
+    int a0 = 0, a1 = 0;
+    while (a0 + 1 < p.axes && f0 >= p.end[a0]) ++a0;
+    while (a1 + 1 < p.axes && f0 + N - 1 >= p.end[a1]) ++a1;
+    if (a0 == a1) {
+        const int64_t pos = p.positions[a0 * p.T + t];
+        if ((uint64_t)pos < (uint64_t)p.rows) {
+            const float4* row = (const float4*)(p.table + pos * p.rot + f0);
+#pragma unroll
+            for (int i = 0; i < N / 4; ++i) {
+                const float4 u = __ldg(row + i), v = __ldg(row + half / 4 + i);
+                cs[4 * i] = u.x; cs[4 * i + 1] = u.y; cs[4 * i + 2] = u.z; cs[4 * i + 3] = u.w;
+                sn[4 * i] = v.x; sn[4 * i + 1] = v.y; sn[4 * i + 2] = v.z; sn[4 * i + 3] = v.w;
+            }
+            return;
+        }
+        record_status(p.status, NVFP4_ERR_BAD_INDEX);
+#pragma unroll
+        for (int i = 0; i < N; ++i) { cs[i] = 1.f; sn[i] = 0.f; }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int64_t pos = axis_position(p, t, f0 + i);
+        cs[i] = pos < 0 ? 1.f : p.table[pos * p.rot + f0 + i];
+        sn[i] = pos < 0 ? 0.f : p.table[pos * p.rot + half + f0 + i];
+    }
+}
+
+// rot a multiple of 16 (INTER: of 8): a thread takes the 16-byte piece c of several
+// heads of one token, L threads a head (a power of two), so that its cosines and
+// sines are read once a token; the other half of a pair comes by shuffle.
+// Bound by memory: q, k, v in, q and the cache rows out.  The pieces of four heads
+// are loaded before the position's table row, whose address waits for the position.
+// `per` head groups a token (a power of two), L * per threads, 256 a block.
+template <bool F16, bool INTER, bool E4M3, int U>
+__global__ void __launch_bounds__(256) rope_write_kernel(const RopeParams p, int L, int per) {
+    pdl_wait_previous();
+    pdl_launch_dependents();
+    const int c = threadIdx.x % L, group = threadIdx.x / L;
+    const int64_t t = (int64_t)blockIdx.x * (256 / (L * per)) + group / per;
+    const bool live = t < p.T && c * 8 < p.D;
+    const int heads = p.Hq + 2 * p.Hkv, stride = per * gridDim.y;
+    const int first = blockIdx.y * per + group % per;
+    const bool turns = c * 8 < p.rot;
+    const int back = p.rot / 16;                       // pieces between the halves of a pair
+    const int mate = (threadIdx.x & 31) + (c < back ? back : -back);
+
+    int64_t slot = -1, page = 0;
+    int at = 0;
+    float cs[8], sn[8];
+    bool ready = false;
+    for (int h0 = 0; h0 < heads; h0 += stride * U) {   // the same trips for every thread: the shuffles below
+        uint4 x[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int h = h0 + i * stride + first;
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (!live || h >= heads) continue;
+            const uint16_t* from = h < p.Hq ? p.q + t * p.q_token + h * p.q_head
+                                 : h < p.Hq + p.Hkv ? p.k + t * p.k_token + (h - p.Hq) * p.k_head
+                                                    : p.v + t * p.v_token + (h - p.Hq - p.Hkv) * p.v_head;
+            x[i] = ldg_once(from + c * 8);
+        }
+        if (!ready) {
+            ready = true;
+            if (live) {
+                slot = p.slots[t];
+                if (slot >= p.cache.num_slots) {
+                    record_status(p.status, NVFP4_ERR_BAD_INDEX);
+                    slot = -1;
+                }
+                if (turns) turn_of<INTER>(p, t, c, cs, sn);
+                if (slot >= 0) p.cache.split(slot, &page, &at);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (h0 + i * stride >= heads) break;       // no thread of the block has a head left
+            const int h = h0 + i * stride + first;
+            const int kind = h < p.Hq ? 0 : h < p.Hq + p.Hkv ? 1 : 2;       // query, key, value
+            const uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 u = act2_to_f32<F16>(in[j]);
+                y[2 * j] = u.x;
+                y[2 * j + 1] = u.y;
+            }
+            if constexpr (INTER) {
+                if (kind < 2 && turns) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float a = y[2 * j], b = y[2 * j + 1];
+                        y[2 * j] = __fsub_rn(__fmul_rn(a, cs[j]), __fmul_rn(b, sn[j]));
+                        y[2 * j + 1] = __fadd_rn(__fmul_rn(b, cs[j]), __fmul_rn(a, sn[j]));
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 o = act2_to_f32<F16>(__shfl_sync(0xffffffffu, in[j], mate));
+                    if (kind < 2 && turns) {
+                        const float a = __fmul_rn(o.x, sn[2 * j]), b = __fmul_rn(o.y, sn[2 * j + 1]);
+                        const float d = __fmul_rn(y[2 * j], cs[2 * j]), e = __fmul_rn(y[2 * j + 1], cs[2 * j + 1]);
+                        y[2 * j] = c < back ? __fsub_rn(d, a) : __fadd_rn(d, a);
+                        y[2 * j + 1] = c < back ? __fsub_rn(e, b) : __fadd_rn(e, b);
+                    }
+                }
+            }
+            float s = 1.f;
+            if (E4M3) {
+                float amax = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(y[j]));
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1)
+                    if (o < L) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                s = e4m3_scale(amax);
+            }
+            if (!live || h >= heads) continue;
+            if (kind == 0 || !E4M3) {
+                const uint4 o = make_uint4(f32_to_act2<F16>(y[0], y[1]), f32_to_act2<F16>(y[2], y[3]),
+                                           f32_to_act2<F16>(y[4], y[5]), f32_to_act2<F16>(y[6], y[7]));
+                if (kind == 0) {
+                    *(uint4*)(p.q_out + (t * p.Hq + h) * p.D + c * 8) = o;
+                } else if (slot >= 0) {
+                    uint8_t* row = (kind == 1 ? p.cache.k : p.cache.v) + p.cache.row(page, h - p.Hq - (kind - 1) * p.Hkv, at);
+                    *(uint4*)(row + c * 16) = o;
+                }
+            } else if (slot >= 0) {
+                const int kh = h - p.Hq - (kind - 1) * p.Hkv;
+                const float inv = __frcp_rn(s);
+                uint32_t o[2];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t two = f32_to_e4m3x2(e4m3_quotient(y[2 * j], s, inv), e4m3_quotient(y[2 * j + 1], s, inv));
+                    o[j >> 1] = j & 1 ? o[j >> 1] | two << 16 : two;
+                }
+                *(uint2*)((kind == 1 ? p.cache.k : p.cache.v) + p.cache.row(page, kh, at) + c * 8) = make_uint2(o[0], o[1]);
+                if (c == 0) (kind == 1 ? p.cache.k_scale : p.cache.v_scale)[p.cache.scale_at(page, kh, at)] = s;
+            }
+        }
+    }
+}
+
+template <bool F16, bool INTER>
+const void* rope_kernel(bool e4m3, bool one) {
+    if (one) return e4m3 ? (const void*)rope_write_kernel<F16, INTER, true, 1> : (const void*)rope_write_kernel<F16, INTER, false, 1>;
+    return e4m3 ? (const void*)rope_write_kernel<F16, INTER, true, 4> : (const void*)rope_write_kernel<F16, INTER, false, 4>;
+}
+
+nvfp4_status launch_after(const void* kernel, dim3 grid, dim3 block, void** args, cudaStream_t stream, const char* fn) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return check_cuda(cudaLaunchKernelExC(&cfg, kernel, args), fn);
+}
+
+nvfp4_status launch_rope(RopeParams p, bool f16, bool inter, cudaStream_t stream, const char* fn) {
+    const int heads = p.Hq + 2 * p.Hkv;
+    if (p.rot % (inter ? 8 : 16) != 0) {
+        const void* kernel = f16 ? (inter ? (const void*)rope_write_any_kernel<true, true> : (const void*)rope_write_any_kernel<true, false>)
+                                 : (inter ? (const void*)rope_write_any_kernel<false, true> : (const void*)rope_write_any_kernel<false, false>);
+        void* args[] = {&p};
+        return launch_after(kernel, dim3((unsigned)std::min<int64_t>(ceil_div(p.T * heads, 8), (int64_t)sm_count() * 8)), dim3(256), args, stream, fn);
+    }
+    int L = 2, per = 1;
+    while (L * 8 < p.D) L *= 2;
+    // Many tokens: about four heads a thread, all in flight.  Few tokens: one head
+    // a thread over as many blocks as that takes, for the shortest way through.
+    const bool one = p.T * heads * L <= (int64_t)sm_count() * 1024;
+    while (per * 2 * L <= 256 && (one ? per < heads : per * 4 < heads)) per *= 2;
+    const int tokens = 256 / (L * per);                // a block's
+    dim3 grid((unsigned)ceil_div(p.T, tokens), one ? (unsigned)ceil_div(heads, per) : 1);
+    const void* kernel = f16 ? (inter ? rope_kernel<true, true>(p.cache.e4m3, one) : rope_kernel<true, false>(p.cache.e4m3, one))
+                             : (inter ? rope_kernel<false, true>(p.cache.e4m3, one) : rope_kernel<false, false>(p.cache.e4m3, one));
+    void* args[] = {&p, &L, &per};
+    return launch_after(kernel, grid, dim3(256), args, stream, fn);
 }
 
 struct ReadParams {
@@ -151,7 +348,9 @@ struct ReadParams {
 
 // A thread takes 16 elements of one row.
 template <bool F16, bool E4M3>
-__global__ void __launch_bounds__(256) cache_read_kernel(ReadParams p) {
+__global__ void __launch_bounds__(256) cache_read_kernel(const ReadParams p) {
+    pdl_wait_previous();
+    pdl_launch_dependents();
     const int per = p.cache.D / 16;
     const int64_t total = p.T * p.cache.heads * per;
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
@@ -166,8 +365,9 @@ __global__ void __launch_bounds__(256) cache_read_kernel(ReadParams p) {
         for (int kv = 0; kv < 2; ++kv) {
             uint4 out[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
             if (held) {
-                const int64_t page = slot / p.cache.page_size;
-                const int at = (int)(slot % p.cache.page_size);
+                int64_t page;
+                int at;
+                p.cache.split(slot, &page, &at);
                 const uint8_t* src = (kv == 0 ? p.cache.k : p.cache.v) + p.cache.row(page, h, at) + c * (E4M3 ? 16 : 32);
                 if (!E4M3) {
                     out[0] = ((const uint4*)src)[0];
@@ -247,16 +447,7 @@ extern "C" nvfp4_status nvfp4_rope_cache_write(const void* q, int64_t q_token_st
     p.positions = positions; p.table = table; p.slots = slots; p.q_out = (uint16_t*)q_out;
     p.T = T; p.rows = table_rows; p.Hq = (int)Hq; p.Hkv = p.cache.heads; p.D = (int)D; p.rot = (int)rot; p.axes = axes;
     cudaStream_t s = (cudaStream_t)stream;
-    const int64_t warps = T * (Hq + 2 * p.Hkv);
-    const int grid = (int)std::min<int64_t>(ceil_div(warps, 8), (int64_t)sm_count() * 8);
-    if (f16) {
-        if (interleaved) rope_write_any_kernel<true, true><<<grid, 256, 0, s>>>(p);
-        else rope_write_any_kernel<true, false><<<grid, 256, 0, s>>>(p);
-    } else {
-        if (interleaved) rope_write_any_kernel<false, true><<<grid, 256, 0, s>>>(p);
-        else rope_write_any_kernel<false, false><<<grid, 256, 0, s>>>(p);
-    }
-    return check_cuda(cudaGetLastError(), fn);
+    return launch_rope(p, f16 != 0, interleaved != 0, s, fn);
 }
 
 extern "C" nvfp4_status nvfp4_kv_cache_read(const nvfp4_kv_cache* cache, const int64_t* slots, int64_t T, int f16,
@@ -275,12 +466,9 @@ extern "C" nvfp4_status nvfp4_kv_cache_read(const nvfp4_kv_cache* cache, const i
     p.slots = slots; p.k_out = (uint16_t*)k_out; p.v_out = (uint16_t*)v_out; p.T = T;
     cudaStream_t s = (cudaStream_t)stream;
     const int64_t threads = T * p.cache.heads * (p.cache.D / 16);
-    const int grid = (int)std::min<int64_t>(ceil_div(threads, 256), (int64_t)sm_count() * 16);
-    if (p.cache.e4m3) {
-        if (f16) cache_read_kernel<true, true><<<grid, 256, 0, s>>>(p);
-        else cache_read_kernel<false, true><<<grid, 256, 0, s>>>(p);
-    } else {
-        cache_read_kernel<false, false><<<grid, 256, 0, s>>>(p);        // a copy: the type does not matter
-    }
-    return check_cuda(cudaGetLastError(), fn);
+    const dim3 grid((unsigned)std::min<int64_t>(ceil_div(threads, 256), (int64_t)sm_count() * 16));
+    const void* kernel = !p.cache.e4m3 ? (const void*)cache_read_kernel<false, false>       // a copy: the type does not matter
+                       : f16 ? (const void*)cache_read_kernel<true, true> : (const void*)cache_read_kernel<false, true>;
+    void* args[] = {&p};
+    return launch_after(kernel, grid, dim3(256), args, s, fn);
 }

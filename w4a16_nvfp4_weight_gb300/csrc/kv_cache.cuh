@@ -16,7 +16,16 @@ struct CacheView {
     int64_t num_pages, num_slots;  // slots = pages * page_size
     int64_t page_bytes, head_bytes, token_bytes;
     int page_size, heads, D;
+    int page_shift;                // log2(page_size), or -1
     bool e4m3;
+
+    // Page and place of a slot below num_slots (a 64-bit division only where nothing shorter will do).
+    __device__ void split(int64_t slot, int64_t* page, int* at) const {
+        if (page_shift >= 0) *page = slot >> page_shift;
+        else if (num_slots <= INT32_MAX) *page = (int32_t)slot / page_size;
+        else *page = slot / page_size;
+        *at = (int)(slot - *page * page_size);
+    }
 
     // Byte offset of token `at` of `page`, head h: 64-bit, a cache passes 4 GB.
     __host__ __device__ int64_t row(int64_t page, int h, int at) const {
