@@ -147,160 +147,187 @@ __global__ void __launch_bounds__(256) rope_write_any_kernel(const RopeParams p)
     }
 }
 
-// Cosines and sines of the eight elements of piece c (INTER: of its four pairs).
-template <bool INTER>
-__device__ __forceinline__ void turn_of(const RopeParams& p, int64_t t, int c, float cs[8], float sn[8]) {
-    constexpr int N = INTER ? 4 : 8;
-    const int half = p.rot / 2, f0 = INTER ? c * 4 : c * 8 >= half ? c * 8 - half : c * 8;
-    int a0 = 0, a1 = 0;
-    while (a0 + 1 < p.axes && f0 >= p.end[a0]) ++a0;
-    while (a1 + 1 < p.axes && f0 + N - 1 >= p.end[a1]) ++a1;
-    if (a0 == a1) {
-        const int64_t pos = p.positions[a0 * p.T + t];
-        if ((uint64_t)pos < (uint64_t)p.rows) {
-            const float4* row = (const float4*)(p.table + pos * p.rot + f0);
-#pragma unroll
-            for (int i = 0; i < N / 4; ++i) {
-                const float4 u = __ldg(row + i), v = __ldg(row + half / 4 + i);
-                cs[4 * i] = u.x; cs[4 * i + 1] = u.y; cs[4 * i + 2] = u.z; cs[4 * i + 3] = u.w;
-                sn[4 * i] = v.x; sn[4 * i + 1] = v.y; sn[4 * i + 2] = v.z; sn[4 * i + 3] = v.w;
-            }
-            return;
-        }
-        record_status(p.status, NVFP4_ERR_BAD_INDEX);
-#pragma unroll
-        for (int i = 0; i < N; ++i) { cs[i] = 1.f; sn[i] = 0.f; }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int64_t pos = axis_position(p, t, f0 + i);
-        cs[i] = pos < 0 ? 1.f : p.table[pos * p.rot + f0 + i];
-        sn[i] = pos < 0 ? 0.f : p.table[pos * p.rot + half + f0 + i];
-    }
+// Two 32-bit values an instruction.
+struct F2 { uint64_t v; };
+__device__ __forceinline__ F2 make_f2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 both(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+// Sums of products one value at a time: a packed addition after a packed product
+// came out as one fused operation, with one rounding instead of two.
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    const float2 u = both(a), v = both(b);
+    return make_f2(__fadd_rn(u.x, v.x), __fadd_rn(u.y, v.y));
+}
+__device__ __forceinline__ F2 sub2(F2 a, F2 b) {
+    const float2 u = both(a), v = both(b);
+    return make_f2(__fsub_rn(u.x, v.x), __fsub_rn(u.y, v.y));
 }
 
-// rot a multiple of 16 (INTER: of 8): a thread takes the 16-byte piece c of several
-// heads of one token, L threads a head (a power of two), so that its cosines and
-// sines are read once a token; the other half of a pair comes by shuffle.
-// Bound by memory: q, k, v in, q and the cache rows out.  The pieces of four heads
-// are loaded before the position's table row, whose address waits for the position.
-// `per` head groups a token (a power of two), L * per threads, 256 a block.
+// rot a multiple of 16: a thread takes 16 elements of several heads of one token,
+// both sides of eight pairs, so that nothing is exchanged: pieces j and j + rot/16
+// of 8 elements (INTER: 2j and 2j + 1), past rot two neighbouring pieces as they
+// are.  L threads a head (a power of two), `per` head groups a token (a power of
+// two), 256 threads a block.
+// Bound by memory (q, k, v in, q and the cache rows out) and not far from it by
+// instructions: 24.6 us (4.86 TB/s) for 4096 tokens of 40 + 2 * 8 heads of 128
+// with three axes, where a piece of 8 a thread with its mate's by shuffle (176
+// instructions a warp for two heads) took 30.  The rows of U heads are loaded first; then
+// the block fetches its tokens' cosines and sines into shared memory, a thread a
+// frequency, whose addresses wait for the positions (each thread fetching its
+// own through L1: 40 us).
 template <bool F16, bool INTER, bool E4M3, int U>
-__global__ void __launch_bounds__(256) rope_write_kernel(const RopeParams p, int L, int per) {
+__global__ void __launch_bounds__(256, 3) rope_write_kernel(const RopeParams p, int L, int per) {
     pdl_wait_previous();
     pdl_launch_dependents();
-    const int c = threadIdx.x % L, group = threadIdx.x / L;
-    const int64_t t = (int64_t)blockIdx.x * (256 / (L * per)) + group / per;
-    const bool live = t < p.T && c * 8 < p.D;
+    const int j = threadIdx.x & (L - 1), group = threadIdx.x / L;
+    const int tokens = 256 / (L * per);                // a block's
+    const int64_t t = (int64_t)blockIdx.x * tokens + group / per;
+    const bool live = t < p.T && j * 16 < p.D;
     const int heads = p.Hq + 2 * p.Hkv, stride = per * gridDim.y;
-    const int first = blockIdx.y * per + group % per;
-    const bool turns = c * 8 < p.rot;
-    const int back = p.rot / 16;                       // pieces between the halves of a pair
-    const int mate = (threadIdx.x & 31) + (c < back ? back : -back);
+    const int first = blockIdx.y * per + (group & (per - 1));
+    const bool turns = j * 16 < p.rot;
+    const int half = p.rot / 2;
+    const int e0 = INTER || !turns ? j * 16 : j * 8;               // first element of the two pieces
+    const int e1 = INTER || !turns ? j * 16 + 8 : half + j * 8;
+    const uint32_t same = ((1u << L) - 1) << (threadIdx.x & 31 & ~(L - 1));     // the lanes of this head
+    F2 cs[4], sn[4];
+    int64_t row = -1, scale_row = 0;                   // byte offset of the token's cache row of head 0
 
-    int64_t slot = -1, page = 0;
-    int at = 0;
-    float cs[8], sn[8];
-    bool ready = false;
-    for (int h0 = 0; h0 < heads; h0 += stride * U) {   // the same trips for every thread: the shuffles below
-        uint4 x[U];
+    __shared__ __align__(16) float turn[256 * 16];     // [token][cosines, sines]: at most 256 / L tokens of 16 L
+    for (int h0 = 0; h0 < heads; h0 += stride * U) {
+        uint4 x[U][2];
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int h = h0 + i * stride + first;
-            x[i] = make_uint4(0, 0, 0, 0);
+            x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);            // lanes past D join in the row's amax
             if (!live || h >= heads) continue;
             const uint16_t* from = h < p.Hq ? p.q + t * p.q_token + h * p.q_head
                                  : h < p.Hq + p.Hkv ? p.k + t * p.k_token + (h - p.Hq) * p.k_head
                                                     : p.v + t * p.v_token + (h - p.Hq - p.Hkv) * p.v_head;
-            x[i] = ldg_once(from + c * 8);
+            x[i][0] = ldg_once(from + e0);
+            x[i][1] = ldg_once(from + e1);
         }
-        if (!ready) {
-            ready = true;
-            if (live) {
-                slot = p.slots[t];
-                if (slot >= p.cache.num_slots) {
-                    record_status(p.status, NVFP4_ERR_BAD_INDEX);
-                    slot = -1;
+        if (h0 == 0) {
+            const int64_t slot = live ? p.slots[t] : -1;
+            for (int i = threadIdx.x; i < tokens * half; i += 256) {
+                const int n = tokens == 1 ? 0 : i / half, f = i - n * half;
+                const int64_t u = (int64_t)blockIdx.x * tokens + n;
+                if (u >= p.T) break;
+                const int64_t pos = axis_position(p, u, f);
+                turn[n * p.rot + f] = pos < 0 ? 1.f : p.table[pos * p.rot + f];
+                turn[n * p.rot + half + f] = pos < 0 ? 0.f : p.table[pos * p.rot + half + f];
+            }
+            __syncthreads();
+            if (slot >= p.cache.num_slots) {
+                record_status(p.status, NVFP4_ERR_BAD_INDEX);
+            } else if (slot >= 0) {
+                int64_t page;
+                int at;
+                p.cache.split(slot, &page, &at);
+                row = p.cache.row(page, 0, at);
+                scale_row = p.cache.scale_at(page, 0, at);
+            }
+            if (turns) {
+                const float4* from = (const float4*)(turn + group / per * p.rot + j * 8);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float4 u = from[i], w = from[half / 4 + i];
+                    cs[2 * i] = make_f2(u.x, u.y); cs[2 * i + 1] = make_f2(u.z, u.w);
+                    sn[2 * i] = make_f2(w.x, w.y); sn[2 * i + 1] = make_f2(w.z, w.w);
                 }
-                if (turns) turn_of<INTER>(p, t, c, cs, sn);
-                if (slot >= 0) p.cache.split(slot, &page, &at);
             }
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            if (h0 + i * stride >= heads) break;       // no thread of the block has a head left
             const int h = h0 + i * stride + first;
-            const int kind = h < p.Hq ? 0 : h < p.Hq + p.Hkv ? 1 : 2;       // query, key, value
-            const uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-            float y[8];
+            if (h >= heads) break;                     // all lanes of a head together
+            const bool value = h >= p.Hq + p.Hkv, codes = E4M3 && h >= p.Hq, moves = !value && turns;
+            uint32_t w[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w, x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
+            F2 a[4], b[4];                             // the first and second sides of the pairs
+            if (moves || codes) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 u = act2_to_f32<F16>(in[j]);
-                y[2 * j] = u.x;
-                y[2 * j + 1] = u.y;
-            }
-            if constexpr (INTER) {
-                if (kind < 2 && turns) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float a = y[2 * j], b = y[2 * j + 1];
-                        y[2 * j] = __fsub_rn(__fmul_rn(a, cs[j]), __fmul_rn(b, sn[j]));
-                        y[2 * j + 1] = __fadd_rn(__fmul_rn(b, cs[j]), __fmul_rn(a, sn[j]));
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 o = act2_to_f32<F16>(__shfl_sync(0xffffffffu, in[j], mate));
-                    if (kind < 2 && turns) {
-                        const float a = __fmul_rn(o.x, sn[2 * j]), b = __fmul_rn(o.y, sn[2 * j + 1]);
-                        const float d = __fmul_rn(y[2 * j], cs[2 * j]), e = __fmul_rn(y[2 * j + 1], cs[2 * j + 1]);
-                        y[2 * j] = c < back ? __fsub_rn(d, a) : __fadd_rn(d, a);
-                        y[2 * j + 1] = c < back ? __fsub_rn(e, b) : __fadd_rn(e, b);
+                for (int n = 0; n < 4; ++n) {
+                    const float2 u = act2_to_f32<F16>(w[INTER ? 2 * n : n]), v = act2_to_f32<F16>(w[INTER ? 2 * n + 1 : n + 4]);
+                    a[n] = INTER ? make_f2(u.x, v.x) : make_f2(u.x, u.y);
+                    b[n] = INTER ? make_f2(u.y, v.y) : make_f2(v.x, v.y);
+                    if (moves) {
+                        const F2 c = a[n];
+                        a[n] = sub2(mul2(c, cs[n]), mul2(b[n], sn[n]));
+                        b[n] = add2(mul2(b[n], cs[n]), mul2(c, sn[n]));
                     }
                 }
             }
-            float s = 1.f;
-            if (E4M3) {
-                float amax = 0.f;
+            if (!codes) {
+                if (moves) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(y[j]));
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1)
-                    if (o < L) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                s = e4m3_scale(amax);
-            }
-            if (!live || h >= heads) continue;
-            if (kind == 0 || !E4M3) {
-                const uint4 o = make_uint4(f32_to_act2<F16>(y[0], y[1]), f32_to_act2<F16>(y[2], y[3]),
-                                           f32_to_act2<F16>(y[4], y[5]), f32_to_act2<F16>(y[6], y[7]));
-                if (kind == 0) {
-                    *(uint4*)(p.q_out + (t * p.Hq + h) * p.D + c * 8) = o;
-                } else if (slot >= 0) {
-                    uint8_t* row = (kind == 1 ? p.cache.k : p.cache.v) + p.cache.row(page, h - p.Hq - (kind - 1) * p.Hkv, at);
-                    *(uint4*)(row + c * 16) = o;
+                    for (int n = 0; n < 4; ++n) {
+                        const float2 u = both(a[n]), v = both(b[n]);
+                        w[INTER ? 2 * n : n] = INTER ? f32_to_act2<F16>(u.x, v.x) : f32_to_act2<F16>(u.x, u.y);
+                        w[INTER ? 2 * n + 1 : n + 4] = INTER ? f32_to_act2<F16>(u.y, v.y) : f32_to_act2<F16>(v.x, v.y);
+                    }
                 }
-            } else if (slot >= 0) {
-                const int kh = h - p.Hq - (kind - 1) * p.Hkv;
-                const float inv = __frcp_rn(s);
-                uint32_t o[2];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t two = f32_to_e4m3x2(e4m3_quotient(y[2 * j], s, inv), e4m3_quotient(y[2 * j + 1], s, inv));
-                    o[j >> 1] = j & 1 ? o[j >> 1] | two << 16 : two;
-                }
-                *(uint2*)((kind == 1 ? p.cache.k : p.cache.v) + p.cache.row(page, kh, at) + c * 8) = make_uint2(o[0], o[1]);
-                if (c == 0) (kind == 1 ? p.cache.k_scale : p.cache.v_scale)[p.cache.scale_at(page, kh, at)] = s;
+                if (!live || (h >= p.Hq && row < 0)) continue;
+                uint16_t* to = h < p.Hq ? p.q_out + (t * p.Hq + h) * p.D
+                             : (uint16_t*)((value ? p.cache.v + (h - p.Hq - p.Hkv) * p.cache.head_bytes
+                                                  : p.cache.k + (h - p.Hq) * p.cache.head_bytes) + row);
+                *(uint4*)(to + e0) = make_uint4(w[0], w[1], w[2], w[3]);
+                *(uint4*)(to + e1) = make_uint4(w[4], w[5], w[6], w[7]);
+                continue;
             }
+            float amax = 0.f;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const float2 u = both(a[n]), v = both(b[n]);
+                amax = fmaxf(fmaxf(amax, fmaxf(fabsf(u.x), fabsf(u.y))), fmaxf(fabsf(v.x), fabsf(v.y)));
+            }
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1)
+                if (o < L) amax = fmaxf(amax, __shfl_xor_sync(same, amax, o));
+            if (!live || row < 0) continue;
+            const float s = e4m3_scale(amax), inv = __frcp_rn(s);
+            const int kh = h - p.Hq - (value ? p.Hkv : 0);
+            uint32_t o[4];                             // codes of the pieces at e0 and e1
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const float2 u = both(a[n]), v = both(b[n]);
+                const float ua = e4m3_quotient(u.x, s, inv), ub = e4m3_quotient(u.y, s, inv);
+                const float va = e4m3_quotient(v.x, s, inv), vb = e4m3_quotient(v.y, s, inv);
+                // half words in the order of the elements
+                const uint32_t one = INTER ? f32_to_e4m3x2(ua, va) : f32_to_e4m3x2(ua, ub);
+                const uint32_t two = INTER ? f32_to_e4m3x2(ub, vb) : f32_to_e4m3x2(va, vb);
+                if (INTER) {
+                    o[n] = one | two << 16;
+                } else {
+                    o[n >> 1] = n & 1 ? o[n >> 1] | one << 16 : one;
+                    o[2 + (n >> 1)] = n & 1 ? o[2 + (n >> 1)] | two << 16 : two;
+                }
+            }
+            uint8_t* to = (value ? p.cache.v : p.cache.k) + kh * p.cache.head_bytes + row;
+            *(uint2*)(to + e0) = make_uint2(o[0], o[1]);
+            *(uint2*)(to + e1) = make_uint2(o[2], o[3]);
+            if (j == 0) (value ? p.cache.v_scale : p.cache.k_scale)[scale_row + (int64_t)kh * p.cache.page_size] = s;
         }
     }
 }
 
+constexpr int kManyHeads = 4;      // heads a thread takes where there are many tokens
+
 template <bool F16, bool INTER>
 const void* rope_kernel(bool e4m3, bool one) {
     if (one) return e4m3 ? (const void*)rope_write_kernel<F16, INTER, true, 1> : (const void*)rope_write_kernel<F16, INTER, false, 1>;
-    return e4m3 ? (const void*)rope_write_kernel<F16, INTER, true, 4> : (const void*)rope_write_kernel<F16, INTER, false, 4>;
+    return e4m3 ? (const void*)rope_write_kernel<F16, INTER, true, kManyHeads> : (const void*)rope_write_kernel<F16, INTER, false, kManyHeads>;
 }
 
 nvfp4_status launch_after(const void* kernel, dim3 grid, dim3 block, void** args, cudaStream_t stream, const char* fn) {
@@ -318,20 +345,21 @@ nvfp4_status launch_after(const void* kernel, dim3 grid, dim3 block, void** args
 
 nvfp4_status launch_rope(RopeParams p, bool f16, bool inter, cudaStream_t stream, const char* fn) {
     const int heads = p.Hq + 2 * p.Hkv;
-    if (p.rot % (inter ? 8 : 16) != 0) {
+    if (p.rot % 16 != 0) {
         const void* kernel = f16 ? (inter ? (const void*)rope_write_any_kernel<true, true> : (const void*)rope_write_any_kernel<true, false>)
                                  : (inter ? (const void*)rope_write_any_kernel<false, true> : (const void*)rope_write_any_kernel<false, false>);
         void* args[] = {&p};
         return launch_after(kernel, dim3((unsigned)std::min<int64_t>(ceil_div(p.T * heads, 8), (int64_t)sm_count() * 8)), dim3(256), args, stream, fn);
     }
-    int L = 2, per = 1;
-    while (L * 8 < p.D) L *= 2;
-    // Many tokens: about four heads a thread, all in flight.  Few tokens: one head
-    // a thread over as many blocks as that takes, for the shortest way through.
+    int L = 1, per = 1;
+    while (L * 16 < p.D) L *= 2;
+    // Many tokens: about four heads a thread, all in flight (4096 tokens: 24.6 us;
+    // three 31.0, two 28.5).  Few tokens: one head a thread over as many blocks
+    // as that takes, for the shortest way through.
     const bool one = p.T * heads * L <= (int64_t)sm_count() * 1024;
-    while (per * 2 * L <= 256 && (one ? per < heads : per * 4 < heads)) per *= 2;
+    while (per * 2 * L <= 256 && (one ? per < heads : per * kManyHeads < heads)) per *= 2;
     const int tokens = 256 / (L * per);                // a block's
-    dim3 grid((unsigned)ceil_div(p.T, tokens), one ? (unsigned)ceil_div(heads, per) : 1);
+    dim3 grid((unsigned)ceil_div(p.T, tokens), (unsigned)ceil_div(heads, per * (one ? 1 : kManyHeads)));
     const void* kernel = f16 ? (inter ? rope_kernel<true, true>(p.cache.e4m3, one) : rope_kernel<true, false>(p.cache.e4m3, one))
                              : (inter ? rope_kernel<false, true>(p.cache.e4m3, one) : rope_kernel<false, false>(p.cache.e4m3, one));
     void* args[] = {&p, &L, &per};
