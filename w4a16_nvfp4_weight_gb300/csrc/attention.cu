@@ -59,6 +59,7 @@ struct AttnParams {
     int* joins;                    // workspace: [blocks][2], unit and last block of a unit that starts here and goes on
     int B, Hq, G, chunks, units;   // chunks: head groups of one key head; units = heads * chunks a sequence
     int width;
+    bool whole_pages;              // a step lies in one page (page_size a multiple of 16)
     int window;                    // 0: none
     float scale_log2;              // softmax_scale * log2(e)
     int* status;
@@ -202,15 +203,18 @@ struct Place {
     }
 };
 
-// First step of global warp w of `warps`: equal ranges, or (fewer steps than
-// warps) one step a warp, packed into the first blocks.
-__device__ __forceinline__ int range_start(int w, int warps, int total) {
-    return total < warps ? min(w, total) : (int)((int64_t)w * total / warps);
-}
-// The warp whose range holds step x.
-__device__ __forceinline__ int range_of(int x, int warps, int total) {
-    return total < warps ? x : (int)((((int64_t)x + 1) * warps - 1) / total);
-}
+// The steps' ranges: the first `rest` warps have one step more than the others
+// (fewer steps than warps: one step a warp, packed into the first blocks).
+struct Ranges {
+    int each, rest;
+    __device__ __forceinline__ Ranges(int total, int warps) : each(total / warps), rest(total % warps) {}
+    __device__ __forceinline__ int start(int w) const { return w * each + min(w, rest); }
+    // The warp whose range holds step x.
+    __device__ __forceinline__ int holder(int x) const {
+        const int big = rest * (each + 1);
+        return x < big ? x / (each + 1) : rest + (x - big) / each;
+    }
+};
 
 template <bool F16, bool E4M3, int DP, int NT>
 __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, Shape<E4M3, DP, NT>::kCtas)
@@ -256,10 +260,10 @@ attend_kernel(const AttnParams p) {
         int at = before + incl - mine;
         if (mine > 0) {
             int starts[W];
+            const Ranges ranges(total, warps);
 #pragma unroll
-            for (int w = 0; w < W; ++w) starts[w] = range_start(blockIdx.x * W + w, warps, total);
-            const int end = at + mine;
-            if (starts[0] < end && starts[W - 1] >= at) {
+            for (int w = 0; w < W; ++w) starts[w] = ranges.start(blockIdx.x * W + w);
+            if (starts[0] < at + mine && starts[W - 1] >= at) {
                 for (int b = b0; b < b1; ++b) {
                     const int n = steps_of(p, checked_length(p, b)) * p.units;
 #pragma unroll
@@ -272,8 +276,9 @@ attend_kernel(const AttnParams p) {
                 }
             }
         }
-        a = range_start(gw, warps, total);
-        e = range_start(gw + 1, warps, total);
+        const Ranges ranges(total, warps);
+        a = ranges.start(gw);
+        e = ranges.start(gw + 1);
         __syncthreads();
     }
 
@@ -308,52 +313,90 @@ attend_kernel(const AttnParams p) {
         Place c = f;                                            // the step to compute
         int unit_start = a - (c.step - c.s_lo);                 // global number of the unit's first step
 
-        // Lane l keeps the page and place of token l % 16 of the next step to copy.
-        int page = -1, at = 0;
-        auto locate = [&] {
-            const int t = f.step * kStep + (lane & 15);
-            page = -1;
-            if (t >= f.lo && t < f.n) {
+        // The page of a step's tokens (lane l: of token l % 16) is loaded well before its rows.
+        struct Rows { int page, at, kh, b_lo, b_n; };           // at: place in the page; token range as offsets from the step's first
+        auto locate = [&](const Place& f) {
+            Rows r;
+            const int t = f.step * kStep + (p.whole_pages ? 0 : lane & 15);
+            r.kh = p.chunks == 1 ? f.u : f.u / p.chunks;
+            r.b_lo = f.lo - f.step * kStep;
+            r.b_n = f.n - f.step * kStep;
+            r.page = 0;
+            r.at = 0;
+            if (p.whole_pages || (t >= f.lo && t < f.n)) {
                 const int i = p.cache.page_shift >= 0 ? t >> p.cache.page_shift : t / p.cache.page_size;
-                at = t - i * p.cache.page_size;
-                page = p.block_table[f.b * p.table_stride + i];
-                if ((uint32_t)page >= (uint32_t)p.cache.num_pages) {
-                    record_status(p.status, NVFP4_ERR_BAD_INDEX);
-                    page = 0;
-                }
+                r.at = t - i * p.cache.page_size;
+                r.page = p.block_table[f.b * p.table_stride + i];
             }
+            return r;
         };
         const int r0 = lane / CH, c0 = lane % CH;
-        int next = a;                                           // its number
-        auto copy = [&](int stage) {
-            if (next < e) {
-                const int kh = p.chunks == 1 ? f.u : f.u / p.chunks;
-                const int64_t off = page < 0 ? -1 : p.cache.row(page, kh, at);
-                const uint32_t dst = ring_s + stage * S::kStage;
+        const int64_t lane_off = r0 * p.cache.token_bytes + c0 * 16;
+        auto copy = [&](Rows r, int stage) {
+            const uint32_t dst = ring_s + stage * S::kStage;
+            if ((uint32_t)r.page >= (uint32_t)p.cache.num_pages) {
+                record_status(p.status, NVFP4_ERR_BAD_INDEX);
+                r.page = 0;
+            }
+            if (p.whole_pages) {                                // 16 rows of one page, evenly spaced
+                const int64_t off = p.cache.row(r.page, r.kh, r.at) + lane_off;
+                const uint8_t *k = p.cache.k + off, *v = p.cache.v + off;
+                if (c0 < held_chunks) {
 #pragma unroll
-                for (int i = 0; i < CH / 2; ++i) {              // 32 / CH rows an instruction
-                    const int r = i * (32 / CH) + r0;
-                    const int64_t o = __shfl_sync(0xffffffffu, off, r);
-                    if (c0 < held_chunks) {
-                        const int64_t from = (o < 0 ? 0 : o) + c0 * 16;
-                        cp_async16(dst + r * S::kRow + key_chunk<E4M3, CH>(r, c0) * 16, p.cache.k + from, o >= 0);
-                        cp_async16(dst + S::kTile + r * S::kRow + value_chunk<E4M3, CH>(r, c0) * 16, p.cache.v + from, o >= 0);
+                    for (int i = 0; i < CH / 2; ++i) {          // 32 / CH rows an instruction
+                        const int x = i * (32 / CH) + r0;
+                        const bool held = x >= r.b_lo && x < r.b_n;
+                        cp_async16(dst + x * S::kRow + key_chunk<E4M3, CH>(x, c0) * 16, k, held);
+                        cp_async16(dst + S::kTile + x * S::kRow + value_chunk<E4M3, CH>(x, c0) * 16, v, held);
+                        k += (32 / CH) * p.cache.token_bytes;
+                        v += (32 / CH) * p.cache.token_bytes;
                     }
                 }
                 if (E4M3) {                                     // lanes 0-15 the keys' scales, 16-31 the values'
-                    const float* s = lane < 16 ? p.cache.k_scale : p.cache.v_scale;
-                    cp_async4(dst + 2 * S::kTile + lane * 4, s + (page < 0 ? 0 : p.cache.scale_at(page, kh, at)), page >= 0);
+                    const int x = lane & 15;
+                    cp_async4(dst + 2 * S::kTile + lane * 4,
+                              (lane < 16 ? p.cache.k_scale : p.cache.v_scale) + p.cache.scale_at(r.page, r.kh, r.at) + x,
+                              x >= r.b_lo && x < r.b_n);
                 }
-                if (++next < e) {
-                    f.advance(p);
-                    locate();
+            } else {
+                const int64_t off = p.cache.row(r.page, r.kh, r.at);
+#pragma unroll
+                for (int i = 0; i < CH / 2; ++i) {
+                    const int x = i * (32 / CH) + r0;
+                    const int64_t from = __shfl_sync(0xffffffffu, off, x) + c0 * 16;
+                    const bool held = x >= r.b_lo && x < r.b_n;
+                    if (c0 < held_chunks) {
+                        cp_async16(dst + x * S::kRow + key_chunk<E4M3, CH>(x, c0) * 16, p.cache.k + from, held);
+                        cp_async16(dst + S::kTile + x * S::kRow + value_chunk<E4M3, CH>(x, c0) * 16, p.cache.v + from, held);
+                    }
+                }
+                if (E4M3)
+                    cp_async4(dst + 2 * S::kTile + lane * 4,
+                              (lane < 16 ? p.cache.k_scale : p.cache.v_scale) + p.cache.scale_at(r.page, r.kh, r.at),
+                              (lane & 15) >= r.b_lo && (lane & 15) < r.b_n);
+            }
+        };
+        // The first stages' pages are loaded together, then one step ahead.
+        int next = a;                                           // number of the step that `ahead` belongs to
+        Rows ahead;
+        {
+            Rows first[S::kStages];
+#pragma unroll
+            for (int s = 0; s < S::kStages; ++s) {
+                if (next < e) {
+                    first[s] = locate(f);
+                    if (next + 1 < e) f.advance(p);
+                    ++next;
                 }
             }
-            cp_async_commit();
-        };
-        locate();
 #pragma unroll
-        for (int s = 0; s < S::kStages - 1; ++s) copy(s);
+            for (int s = 0; s < S::kStages - 1; ++s) {
+                if (a + s < e) copy(first[s], s);
+                cp_async_commit();
+            }
+            ahead = first[S::kStages - 1];
+            next = a + S::kStages - 1;
+        }
 
         uint32_t qf[KS][NT][2];
         float o[KS][NT][4], m[NT][2], l[NT][2], qs[NT][2];
@@ -414,7 +457,14 @@ attend_kernel(const AttnParams p) {
 
             cp_async_wait<S::kStages - 2>();
             __syncwarp();                                       // the stage is whole, and every lane is done with the one before
-            copy(stage == 0 ? S::kStages - 1 : stage - 1);
+            if (next < e) {
+                copy(ahead, stage == 0 ? S::kStages - 1 : stage - 1);
+                if (++next < e) {
+                    ahead = locate(f);
+                    if (next + 1 < e) f.advance(p);
+                }
+            }
+            cp_async_commit();
             const uint32_t ks_s = ring_s + stage * S::kStage, vs_s = ks_s + S::kTile;
             stage = stage + 1 == S::kStages ? 0 : stage + 1;
 
@@ -621,7 +671,8 @@ attend_kernel(const AttnParams p) {
         piece_unit[2 * warp + 1] = tail_unit; piece_lo[2 * warp + 1] = tail_lo; piece_hi[2 * warp + 1] = tail_hi;
     }
     __syncthreads();
-    const int block_lo = range_start(blockIdx.x * W, warps, total), block_hi = range_start(blockIdx.x * W + W, warps, total);
+    const Ranges ranges(total, warps);
+    const int block_lo = ranges.start(blockIdx.x * W), block_hi = ranges.start(blockIdx.x * W + W);
     int goes_on = -1, goes_to = 0;
     for (int i = 0; i < 2 * W;) {
         const int unit = piece_unit[i];
@@ -633,34 +684,34 @@ attend_kernel(const AttnParams p) {
         float* to = p.parts + ((size_t)blockIdx.x * 2 + (lo < block_lo ? 0 : 1)) * S::kPart;
         if (!whole && lo >= block_lo) {
             goes_on = unit;
-            goes_to = range_of(hi - 1, warps, total) / W;
+            goes_to = ranges.holder(hi - 1) / W;
         }
         const int b = unit / p.units, u = unit - b * p.units, kh = u / p.chunks, h0 = (u - kh * p.chunks) * S::kHeads;
         const int64_t row = (int64_t)b * p.Hq + kh * p.G + h0;
         const int heads = min(S::kHeads, p.G - h0);
-        for (int x = tid; x < heads * DP; x += W * 32) {
+        // a thread four dimensions of one head
+        for (int x = tid * 4; x < heads * DP; x += W * 32 * 4) {
             const int hl = x / DP, d = x % DP;
             if (d >= D) continue;
-            float top = -INFINITY, sum = 0.f, v = 0.f;
+            float top = -INFINITY, sum = 0.f;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int y = i; y < j; ++y) {
                 if (piece_unit[y] < 0) continue;
                 const float* part = y & 1 ? (const float*)(ring_all + (y >> 1) * S::kRing)
                                           : warp_parts + (size_t)(blockIdx.x * W + (y >> 1)) * S::kPart;
-                top = fmaxf(top, part[S::kHeads * DP + hl]);
-            }
-            for (int y = i; y < j; ++y) {
-                if (piece_unit[y] < 0) continue;
-                const float* part = y & 1 ? (const float*)(ring_all + (y >> 1) * S::kRing)
-                                          : warp_parts + (size_t)(blockIdx.x * W + (y >> 1)) * S::kPart;
-                const float mine = part[S::kHeads * DP + hl], f = mine == top ? 1.f : ex2(mine - top);
-                sum += f * part[S::kHeads * (DP + 1) + hl];
-                v += f * part[x];
+                const float mine = part[S::kHeads * DP + hl], to_top = fmaxf(top, mine);
+                const float fo = top == to_top ? 1.f : ex2(top - to_top), fn = mine == to_top ? 1.f : ex2(mine - to_top);
+                const float4 o = *(const float4*)(part + x);
+                sum = sum * fo + part[S::kHeads * (DP + 1) + hl] * fn;
+                v.x = v.x * fo + o.x * fn; v.y = v.y * fo + o.y * fn; v.z = v.z * fo + o.z * fn; v.w = v.w * fo + o.w * fn;
+                top = to_top;
             }
             if (whole) {
-                p.out[(row + hl) * D + d] = f32_to_act_bits<F16>(v / sum);
+                const float inv = 1.f / sum;
+                *(uint2*)(p.out + (row + hl) * D + d) = make_uint2(f32_to_act2<F16>(v.x * inv, v.y * inv), f32_to_act2<F16>(v.z * inv, v.w * inv));
                 if (p.lse && d == 0) p.lse[row + hl] = (top + log2f(sum)) * 0.693147180559945309f;
             } else {
-                to[x] = v;
+                *(float4*)(to + x) = v;
                 if (d == 0) {
                     to[S::kHeads * DP + hl] = top;
                     to[S::kHeads * (DP + 1) + hl] = sum;
@@ -684,16 +735,31 @@ __global__ void __launch_bounds__(DP) join_kernel(const AttnParams p, int group)
     const int unit = p.joins[2 * x], to = p.joins[2 * x + 1];
     if (unit < 0) return;
     const int b = unit / p.units, u = unit - b * p.units, kh = u / p.chunks, h0 = (u - kh * p.chunks) * group;
-    if (h0 + hl >= p.G || d >= D) return;
-    const int size = group * (DP + 2);
+    if (h0 + hl >= p.G) return;
+    const int size = group * (DP + 2), lane = threadIdx.x & 31;
+    // Lane y holds the maximum and sum of piece y, 32 pieces at a time.
+    const auto part = [&](int y) { return p.parts + ((size_t)y * 2 + (y == x)) * size; };
     float top = -INFINITY, sum = 0.f, v = 0.f;
-    for (int y = x; y <= to; ++y) top = fmaxf(top, p.parts[((size_t)y * 2 + (y == x)) * size + group * DP + hl]);
-    for (int y = x; y <= to; ++y) {
-        const float* part = p.parts + ((size_t)y * 2 + (y == x)) * size;
-        const float mine = part[group * DP + hl], f = mine == top ? 1.f : ex2(mine - top);
-        sum += f * part[group * (DP + 1) + hl];
-        v += f * part[hl * DP + d];
+    for (int y0 = x; y0 <= to; y0 += 32) {
+        const int n = min(32, to + 1 - y0);
+        const float mine = lane < n ? part(y0 + lane)[group * DP + hl] : -INFINITY;
+        const float mass = lane < n ? part(y0 + lane)[group * (DP + 1) + hl] : 0.f;
+        float high = mine;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, o));
+        high = fmaxf(high, top);
+        const float fo = top == high ? 1.f : ex2(top - high), fn = mine == high ? 1.f : ex2(mine - high);
+        sum *= fo;
+        v *= fo;
+        top = high;
+#pragma unroll 8
+        for (int y = 0; y < n; ++y) {
+            const float f = __shfl_sync(0xffffffffu, fn, y);
+            sum += f * __shfl_sync(0xffffffffu, mass, y);
+            v += f * part(y0 + y)[hl * DP + d];
+        }
     }
+    if (d >= D) return;
     const int64_t row = (int64_t)b * p.Hq + kh * p.G + h0 + hl;
     p.out[row * D + d] = f32_to_act_bits<F16>(v / sum);
     if (p.lse && d == 0) p.lse[row] = (top + log2f(sum)) * 0.693147180559945309f;
@@ -798,6 +864,7 @@ extern "C" nvfp4_status nvfp4_paged_attention(const void* q, int64_t q_row_strid
     p.units = p.cache.heads * p.chunks;
     p.window = (int)std::min<int64_t>(window, INT32_MAX);
     p.scale_log2 = softmax_scale * 1.44269504088896341f;
+    p.whole_pages = p.cache.page_size % kStep == 0;
     cudaStream_t s = (cudaStream_t)stream;
     if (p.cache.e4m3) return f16 ? launch_shape<true, true>(p, DP, NT, workspace, s) : launch_shape<false, true>(p, DP, NT, workspace, s);
     return f16 ? launch_shape<true, false>(p, DP, NT, workspace, s) : launch_shape<false, false>(p, DP, NT, workspace, s);
