@@ -45,7 +45,7 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kStep = 16;          // tokens a step
-constexpr size_t kSmemPerSm = 228 * 1024, kReservedPerCta = 1024, kMaxSmem = 227 * 1024;
+constexpr size_t kMaxSmem = 227 * 1024;
 
 struct AttnParams {
     const uint16_t* q;             // strides q_row, q_head (elements)
@@ -56,7 +56,6 @@ struct AttnParams {
     uint16_t* out;                 // [B, Hq, D]
     float* lse;                    // [B, Hq] or null
     float* parts;                  // workspace: partial results of blocks, then of warps
-    int* joins;                    // workspace: [blocks][2], unit and last block of a unit that starts here and goes on
     int B, Hq, G, chunks, units;   // chunks: head groups of one key head; units = heads * chunks a sequence
     int width;
     bool whole_pages;              // a step lies in one page (page_size a multiple of 16)
@@ -66,6 +65,13 @@ struct AttnParams {
     CacheView cache;
 };
 
+// By the bytes of a row, and the output values a lane holds: warps a block (one
+// block an SM) and steps in a warp's ring.  As many bytes in flight as shared
+// memory holds, and as many warps as that and the registers leave: steps of 4 KB
+// need sixteen to be computed as fast as they come.
+constexpr int attn_warps(int row, int values) { return row > 256 ? 4 : row > 128 || values >= 64 ? 8 : 16; }
+constexpr int attn_stages(int row, int values) { return row == 64 ? 4 : row == 128 && values >= 64 ? 6 : 3; }
+
 // Shape of an instance: DP padded head size, NT tiles of 8 query heads.
 template <bool E4M3, int DP, int NT>
 struct Shape {
@@ -73,24 +79,19 @@ struct Shape {
     static constexpr int kChunks = kRow / 16;                   // 16-byte chunks a row
     static constexpr int kTile = kStep * kRow;
     static constexpr int kStage = 2 * kTile + (E4M3 ? 2 * kStep * 4 : 0);
-    // Warps and ring depth: as many bytes in flight as shared memory holds; the
-    // 512-byte rows of 256 dimensions leave room for four warps.
-    static constexpr int kWarps = kRow == 512 ? 4 : 8;
-    static constexpr int kStages = kRow == 64 ? 4 : 3;
+    static constexpr int kWarps = attn_warps(kRow, DP / 4 * NT);
+    static constexpr int kStages = attn_stages(kRow, DP / 4 * NT);
     static constexpr int kRing = kStages * kStage;
     static constexpr size_t kSmem = (size_t)kWarps * kRing;
-    static constexpr int kByRing = (int)(kSmemPerSm / (kSmem + kReservedPerCta));
-    static constexpr int kCtas = kByRing < 1 ? 1 : kByRing > 2 ? 2 : kByRing;
     static constexpr int kHeads = 8 * NT;
     static constexpr int kPart = kHeads * (DP + 2);             // floats of a partial result: o, m, l
-    static_assert(kSmem <= kMaxSmem && kPart * 4 <= kRing, "ring");
+    static constexpr int kPitch = DP + 4;                       // floats from head to head in shared memory
+    static_assert(kSmem + 10240 <= kMaxSmem && kHeads * kPitch * 4 <= kRing && 8 * kPitch * 4 <= kStage, "ring");
 };
 
 // Partial results in the workspace: two a block, then one a warp.
-inline size_t workspace_for(int row, int heads, int DP, int64_t sms) {
-    const int warps = row == 512 ? 4 : 8;
-    const size_t ctas = 2 * (size_t)sms;
-    return round_up(ctas * 8, 256) + ctas * (2 + warps) * heads * (DP + 2) * sizeof(float);
+inline size_t workspace_for(int heads, int DP, int64_t sms) {
+    return (size_t)sms * (2 + 16) * heads * (DP + 2) * sizeof(float);      // at most 16 warps a block
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -162,13 +163,49 @@ __device__ __forceinline__ int out_dim(int mt, int half, int g) {
     return ((mt >> 3) * 8 + g) * 16 + (mt & 7) * 2 + half;
 }
 
+// Output tile nt (8 heads) of a warp to rows of DP + 4 floats, a head each.
+template <bool E4M3, int DP, int NT>
+__device__ __forceinline__ void store_heads(float* to, const float (&o)[DP / 16][NT][4], int nt, int g, int q4) {
+    to += q4 * 2 * (DP + 4) + (E4M3 ? g * (DP == 64 ? 8 : 16) : g);
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int mt = 0; mt < DP / 16; ++mt) {
+            float* at = to + x * (DP + 4) + out_dim<E4M3, DP>(mt, 0, 0);
+            if (!E4M3) {
+                at[0] = o[mt][nt][x];
+                at[8] = o[mt][nt][2 + x];
+            } else if (mt % 2 == 0) {                           // two tiles have four dimensions in a row
+                *(float4*)at = make_float4(o[mt][nt][x], o[mt][nt][2 + x], o[mt + 1][nt][x], o[mt + 1][nt][2 + x]);
+            }
+        }
+}
+
+__device__ __forceinline__ float reciprocal(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float log_sum(float m, float l) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(l));
+    return (m + y) * 0.693147180559945309f;
+}
+// exp2(m - top) for m <= top, and 1 for two equal infinities.
+__device__ __forceinline__ float factor(float m, float top) { return m == top ? 1.f : ex2(m - top); }
+
+// Four dimensions of the output, normalised.
+template <bool F16>
+__device__ __forceinline__ void store_out(uint16_t* to, float4 v, float inv) {
+    *(uint2*)to = make_uint2(f32_to_act2<F16>(v.x * inv, v.y * inv), f32_to_act2<F16>(v.z * inv, v.w * inv));
+}
+
 // Tokens of sequence b that the table can hold; a length outside is recorded and clamped.
 __device__ __forceinline__ int checked_length(const AttnParams& p, int b) {
-    const int n = p.lengths[b];
-    const int64_t most = (int64_t)p.width * p.cache.page_size;
-    if (n < 0 || n > most) {
+    const int n = p.lengths[b], most = p.width * p.cache.page_size;
+    if ((uint32_t)n > (uint32_t)most) {
         record_status(p.status, NVFP4_ERR_BAD_INDEX);
-        return n < 0 ? 0 : (int)most;
+        return n < 0 ? 0 : most;
     }
     return n;
 }
@@ -216,30 +253,16 @@ struct Ranges {
     }
 };
 
-template <bool F16, bool E4M3, int DP, int NT>
-__global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, Shape<E4M3, DP, NT>::kCtas)
-attend_kernel(const AttnParams p) {
-    using S = Shape<E4M3, DP, NT>;
-    constexpr int W = S::kWarps, CH = S::kChunks, KS = DP / 16;
-    constexpr bool H = F16 || E4M3;                             // FP16 operands in the MMAs
-    extern __shared__ __align__(1024) uint8_t ring_all[];
-    __shared__ int scan_sm[W];
-    __shared__ int start_sm[W][2];                              // sequence of a warp's first step, and its first step
-    __shared__ int piece_unit[2 * W], piece_lo[2 * W], piece_hi[2 * W];
+// The numbering of all steps, by a block of WARPS warps: thread t takes `per`
+// sequences from t * per on; sm holds the first step of each thread's.
+template <int WARPS>
+struct Numbering {
+    int per, total;
 
-    pdl_wait_previous();
-    pdl_launch_dependents();                                    // the joining kernel waits for this one's end
-
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int g = lane >> 2, q4 = lane & 3;
-    const int warps = gridDim.x * W, gw = blockIdx.x * W + warp;
-    const int D = p.cache.D;
-
-    // ---- number the steps: a scan over the sequences' lengths
-    int total, a, e;
-    {
-        const int per = (p.B + W * 32 - 1) / (W * 32);
-        const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+    __device__ __forceinline__ void count(const AttnParams& p, int* sm, int* sums) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        per = (p.B + WARPS * 32 - 1) / (WARPS * 32);
+        const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
         int mine = 0;
         for (int b = b0; b < b1; ++b) mine += steps_of(p, checked_length(p, b)) * p.units;
         int incl = mine;
@@ -248,42 +271,56 @@ attend_kernel(const AttnParams p) {
             const int u = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += u;
         }
-        if (lane == 31) scan_sm[warp] = incl;
+        if (lane == 31) sums[warp] = incl;
         __syncthreads();
-        int before = 0;
-        total = 0;
+        int s = lane < WARPS ? sums[lane] : 0, before = lane < warp ? s : 0;
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
-            if (w < warp) before += scan_sm[w];
-            total += scan_sm[w];
+        for (int o = 16; o > 0; o >>= 1) {
+            s += __shfl_xor_sync(0xffffffffu, s, o);
+            before += __shfl_xor_sync(0xffffffffu, before, o);
         }
-        int at = before + incl - mine;
-        if (mine > 0) {
-            int starts[W];
-            const Ranges ranges(total, warps);
-#pragma unroll
-            for (int w = 0; w < W; ++w) starts[w] = ranges.start(blockIdx.x * W + w);
-            if (starts[0] < at + mine && starts[W - 1] >= at) {
-                for (int b = b0; b < b1; ++b) {
-                    const int n = steps_of(p, checked_length(p, b)) * p.units;
-#pragma unroll
-                    for (int w = 0; w < W; ++w)
-                        if (starts[w] >= at && starts[w] < at + n) {
-                            start_sm[w][0] = b;
-                            start_sm[w][1] = at;
-                        }
-                    at += n;
-                }
-            }
-        }
-        const Ranges ranges(total, warps);
-        a = ranges.start(gw);
-        e = ranges.start(gw + 1);
+        total = s;
+        sm[threadIdx.x] = before + incl - mine;
         __syncthreads();
     }
+    // The sequence that holds step x < total, and its first step (a whole warp asks).
+    __device__ __forceinline__ int find(const AttnParams& p, const int* sm, int x, int* first) const {
+        int t = -1;
+#pragma unroll 4
+        for (int k = 0; k < WARPS * 32; k += 32) t += __popc(__ballot_sync(0xffffffffu, sm[k + (threadIdx.x & 31)] <= x));
+        int b = t * per, at = sm[t];
+        for (int n; per > 1 && x >= at + (n = steps_of(p, checked_length(p, b)) * p.units); ++b) at += n;
+        *first = at;
+        return b;
+    }
+};
+
+template <bool F16, bool E4M3, int DP, int NT>
+__global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_kernel(const AttnParams p) {
+    using S = Shape<E4M3, DP, NT>;
+    constexpr int W = S::kWarps, CH = S::kChunks, KS = DP / 16, ST = S::kStages;
+    constexpr bool H = F16 || E4M3;                             // FP16 operands in the MMAs
+    extern __shared__ __align__(1024) uint8_t ring_all[];
+    __shared__ int first_sm[W * 32], sums[W];
+    // Pieces of units, two a warp: the rest of a unit that an earlier warp began, and the last of the range.
+    __shared__ int piece_unit[2 * W], piece_lo[2 * W], piece_hi[2 * W];
+    __shared__ float piece_m[2 * W][S::kHeads], piece_l[2 * W][S::kHeads];
+
+    pdl_wait_previous();
+    pdl_launch_dependents();                                    // the joining kernel numbers the steps meanwhile
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, q4 = lane & 3;
+    const int gw = blockIdx.x * W + warp;
+    const int D = p.cache.D;
+
+    Numbering<W> steps;
+    steps.count(p, first_sm, sums);
+    const Ranges ranges(steps.total, gridDim.x * W);
+    const int a = ranges.start(gw), e = ranges.start(gw + 1);
 
     // ---- sequences without a token
-    for (int b = gw; b < p.B; b += warps) {
+    for (int b = gw; b < p.B; b += gridDim.x * W) {
         if (steps_of(p, checked_length(p, b)) > 0) continue;
         uint4* o = (uint4*)(p.out + (int64_t)b * p.Hq * D);
         for (int i = lane; i < p.Hq * D / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
@@ -298,154 +335,106 @@ attend_kernel(const AttnParams p) {
         __syncwarp();
     }
     float* const warp_parts = p.parts + (size_t)gridDim.x * 2 * S::kPart;
-    int head_unit = -1, head_lo = 0, head_hi = 0, tail_unit = -1, tail_lo = 0, tail_hi = 0;
+    int head_unit = -1, tail_unit = -1;
 
     if (a < e) {
-        const int held_chunks = D * (E4M3 ? 1 : 2) / 16;
         Place f;                                                // the next step to copy
-        f.b = start_sm[warp][0];
+        int unit_start;                                         // number of the computed unit's first step
+        f.b = steps.find(p, first_sm, a, &unit_start);
         f.sequence(p);
         {
-            const int in = a - start_sm[warp][1], steps = f.s_hi - f.s_lo;
-            f.u = in / steps;
-            f.step = f.s_lo + in % steps;
+            const int in = a - unit_start, each = f.s_hi - f.s_lo;
+            f.u = in / each;
+            f.step = f.s_lo + in - f.u * each;
+            unit_start += f.u * each;
         }
         Place c = f;                                            // the step to compute
-        int unit_start = a - (c.step - c.s_lo);                 // global number of the unit's first step
 
-        // The page of a step's tokens (lane l: of token l % 16) is loaded well before its rows.
-        struct Rows { int page, at, kh, b_lo, b_n; };           // at: place in the page; token range as offsets from the step's first
-        auto locate = [&](const Place& f) {
-            Rows r;
-            const int t = f.step * kStep + (p.whole_pages ? 0 : lane & 15);
-            r.kh = p.chunks == 1 ? f.u : f.u / p.chunks;
-            r.b_lo = f.lo - f.step * kStep;
-            r.b_n = f.n - f.step * kStep;
-            r.page = 0;
-            r.at = 0;
-            if (p.whole_pages || (t >= f.lo && t < f.n)) {
-                const int i = p.cache.page_shift >= 0 ? t >> p.cache.page_shift : t / p.cache.page_size;
-                r.at = t - i * p.cache.page_size;
-                r.page = p.block_table[f.b * p.table_stride + i];
-            }
-            return r;
+        // Table entries [base, base + 64) of sequence window_b, two a lane.  The second
+        // half is loaded when the first is entered, long before it is needed.
+        int near = 0, far = 0, base = 0, window_b = -1;
+        auto entry = [&](int t) { return p.cache.page_shift >= 0 ? t >> p.cache.page_shift : t / p.cache.page_size; };
+        auto load_entries = [&](int i) {
+            return i <= entry(f.n - 1) ? p.block_table[f.b * p.table_stride + i] : 0;
         };
-        const int r0 = lane / CH, c0 = lane % CH;
-        const int64_t lane_off = r0 * p.cache.token_bytes + c0 * 16;
-        auto copy = [&](Rows r, int stage) {
+        const int held_chunks = D * (E4M3 ? 1 : 2) / 16, r0 = lane / CH, c0 = lane % CH;
+        auto copy = [&](int stage) {
             const uint32_t dst = ring_s + stage * S::kStage;
-            if ((uint32_t)r.page >= (uint32_t)p.cache.num_pages) {
-                record_status(p.status, NVFP4_ERR_BAD_INDEX);
-                r.page = 0;
+            const int s0 = f.step * kStep, i0 = entry(max(s0, f.lo));
+            if (f.b != window_b || i0 < base || i0 >= base + 64) {
+                window_b = f.b;
+                base = i0;
+                near = load_entries(base + lane);
+                far = load_entries(base + 32 + lane);
+            } else if (i0 >= base + 32) {
+                base += 32;
+                near = far;
+                far = load_entries(base + 32 + lane);
             }
-            if (p.whole_pages) {                                // 16 rows of one page, evenly spaced
-                const int64_t off = p.cache.row(r.page, r.kh, r.at) + lane_off;
-                const uint8_t *k = p.cache.k + off, *v = p.cache.v + off;
+            // the page and place of token lane % 16; those not held take a neighbour's
+            const int t = min(max(s0 + (lane & 15), f.lo), f.n - 1), i = entry(t);
+            const int n0 = __shfl_sync(0xffffffffu, near, (i - base) & 31), n1 = __shfl_sync(0xffffffffu, far, (i - base) & 31);
+            int page = i - base < 32 ? n0 : n1;
+            if ((uint32_t)page >= (uint32_t)p.cache.num_pages) {
+                record_status(p.status, NVFP4_ERR_BAD_INDEX);
+                page = 0;
+            }
+            const int at = t - i * p.cache.page_size, kh = p.chunks == 1 ? f.u : f.u / p.chunks;
+            const int64_t off = p.cache.row(page, kh, at);
+            const int r_lo = f.lo - s0, r_hi = f.n - s0;        // rows [r_lo, r_hi) are held
+            if (p.whole_pages && r_lo <= 0) {                   // rows evenly spaced from the first one on
+                const int64_t from = __shfl_sync(0xffffffffu, off, 0) + r0 * p.cache.token_bytes + c0 * 16;
+                const uint8_t *k = p.cache.k + from, *v = p.cache.v + from;
                 if (c0 < held_chunks) {
 #pragma unroll
-                    for (int i = 0; i < CH / 2; ++i) {          // 32 / CH rows an instruction
-                        const int x = i * (32 / CH) + r0;
-                        const bool held = x >= r.b_lo && x < r.b_n;
-                        cp_async16(dst + x * S::kRow + key_chunk<E4M3, CH>(x, c0) * 16, k, held);
-                        cp_async16(dst + S::kTile + x * S::kRow + value_chunk<E4M3, CH>(x, c0) * 16, v, held);
+                    for (int j = 0; j < CH / 2; ++j) {          // 32 / CH rows an instruction
+                        const int r = j * (32 / CH) + r0;
+                        cp_async16(dst + r * S::kRow + key_chunk<E4M3, CH>(r, c0) * 16, k, r < r_hi);
+                        cp_async16(dst + S::kTile + r * S::kRow + value_chunk<E4M3, CH>(r, c0) * 16, v, r < r_hi);
                         k += (32 / CH) * p.cache.token_bytes;
                         v += (32 / CH) * p.cache.token_bytes;
                     }
                 }
-                if (E4M3) {                                     // lanes 0-15 the keys' scales, 16-31 the values'
-                    const int x = lane & 15;
-                    cp_async4(dst + 2 * S::kTile + lane * 4,
-                              (lane < 16 ? p.cache.k_scale : p.cache.v_scale) + p.cache.scale_at(r.page, r.kh, r.at) + x,
-                              x >= r.b_lo && x < r.b_n);
-                }
             } else {
-                const int64_t off = p.cache.row(r.page, r.kh, r.at);
 #pragma unroll
-                for (int i = 0; i < CH / 2; ++i) {
-                    const int x = i * (32 / CH) + r0;
-                    const int64_t from = __shfl_sync(0xffffffffu, off, x) + c0 * 16;
-                    const bool held = x >= r.b_lo && x < r.b_n;
+                for (int j = 0; j < CH / 2; ++j) {
+                    const int r = j * (32 / CH) + r0;
+                    const int64_t from = __shfl_sync(0xffffffffu, off, r) + c0 * 16;
                     if (c0 < held_chunks) {
-                        cp_async16(dst + x * S::kRow + key_chunk<E4M3, CH>(x, c0) * 16, p.cache.k + from, held);
-                        cp_async16(dst + S::kTile + x * S::kRow + value_chunk<E4M3, CH>(x, c0) * 16, p.cache.v + from, held);
+                        cp_async16(dst + r * S::kRow + key_chunk<E4M3, CH>(r, c0) * 16, p.cache.k + from, r >= r_lo && r < r_hi);
+                        cp_async16(dst + S::kTile + r * S::kRow + value_chunk<E4M3, CH>(r, c0) * 16, p.cache.v + from, r >= r_lo && r < r_hi);
                     }
                 }
-                if (E4M3)
-                    cp_async4(dst + 2 * S::kTile + lane * 4,
-                              (lane < 16 ? p.cache.k_scale : p.cache.v_scale) + p.cache.scale_at(r.page, r.kh, r.at),
-                              (lane & 15) >= r.b_lo && (lane & 15) < r.b_n);
             }
+            if (E4M3)                                           // lanes 0-15 the keys' scales, 16-31 the values'
+                cp_async4(dst + 2 * S::kTile + lane * 4,
+                          (lane < 16 ? p.cache.k_scale : p.cache.v_scale) + p.cache.scale_at(page, kh, at),
+                          (lane & 15) >= r_lo && (lane & 15) < r_hi);
         };
-        // The first stages' pages are loaded together, then one step ahead.
-        int next = a;                                           // number of the step that `ahead` belongs to
-        Rows ahead;
-        {
-            Rows first[S::kStages];
-#pragma unroll
-            for (int s = 0; s < S::kStages; ++s) {
-                if (next < e) {
-                    first[s] = locate(f);
-                    if (next + 1 < e) f.advance(p);
-                    ++next;
-                }
-            }
-#pragma unroll
-            for (int s = 0; s < S::kStages - 1; ++s) {
-                if (a + s < e) copy(first[s], s);
-                cp_async_commit();
-            }
-            ahead = first[S::kStages - 1];
-            next = a + S::kStages - 1;
-        }
 
         uint32_t qf[KS][NT][2];
         float o[KS][NT][4], m[NT][2], l[NT][2], qs[NT][2];
-        int stage = 0;
-        bool fresh = true;                                      // a unit begins
-        int seg_begin = a;
-        for (int i = a; i < e; ++i) {
+        bool fresh = true, unscaled = true;                     // a unit begins; its query is not yet scaled
+        int seg_begin = a, fill = 0, stage = 0;
+        for (int i = a - (ST - 1); i < e; ++i) {                // the first trips only fill the ring
             if (fresh) {
                 fresh = false;
+                unscaled = true;
                 const int kh = p.chunks == 1 ? c.u : c.u / p.chunks;
                 const int h0 = (c.u - kh * p.chunks) * S::kHeads;       // first head of the group
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const int hg = h0 + nt * 8 + g;
                     const bool held = hg < p.G;
-                    const uint16_t* qr = p.q + c.b * p.q_row + (int64_t)(kh * p.G + (held ? hg : 0)) * p.q_head;
+                    const uint16_t* qr = p.q + c.b * p.q_row + (int64_t)(kh * p.G + (held ? hg : 0)) * p.q_head + q4 * (E4M3 ? 16 : 2);
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
-                            const int d = E4M3 ? ((ks >> 2) * 4 + q4) * 16 + (ks & 3) * 4 + x * 2 : ks * 16 + x * 8 + q4 * 2;
-                            qf[ks][nt][x] = held && d < D ? *(const uint32_t*)(qr + d) : 0u;
+                            const int d = E4M3 ? (ks >> 2) * 64 + (ks & 3) * 4 + x * 2 : ks * 16 + x * 8;
+                            qf[ks][nt][x] = held && d + q4 * (E4M3 ? 16 : 2) < D ? *(const uint32_t*)(qr + d) : 0u;
                         }
                     qs[nt][0] = qs[nt][1] = p.scale_log2;
-                    if (E4M3 && !F16) {
-                        float top = 0.f;
-#pragma unroll
-                        for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const float2 v = act2_to_f32<false>(qf[ks][nt][x]);
-                                top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
-                            }
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                        int ex = top > 0.f && top < INFINITY ? 14 - (int)((__float_as_uint(top) >> 23) & 255) + 127 : 0;
-                        ex = min(ex, 100);
-                        const float up = __uint_as_float((uint32_t)(ex + 127) << 23), down = __uint_as_float((uint32_t)(127 - ex) << 23);
-#pragma unroll
-                        for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const float2 v = act2_to_f32<false>(qf[ks][nt][x]);
-                                qf[ks][nt][x] = f32_to_act2<true>(v.x * up, v.y * up);
-                            }
-                        // the accumulator's columns are heads 2 q4 and 2 q4 + 1
-                        qs[nt][0] *= __shfl_sync(0xffffffffu, down, q4 * 8);
-                        qs[nt][1] *= __shfl_sync(0xffffffffu, down, q4 * 8 + 4);
-                    }
                     m[nt][0] = m[nt][1] = -INFINITY;
                     l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
@@ -455,18 +444,44 @@ attend_kernel(const AttnParams p) {
                 }
             }
 
-            cp_async_wait<S::kStages - 2>();
-            __syncwarp();                                       // the stage is whole, and every lane is done with the one before
-            if (next < e) {
-                copy(ahead, stage == 0 ? S::kStages - 1 : stage - 1);
-                if (++next < e) {
-                    ahead = locate(f);
-                    if (next + 1 < e) f.advance(p);
+            __syncwarp();                                       // every lane is done with the stage that is filled next
+            if (i + ST - 1 < e) {
+                copy(fill);
+                if (i + ST < e) f.advance(p);
+            }
+            fill = fill + 1 == ST ? 0 : fill + 1;
+            cp_async_commit();
+            if (i < a) continue;
+
+            cp_async_wait<ST - 1>();
+            __syncwarp();
+            if (E4M3 && !F16 && unscaled) {                     // BF16 to FP16, each row's largest element to 2^14
+                unscaled = false;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    uint32_t top = 0;                       // magnitudes of BF16 are in the order of their bits
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) top = __vmaxu2(top, qf[ks][nt][x] & 0x7fff7fffu);
+                    top = max(top & 0xffffu, top >> 16);
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    const int ex = top == 0 || top >= 0x7f80u ? 0 : min(141 - (int)(top >> 7), 100);
+                    const float up = __uint_as_float((uint32_t)(ex + 127) << 23), down = __uint_as_float((uint32_t)(127 - ex) << 23);
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const float2 v = act2_to_f32<false>(qf[ks][nt][x]);
+                            qf[ks][nt][x] = f32_to_act2<true>(v.x * up, v.y * up);
+                        }
+                    // the accumulator's columns are heads 2 q4 and 2 q4 + 1
+                    qs[nt][0] *= __shfl_sync(0xffffffffu, down, q4 * 8);
+                    qs[nt][1] *= __shfl_sync(0xffffffffu, down, q4 * 8 + 4);
                 }
             }
-            cp_async_commit();
             const uint32_t ks_s = ring_s + stage * S::kStage, vs_s = ks_s + S::kTile;
-            stage = stage + 1 == S::kStages ? 0 : stage + 1;
 
             // ---- scores of 16 tokens (rows g, g + 8) x 8 heads (columns 2 q4, 2 q4 + 1)
             float z[NT][4], z2[NT][4];
@@ -600,8 +615,7 @@ attend_kernel(const AttnParams p) {
             const bool unit_end = c.step + 1 == c.s_hi, last = i + 1 == e;
             if (unit_end || last) {
                 const int unit = c.b * p.units + c.u, unit_hi = unit_start + c.s_hi - c.s_lo;
-                const int kh = p.chunks == 1 ? c.u : c.u / p.chunks;
-                const int h0 = (c.u - kh * p.chunks) * S::kHeads;
+                const bool whole = unit_end && seg_begin == unit_start;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -610,159 +624,197 @@ attend_kernel(const AttnParams p) {
                         l[nt][x] += __shfl_xor_sync(0xffffffffu, l[nt][x], 8);
                         l[nt][x] += __shfl_xor_sync(0xffffffffu, l[nt][x], 16);
                     }
-                if (unit_end && seg_begin == unit_start) {      // all of it: the result
-                    const int64_t row = (int64_t)c.b * p.Hq + kh * p.G;
+                if (!whole) {
+                    const int y = 2 * warp + last;
+                    if (lane == 0) { piece_lo[y] = unit_start; piece_hi[y] = unit_hi; }
+                    if (g == 0) {
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const int hg = h0 + nt * 8 + q4 * 2 + x;
-                            if (hg >= p.G) continue;
-                            const float inv = 1.f / l[nt][x];
-#pragma unroll
-                            for (int mt = 0; mt < KS; ++mt)
-#pragma unroll
-                                for (int half = 0; half < 2; ++half) {
-                                    const int d = out_dim<E4M3, DP>(mt, half, g);
-                                    if (d < D) p.out[(row + hg) * D + d] = f32_to_act_bits<F16>(o[mt][nt][half * 2 + x] * inv);
-                                }
-                            if (p.lse && g == 0) p.lse[row + hg] = (m[nt][x] + log2f(l[nt][x])) * 0.693147180559945309f;
-                        }
-                } else {
-                    // A piece of a unit.  The last one of the range goes to the ring, where
-                    // nothing is in flight any more; one before (the rest of a unit that an
-                    // earlier warp began) to the workspace.
-                    float* part = warp_parts + (size_t)gw * S::kPart;
-                    if (last) {
-                        cp_async_wait<0>();
-                        __syncwarp();
-                        part = (float*)ring;
-                        tail_unit = unit; tail_lo = unit_start; tail_hi = unit_hi;
-                    } else {
-                        head_unit = unit; head_lo = unit_start; head_hi = unit_hi;
+                            for (int x = 0; x < 2; ++x) {
+                                piece_m[y][nt * 8 + q4 * 2 + x] = m[nt][x];
+                                piece_l[y][nt * 8 + q4 * 2 + x] = l[nt][x];
+                            }
                     }
+                }
+                if (!whole && last) {
+                    // The last piece of the range stays in the ring: nothing is in flight any more.
+                    cp_async_wait<0>();
+                    __syncwarp();
+                    tail_unit = unit;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt) store_heads<E4M3, DP, NT>((float*)ring + nt * 8 * S::kPitch, o, nt, g, q4);
+                } else {
+                    // A whole unit goes out, the rest of one that an earlier warp began to the
+                    // workspace: eight heads at a time through the stage just read, which is
+                    // filled again after the next trip's __syncwarp.
+                    if (!whole) head_unit = unit;
+                    float* const buf = (float*)(ring + stage * S::kStage);
+                    const int kh = p.chunks == 1 ? c.u : c.u / p.chunks, h0 = (c.u - kh * p.chunks) * S::kHeads;
+                    const int64_t row = (int64_t)c.b * p.Hq + kh * p.G + h0;
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const int hl = nt * 8 + q4 * 2 + x;
+                    for (int nt = 0; nt < NT; ++nt) {
+                        __syncwarp();
+                        store_heads<E4M3, DP, NT>(buf, o, nt, g, q4);
+                        __syncwarp();
+                        const float inv0 = reciprocal(l[nt][0]), inv1 = reciprocal(l[nt][1]);
+#pragma unroll 1
+                        for (int x = lane; x < 8 * (DP / 4); x += 32) {
+                            const int hl = x / (DP / 4), d = x % (DP / 4) * 4;
+                            const float4 v = *(const float4*)(buf + hl * S::kPitch + d);
+                            const float even = __shfl_sync(0xffffffffu, inv0, hl >> 1), odd = __shfl_sync(0xffffffffu, inv1, hl >> 1);
+                            if (!whole) *(float4*)(warp_parts + (size_t)gw * S::kPart + (nt * 8 + hl) * DP + d) = v;
+                            else if (h0 + nt * 8 + hl < p.G && d < D)
+                                store_out<F16>(p.out + (row + nt * 8 + hl) * D + d, v, hl & 1 ? odd : even);
+                        }
+                        if (whole && p.lse && g == 0) {
 #pragma unroll
-                            for (int mt = 0; mt < KS; ++mt)
-#pragma unroll
-                                for (int half = 0; half < 2; ++half)
-                                    part[hl * DP + out_dim<E4M3, DP>(mt, half, g)] = o[mt][nt][half * 2 + x];
-                            if (g == 0) {
-                                part[S::kHeads * DP + hl] = m[nt][x];
-                                part[S::kHeads * (DP + 1) + hl] = l[nt][x];
+                            for (int x = 0; x < 2; ++x) {
+                                const int hl = nt * 8 + q4 * 2 + x;
+                                if (h0 + hl < p.G) p.lse[row + hl] = log_sum(m[nt][x], l[nt][x]);
                             }
                         }
+                    }
+                    if (D < DP) {                               // the columns that no copy fills
+                        __syncwarp();
+                        for (int x = lane; x < S::kStage / 16; x += 32) ((uint4*)buf)[x] = make_uint4(0, 0, 0, 0);
+                    }
                 }
                 unit_start = unit_hi;
                 seg_begin = i + 1;
                 fresh = true;
             }
+            stage = stage + 1 == ST ? 0 : stage + 1;
             if (!last) c.advance(p);
         }
     }
 
     // ---- join the block's pieces
     if (lane == 0) {
-        piece_unit[2 * warp] = head_unit; piece_lo[2 * warp] = head_lo; piece_hi[2 * warp] = head_hi;
-        piece_unit[2 * warp + 1] = tail_unit; piece_lo[2 * warp + 1] = tail_lo; piece_hi[2 * warp + 1] = tail_hi;
+        piece_unit[2 * warp] = head_unit;
+        piece_unit[2 * warp + 1] = tail_unit;
     }
-    __syncthreads();
-    const Ranges ranges(total, warps);
+    if (!__syncthreads_or(head_unit >= 0 || tail_unit >= 0)) return;
     const int block_lo = ranges.start(blockIdx.x * W), block_hi = ranges.start(blockIdx.x * W + W);
-    int goes_on = -1, goes_to = 0;
-    for (int i = 0; i < 2 * W;) {
-        const int unit = piece_unit[i];
-        if (unit < 0) { ++i; continue; }
-        const int lo = piece_lo[i], hi = piece_hi[i];
-        int j = i + 1;
-        while (j < 2 * W && (piece_unit[j] == unit || piece_unit[j] < 0)) ++j;
-        const bool whole = lo >= block_lo && hi <= block_hi;
-        float* to = p.parts + ((size_t)blockIdx.x * 2 + (lo < block_lo ? 0 : 1)) * S::kPart;
-        if (!whole && lo >= block_lo) {
-            goes_on = unit;
-            goes_to = ranges.holder(hi - 1) / W;
-        }
+    // Every warp makes out the block's runs of pieces of one unit: the last pieces of
+    // neighbouring warps, then the first of the warp after them where the unit ends in
+    // it; a first piece whose unit began in an earlier block is a run of its own.
+    const int tail = lane < W ? piece_unit[2 * lane + 1] : -1, head = lane < W ? piece_unit[2 * lane] : -1;
+    const int left = __shfl_up_sync(0xffffffffu, tail, 1);
+    const bool joined = head >= 0 && lane > 0 && left == head;
+    const uint32_t change = __ballot_sync(0xffffffffu, lane >= W || lane == 0 || tail != left);
+    const uint32_t ends = __ballot_sync(0xffffffffu, joined);
+    static_assert(W <= 16, "two sets of runs in 32 bits");
+    uint32_t runs = __ballot_sync(0xffffffffu, tail >= 0 && (lane == 0 || tail != left)) |
+                    __ballot_sync(0xffffffffu, head >= 0 && !joined) << 16;
+    // A thread takes four dimensions of one head; small units side by side.
+    constexpr int E = S::kHeads * DP / 4, PER = E < W * 32 ? W * 32 / E : 1;
+#pragma unroll 1
+    for (int rank = 0; runs != 0; ++rank, runs &= runs - 1) {
+        if (PER > 1 && rank % PER != tid / E) continue;
+        const int bit = __ffs(runs) - 1, w0 = bit & 15;
+        const int w1 = bit >= 16 ? w0 : w0 + __ffs(change >> (w0 + 1));         // last pieces of warps [w0, w1)
+        const int wh = bit >= 16 ? w0 : w1 < W && (ends >> w1 & 1) ? w1 : -1;   // the first piece of this warp
+        const int y0 = bit >= 16 ? 2 * w0 : 2 * w0 + 1, unit = piece_unit[y0], lo = piece_lo[y0], hi = piece_hi[y0];
         const int b = unit / p.units, u = unit - b * p.units, kh = u / p.chunks, h0 = (u - kh * p.chunks) * S::kHeads;
-        const int64_t row = (int64_t)b * p.Hq + kh * p.G + h0;
-        const int heads = min(S::kHeads, p.G - h0);
-        // a thread four dimensions of one head
-        for (int x = tid * 4; x < heads * DP; x += W * 32 * 4) {
-            const int hl = x / DP, d = x % DP;
-            if (d >= D) continue;
-            float top = -INFINITY, sum = 0.f;
+#pragma unroll 1
+        for (int x = PER > 1 ? tid % E : tid; x < E; x += W * 32) {
+            const int hl = x / (DP / 4), d = x % (DP / 4) * 4;
+            if (h0 + hl >= p.G || d >= D) continue;
+            float top = wh >= 0 ? piece_m[2 * wh][hl] : -INFINITY, sum = 0.f;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int y = i; y < j; ++y) {
-                if (piece_unit[y] < 0) continue;
-                const float* part = y & 1 ? (const float*)(ring_all + (y >> 1) * S::kRing)
-                                          : warp_parts + (size_t)(blockIdx.x * W + (y >> 1)) * S::kPart;
-                const float mine = part[S::kHeads * DP + hl], to_top = fmaxf(top, mine);
-                const float fo = top == to_top ? 1.f : ex2(top - to_top), fn = mine == to_top ? 1.f : ex2(mine - to_top);
-                const float4 o = *(const float4*)(part + x);
-                sum = sum * fo + part[S::kHeads * (DP + 1) + hl] * fn;
-                v.x = v.x * fo + o.x * fn; v.y = v.y * fo + o.y * fn; v.z = v.z * fo + o.z * fn; v.w = v.w * fo + o.w * fn;
-                top = to_top;
+#pragma unroll 4
+            for (int w = w0; w < w1; ++w) top = fmaxf(top, piece_m[2 * w + 1][hl]);
+#pragma unroll 4
+            for (int w = w0; w < w1; ++w) {
+                const float t = factor(piece_m[2 * w + 1][hl], top);
+                const float4 o = *(const float4*)((const float*)(ring_all + w * S::kRing) + hl * S::kPitch + d);
+                sum += t * piece_l[2 * w + 1][hl];
+                v.x += t * o.x; v.y += t * o.y; v.z += t * o.z; v.w += t * o.w;
             }
-            if (whole) {
-                const float inv = 1.f / sum;
-                *(uint2*)(p.out + (row + hl) * D + d) = make_uint2(f32_to_act2<F16>(v.x * inv, v.y * inv), f32_to_act2<F16>(v.z * inv, v.w * inv));
-                if (p.lse && d == 0) p.lse[row + hl] = (top + log2f(sum)) * 0.693147180559945309f;
+            if (wh >= 0) {
+                const float t = factor(piece_m[2 * wh][hl], top);
+                const float4 o = *(const float4*)(warp_parts + (size_t)(blockIdx.x * W + wh) * S::kPart + hl * DP + d);
+                sum += t * piece_l[2 * wh][hl];
+                v.x += t * o.x; v.y += t * o.y; v.z += t * o.z; v.w += t * o.w;
+            }
+            if (lo >= block_lo && hi <= block_hi) {
+                const int64_t row = (int64_t)b * p.Hq + kh * p.G + h0 + hl;
+                store_out<F16>(p.out + row * D + d, v, reciprocal(sum));
+                if (p.lse && d == 0) p.lse[row] = log_sum(top, sum);
             } else {
-                *(float4*)(to + x) = v;
+                float* to = p.parts + ((size_t)blockIdx.x * 2 + (lo >= block_lo)) * S::kPart;
+                *(float4*)(to + hl * DP + d) = v;
                 if (d == 0) {
                     to[S::kHeads * DP + hl] = top;
                     to[S::kHeads * (DP + 1) + hl] = sum;
                 }
             }
         }
-        i = j;
-    }
-    if (tid == 0) {
-        p.joins[2 * blockIdx.x] = goes_on;
-        p.joins[2 * blockIdx.x + 1] = goes_to;
     }
 }
 
-// Joins a unit that starts in block x and goes on, up to block joins[x][1]; a
-// block a head, a thread a dimension.
-template <bool F16, int DP>
-__global__ void __launch_bounds__(DP) join_kernel(const AttnParams p, int group) {
-    pdl_wait_previous();
-    const int x = blockIdx.x, hl = blockIdx.y, d = threadIdx.x, D = p.cache.D;
-    const int unit = p.joins[2 * x], to = p.joins[2 * x + 1];
-    if (unit < 0) return;
-    const int b = unit / p.units, u = unit - b * p.units, kh = u / p.chunks, h0 = (u - kh * p.chunks) * group;
-    if (h0 + hl >= p.G) return;
-    const int size = group * (DP + 2), lane = threadIdx.x & 31;
-    // Lane y holds the maximum and sum of piece y, 32 pieces at a time.
-    const auto part = [&](int y) { return p.parts + ((size_t)y * 2 + (y == x)) * size; };
-    float top = -INFINITY, sum = 0.f, v = 0.f;
-    for (int y0 = x; y0 <= to; y0 += 32) {
-        const int n = min(32, to + 1 - y0);
-        const float mine = lane < n ? part(y0 + lane)[group * DP + hl] : -INFINITY;
-        const float mass = lane < n ? part(y0 + lane)[group * (DP + 1) + hl] : 0.f;
-        float high = mine;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, o));
-        high = fmaxf(high, top);
-        const float fo = top == high ? 1.f : ex2(top - high), fn = mine == high ? 1.f : ex2(mine - high);
-        sum *= fo;
-        v *= fo;
-        top = high;
-#pragma unroll 8
-        for (int y = 0; y < n; ++y) {
-            const float f = __shfl_sync(0xffffffffu, fn, y);
-            sum += f * __shfl_sync(0xffffffffu, mass, y);
-            v += f * part(y0 + y)[hl * DP + d];
-        }
+// Joins the unit that starts in block x of the kernel above and goes on in the
+// next ones, if there is one.  It finds that unit from the lengths while that
+// kernel still runs, so that only the pieces' own loads come after it.
+template <bool F16, bool E4M3, int DP, int NT>
+__global__ void __launch_bounds__(128, 8) join_kernel(const AttnParams p) {
+    using S = Shape<E4M3, DP, NT>;
+    constexpr int W = S::kWarps, N = 4;                         // pieces in flight
+    __shared__ int first_sm[128], sums[4];
+    const int x = blockIdx.x, D = p.cache.D;
+    Numbering<4> steps;
+    steps.count(p, first_sm, sums);
+    const Ranges ranges(steps.total, gridDim.x * W);
+    const int lo = ranges.start(x * W), hi = ranges.start(x * W + W);
+    int b = 0, u = 0, to = -1;
+    if (hi > lo) {
+        int first;
+        b = steps.find(p, first_sm, hi - 1, &first);
+        const int each = steps_of(p, checked_length(p, b));
+        u = (hi - 1 - first) / each;
+        const int unit_lo = first + u * each, unit_hi = unit_lo + each;
+        if (unit_lo >= lo && unit_hi > hi) to = ranges.holder(unit_hi - 1) / W;
     }
-    if (d >= D) return;
-    const int64_t row = (int64_t)b * p.Hq + kh * p.G + h0 + hl;
-    p.out[row * D + d] = f32_to_act_bits<F16>(v / sum);
-    if (p.lse && d == 0) p.lse[row] = (top + log2f(sum)) * 0.693147180559945309f;
+    pdl_wait_previous();
+    pdl_launch_dependents();
+    if (to < 0) return;
+    const int kh = u / p.chunks, h0 = (u - kh * p.chunks) * S::kHeads, heads = min(S::kHeads, p.G - h0);
+    const auto part = [&](int y) { return p.parts + ((size_t)y * 2 + (y == x)) * S::kPart; };
+    for (int i = threadIdx.x; i < heads * (DP / 4); i += 128) {
+        const int hl = i / (DP / 4), d = i % (DP / 4) * 4;
+        if (d >= D) continue;
+        float top = -INFINITY, sum = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int y0 = x; y0 <= to; y0 += N) {
+            float m[N], l[N], high = top;
+            float4 o[N];
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const float* from = part(min(y0 + k, to));
+                m[k] = from[S::kHeads * DP + hl];
+                l[k] = from[S::kHeads * (DP + 1) + hl];
+                o[k] = *(const float4*)(from + hl * DP + d);
+            }
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                if (y0 + k <= to) high = fmaxf(high, m[k]);
+            const float keep = factor(top, high);
+            sum *= keep;
+            v.x *= keep; v.y *= keep; v.z *= keep; v.w *= keep;
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                if (y0 + k > to) continue;
+                const float t = factor(m[k], high);
+                sum += t * l[k];
+                v.x += t * o[k].x; v.y += t * o[k].y; v.z += t * o[k].z; v.w += t * o[k].w;
+            }
+            top = high;
+        }
+        const int64_t row = (int64_t)b * p.Hq + kh * p.G + h0 + hl;
+        store_out<F16>(p.out + row * D + d, v, reciprocal(sum));
+        if (p.lse && d == 0) p.lse[row] = log_sum(top, sum);
+    }
 }
 
 template <bool F16, bool E4M3, int DP, int NT>
@@ -773,9 +825,8 @@ nvfp4_status launch_attention(AttnParams p, void* workspace, cudaStream_t stream
     if (most > INT32_MAX)
         return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s: %lld steps of 16 tokens and heads in one call, above 2^31", fn, (long long)most);
     // as many blocks as the longest lengths could use, at most one wave
-    const int ctas = (int)std::max<int64_t>(1, std::min<int64_t>((int64_t)sm_count() * S::kCtas, ceil_div(most, S::kWarps)));
-    p.joins = (int*)workspace;
-    p.parts = (float*)((uint8_t*)workspace + round_up((int64_t)ctas * 8, 256));
+    const int ctas = (int)std::max<int64_t>(1, std::min<int64_t>(sm_count(), ceil_div(most, S::kWarps)));
+    p.parts = (float*)workspace;
     auto kernel = attend_kernel<F16, E4M3, DP, NT>;
     static std::atomic<uint64_t> opted_in{0};                   // devices whose instance has its shared memory limit raised
     int dev = 0;
@@ -800,10 +851,9 @@ nvfp4_status launch_attention(AttnParams p, void* workspace, cudaStream_t stream
     e = cudaLaunchKernelEx(&cfg, kernel, p);
     if (e != cudaSuccess) return check_cuda(e, fn);
     if (ctas == 1) return NVFP4_OK;                             // nothing goes on
-    cfg.gridDim = dim3((unsigned)ctas, (unsigned)std::min(S::kHeads, p.G));
-    cfg.blockDim = dim3(DP);
+    cfg.blockDim = dim3(128);
     cfg.dynamicSmemBytes = 0;
-    return check_cuda(cudaLaunchKernelEx(&cfg, join_kernel<F16, DP>, p, (int)S::kHeads), fn);
+    return check_cuda(cudaLaunchKernelEx(&cfg, join_kernel<F16, E4M3, DP, NT>, p), fn);
 }
 
 template <bool F16, bool E4M3>
@@ -824,7 +874,7 @@ using namespace nvfp4;
 extern "C" size_t nvfp4_paged_attention_workspace(int64_t B, int64_t Hq, int64_t heads, int64_t head_dim) {
     if (B <= 0 || heads <= 0 || Hq <= 0 || Hq % heads != 0 || head_dim <= 0 || head_dim > kMaxHeadDim) return 0;
     const int DP = padded_dim(head_dim), group = 8 * head_tiles(Hq / heads);
-    return std::max(workspace_for(2 * DP, group, DP, sm_count()), workspace_for(DP, group, DP, sm_count()));
+    return workspace_for(group, DP, sm_count());
 }
 
 extern "C" nvfp4_status nvfp4_paged_attention(const void* q, int64_t q_row_stride, int64_t q_head_stride,
