@@ -86,7 +86,7 @@ def _compile_binding():
 def _link_binding(obj):
     lib = os.path.join(_torch_dir(), "lib")
     _run(["g++", "-shared", "-o", BINDING + ".tmp", obj, "-L" + BUILD, "-L" + lib, "-lnvfp4w4a16", "-ltorch_python",
-          "-ltorch", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib], "linking the binding")
+          "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib], "linking the binding")
     os.replace(BINDING + ".tmp", BINDING)
 
 
