@@ -444,7 +444,11 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
                 }
             }
 
-            __syncwarp();                                       // every lane is done with the stage that is filled next
+            // Step i has come, and every lane is done with the stage that is filled next.
+            // (Waiting after the fill, with a third step in flight, was 2 to 3 % slower on long
+            // sequences: 341 against 332 us for 64 of up to 16384 tokens.)
+            cp_async_wait<ST - 2>();
+            __syncwarp();
             if (i + ST - 1 < e) {
                 copy(fill);
                 if (i + ST < e) f.advance(p);
@@ -453,8 +457,6 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
             cp_async_commit();
             if (i < a) continue;
 
-            cp_async_wait<ST - 1>();
-            __syncwarp();
             if (E4M3 && !F16 && unscaled) {                     // BF16 to FP16, each row's largest element to 2^14
                 unscaled = false;
 #pragma unroll
