@@ -14,7 +14,9 @@
 //    sequences are numbered through (sequence, head, token) on the device, from
 //    the lengths, and cut into equal contiguous ranges, one a warp of a grid
 //    that fills the GPU once.  So a ragged batch, one long sequence and many
-//    short ones all load every SM alike, and the host needs no length.
+//    short ones all load every SM alike, and the host needs no length.  Each
+//    (sequence, head) skips kUnitCost numbers before its first step: its query,
+//    its output and the joins take about that long.
 //  - A warp runs its range alone: it copies its steps' rows into its own ring
 //    in shared memory (cp.async, two steps ahead and more), and no barrier is met until
 //    the range is done.  Page numbers are loaded a step before their rows.
@@ -45,6 +47,7 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kStep = 16;          // tokens a step
+constexpr int kUnitCost = 4;       // steps' worth of time that the start and end of a unit take
 constexpr size_t kMaxSmem = 227 * 1024;
 
 struct AttnParams {
@@ -240,13 +243,13 @@ struct Place {
     }
 };
 
-// The steps' ranges: the first `rest` warps have one step more than the others
-// (fewer steps than warps: one step a warp, packed into the first blocks).
+// The ranges of numbers: the first `rest` warps have one more than the others
+// (fewer numbers than warps: one a warp, packed into the first blocks).
 struct Ranges {
     int each, rest;
     __device__ __forceinline__ Ranges(int total, int warps) : each(total / warps), rest(total % warps) {}
     __device__ __forceinline__ int start(int w) const { return w * each + min(w, rest); }
-    // The warp whose range holds step x.
+    // The warp whose range holds number x.
     __device__ __forceinline__ int holder(int x) const {
         const int big = rest * (each + 1);
         return x < big ? x / (each + 1) : rest + (x - big) / each;
@@ -254,7 +257,12 @@ struct Ranges {
 };
 
 // The numbering of all steps, by a block of WARPS warps: thread t takes `per`
-// sequences from t * per on; sm holds the first step of each thread's.
+// sequences from t * per on; sm holds the first number of each thread's.
+__device__ __forceinline__ int numbers_of(const AttnParams& p, int b) {
+    const int n = steps_of(p, checked_length(p, b));
+    return n > 0 ? (n + kUnitCost) * p.units : 0;
+}
+
 template <int WARPS>
 struct Numbering {
     int per, total;
@@ -264,7 +272,7 @@ struct Numbering {
         per = (p.B + WARPS * 32 - 1) / (WARPS * 32);
         const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
         int mine = 0;
-        for (int b = b0; b < b1; ++b) mine += steps_of(p, checked_length(p, b)) * p.units;
+        for (int b = b0; b < b1; ++b) mine += numbers_of(p, b);
         int incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -283,13 +291,13 @@ struct Numbering {
         sm[threadIdx.x] = before + incl - mine;
         __syncthreads();
     }
-    // The sequence that holds step x < total, and its first step (a whole warp asks).
+    // The sequence that holds number x < total, and its first number (a whole warp asks).
     __device__ __forceinline__ int find(const AttnParams& p, const int* sm, int x, int* first) const {
         int t = -1;
 #pragma unroll 4
         for (int k = 0; k < WARPS * 32; k += 32) t += __popc(__ballot_sync(0xffffffffu, sm[k + (threadIdx.x & 31)] <= x));
         int b = t * per, at = sm[t];
-        for (int n; per > 1 && x >= at + (n = steps_of(p, checked_length(p, b)) * p.units); ++b) at += n;
+        for (int n; per > 1 && x >= at + (n = numbers_of(p, b)); ++b) at += n;
         *first = at;
         return b;
     }
@@ -337,18 +345,21 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
     float* const warp_parts = p.parts + (size_t)gridDim.x * 2 * S::kPart;
     int head_unit = -1, tail_unit = -1;
 
+    Place c;                                                    // the step to compute
+    int at_c = e, unit_first = 0;                               // its number, and that of its unit's first step
     if (a < e) {
-        Place f;                                                // the next step to copy
-        int unit_start;                                         // number of the computed unit's first step
-        f.b = steps.find(p, first_sm, a, &unit_start);
-        f.sequence(p);
-        {
-            const int in = a - unit_start, each = f.s_hi - f.s_lo;
-            f.u = in / each;
-            f.step = f.s_lo + in - f.u * each;
-            unit_start += f.u * each;
-        }
-        Place c = f;                                            // the step to compute
+        c.b = steps.find(p, first_sm, a, &unit_first);
+        c.sequence(p);
+        const int in = a - unit_first, each = c.s_hi - c.s_lo + kUnitCost;
+        c.u = in / each;
+        const int x = max(in - c.u * each - kUnitCost, 0);
+        unit_first += c.u * each + kUnitCost;
+        c.step = c.s_lo + x;
+        at_c = unit_first + x;
+    }
+    if (at_c < e) {
+        Place f = c;                                            // the next step to copy
+        int at_f = at_c;
 
         // Table entries [base, base + 64) of sequence window_b, two a lane.  The second
         // half is loaded when the first is entered, long before it is needed.
@@ -415,8 +426,9 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
         uint32_t qf[KS][NT][2];
         float o[KS][NT][4], m[NT][2], l[NT][2], qs[NT][2];
         bool fresh = true, unscaled = true;                     // a unit begins; its query is not yet scaled
-        int seg_begin = a, fill = 0, stage = 0;
-        for (int i = a - (ST - 1); i < e; ++i) {                // the first trips only fill the ring
+        int seg_begin = at_c, fill = 0, stage = 0;
+        bool last = false;
+        for (int trip = 1 - ST; !last; ++trip) {                // the first trips only fill the ring
             if (fresh) {
                 fresh = false;
                 unscaled = true;
@@ -444,18 +456,19 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
                 }
             }
 
-            // Step i has come, and every lane is done with the stage that is filled next.
+            // This trip's step has come, and every lane is done with the stage that is filled next.
             // (Waiting after the fill, with a third step in flight, was 2 to 3 % slower on long
             // sequences: 341 against 332 us for 64 of up to 16384 tokens.)
             cp_async_wait<ST - 2>();
             __syncwarp();
-            if (i + ST - 1 < e) {
+            if (at_f < e) {
                 copy(fill);
-                if (i + ST < e) f.advance(p);
+                at_f += f.step + 1 == f.s_hi ? 1 + kUnitCost : 1;
+                if (at_f < e) f.advance(p);
             }
             fill = fill + 1 == ST ? 0 : fill + 1;
             cp_async_commit();
-            if (i < a) continue;
+            if (trip < 0) continue;
 
             if (E4M3 && !F16 && unscaled) {                     // BF16 to FP16, each row's largest element to 2^14
                 unscaled = false;
@@ -614,10 +627,12 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
             }
 
             // ---- the end of a unit, or of the range
-            const bool unit_end = c.step + 1 == c.s_hi, last = i + 1 == e;
+            const bool unit_end = c.step + 1 == c.s_hi;
+            at_c += unit_end ? 1 + kUnitCost : 1;
+            last = at_c >= e;
             if (unit_end || last) {
-                const int unit = c.b * p.units + c.u, unit_hi = unit_start + c.s_hi - c.s_lo;
-                const bool whole = unit_end && seg_begin == unit_start;
+                const int unit = c.b * p.units + c.u, unit_hi = unit_first + c.s_hi - c.s_lo;
+                const bool whole = unit_end && seg_begin == unit_first;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -628,7 +643,7 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
                     }
                 if (!whole) {
                     const int y = 2 * warp + last;
-                    if (lane == 0) { piece_lo[y] = unit_start; piece_hi[y] = unit_hi; }
+                    if (lane == 0) { piece_lo[y] = unit_first; piece_hi[y] = unit_hi; }
                     if (g == 0) {
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
@@ -660,8 +675,9 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
                         store_heads<E4M3, DP, NT>(buf, o, nt, g, q4);
                         __syncwarp();
                         const float inv0 = reciprocal(l[nt][0]), inv1 = reciprocal(l[nt][1]);
-#pragma unroll 1
-                        for (int x = lane; x < 8 * (DP / 4); x += 32) {
+#pragma unroll 4
+                        for (int y = 0; y < DP / 16; ++y) {
+                            const int x = y * 32 + lane;
                             const int hl = x / (DP / 4), d = x % (DP / 4) * 4;
                             const float4 v = *(const float4*)(buf + hl * S::kPitch + d);
                             const float even = __shfl_sync(0xffffffffu, inv0, hl >> 1), odd = __shfl_sync(0xffffffffu, inv1, hl >> 1);
@@ -682,8 +698,8 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
                         for (int x = lane; x < S::kStage / 16; x += 32) ((uint4*)buf)[x] = make_uint4(0, 0, 0, 0);
                     }
                 }
-                unit_start = unit_hi;
-                seg_begin = i + 1;
+                unit_first = unit_hi + kUnitCost;
+                seg_begin = at_c;
                 fresh = true;
             }
             stage = stage + 1 == ST ? 0 : stage + 1;
@@ -756,66 +772,93 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
     }
 }
 
-// Joins the unit that starts in block x of the kernel above and goes on in the
-// next ones, if there is one.  It finds that unit from the lengths while that
-// kernel still runs, so that only the pieces' own loads come after it.
+// Joins the units that lie in several blocks of the kernel above, each by those
+// same blocks' numbers here: block x of a unit's P takes a P-th of its output, its
+// threads that many elements and the pieces in turn.  The units are found from
+// the lengths while that kernel still runs, so only the pieces' own loads, all at
+// once, come after it.
 template <bool F16, bool E4M3, int DP, int NT>
 __global__ void __launch_bounds__(128, 8) join_kernel(const AttnParams p) {
     using S = Shape<E4M3, DP, NT>;
-    constexpr int W = S::kWarps, N = 4;                         // pieces in flight
+    constexpr int W = S::kWarps, N = 4;                         // pieces in flight a thread
     __shared__ int first_sm[128], sums[4];
-    const int x = blockIdx.x, D = p.cache.D;
+    __shared__ float part_m[128], part_l[128];
+    __shared__ float4 part_o[128];
+    const int x = blockIdx.x, tid = threadIdx.x, D = p.cache.D;
     Numbering<4> steps;
     steps.count(p, first_sm, sums);
     const Ranges ranges(steps.total, gridDim.x * W);
     const int lo = ranges.start(x * W), hi = ranges.start(x * W + W);
-    int b = 0, u = 0, to = -1;
+    // Half the threads take the unit at the start of the block's range, if an earlier
+    // block began it, the others the one at its end, if it begins here and goes on.
+    const int k = tid / 64, at = k == 0 ? lo : hi - 1;
+    int b = 0, u = 0, from = 0, to = -1;
     if (hi > lo) {
         int first;
-        b = steps.find(p, first_sm, hi - 1, &first);
-        const int each = steps_of(p, checked_length(p, b));
-        u = (hi - 1 - first) / each;
-        const int unit_lo = first + u * each, unit_hi = unit_lo + each;
-        if (unit_lo >= lo && unit_hi > hi) to = ranges.holder(unit_hi - 1) / W;
+        b = steps.find(p, first_sm, at, &first);
+        const int each = steps_of(p, checked_length(p, b)) + kUnitCost;
+        u = (at - first) / each;
+        const int unit_lo = first + u * each + kUnitCost, unit_hi = first + (u + 1) * each;
+        if (k == 0 ? unit_lo < lo : unit_lo >= lo && unit_lo < hi && unit_hi > hi) {
+            from = ranges.holder(unit_lo) / W;
+            to = ranges.holder(unit_hi - 1) / W;
+        }
     }
+    const int kh = u / p.chunks, h0 = (u - kh * p.chunks) * S::kHeads, E = min(S::kHeads, p.G - h0) * (DP / 4);
+    const int P = to - from + 1, share = to < 0 ? 0 : (E + P - 1) / P, e1 = min(E, (x - from + 1) * share);
     pdl_wait_previous();
     pdl_launch_dependents();
-    if (to < 0) return;
-    const int kh = u / p.chunks, h0 = (u - kh * p.chunks) * S::kHeads, heads = min(S::kHeads, p.G - h0);
-    const auto part = [&](int y) { return p.parts + ((size_t)y * 2 + (y == x)) * S::kPart; };
-    for (int i = threadIdx.x; i < heads * (DP / 4); i += 128) {
-        const int hl = i / (DP / 4), d = i % (DP / 4) * 4;
-        if (d >= D) continue;
+    if (to < 0) return;                                         // the barriers below are this half's own
+    for (int base = (x - from) * share; base < e1; base += 64) {
+        const int n = min(64, e1 - base), groups = min(64 / n, (P + N - 1) / N), group = tid % 64 / n, el = tid % 64 - group * n;
+        const int e = base + el, hl = e / (DP / 4), d = e % (DP / 4) * 4;
         float top = -INFINITY, sum = 0.f;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int y0 = x; y0 <= to; y0 += N) {
-            float m[N], l[N], high = top;
-            float4 o[N];
+        if (group < groups && d < D) {
+            for (int y0 = from + group; y0 <= to; y0 += groups * N) {
+                float m[N], l[N], high = top;
+                float4 o[N];
 #pragma unroll
-            for (int k = 0; k < N; ++k) {
-                const float* from = part(min(y0 + k, to));
-                m[k] = from[S::kHeads * DP + hl];
-                l[k] = from[S::kHeads * (DP + 1) + hl];
-                o[k] = *(const float4*)(from + hl * DP + d);
+                for (int i = 0; i < N; ++i) {
+                    const int y = min(y0 + i * groups, to);
+                    const float* part = p.parts + ((size_t)y * 2 + (y == from)) * S::kPart;
+                    m[i] = part[S::kHeads * DP + hl];
+                    l[i] = part[S::kHeads * (DP + 1) + hl];
+                    o[i] = *(const float4*)(part + hl * DP + d);
+                }
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    if (y0 + i * groups <= to) high = fmaxf(high, m[i]);
+                const float keep = factor(top, high);
+                sum *= keep;
+                v.x *= keep; v.y *= keep; v.z *= keep; v.w *= keep;
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    if (y0 + i * groups > to) continue;
+                    const float t = factor(m[i], high);
+                    sum += t * l[i];
+                    v.x += t * o[i].x; v.y += t * o[i].y; v.z += t * o[i].z; v.w += t * o[i].w;
+                }
+                top = high;
             }
-#pragma unroll
-            for (int k = 0; k < N; ++k)
-                if (y0 + k <= to) high = fmaxf(high, m[k]);
-            const float keep = factor(top, high);
-            sum *= keep;
-            v.x *= keep; v.y *= keep; v.z *= keep; v.w *= keep;
-#pragma unroll
-            for (int k = 0; k < N; ++k) {
-                if (y0 + k > to) continue;
-                const float t = factor(m[k], high);
-                sum += t * l[k];
-                v.x += t * o[k].x; v.y += t * o[k].y; v.z += t * o[k].z; v.w += t * o[k].w;
-            }
-            top = high;
         }
-        const int64_t row = (int64_t)b * p.Hq + kh * p.G + h0 + hl;
-        store_out<F16>(p.out + row * D + d, v, reciprocal(sum));
-        if (p.lse && d == 0) p.lse[row] = log_sum(top, sum);
+        part_m[tid] = top;
+        part_l[tid] = sum;
+        part_o[tid] = v;
+        named_bar_sync(1 + k, 64);
+        if (group == 0 && d < D) {
+            for (int i = tid + n; i < k * 64 + groups * n; i += n) {
+                const float high = fmaxf(top, part_m[i]), keep = factor(top, high), t = factor(part_m[i], high);
+                const float4 o = part_o[i];
+                sum = sum * keep + t * part_l[i];
+                v.x = v.x * keep + t * o.x; v.y = v.y * keep + t * o.y; v.z = v.z * keep + t * o.z; v.w = v.w * keep + t * o.w;
+                top = high;
+            }
+            const int64_t row = (int64_t)b * p.Hq + kh * p.G + h0 + hl;
+            store_out<F16>(p.out + row * D + d, v, reciprocal(sum));
+            if (p.lse && d == 0) p.lse[row] = log_sum(top, sum);
+        }
+        named_bar_sync(1 + k, 64);
     }
 }
 
@@ -823,7 +866,7 @@ template <bool F16, bool E4M3, int DP, int NT>
 nvfp4_status launch_attention(AttnParams p, void* workspace, cudaStream_t stream) {
     using S = Shape<E4M3, DP, NT>;
     const char* fn = "nvfp4_paged_attention";
-    const int64_t most = (int64_t)p.B * p.units * (ceil_div((int64_t)p.width * p.cache.page_size, kStep) + 1);
+    const int64_t most = (int64_t)p.B * p.units * (ceil_div((int64_t)p.width * p.cache.page_size, kStep) + 1 + kUnitCost);
     if (most > INT32_MAX)
         return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s: %lld steps of 16 tokens and heads in one call, above 2^31", fn, (long long)most);
     // as many blocks as the longest lengths could use, at most one wave
