@@ -54,6 +54,7 @@ nvfp4_status check_cache(const char* fn, const nvfp4_kv_cache* c, CacheView* vie
 namespace {
 
 constexpr int kMaxAxes = 4;
+constexpr int kRopeThreads = 128;
 
 struct RopeParams {
     const uint16_t *q, *k, *v;
@@ -139,47 +140,19 @@ __global__ void __launch_bounds__(256) rope_write_any_kernel(const RopeParams p)
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const float s = e4m3_scale(amax), inv = __frcp_rn(s);
+        const float s = e4m3_scale(amax), inv = e4m3_inverse(s);
         if (lane == 0) (kind == 1 ? p.cache.k_scale : p.cache.v_scale)[p.cache.scale_at(page, h, at)] = s;
 #pragma unroll
         for (int i = 0; i < kMaxHeadDim / 32; ++i)
-            if (lane + 32 * i < p.D) row[lane + 32 * i] = (uint8_t)f32_to_e4m3x2(e4m3_quotient(y[i], s, inv), 0.f);
+            if (lane + 32 * i < p.D) row[lane + 32 * i] = e4m3_code(y[i], s, inv);
     }
-}
-
-// Two 32-bit values an instruction.
-struct F2 { uint64_t v; };
-__device__ __forceinline__ F2 make_f2(float lo, float hi) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ float2 both(F2 a) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-    return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-// Sums of products one value at a time: a packed addition after a packed product
-// came out as one fused operation, with one rounding instead of two.
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-    const float2 u = both(a), v = both(b);
-    return make_f2(__fadd_rn(u.x, v.x), __fadd_rn(u.y, v.y));
-}
-__device__ __forceinline__ F2 sub2(F2 a, F2 b) {
-    const float2 u = both(a), v = both(b);
-    return make_f2(__fsub_rn(u.x, v.x), __fsub_rn(u.y, v.y));
 }
 
 // rot a multiple of 16: a thread takes 16 elements of several heads of one token,
 // both sides of eight pairs, so that nothing is exchanged: pieces j and j + rot/16
 // of 8 elements (INTER: 2j and 2j + 1), past rot two neighbouring pieces as they
 // are.  L threads a head (a power of two), `per` head groups a token (a power of
-// two), 256 threads a block.
+// two), kRopeThreads a block.
 // Bound by memory (q, k, v in, q and the cache rows out) and not far from it by
 // instructions: 24.6 us (4.86 TB/s) for 4096 tokens of 40 + 2 * 8 heads of 128
 // with three axes, where a piece of 8 a thread with its mate's by shuffle (176
@@ -188,11 +161,11 @@ __device__ __forceinline__ F2 sub2(F2 a, F2 b) {
 // frequency, whose addresses wait for the positions (each thread fetching its
 // own through L1: 40 us).
 template <bool F16, bool INTER, bool E4M3, int U>
-__global__ void __launch_bounds__(256, 3) rope_write_kernel(const RopeParams p, int L, int per) {
+__global__ void __launch_bounds__(kRopeThreads, (E4M3 && U > 1 ? 640 : 768) / kRopeThreads) rope_write_kernel(const RopeParams p, int L, int per) {
     pdl_wait_previous();
     pdl_launch_dependents();
     const int j = threadIdx.x & (L - 1), group = threadIdx.x / L;
-    const int tokens = 256 / (L * per);                // a block's
+    const int tokens = kRopeThreads / (L * per);               // a block's
     const int64_t t = (int64_t)blockIdx.x * tokens + group / per;
     const bool live = t < p.T && j * 16 < p.D;
     const int heads = p.Hq + 2 * p.Hkv, stride = per * gridDim.y;
@@ -205,7 +178,7 @@ __global__ void __launch_bounds__(256, 3) rope_write_kernel(const RopeParams p, 
     F2 cs[4], sn[4];
     int64_t row = -1, scale_row = 0;                   // byte offset of the token's cache row of head 0
 
-    __shared__ __align__(16) float turn[256 * 16];     // [token][cosines, sines]: at most 256 / L tokens of 16 L
+    __shared__ __align__(16) float turn[kRopeThreads * 16];    // [token][cosines, sines]: at most kRopeThreads / L tokens of 16 L
     for (int h0 = 0; h0 < heads; h0 += stride * U) {
         uint4 x[U][2];
 #pragma unroll
@@ -221,7 +194,7 @@ __global__ void __launch_bounds__(256, 3) rope_write_kernel(const RopeParams p, 
         }
         if (h0 == 0) {
             const int64_t slot = live ? p.slots[t] : -1;
-            for (int i = threadIdx.x; i < tokens * half; i += 256) {
+            for (int i = threadIdx.x; i < tokens * half; i += kRopeThreads) {
                 const int n = tokens == 1 ? 0 : i / half, f = i - n * half;
                 const int64_t u = (int64_t)blockIdx.x * tokens + n;
                 if (u >= p.T) break;
@@ -296,22 +269,24 @@ __global__ void __launch_bounds__(256, 3) rope_write_kernel(const RopeParams p, 
             for (int o = 8; o > 0; o >>= 1)
                 if (o < L) amax = fmaxf(amax, __shfl_xor_sync(same, amax, o));
             if (!live || row < 0) continue;
-            const float s = e4m3_scale(amax), inv = __frcp_rn(s);
+            const float s = e4m3_scale(amax), inv = e4m3_inverse(s);
             const int kh = h - p.Hq - (value ? p.Hkv : 0);
+            const F2 minus_s = make_f2(-s, -s), inv2 = make_f2(inv, inv);
             uint32_t o[4];                             // codes of the pieces at e0 and e1
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-                const float2 u = both(a[n]), v = both(b[n]);
-                const float ua = e4m3_quotient(u.x, s, inv), ub = e4m3_quotient(u.y, s, inv);
-                const float va = e4m3_quotient(v.x, s, inv), vb = e4m3_quotient(v.y, s, inv);
-                // half words in the order of the elements
-                const uint32_t one = INTER ? f32_to_e4m3x2(ua, va) : f32_to_e4m3x2(ua, ub);
-                const uint32_t two = INTER ? f32_to_e4m3x2(ub, vb) : f32_to_e4m3x2(va, vb);
+                F2 one = a[n], two = b[n];             // in the order of the elements
                 if (INTER) {
-                    o[n] = one | two << 16;
+                    const float2 u = both(a[n]), v = both(b[n]);
+                    one = make_f2(u.x, v.x);
+                    two = make_f2(u.y, v.y);
+                }
+                const uint32_t x = e4m3_codes(one, minus_s, inv2), y = e4m3_codes(two, minus_s, inv2);
+                if (INTER) {
+                    o[n] = x | y << 16;
                 } else {
-                    o[n >> 1] = n & 1 ? o[n >> 1] | one << 16 : one;
-                    o[2 + (n >> 1)] = n & 1 ? o[2 + (n >> 1)] | two << 16 : two;
+                    o[n >> 1] = n & 1 ? o[n >> 1] | x << 16 : x;
+                    o[2 + (n >> 1)] = n & 1 ? o[2 + (n >> 1)] | y << 16 : y;
                 }
             }
             uint8_t* to = (value ? p.cache.v : p.cache.k) + kh * p.cache.head_bytes + row;
@@ -357,13 +332,13 @@ nvfp4_status launch_rope(RopeParams p, bool f16, bool inter, cudaStream_t stream
     // three 31.0, two 28.5).  Few tokens: one head a thread over as many blocks
     // as that takes, for the shortest way through.
     const bool one = p.T * heads * L <= (int64_t)sm_count() * 1024;
-    while (per * 2 * L <= 256 && (one ? per < heads : per * kManyHeads < heads)) per *= 2;
-    const int tokens = 256 / (L * per);                // a block's
+    while (per * 2 * L <= kRopeThreads && (one ? per < heads : per * kManyHeads < heads)) per *= 2;
+    const int tokens = kRopeThreads / (L * per);                // a block's
     dim3 grid((unsigned)ceil_div(p.T, tokens), (unsigned)ceil_div(heads, per * (one ? 1 : kManyHeads)));
     const void* kernel = f16 ? (inter ? rope_kernel<true, true>(p.cache.e4m3, one) : rope_kernel<true, false>(p.cache.e4m3, one))
                              : (inter ? rope_kernel<false, true>(p.cache.e4m3, one) : rope_kernel<false, false>(p.cache.e4m3, one));
     void* args[] = {&p, &L, &per};
-    return launch_after(kernel, grid, dim3(256), args, stream, fn);
+    return launch_after(kernel, grid, dim3(kRopeThreads), args, stream, fn);
 }
 
 struct ReadParams {

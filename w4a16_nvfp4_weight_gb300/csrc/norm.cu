@@ -51,25 +51,28 @@ __device__ __forceinline__ float row_reduce(float v, float* sm) {
     return lane_reduce<MAX>(v);
 }
 
+// Threads of a row at most: V pieces a thread have to fit in the registers.
+constexpr int norm_threads(int V) { return V == 1 ? 1024 : 512; }
+
 // Rows of 16-byte pieces: a row's threads keep it in registers, V pieces of 8
 // elements each, so that it is read once.
 // Bound by memory: 2 or 3 passes' worth of bytes a row (x, residual in; r, y
 // out), all loads issued before the first use, and the weights' (from L2) before
-// the one barrier of the sum.
+// the one barrier of the sum.  The E4M3 output is not far from its instructions'
+// time: values are kept for both of its passes, and computed in pairs.
 template <bool F16, bool E4M3, int V>
-__global__ void __launch_bounds__(1024) norm_rows_kernel(const NormParams p) {
+__global__ void __launch_bounds__(norm_threads(V)) norm_rows_kernel(const NormParams p) {
     __shared__ float sm[2][32];
     pdl_wait_previous();
     pdl_launch_dependents();
     const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     if (t >= p.T) return;                              // whole warps: several rows a block have a warp each
     const int pieces = (int)(p.H / 8);
-    uint4 r[V], w[V];
-    float sum = 0.f;
+    uint4 x[V], w[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = i * blockDim.x + threadIdx.x;
-        r[i] = c < pieces ? ldg_once(p.x + t * p.x_stride + c * 8) : make_uint4(0, 0, 0, 0);
+        x[i] = c < pieces ? ldg_once(p.x + t * p.x_stride + c * 8) : make_uint4(0, 0, 0, 0);
     }
     if (p.residual) {
 #pragma unroll
@@ -80,14 +83,14 @@ __global__ void __launch_bounds__(1024) norm_rows_kernel(const NormParams p) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int c = i * blockDim.x + threadIdx.x;
-            uint32_t* a = &r[i].x;
+            uint32_t* a = &x[i].x;
             const uint32_t* b = &w[i].x;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float2 u = act2_to_f32<F16>(a[j]), v = act2_to_f32<F16>(b[j]);
                 a[j] = f32_to_act2<F16>(u.x + v.x, u.y + v.y);
             }
-            if (c < pieces) *(uint4*)(p.residual_out + t * p.H + c * 8) = r[i];
+            if (c < pieces) *(uint4*)(p.residual_out + t * p.H + c * 8) = x[i];
         }
     }
 #pragma unroll
@@ -95,28 +98,36 @@ __global__ void __launch_bounds__(1024) norm_rows_kernel(const NormParams p) {
         const int c = i * blockDim.x + threadIdx.x;
         w[i] = c < pieces ? *(const uint4*)(p.weight + c * 8) : make_uint4(0, 0, 0, 0);
     }
+    F2 sums = make_f2(0.f, 0.f), y[V][4];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const uint32_t* a = &r[i].x;
+        const uint32_t* a = &x[i].x;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float2 u = act2_to_f32<F16>(a[j]);
-            sum += u.x * u.x + u.y * u.y;
+            y[i][j] = widen2<F16>(a[j]);
+            sums = fma2(y[i][j], y[i][j], sums);
         }
     }
-    const float rstd = rsqrtf(row_reduce<false>(sum, sm[0]) / (float)p.H + p.eps);
+    const float2 sum = both(sums);
+    const float rstd = rsqrtf(row_reduce<false>(sum.x + sum.y, sm[0]) / (float)p.H + p.eps);
+    const F2 rstd2 = make_f2(rstd, rstd);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const uint32_t* b = &w[i].x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[i][j] = mul2(mul2(y[i][j], rstd2), widen2<F16>(b[j]));
+    }
     if constexpr (!E4M3) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int c = i * blockDim.x + threadIdx.x;
-            uint32_t* a = &r[i].x;
-            const uint32_t* b = &w[i].x;
+            uint32_t o[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float2 u = act2_to_f32<F16>(a[j]), v = act2_to_f32<F16>(b[j]);
-                a[j] = f32_to_act2<F16>(u.x * rstd * v.x, u.y * rstd * v.y);
+                const float2 u = both(y[i][j]);
+                o[j] = f32_to_act2<F16>(u.x, u.y);
             }
-            if (c < pieces) *(uint4*)((uint16_t*)p.y + t * p.H + c * 8) = r[i];
+            if (c < pieces) *(uint4*)((uint16_t*)p.y + t * p.H + c * 8) = make_uint4(o[0], o[1], o[2], o[3]);
         }
     } else {
         const bool by_row = p.group == p.H;
@@ -124,12 +135,11 @@ __global__ void __launch_bounds__(1024) norm_rows_kernel(const NormParams p) {
         float amax[V], top = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const uint32_t *a = &r[i].x, *b = &w[i].x;
             amax[i] = 0.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float2 u = act2_to_f32<F16>(a[j]), v = act2_to_f32<F16>(b[j]);
-                amax[i] = fmaxf(amax[i], fmaxf(fabsf(u.x * rstd * v.x), fabsf(u.y * rstd * v.y)));
+                const float2 u = both(y[i][j]);
+                amax[i] = fmaxf(fmaxf(amax[i], fabsf(u.x)), fabsf(u.y));
             }
             top = fmaxf(top, amax[i]);
         }
@@ -138,18 +148,13 @@ __global__ void __launch_bounds__(1024) norm_rows_kernel(const NormParams p) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int c = i * blockDim.x + threadIdx.x;
-            const float s = e4m3_scale(by_row ? top : lane_reduce<true>(amax[i], lanes)), inv = __frcp_rn(s);
+            const float s = e4m3_scale(by_row ? top : lane_reduce<true>(amax[i], lanes)), inv = e4m3_inverse(s);
             if (c >= pieces) continue;
             if (by_row ? c == 0 : threadIdx.x % lanes == 0) p.scales[t * groups + (by_row ? 0 : c / lanes)] = s;
-            const uint32_t *a = &r[i].x, *b = &w[i].x;
-            uint32_t o[2];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 u = act2_to_f32<F16>(a[j]), v = act2_to_f32<F16>(b[j]);
-                const uint32_t two = f32_to_e4m3x2(e4m3_quotient(u.x * rstd * v.x, s, inv), e4m3_quotient(u.y * rstd * v.y, s, inv));
-                o[j >> 1] = j & 1 ? o[j >> 1] | two << 16 : two;
-            }
-            *(uint2*)((uint8_t*)p.y + t * p.H + c * 8) = make_uint2(o[0], o[1]);
+            const F2 minus_s = make_f2(-s, -s), inv2 = make_f2(inv, inv);
+            const uint32_t o0 = e4m3_codes(y[i][0], minus_s, inv2), o1 = e4m3_codes(y[i][1], minus_s, inv2);
+            const uint32_t o2 = e4m3_codes(y[i][2], minus_s, inv2), o3 = e4m3_codes(y[i][3], minus_s, inv2);
+            *(uint2*)((uint8_t*)p.y + t * p.H + c * 8) = make_uint2(o0 | o1 << 16, o2 | o3 << 16);
         }
     }
 }
@@ -187,9 +192,9 @@ __global__ void __launch_bounds__(256) norm_any_kernel(const NormParams p) {
     if (p.group == p.H) {
         float amax = 0.f;
         for (int64_t i = threadIdx.x; i < p.H; i += blockDim.x) amax = fmaxf(amax, fabsf(value(i)));
-        const float s = e4m3_scale(row_reduce<true>(amax, sm[1])), inv = __frcp_rn(s);
+        const float s = e4m3_scale(row_reduce<true>(amax, sm[1])), inv = e4m3_inverse(s);
         if (threadIdx.x == 0) p.scales[t] = s;
-        for (int64_t i = threadIdx.x; i < p.H; i += blockDim.x) y[i] = (uint8_t)f32_to_e4m3x2(e4m3_quotient(value(i), s, inv), 0.f);
+        for (int64_t i = threadIdx.x; i < p.H; i += blockDim.x) y[i] = e4m3_code(value(i), s, inv);
         return;
     }
     const int64_t groups = p.H / p.group;              // a warp takes a group at a time
@@ -197,10 +202,10 @@ __global__ void __launch_bounds__(256) norm_any_kernel(const NormParams p) {
     for (int64_t g = threadIdx.x >> 5; g < groups; g += blockDim.x >> 5) {
         float amax = 0.f;
         for (int64_t i = g * p.group + lane; i < (g + 1) * p.group; i += 32) amax = fmaxf(amax, fabsf(value(i)));
-        const float s = e4m3_scale(lane_reduce<true>(amax)), inv = __frcp_rn(s);
+        const float s = e4m3_scale(lane_reduce<true>(amax)), inv = e4m3_inverse(s);
         if (lane == 0) p.scales[t * groups + g] = s;
         for (int64_t i = g * p.group + lane; i < (g + 1) * p.group; i += 32)
-            y[i] = (uint8_t)f32_to_e4m3x2(e4m3_quotient(value(i), s, inv), 0.f);
+            y[i] = e4m3_code(value(i), s, inv);
     }
 }
 
@@ -209,7 +214,8 @@ const void* rows_kernel(bool e4m3, int V) {
     switch (V) {
         case 1: return e4m3 ? (const void*)norm_rows_kernel<F16, true, 1> : (const void*)norm_rows_kernel<F16, false, 1>;
         case 2: return e4m3 ? (const void*)norm_rows_kernel<F16, true, 2> : (const void*)norm_rows_kernel<F16, false, 2>;
-        default: return e4m3 ? (const void*)norm_rows_kernel<F16, true, 4> : (const void*)norm_rows_kernel<F16, false, 4>;
+        case 4: return e4m3 ? (const void*)norm_rows_kernel<F16, true, 4> : (const void*)norm_rows_kernel<F16, false, 4>;
+        default: return e4m3 ? (const void*)norm_rows_kernel<F16, true, 8> : (const void*)norm_rows_kernel<F16, false, 8>;
     }
 }
 
@@ -226,7 +232,7 @@ nvfp4_status launch_norm(const NormParams& p, bool f16, cudaStream_t stream) {
         // with few threads to join); few rows take as many threads as they have
         // pieces, for the shortest way through one row.
         int V = p.T > sm_count() * 2 ? 4 : 1;
-        while (pieces > 1024 * V) V *= 2;
+        while (pieces > norm_threads(V) * V) V *= 2;
         block = dim3((unsigned)round_up(ceil_div(pieces, V), 32));
         if (block.x == 32) block.y = p.T > sm_count() * 2 ? 8 : 1;    // a warp a row
         kernel = f16 ? rows_kernel<true>(e4m3, V) : rows_kernel<false>(e4m3, V);
