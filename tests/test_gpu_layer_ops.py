@@ -378,6 +378,38 @@ def test_paged_attention(lengths, Hq, Hkv, D, page, act, kind, layout, window):
     assert torch.equal(lse.view(torch.int32), lse2.view(torch.int32))
 
 
+SPLIT_CASES = [
+    # lengths, Hq, Hkv, D, page, act, kind, layout, window
+    ([70001], 8, 1, 128, 16, "bf16", "16", "hnd", 0),            # one unit over every block
+    ([70001], 12, 1, 128, 16, "bf16", "e4m3", "hnd", 0),
+    ([30000, 1, 0, 257], 2, 2, 80, 24, "f16", "e4m3", "pool", 0),
+    ([30000, 1, 0, 257], 20, 1, 64, 24, "bf16", "16", "nhd", 5000),
+    ([20000, 300], 8, 2, 256, 64, "bf16", "16", "hnd", 0),
+    ([20000, 300], 32, 2, 256, 64, "f16", "e4m3", "hnd", 0),
+    ([6000, 5999], 4, 4, 48, 1, "bf16", "e4m3", "hnd", 4097),
+    ([1] * 40 + [12000] + [17] * 40, 8, 4, 128, 16, "bf16", "16", "hnd", 0),
+    ([(i * 37) % 90 for i in range(1500)], 2, 1, 64, 16, "bf16", "16", "hnd", 0),
+    ([255, 256, 1, 0, 16, 200], 16, 4, 128, 16, "bf16", "e4m3", "hnd", 0),        # units kept whole
+    ([(i * 53) % 257 for i in range(700)], 8, 2, 64, 128, "f16", "16", "hnd", 0),
+    ([9000, 100, 3], 8, 2, 128, 16, "bf16", "16", "hnd", 200),   # short windows of a long cache
+]
+
+
+@pytest.mark.parametrize("lengths,Hq,Hkv,D,page,act,kind,layout,window", SPLIT_CASES)
+def test_paged_attention_splits_and_joins(lengths, Hq, Hkv, D, page, act, kind, layout, window):
+    """Units cut into many pieces, many units a block, and both in one call; the same
+    bits on a second call, and with a table wider than any length needs."""
+    case = _attention_case(lengths, Hq, Hkv, D, page, act, kind, len(lengths) + D + Hq, layout)
+    out, lse = _check_attention(*case, page, act, kind, window)
+    again = nv.paged_attention(case[1], block_table=case[2], lengths=case[3], window=window, **case[0])
+    assert torch.equal(out.view(torch.int16), again.view(torch.int16))
+    wide = torch.full((len(lengths), case[2].shape[1] + 4000 // page), -1, dtype=torch.int32, device="cuda")
+    wide[:, :case[2].shape[1]] = case[2]
+    out, _ = nv.paged_attention(case[1], block_table=wide, lengths=case[3], window=window, return_lse=True, **case[0])
+    gu.check_device_status()
+    _check_attention(case[0], case[1], wide, *case[3:], page, act, kind, window)
+
+
 @pytest.mark.parametrize("kind", ["16", "e4m3"])
 @pytest.mark.parametrize("scale", [0.0, -0.1, 2.0])
 def test_paged_attention_scales_and_peaked_rows(kind, scale):
