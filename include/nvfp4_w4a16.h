@@ -446,7 +446,8 @@ typedef enum { NVFP4_OUT_16 = 0, NVFP4_OUT_E4M3 = 1 } nvfp4_out_type;
  *                residual or X where that is dense (element for element in place).
  *  group         0, 16, 32, 64, 128 or 256, dividing H (0 for 16-bit output).
  * H in [1, 2^24], any width, stride and alignment; rows whose width, strides and
- * pointers are multiples of 16 bytes run on vector loads.  T == 0 launches nothing.
+ * pointers are multiples of 16 bytes run on vector loads, others on 4- or 2-byte
+ * ones.  T == 0 launches nothing.
  */
 nvfp4_status nvfp4_rms_norm(const void* X, int64_t x_stride, const void* residual, int64_t residual_stride,
                             const void* weight, int64_t T, int64_t H, float eps, int out_type, int64_t group,

@@ -143,6 +143,31 @@ def test_norm_special_values():
     assert torch.all(c[4].float() == 448) and nv.rms_norm(x[:0], w).shape == (0, 256)
 
 
+@pytest.mark.parametrize("T,H", [(1, 3), (2, 65), (700, 33), (17, 268), (900, 268), (350, 1001), (2, 8190), (400, 4098),
+                                 (3, 16383), (320, 16384), (2, 16386), (330, 12345)])
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+def test_norm_widths_that_are_no_multiple_of_eight(T, H, act):
+    g = _gen(T * 3 + H)
+    x, w, r = _randn(g, (T, H), act), _randn(g, (H,), act), _randn(g, (T, H), act)
+    y, added = nv.rms_norm(x, w, residual=r)
+    assert torch.equal(added, (x.float() + r.float()).to(DT[act]))
+    ref = layer.rms_norm(_np(added), _np(w), 1e-6)
+    _close16(y, ref, act)
+    _close16(nv.rms_norm(added, w), ref, act)
+    codes, scales = nv.rms_norm_e4m3(added, w)
+    s = np.maximum(np.abs(ref).max(-1, keepdims=True) / 448, 2.0 ** -100)
+    assert np.all(np.abs(_np(scales) - s) <= 2.0 ** -13 * s)
+    q = ref / _np(scales)
+    _, e = np.frexp(q)
+    step = np.exp2(np.maximum(e.astype(float) - 4, -9.0))
+    assert np.all(np.abs(_np(codes.float()) - q) <= step / 2 * (1 + 2.0 ** -8) + 2.0 ** -13 * np.abs(q))
+    # views whose rows start anywhere
+    if H > 40:
+        for cut in (1, 2):
+            v = added[:, cut:H - 7]
+            _close16(nv.rms_norm(v, w[:H - 7 - cut].contiguous()), layer.rms_norm(_np(v), _np(w)[:H - 7 - cut], 1e-6), act)
+
+
 # ----------------------------------------------------- cache write and read ---
 
 def _make_cache(pages, heads, page, D, act, kind, fill=float("nan"), layout="hnd"):
@@ -235,6 +260,14 @@ def test_rope_cache_write_and_read(T, Hq, Hkv, D, rot, page, sections, inter, ac
     for n, t in c.items():
         a, b = ((u.view(torch.uint8) if u.dtype == E4M3 else u)[other // page, :, other % page] for u in (t, before[n]))
         assert torch.equal(torch.nan_to_num(a.float(), nan=-5.0), torch.nan_to_num(b.float(), nan=-5.0))
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D,rot,sections,inter,kind", [
+    (3, 4, 2, 80, 40, None, False, "e4m3"), (900, 6, 2, 80, 40, [8, 7, 5], False, "16"), (40, 3, 1, 256, 136, [1, 0, 67], False, "e4m3"),
+    (1300, 2, 2, 112, 56, None, True, "e4m3"), (7, 8, 8, 48, 24, [12], True, "16"), (2000, 12, 4, 256, 256, None, True, "e4m3"),
+    (5, 1, 1, 16, 8, None, False, "e4m3"), (600, 192, 16, 80, 40, [8, 6, 6], False, "e4m3")])
+def test_rope_on_half_heads(T, Hq, Hkv, D, rot, sections, inter, kind):
+    test_rope_cache_write_and_read(T, Hq, Hkv, D, rot, 16, sections, inter, "bf16", kind, "hnd")
 
 
 def test_rope_in_place_and_separate_tensors():

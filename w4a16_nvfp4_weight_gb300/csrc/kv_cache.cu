@@ -148,49 +148,69 @@ __global__ void __launch_bounds__(256) rope_write_any_kernel(const RopeParams p)
     }
 }
 
-// rot a multiple of 16: a thread takes 16 elements of several heads of one token,
-// both sides of eight pairs, so that nothing is exchanged: pieces j and j + rot/16
-// of 8 elements (INTER: 2j and 2j + 1), past rot two neighbouring pieces as they
-// are.  L threads a head (a power of two), `per` head groups a token (a power of
-// two), kRopeThreads a block.
+// A piece of PE elements of a row (8: 16 bytes, 4: 8 bytes) as words.
+template <int PE>
+__device__ __forceinline__ void load_piece(uint32_t* w, const uint16_t* from) {
+    if constexpr (PE == 8) {
+        const uint4 v = ldg_once(from);
+        w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    } else {
+        asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(from) : "memory");
+    }
+}
+template <int WORDS>
+__device__ __forceinline__ void store_words(void* to, const uint32_t* w) {
+    if constexpr (WORDS == 4) *(uint4*)to = make_uint4(w[0], w[1], w[2], w[3]);
+    else if constexpr (WORDS == 2) *(uint2*)to = make_uint2(w[0], w[1]);
+    else *(uint32_t*)to = w[0];
+}
+
+// rot a multiple of 2 PE: a thread takes 2 PE elements of several heads of one
+// token, both sides of PE pairs, so that nothing is exchanged: pieces j and
+// j + rot/(2 PE) of PE elements (INTER: 2j and 2j + 1), past rot two neighbouring
+// pieces as they are.  PE is 8 where rot allows it, else 4.  L threads a head (a
+// power of two), `per` head groups a token (a power of two), kRopeThreads a block.
 // Bound by memory (q, k, v in, q and the cache rows out) and not far from it by
-// instructions: 24.6 us (4.86 TB/s) for 4096 tokens of 40 + 2 * 8 heads of 128
+// instructions: 23.5 us (5.1 TB/s) for 4096 tokens of 40 + 2 * 8 heads of 128
 // with three axes, where a piece of 8 a thread with its mate's by shuffle (176
-// instructions a warp for two heads) took 30.  The rows of U heads are loaded first; then
-// the block fetches its tokens' cosines and sines into shared memory, a thread a
-// frequency, whose addresses wait for the positions (each thread fetching its
-// own through L1: 40 us).
-template <bool F16, bool INTER, bool E4M3, int U>
-__global__ void __launch_bounds__(kRopeThreads, (E4M3 && U > 1 ? 640 : 768) / kRopeThreads) rope_write_kernel(const RopeParams p, int L, int per) {
+// instructions a warp for two heads) took 30.  The rows of U heads are loaded first;
+// then the block fetches its tokens' cosines and sines into shared memory, a
+// thread a frequency, whose addresses wait for the positions (each thread fetching
+// its own through L1: 40 us).
+template <bool F16, bool INTER, bool E4M3, int U, int PE>
+__global__ void __launch_bounds__(kRopeThreads, (E4M3 && U > 1 ? 640 : 768) / kRopeThreads)
+rope_write_kernel(const RopeParams p, int L, int per) {
+    constexpr int PW = PE / 2;                         // words of a piece, pairs of frequencies
     pdl_wait_previous();
     pdl_launch_dependents();
     const int j = threadIdx.x & (L - 1), group = threadIdx.x / L;
-    const int tokens = kRopeThreads / (L * per);               // a block's
+    const int tokens = kRopeThreads / (L * per);       // a block's
     const int64_t t = (int64_t)blockIdx.x * tokens + group / per;
-    const bool live = t < p.T && j * 16 < p.D;
+    const bool live = t < p.T && j * 2 * PE < p.D;
     const int heads = p.Hq + 2 * p.Hkv, stride = per * gridDim.y;
     const int first = blockIdx.y * per + (group & (per - 1));
-    const bool turns = j * 16 < p.rot;
+    const bool turns = j * 2 * PE < p.rot;
     const int half = p.rot / 2;
-    const int e0 = INTER || !turns ? j * 16 : j * 8;               // first element of the two pieces
-    const int e1 = INTER || !turns ? j * 16 + 8 : half + j * 8;
-    const uint32_t same = ((1u << L) - 1) << (threadIdx.x & 31 & ~(L - 1));     // the lanes of this head
-    F2 cs[4], sn[4];
+    const int e0 = INTER || !turns ? j * 2 * PE : j * PE;          // first element of the two pieces
+    const int e1 = INTER || !turns ? j * 2 * PE + PE : half + j * PE;
+    const uint32_t same = (L == 32 ? 0xffffffffu : (1u << L) - 1) << (threadIdx.x & 31 & ~(L - 1));     // the lanes of this head
+    F2 cs[PW], sn[PW];
     int64_t row = -1, scale_row = 0;                   // byte offset of the token's cache row of head 0
 
-    __shared__ __align__(16) float turn[kRopeThreads * 16];    // [token][cosines, sines]: at most kRopeThreads / L tokens of 16 L
+    __shared__ __align__(16) float turn[kRopeThreads * 2 * PE];    // [token][cosines, sines]: kRopeThreads / L tokens of 2 PE L at most
     for (int h0 = 0; h0 < heads; h0 += stride * U) {
-        uint4 x[U][2];
+        uint32_t x[U][2 * PW];
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int h = h0 + i * stride + first;
-            x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);            // lanes past D join in the row's amax
+#pragma unroll
+            for (int n = 0; n < 2 * PW; ++n) x[i][n] = 0;          // lanes past D join in the row's amax
             if (!live || h >= heads) continue;
             const uint16_t* from = h < p.Hq ? p.q + t * p.q_token + h * p.q_head
                                  : h < p.Hq + p.Hkv ? p.k + t * p.k_token + (h - p.Hq) * p.k_head
                                                     : p.v + t * p.v_token + (h - p.Hq - p.Hkv) * p.v_head;
-            x[i][0] = ldg_once(from + e0);
-            x[i][1] = ldg_once(from + e1);
+            load_piece<PE>(x[i], from + e0);
+            load_piece<PE>(x[i] + PW, from + e1);
         }
         if (h0 == 0) {
             const int64_t slot = live ? p.slots[t] : -1;
@@ -213,9 +233,9 @@ __global__ void __launch_bounds__(kRopeThreads, (E4M3 && U > 1 ? 640 : 768) / kR
                 scale_row = p.cache.scale_at(page, 0, at);
             }
             if (turns) {
-                const float4* from = (const float4*)(turn + group / per * p.rot + j * 8);
+                const float4* from = (const float4*)(turn + group / per * p.rot + j * PE);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < PE / 4; ++i) {
                     const float4 u = from[i], w = from[half / 4 + i];
                     cs[2 * i] = make_f2(u.x, u.y); cs[2 * i + 1] = make_f2(u.z, u.w);
                     sn[2 * i] = make_f2(w.x, w.y); sn[2 * i + 1] = make_f2(w.z, w.w);
@@ -227,12 +247,12 @@ __global__ void __launch_bounds__(kRopeThreads, (E4M3 && U > 1 ? 640 : 768) / kR
             const int h = h0 + i * stride + first;
             if (h >= heads) break;                     // all lanes of a head together
             const bool value = h >= p.Hq + p.Hkv, codes = E4M3 && h >= p.Hq, moves = !value && turns;
-            uint32_t w[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w, x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
-            F2 a[4], b[4];                             // the first and second sides of the pairs
+            uint32_t* w = x[i];
+            F2 a[PW], b[PW];                           // the first and second sides of the pairs
             if (moves || codes) {
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const float2 u = act2_to_f32<F16>(w[INTER ? 2 * n : n]), v = act2_to_f32<F16>(w[INTER ? 2 * n + 1 : n + 4]);
+                for (int n = 0; n < PW; ++n) {
+                    const float2 u = act2_to_f32<F16>(w[INTER ? 2 * n : n]), v = act2_to_f32<F16>(w[INTER ? 2 * n + 1 : n + PW]);
                     a[n] = INTER ? make_f2(u.x, v.x) : make_f2(u.x, u.y);
                     b[n] = INTER ? make_f2(u.y, v.y) : make_f2(v.x, v.y);
                     if (moves) {
@@ -245,53 +265,53 @@ __global__ void __launch_bounds__(kRopeThreads, (E4M3 && U > 1 ? 640 : 768) / kR
             if (!codes) {
                 if (moves) {
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) {
+                    for (int n = 0; n < PW; ++n) {
                         const float2 u = both(a[n]), v = both(b[n]);
                         w[INTER ? 2 * n : n] = INTER ? f32_to_act2<F16>(u.x, v.x) : f32_to_act2<F16>(u.x, u.y);
-                        w[INTER ? 2 * n + 1 : n + 4] = INTER ? f32_to_act2<F16>(u.y, v.y) : f32_to_act2<F16>(v.x, v.y);
+                        w[INTER ? 2 * n + 1 : n + PW] = INTER ? f32_to_act2<F16>(u.y, v.y) : f32_to_act2<F16>(v.x, v.y);
                     }
                 }
                 if (!live || (h >= p.Hq && row < 0)) continue;
                 uint16_t* to = h < p.Hq ? p.q_out + (t * p.Hq + h) * p.D
                              : (uint16_t*)((value ? p.cache.v + (h - p.Hq - p.Hkv) * p.cache.head_bytes
                                                   : p.cache.k + (h - p.Hq) * p.cache.head_bytes) + row);
-                *(uint4*)(to + e0) = make_uint4(w[0], w[1], w[2], w[3]);
-                *(uint4*)(to + e1) = make_uint4(w[4], w[5], w[6], w[7]);
+                store_words<PW>(to + e0, w);
+                store_words<PW>(to + e1, w + PW);
                 continue;
             }
             float amax = 0.f;
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
+            for (int n = 0; n < PW; ++n) {
                 const float2 u = both(a[n]), v = both(b[n]);
                 amax = fmaxf(fmaxf(amax, fmaxf(fabsf(u.x), fabsf(u.y))), fmaxf(fabsf(v.x), fabsf(v.y)));
             }
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1)
+            for (int o = 16; o > 0; o >>= 1)
                 if (o < L) amax = fmaxf(amax, __shfl_xor_sync(same, amax, o));
             if (!live || row < 0) continue;
             const float s = e4m3_scale(amax), inv = e4m3_inverse(s);
             const int kh = h - p.Hq - (value ? p.Hkv : 0);
             const F2 minus_s = make_f2(-s, -s), inv2 = make_f2(inv, inv);
-            uint32_t o[4];                             // codes of the pieces at e0 and e1
+            uint32_t o[PW];                            // codes of the pieces at e0 and e1
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
+            for (int n = 0; n < PW; ++n) {
                 F2 one = a[n], two = b[n];             // in the order of the elements
                 if (INTER) {
                     const float2 u = both(a[n]), v = both(b[n]);
                     one = make_f2(u.x, v.x);
                     two = make_f2(u.y, v.y);
                 }
-                const uint32_t x = e4m3_codes(one, minus_s, inv2), y = e4m3_codes(two, minus_s, inv2);
+                const uint32_t c0 = e4m3_codes(one, minus_s, inv2), c1 = e4m3_codes(two, minus_s, inv2);
                 if (INTER) {
-                    o[n] = x | y << 16;
+                    o[n] = c0 | c1 << 16;
                 } else {
-                    o[n >> 1] = n & 1 ? o[n >> 1] | x << 16 : x;
-                    o[2 + (n >> 1)] = n & 1 ? o[2 + (n >> 1)] | y << 16 : y;
+                    o[n >> 1] = n & 1 ? o[n >> 1] | c0 << 16 : c0;
+                    o[PW / 2 + (n >> 1)] = n & 1 ? o[PW / 2 + (n >> 1)] | c1 << 16 : c1;
                 }
             }
             uint8_t* to = (value ? p.cache.v : p.cache.k) + kh * p.cache.head_bytes + row;
-            *(uint2*)(to + e0) = make_uint2(o[0], o[1]);
-            *(uint2*)(to + e1) = make_uint2(o[2], o[3]);
+            store_words<PW / 2>(to + e0, o);
+            store_words<PW / 2>(to + e1, o + PW / 2);
             if (j == 0) (value ? p.cache.v_scale : p.cache.k_scale)[scale_row + (int64_t)kh * p.cache.page_size] = s;
         }
     }
@@ -299,10 +319,15 @@ __global__ void __launch_bounds__(kRopeThreads, (E4M3 && U > 1 ? 640 : 768) / kR
 
 constexpr int kManyHeads = 4;      // heads a thread takes where there are many tokens
 
-template <bool F16, bool INTER>
-const void* rope_kernel(bool e4m3, bool one) {
-    if (one) return e4m3 ? (const void*)rope_write_kernel<F16, INTER, true, 1> : (const void*)rope_write_kernel<F16, INTER, false, 1>;
-    return e4m3 ? (const void*)rope_write_kernel<F16, INTER, true, kManyHeads> : (const void*)rope_write_kernel<F16, INTER, false, kManyHeads>;
+template <bool F16, bool INTER, bool E4M3>
+const void* rope_kernel(bool one, int PE) {
+    if (PE == 8) return one ? (const void*)rope_write_kernel<F16, INTER, E4M3, 1, 8> : (const void*)rope_write_kernel<F16, INTER, E4M3, kManyHeads, 8>;
+    return one ? (const void*)rope_write_kernel<F16, INTER, E4M3, 1, 4> : (const void*)rope_write_kernel<F16, INTER, E4M3, kManyHeads, 4>;
+}
+template <bool F16>
+const void* rope_kernel(bool inter, bool e4m3, bool one, int PE) {
+    if (inter) return e4m3 ? rope_kernel<F16, true, true>(one, PE) : rope_kernel<F16, true, false>(one, PE);
+    return e4m3 ? rope_kernel<F16, false, true>(one, PE) : rope_kernel<F16, false, false>(one, PE);
 }
 
 nvfp4_status launch_after(const void* kernel, dim3 grid, dim3 block, void** args, cudaStream_t stream, const char* fn) {
@@ -320,23 +345,23 @@ nvfp4_status launch_after(const void* kernel, dim3 grid, dim3 block, void** args
 
 nvfp4_status launch_rope(RopeParams p, bool f16, bool inter, cudaStream_t stream, const char* fn) {
     const int heads = p.Hq + 2 * p.Hkv;
-    if (p.rot % 16 != 0) {
+    if (p.rot % 8 != 0) {
         const void* kernel = f16 ? (inter ? (const void*)rope_write_any_kernel<true, true> : (const void*)rope_write_any_kernel<true, false>)
                                  : (inter ? (const void*)rope_write_any_kernel<false, true> : (const void*)rope_write_any_kernel<false, false>);
         void* args[] = {&p};
         return launch_after(kernel, dim3((unsigned)std::min<int64_t>(ceil_div(p.T * heads, 8), (int64_t)sm_count() * 8)), dim3(256), args, stream, fn);
     }
+    const int PE = p.rot % 16 == 0 ? 8 : 4;
     int L = 1, per = 1;
-    while (L * 16 < p.D) L *= 2;
+    while (L * 2 * PE < p.D) L *= 2;
     // Many tokens: about four heads a thread, all in flight (4096 tokens: 24.6 us;
     // three 31.0, two 28.5).  Few tokens: one head a thread over as many blocks
     // as that takes, for the shortest way through.
     const bool one = p.T * heads * L <= (int64_t)sm_count() * 1024;
     while (per * 2 * L <= kRopeThreads && (one ? per < heads : per * kManyHeads < heads)) per *= 2;
-    const int tokens = kRopeThreads / (L * per);                // a block's
+    const int tokens = kRopeThreads / (L * per);       // a block's
     dim3 grid((unsigned)ceil_div(p.T, tokens), (unsigned)ceil_div(heads, per * (one ? 1 : kManyHeads)));
-    const void* kernel = f16 ? (inter ? rope_kernel<true, true>(p.cache.e4m3, one) : rope_kernel<true, false>(p.cache.e4m3, one))
-                             : (inter ? rope_kernel<false, true>(p.cache.e4m3, one) : rope_kernel<false, false>(p.cache.e4m3, one));
+    const void* kernel = f16 ? rope_kernel<true>(inter, p.cache.e4m3, one, PE) : rope_kernel<false>(inter, p.cache.e4m3, one, PE);
     void* args[] = {&p, &L, &per};
     return launch_after(kernel, grid, dim3(kRopeThreads), args, stream, fn);
 }
