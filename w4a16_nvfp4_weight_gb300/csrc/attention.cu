@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
             const uint32_t ks_s = ring_s + stage * S::kStage, vs_s = ks_s + S::kTile;
 
             // ---- scores of 16 tokens (rows g, g + 8) x 8 heads (columns 2 q4, 2 q4 + 1)
-            float z[NT][4], z2[NT][4];
+            float z[NT][4], z2[NT][4];                          // one head tile: two chains of products
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
                     uint32_t af[4];
                     ldmatrix4(af, ks_s + row * S::kRow + key_chunk<E4M3, CH>(row, ks * 2 + ch) * 16);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_16816<H>(ks & 1 ? z2[nt] : z[nt], af, qf[ks][nt][0], qf[ks][nt][1]);
+                    for (int nt = 0; nt < NT; ++nt) mma_16816<H>(NT == 1 && ks & 1 ? z2[nt] : z[nt], af, qf[ks][nt][0], qf[ks][nt][1]);
                 }
             } else {
 #pragma unroll
@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
                                                 e4m3x2_to_f16x2((uint16_t)(lo[w] >> 16)), e4m3x2_to_f16x2((uint16_t)(hi[w] >> 16))};
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
-                            mma_16816<H>(w & 1 ? z2[nt] : z[nt], af, qf[j * 4 + w][nt][0], qf[j * 4 + w][nt][1]);
+                            mma_16816<H>(NT == 1 && w & 1 ? z2[nt] : z[nt], af, qf[j * 4 + w][nt][0], qf[j * 4 + w][nt][1]);
                     }
                 }
             }
@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
                 float s[4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    s[x] = (z[nt][x] + z2[nt][x]) * qs[nt][x & 1];
+                    s[x] = (NT == 1 ? z[nt][x] + z2[nt][x] : z[nt][x]) * qs[nt][x & 1];
                     if (E4M3) s[x] *= x < 2 ? k0 : k1;
                     if (!(x < 2 ? held0 : held1)) s[x] = -INFINITY;
                 }

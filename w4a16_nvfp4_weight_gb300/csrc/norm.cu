@@ -243,8 +243,8 @@ __global__ void __launch_bounds__(1024) norm_narrow_kernel(const NormParams p) {
 // Any width, stride and alignment: a block walks a row element by element, and
 // reads it again (from L1/L2) for the output.
 template <bool F16>
-__global__ void __launch_bounds__(256) norm_any_kernel(const NormParams p) {
-    __shared__ float sm[2][8];
+__global__ void __launch_bounds__(1024) norm_any_kernel(const NormParams p) {
+    __shared__ float sm[2][32];
     pdl_wait_previous();
     pdl_launch_dependents();
     const int64_t t = blockIdx.x;
@@ -317,7 +317,7 @@ nvfp4_status launch_norm(const NormParams& p, bool f16, cudaStream_t stream) {
     const bool rows = p.H % 8 == 0 && pieces <= 4096 && p.x_stride % 8 == 0 && p.res_stride % 8 == 0 && aligned(p.x, 16) &&
                       aligned(p.residual, 16) && aligned(p.weight, 16) && aligned(p.residual_out, 16) && aligned(p.y, e4m3 ? 8 : 16);
     const void* kernel = f16 ? (const void*)norm_any_kernel<true> : (const void*)norm_any_kernel<false>;
-    dim3 block(256);
+    dim3 block(p.H > 4096 ? 1024 : 256);
     if (rows) {
         // Rows that fill the GPU take several pieces a thread: loads in flight, few
         // threads to join and fewer scales' divisions (8192x8192: one 84.6 us, two 79.3,
