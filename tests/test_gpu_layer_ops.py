@@ -461,6 +461,15 @@ def test_paged_attention_strided_query_and_large_queries(kind):
                        nv.paged_attention(case[1].contiguous(), block_table=case[2], lengths=case[3], **case[0]))
 
 
+@pytest.mark.parametrize("all_zero", [True, False])
+def test_paged_attention_of_values_whose_scale_is_zero(all_zero):
+    """Rows of zeros (a scale of 0 is no scale the write gives) weigh as others do."""
+    case = _attention_case([700, 19, 3], 8, 2, 128, 16, "bf16", "e4m3", 82)
+    scales = case[0]["v_scale"]
+    scales[torch.arange(scales.shape[0], device="cuda") % (1 if all_zero else 2) == 0] = 0
+    _check_attention(*case, 16, "bf16", "e4m3")
+
+
 def test_paged_attention_nan_and_infinity_in_held_tokens():
     c, q, table, lengths, slots = _attention_case([40, 40], 4, 2, 64, 16, "bf16", "16", 80)
     c["k_cache"][int(table[0, 1]), 0, 3, 5] = float("nan")
