@@ -10,7 +10,8 @@
 //
 // Bound by the cache's bytes (2 G / element size flop a byte, G query heads a
 // key head), so the kernel is built around keeping loads in flight:
-//  - The unit of work is a step: 16 tokens of one key head.  All steps of all
+//  - The unit of work is a step: 16 tokens of one key head, or 32 where a row has 64
+//    bytes.  All steps of all
 //    sequences are numbered through (sequence, head, token) on the device, from
 //    the lengths, and cut into equal contiguous ranges, one a warp of a grid
 //    that fills the GPU once.  So a ragged batch, one long sequence and many
@@ -46,8 +47,8 @@
 namespace nvfp4 {
 namespace {
 
-constexpr int kStep = 16;          // tokens a step
-constexpr int kWholeUnit = 16;     // units of at most so many steps are not split between blocks
+constexpr int kRows = 16;          // tokens of an MMA; a step has one or two blocks of so many
+constexpr int kWholeUnit = 256;    // units of at most so many tokens are not split between blocks
 constexpr int kUnitCost = 4;       // steps' worth of time that the start and end of a unit take
 constexpr size_t kMaxSmem = 227 * 1024;
 
@@ -62,7 +63,7 @@ struct AttnParams {
     float* parts;                  // workspace: partial results of blocks, then of warps
     int B, Hq, G, chunks, units;   // chunks: head groups of one key head; units = heads * chunks a sequence
     int width;
-    bool whole_pages;              // a step lies in one page (page_size a multiple of 16)
+    bool whole_pages;              // sixteen tokens lie in one page (page_size a multiple of 16)
     int window;                    // 0: none
     bool whole_units;              // no unit is split between blocks
     float scale_log2;              // softmax_scale * log2(e)
@@ -77,13 +78,18 @@ struct AttnParams {
 // tiles take twelve warps and four steps each: 129 us for 16 x 16384 tokens, 96 query
 // and 8 key heads (BF16 query; eight warps and six steps: 138), 29.8 against 28.4 at 2048.
 constexpr int attn_warps(int row, int values) { return row > 256 ? 4 : row > 128 ? 8 : values >= 64 ? 12 : 16; }
-constexpr int attn_stages(int row, int values) { return row == 64 || (row == 128 && values >= 64) ? 4 : 3; }
+constexpr int attn_stages(int row, int values) { return row == 128 && values >= 64 ? 4 : 3; }
 
 // Shape of an instance: DP padded head size, NT tiles of 8 query heads.
 template <bool E4M3, int DP, int NT>
 struct Shape {
     static constexpr int kRow = DP * (E4M3 ? 1 : 2);            // bytes of a row in the ring
     static constexpr int kChunks = kRow / 16;                   // 16-byte chunks a row
+    // Blocks of 16 tokens a step: 2 KB leave most of a step's instructions to finding its
+    // pages and to the softmax, which a second block shares (64 x 8192 tokens, 32 query
+    // and 8 key heads of 64: 100 us; one block 131).  Longer rows have no room for it.
+    static constexpr int kBlocks = kRow == 64 ? 2 : 1;
+    static constexpr int kStep = kRows * kBlocks;
     static constexpr int kTile = kStep * kRow;
     static constexpr int kStage = 2 * kTile + (E4M3 ? 2 * kStep * 4 : 0);
     static constexpr int kWarps = attn_warps(kRow, DP / 4 * NT);
@@ -219,19 +225,21 @@ __device__ __forceinline__ int checked_length(const AttnParams& p, int b) {
 __device__ __forceinline__ int first_token(const AttnParams& p, int n) {
     return p.window > 0 ? max(0, n - p.window) : 0;
 }
+template <int STEP>
 __device__ __forceinline__ int steps_of(const AttnParams& p, int n) {
-    return (n + kStep - 1) / kStep - first_token(p, n) / kStep;
+    return (n + STEP - 1) / STEP - first_token(p, n) / STEP;
 }
 
 // A place in the numbering of steps: sequence, unit (key head and head group), step.
+template <int STEP>
 struct Place {
     int b, u, step, lo, n, s_lo, s_hi;     // tokens [lo, n), steps [s_lo, s_hi) of the sequence
 
     __device__ __forceinline__ void sequence(const AttnParams& p) {
         n = checked_length(p, b);
         lo = first_token(p, n);
-        s_lo = lo / kStep;
-        s_hi = (n + kStep - 1) / kStep;
+        s_lo = lo / STEP;
+        s_hi = (n + STEP - 1) / STEP;
     }
     // Only called where another step follows, so a sequence with tokens is found.
     __device__ __forceinline__ void advance(const AttnParams& p) {
@@ -262,12 +270,13 @@ struct Ranges {
 
 // The numbering of all steps, by a block of WARPS warps: thread t takes `per`
 // sequences from t * per on; sm holds the first number of each thread's.
+template <int STEP>
 __device__ __forceinline__ int numbers_of(const AttnParams& p, int b) {
-    const int n = steps_of(p, checked_length(p, b));
+    const int n = steps_of<STEP>(p, checked_length(p, b));
     return n > 0 ? (n + kUnitCost) * p.units : 0;
 }
 
-template <int WARPS>
+template <int WARPS, int STEP>
 struct Numbering {
     int per, total;
 
@@ -276,7 +285,7 @@ struct Numbering {
         per = (p.B + WARPS * 32 - 1) / (WARPS * 32);
         const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
         int mine = 0;
-        for (int b = b0; b < b1; ++b) mine += numbers_of(p, b);
+        for (int b = b0; b < b1; ++b) mine += numbers_of<STEP>(p, b);
         int incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -301,25 +310,25 @@ struct Numbering {
 #pragma unroll 4
         for (int k = 0; k < WARPS * 32; k += 32) t += __popc(__ballot_sync(0xffffffffu, sm[k + (threadIdx.x & 31)] <= x));
         int b = t * per, at = sm[t];
-        for (int n; per > 1 && x >= at + (n = numbers_of(p, b)); ++b) at += n;
+        for (int n; per > 1 && x >= at + (n = numbers_of<STEP>(p, b)); ++b) at += n;
         *first = at;
         return b;
     }
 };
 
 // The first number of the unit that holds x, or of the next one if x lies behind its first.
-template <int WARPS>
-__device__ __forceinline__ int unit_from(const AttnParams& p, const Numbering<WARPS>& steps, const int* sm, int x) {
+template <int WARPS, int STEP>
+__device__ __forceinline__ int unit_from(const AttnParams& p, const Numbering<WARPS, STEP>& steps, const int* sm, int x) {
     if (x >= steps.total) return steps.total;
     int first;
-    const int b = steps.find(p, sm, x, &first), each = steps_of(p, checked_length(p, b)) + kUnitCost;
+    const int b = steps.find(p, sm, x, &first), each = steps_of<STEP>(p, checked_length(p, b)) + kUnitCost;
     return first + (x - first + each - 1) / each * each;
 }
 
 template <bool F16, bool E4M3, int DP, int NT>
 __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_kernel(const AttnParams p) {
     using S = Shape<E4M3, DP, NT>;
-    constexpr int W = S::kWarps, CH = S::kChunks, KS = DP / 16, ST = S::kStages;
+    constexpr int W = S::kWarps, CH = S::kChunks, KS = DP / 16, ST = S::kStages, TB = S::kBlocks, STEP = S::kStep;
     constexpr bool H = F16 || E4M3;                             // FP16 operands in the MMAs
     extern __shared__ __align__(1024) uint8_t ring_all[];
     __shared__ int first_sm[W * 32], sums[W];
@@ -335,7 +344,7 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
     const int gw = blockIdx.x * W + warp;
     const int D = p.cache.D;
 
-    Numbering<W> steps;
+    Numbering<W, STEP> steps;
     steps.count(p, first_sm, sums);
     // This block's range and this warp's, or, where units are short, a range of whole
     // units (from the first that begins in the block's numbers on) spread over its warps.
@@ -357,7 +366,7 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
 
     // ---- sequences without a token
     for (int b = gw; b < p.B; b += gridDim.x * W) {
-        if (steps_of(p, checked_length(p, b)) > 0) continue;
+        if (steps_of<STEP>(p, checked_length(p, b)) > 0) continue;
         uint4* o = (uint4*)(p.out + (int64_t)b * p.Hq * D);
         for (int i = lane; i < p.Hq * D / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
         if (p.lse)
@@ -373,7 +382,7 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
     float* const warp_parts = p.parts + (size_t)gridDim.x * 2 * S::kPart;
     int head_unit = -1, tail_unit = -1;
 
-    Place c;                                                    // the step to compute
+    Place<STEP> c;                                                    // the step to compute
     int at_c = e, unit_first = 0;                               // its number, and that of its unit's first step
     if (a < e) {
         c.b = steps.find(p, first_sm, a, &unit_first);
@@ -386,7 +395,7 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
         at_c = unit_first + x;
     }
     if (at_c < e) {
-        Place f = c;                                            // the next step to copy
+        Place<STEP> f = c;                                            // the next step to copy
         int at_f = at_c;
 
         // Table entries [base, base + 64) of sequence window_b, two a lane.  The second
@@ -399,7 +408,7 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
         const int held_chunks = D * (E4M3 ? 1 : 2) / 16, r0 = lane / CH, c0 = lane % CH;
         auto copy = [&](int stage) {
             const uint32_t dst = ring_s + stage * S::kStage;
-            const int s0 = f.step * kStep, i0 = entry(max(s0, f.lo));
+            const int s0 = f.step * STEP, i0 = entry(max(s0, f.lo));
             if (f.b != window_b || i0 < base || i0 >= base + 64) {
                 window_b = f.b;
                 base = i0;
@@ -410,8 +419,8 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
                 near = far;
                 far = load_entries(base + 32 + lane);
             }
-            // the page and place of token lane % 16; those not held take a neighbour's
-            const int t = min(max(s0 + (lane & 15), f.lo), f.n - 1), i = entry(t);
+            // the page and place of token lane % STEP; those not held take a neighbour's
+            const int t = min(max(s0 + (lane & (STEP - 1)), f.lo), f.n - 1), i = entry(t);
             const int n0 = __shfl_sync(0xffffffffu, near, (i - base) & 31), n1 = __shfl_sync(0xffffffffu, far, (i - base) & 31);
             int page = i - base < 32 ? n0 : n1;
             if ((uint32_t)page >= (uint32_t)p.cache.num_pages) {
@@ -421,13 +430,15 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
             const int at = t - i * p.cache.page_size, kh = p.chunks == 1 ? f.u : f.u / p.chunks;
             const int64_t off = p.cache.row(page, kh, at);
             const int r_lo = f.lo - s0, r_hi = f.n - s0;        // rows [r_lo, r_hi) are held
-            if (p.whole_pages && r_lo <= 0) {                   // rows evenly spaced from the first one on
-                const int64_t from = __shfl_sync(0xffffffffu, off, 0) + r0 * p.cache.token_bytes + c0 * 16;
-                const uint8_t *k = p.cache.k + from, *v = p.cache.v + from;
-                if (c0 < held_chunks) {
+            if (p.whole_pages && r_lo <= 0) {                   // sixteen rows at a time evenly spaced
+#pragma unroll
+                for (int tb = 0; tb < TB; ++tb) {
+                    const int64_t from = __shfl_sync(0xffffffffu, off, tb * kRows) + r0 * p.cache.token_bytes + c0 * 16;
+                    const uint8_t *k = p.cache.k + from, *v = p.cache.v + from;
+                    if (c0 >= held_chunks) continue;
 #pragma unroll
                     for (int j = 0; j < CH / 2; ++j) {          // 32 / CH rows an instruction
-                        const int r = j * (32 / CH) + r0;
+                        const int r = tb * kRows + j * (32 / CH) + r0;
                         cp_async16(dst + r * S::kRow + key_chunk<E4M3, CH>(r, c0) * 16, k, r < r_hi);
                         cp_async16(dst + S::kTile + r * S::kRow + value_chunk<E4M3, CH>(r, c0) * 16, v, r < r_hi);
                         k += (32 / CH) * p.cache.token_bytes;
@@ -436,7 +447,7 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
                 }
             } else {
 #pragma unroll
-                for (int j = 0; j < CH / 2; ++j) {
+                for (int j = 0; j < TB * CH / 2; ++j) {
                     const int r = j * (32 / CH) + r0;
                     const int64_t from = __shfl_sync(0xffffffffu, off, r) + c0 * 16;
                     if (c0 < held_chunks) {
@@ -445,10 +456,17 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
                     }
                 }
             }
-            if (E4M3)                                           // lanes 0-15 the keys' scales, 16-31 the values'
-                cp_async4(dst + 2 * S::kTile + lane * 4,
-                          (lane < 16 ? p.cache.k_scale : p.cache.v_scale) + p.cache.scale_at(page, kh, at),
-                          (lane & 15) >= r_lo && (lane & 15) < r_hi);
+            if (E4M3) {                                         // of the keys, then of the values
+                const int64_t scale = p.cache.scale_at(page, kh, at);
+                const int r = lane & (STEP - 1);
+                const bool held = r >= r_lo && r < r_hi;
+                if constexpr (TB == 1) {
+                    cp_async4(dst + 2 * S::kTile + lane * 4, (lane < 16 ? p.cache.k_scale : p.cache.v_scale) + scale, held);
+                } else {
+                    cp_async4(dst + 2 * S::kTile + lane * 4, p.cache.k_scale + scale, held);
+                    cp_async4(dst + 2 * S::kTile + (STEP + lane) * 4, p.cache.v_scale + scale, held);
+                }
+            }
         };
 
         uint32_t qf[KS][NT][2];
@@ -527,66 +545,79 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
             const uint32_t ks_s = ring_s + stage * S::kStage, vs_s = ks_s + S::kTile;
 
             // ---- scores of 16 tokens (rows g, g + 8) x 8 heads (columns 2 q4, 2 q4 + 1)
-            float z[NT][4], z2[NT][4];                          // one head tile: two chains of products
+            float z[TB][NT][4], z2[TB][NT][4];                  // one head tile: two chains of products
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int tb = 0; tb < TB; ++tb) {
 #pragma unroll
-                for (int x = 0; x < 4; ++x) z[nt][x] = z2[nt][x] = 0.f;
-            if constexpr (!E4M3) {
-                const int row = (lane & 7) + (lane & 8), ch = lane >> 4;
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    uint32_t af[4];
-                    ldmatrix4(af, ks_s + row * S::kRow + key_chunk<E4M3, CH>(row, ks * 2 + ch) * 16);
+                    for (int x = 0; x < 4; ++x) z[tb][nt][x] = z2[tb][nt][x] = 0.f;
+                if constexpr (!E4M3) {
+                    const int row = tb * kRows + (lane & 7) + (lane & 8), ch = lane >> 4;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_16816<H>(NT == 1 && ks & 1 ? z2[nt] : z[nt], af, qf[ks][nt][0], qf[ks][nt][1]);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < KS / 4; ++j) {
-                    const uint4 w0 = lds128(ks_s + g * S::kRow + key_chunk<E4M3, CH>(g, j * 4 + q4) * 16);
-                    const uint4 w1 = lds128(ks_s + (g + 8) * S::kRow + key_chunk<E4M3, CH>(g + 8, j * 4 + q4) * 16);
-                    const uint32_t lo[4] = {w0.x, w0.y, w0.z, w0.w}, hi[4] = {w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const uint32_t af[4] = {e4m3x2_to_f16x2((uint16_t)lo[w]), e4m3x2_to_f16x2((uint16_t)hi[w]),
-                                                e4m3x2_to_f16x2((uint16_t)(lo[w] >> 16)), e4m3x2_to_f16x2((uint16_t)(hi[w] >> 16))};
+                    for (int ks = 0; ks < KS; ++ks) {
+                        uint32_t af[4];
+                        ldmatrix4(af, ks_s + row * S::kRow + key_chunk<E4M3, CH>(row, ks * 2 + ch) * 16);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
-                            mma_16816<H>(NT == 1 && w & 1 ? z2[nt] : z[nt], af, qf[j * 4 + w][nt][0], qf[j * 4 + w][nt][1]);
+                            mma_16816<H>(NT == 1 && ks & 1 ? z2[tb][nt] : z[tb][nt], af, qf[ks][nt][0], qf[ks][nt][1]);
+                    }
+                } else {
+                    const int row = tb * kRows + g;
+#pragma unroll
+                    for (int j = 0; j < KS / 4; ++j) {
+                        const uint4 w0 = lds128(ks_s + row * S::kRow + key_chunk<E4M3, CH>(row, j * 4 + q4) * 16);
+                        const uint4 w1 = lds128(ks_s + (row + 8) * S::kRow + key_chunk<E4M3, CH>(row + 8, j * 4 + q4) * 16);
+                        const uint32_t lo[4] = {w0.x, w0.y, w0.z, w0.w}, hi[4] = {w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            const uint32_t af[4] = {e4m3x2_to_f16x2((uint16_t)lo[w]), e4m3x2_to_f16x2((uint16_t)hi[w]),
+                                                    e4m3x2_to_f16x2((uint16_t)(lo[w] >> 16)), e4m3x2_to_f16x2((uint16_t)(hi[w] >> 16))};
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma_16816<H>(NT == 1 && w & 1 ? z2[tb][nt] : z[tb][nt], af, qf[j * 4 + w][nt][0], qf[j * 4 + w][nt][1]);
+                        }
                     }
                 }
             }
 
-            // ---- softmax weights
-            const int t0 = c.step * kStep + g;
-            const bool held0 = t0 >= c.lo && t0 < c.n, held1 = t0 + 8 >= c.lo && t0 + 8 < c.n;
-            float k0 = 1.f, k1 = 1.f, v0 = 1.f, v1 = 1.f, lv0 = 0.f, lv1 = 0.f;
-            if (E4M3) {
-                const uint32_t sc = ks_s + 2 * S::kTile;
-                k0 = lds_f32(sc + g * 4); k1 = lds_f32(sc + g * 4 + 32);
-                v0 = lds_f32(sc + 64 + g * 4); v1 = lds_f32(sc + 64 + g * 4 + 32);
-                // a power of two above the scale: weights times scales stay below 1.  At least
-                // 2^-99, above the least scale that is written: a scale of zero leaves l finite.
-                lv0 = (float)max((int)((__float_as_uint(v0) >> 23) & 255) - 126, -99);
-                lv1 = (float)max((int)((__float_as_uint(v1) >> 23) & 255) - 126, -99);
-            }
-            uint32_t pf[NT][2];
+            // ---- softmax weights; a lane has two tokens a block
+            bool held[TB][2];
+            float k_by[TB][2], v_by[TB][2], lv[TB][2];
+#pragma unroll
+            for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int row = tb * kRows + y * 8 + g, t = c.step * STEP + row;
+                    held[tb][y] = t >= c.lo && t < c.n;
+                    k_by[tb][y] = v_by[tb][y] = 1.f;
+                    lv[tb][y] = 0.f;
+                    if (E4M3) {
+                        k_by[tb][y] = lds_f32(ks_s + 2 * S::kTile + row * 4);
+                        v_by[tb][y] = lds_f32(ks_s + 2 * S::kTile + (STEP + row) * 4);
+                        // a power of two above the scale: weights times scales stay below 1.  At least
+                        // 2^-99, above the least scale that is written: a scale of zero leaves l finite.
+                        lv[tb][y] = (float)max((int)((__float_as_uint(v_by[tb][y]) >> 23) & 255) - 126, -99);
+                    }
+                }
+            uint32_t pf[TB][NT][2];
             float keep[NT][2];
             bool grown = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float s[4];
+                float s[TB][4], w[TB][4];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    s[x] = (NT == 1 ? z[nt][x] + z2[nt][x] : z[nt][x]) * qs[nt][x & 1];
-                    if (E4M3) s[x] *= x < 2 ? k0 : k1;
-                    if (!(x < 2 ? held0 : held1)) s[x] = -INFINITY;
-                }
-                float w[4];
+                for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        s[tb][x] = (NT == 1 ? z[tb][nt][x] + z2[tb][nt][x] : z[tb][nt][x]) * qs[nt][x & 1];
+                        if (E4M3) s[tb][x] *= k_by[tb][x >> 1];
+                        if (!held[tb][x >> 1]) s[tb][x] = -INFINITY;
+                    }
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    float top = fmaxf(s[x] + lv0, s[x + 2] + lv1);
+                    float top = fmaxf(s[0][x] + lv[0][0], s[0][x + 2] + lv[0][1]);
+                    if constexpr (TB == 2) top = fmaxf(top, fmaxf(s[TB - 1][x] + lv[TB - 1][0], s[TB - 1][x + 2] + lv[TB - 1][1]));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
@@ -595,13 +626,21 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
                     keep[nt][x] = ex2(m[nt][x] - base);
                     grown |= to > m[nt][x];
                     m[nt][x] = to;
-                    w[x] = ex2(s[x] - base);
-                    w[x + 2] = ex2(s[x + 2] - base);
-                    l[nt][x] = l[nt][x] * keep[nt][x] + (w[x] + w[x + 2]);
+                    float sum = 0.f;
+#pragma unroll
+                    for (int tb = 0; tb < TB; ++tb) {
+                        w[tb][x] = ex2(s[tb][x] - base);
+                        w[tb][x + 2] = ex2(s[tb][x + 2] - base);
+                        sum = tb == 0 ? w[tb][x] + w[tb][x + 2] : sum + (w[tb][x] + w[tb][x + 2]);
+                    }
+                    l[nt][x] = l[nt][x] * keep[nt][x] + sum;
                 }
-                // heads on the MMA's columns: transpose the two 8x8 blocks
-                pf[nt][0] = movmatrix(f32_to_act2<H>(w[0] * v0, w[1] * v0));
-                pf[nt][1] = movmatrix(f32_to_act2<H>(w[2] * v1, w[3] * v1));
+                // heads on the MMA's columns: transpose the 8x8 blocks
+#pragma unroll
+                for (int tb = 0; tb < TB; ++tb) {
+                    pf[tb][nt][0] = movmatrix(f32_to_act2<H>(w[tb][0] * v_by[tb][0], w[tb][1] * v_by[tb][0]));
+                    pf[tb][nt][1] = movmatrix(f32_to_act2<H>(w[tb][2] * v_by[tb][1], w[tb][3] * v_by[tb][1]));
+                }
             }
             if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
@@ -613,45 +652,48 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
             }
 
             // ---- output of 16 dimensions (rows) x 8 heads at a time
-            if constexpr (!E4M3) {
-                const int row = (lane & 7) + ((lane >> 4) << 3), ch = (lane >> 3) & 1;
 #pragma unroll
-                for (int mt = 0; mt < KS; ++mt) {
-                    uint32_t af[4];
-                    ldmatrix4_trans(af, vs_s + row * S::kRow + value_chunk<E4M3, CH>(row, mt * 2 + ch) * 16);
+            for (int tb = 0; tb < TB; ++tb) {
+                if constexpr (!E4M3) {
+                    const int row = tb * kRows + (lane & 7) + ((lane >> 4) << 3), ch = (lane >> 3) & 1;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_16816<H>(o[mt][nt], af, pf[nt][0], pf[nt][1]);
-                }
-            } else {
-                // A lane takes the dimensions of chunk g (half a chunk of 64) of tokens 2 q4, 2 q4 + 1 and
-                // the two 8 on; byte permutes pair the tokens.
-                constexpr int WORDS = DP == 64 ? 2 : 4;
+                    for (int mt = 0; mt < KS; ++mt) {
+                        uint32_t af[4];
+                        ldmatrix4_trans(af, vs_s + row * S::kRow + value_chunk<E4M3, CH>(row, mt * 2 + ch) * 16);
 #pragma unroll
-                for (int j = 0; j < (DP == 64 ? 1 : DP / 128); ++j) {
-                    uint32_t v[4][WORDS];
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int r = 2 * q4 + (x & 1) + (x >> 1) * 8;
-                        if constexpr (DP == 64) {
-                            const uint2 u = lds64(vs_s + r * S::kRow + value_chunk<E4M3, CH>(r, g >> 1) * 16 + (g & 1) * 8);
-                            v[x][0] = u.x; v[x][1] = u.y;
-                        } else {
-                            const uint4 u = lds128(vs_s + r * S::kRow + value_chunk<E4M3, CH>(r, j * 8 + g) * 16);
-                            v[x][0] = u.x; v[x][1] = u.y; v[x][2] = u.z; v[x][3] = u.w;
-                        }
+                        for (int nt = 0; nt < NT; ++nt) mma_16816<H>(o[mt][nt], af, pf[tb][nt][0], pf[tb][nt][1]);
                     }
+                } else {
+                    // A lane takes the dimensions of chunk g (half a chunk of 64) of tokens 2 q4, 2 q4 + 1 and
+                    // the two 8 on; byte permutes pair the tokens.
+                    constexpr int WORDS = DP == 64 ? 2 : 4;
 #pragma unroll
-                    for (int w = 0; w < WORDS; ++w)
+                    for (int j = 0; j < (DP == 64 ? 1 : DP / 128); ++j) {
+                        uint32_t v[4][WORDS];
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            const uint32_t sel = half ? 0x7362 : 0x5140;
-                            const uint32_t lo = __byte_perm(v[0][w], v[1][w], sel), hi = __byte_perm(v[2][w], v[3][w], sel);
-                            const uint32_t af[4] = {e4m3x2_to_f16x2((uint16_t)lo), e4m3x2_to_f16x2((uint16_t)(lo >> 16)),
-                                                    e4m3x2_to_f16x2((uint16_t)hi), e4m3x2_to_f16x2((uint16_t)(hi >> 16))};
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                mma_16816<H>(o[j * 8 + w * 2 + half][nt], af, pf[nt][0], pf[nt][1]);
+                        for (int x = 0; x < 4; ++x) {
+                            const int r = tb * kRows + 2 * q4 + (x & 1) + (x >> 1) * 8;
+                            if constexpr (DP == 64) {
+                                const uint2 u = lds64(vs_s + r * S::kRow + value_chunk<E4M3, CH>(r, g >> 1) * 16 + (g & 1) * 8);
+                                v[x][0] = u.x; v[x][1] = u.y;
+                            } else {
+                                const uint4 u = lds128(vs_s + r * S::kRow + value_chunk<E4M3, CH>(r, j * 8 + g) * 16);
+                                v[x][0] = u.x; v[x][1] = u.y; v[x][2] = u.z; v[x][3] = u.w;
+                            }
                         }
+#pragma unroll
+                        for (int w = 0; w < WORDS; ++w)
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                const uint32_t sel = half ? 0x7362 : 0x5140;
+                                const uint32_t lo = __byte_perm(v[0][w], v[1][w], sel), hi = __byte_perm(v[2][w], v[3][w], sel);
+                                const uint32_t af[4] = {e4m3x2_to_f16x2((uint16_t)lo), e4m3x2_to_f16x2((uint16_t)(lo >> 16)),
+                                                        e4m3x2_to_f16x2((uint16_t)hi), e4m3x2_to_f16x2((uint16_t)(hi >> 16))};
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+                                    mma_16816<H>(o[j * 8 + w * 2 + half][nt], af, pf[tb][nt][0], pf[tb][nt][1]);
+                            }
+                    }
                 }
             }
 
@@ -813,7 +855,7 @@ __global__ void __launch_bounds__(128, 8) join_kernel(const AttnParams p) {
     __shared__ float part_m[128], part_l[128];
     __shared__ float4 part_o[128];
     const int x = blockIdx.x, tid = threadIdx.x, D = p.cache.D;
-    Numbering<4> steps;
+    Numbering<4, S::kStep> steps;
     steps.count(p, first_sm, sums);
     const Ranges ranges(steps.total, gridDim.x * W);
     const int lo = ranges.start(x * W), hi = ranges.start(x * W + W);
@@ -824,7 +866,7 @@ __global__ void __launch_bounds__(128, 8) join_kernel(const AttnParams p) {
     if (hi > lo) {
         int first;
         b = steps.find(p, first_sm, at, &first);
-        const int each = steps_of(p, checked_length(p, b)) + kUnitCost;
+        const int each = steps_of<S::kStep>(p, checked_length(p, b)) + kUnitCost;
         u = (at - first) / each;
         const int unit_lo = first + u * each + kUnitCost, unit_hi = first + (u + 1) * each;
         if (k == 0 ? unit_lo < lo : unit_lo >= lo && unit_lo < hi && unit_hi > hi) {
@@ -894,15 +936,15 @@ template <bool F16, bool E4M3, int DP, int NT>
 nvfp4_status launch_attention(AttnParams p, void* workspace, cudaStream_t stream) {
     using S = Shape<E4M3, DP, NT>;
     const char* fn = "nvfp4_paged_attention";
-    const int64_t most = (int64_t)p.B * p.units * (ceil_div((int64_t)p.width * p.cache.page_size, kStep) + 1 + kUnitCost);
+    const int64_t most = (int64_t)p.B * p.units * (ceil_div((int64_t)p.width * p.cache.page_size, S::kStep) + 1 + kUnitCost);
     if (most > INT32_MAX)
-        return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s: %lld steps of 16 tokens and heads in one call, above 2^31", fn, (long long)most);
+        return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s: %lld steps of tokens and heads in one call, above 2^31", fn, (long long)most);
     // Short units are not split between blocks: there is nothing to join after the
     // kernel.  (8 sequences of 128 tokens 7.0 us and one launch against 8.0 and two; at
     // 500 tokens, 31 steps, splitting wins, 9.2 against 10.4 us.)
     int64_t tokens = (int64_t)p.width * p.cache.page_size;
-    if (p.window > 0) tokens = std::min<int64_t>(tokens, (int64_t)p.window + kStep);
-    p.whole_units = ceil_div(tokens, kStep) <= kWholeUnit;
+    if (p.window > 0) tokens = std::min<int64_t>(tokens, (int64_t)p.window + S::kStep);
+    p.whole_units = tokens <= kWholeUnit;
     // as many blocks as the longest lengths could use, at most one wave
     const int64_t use = p.whole_units ? (int64_t)p.B * p.units : ceil_div(most, S::kWarps);
     const int ctas = (int)std::max<int64_t>(1, std::min<int64_t>(sm_count(), use));
@@ -994,7 +1036,7 @@ extern "C" nvfp4_status nvfp4_paged_attention(const void* q, int64_t q_row_strid
     p.units = p.cache.heads * p.chunks;
     p.window = (int)std::min<int64_t>(window, INT32_MAX);
     p.scale_log2 = softmax_scale * 1.44269504088896341f;
-    p.whole_pages = p.cache.page_size % kStep == 0;
+    p.whole_pages = p.cache.page_size % kRows == 0;
     cudaStream_t s = (cudaStream_t)stream;
     if (p.cache.e4m3) return f16 ? launch_shape<true, true>(p, DP, NT, workspace, s) : launch_shape<false, true>(p, DP, NT, workspace, s);
     return f16 ? launch_shape<true, false>(p, DP, NT, workspace, s) : launch_shape<false, false>(p, DP, NT, workspace, s);
