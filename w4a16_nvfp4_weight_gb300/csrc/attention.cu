@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
     float* const warp_parts = p.parts + (size_t)gridDim.x * 2 * S::kPart;
     int head_unit = -1, tail_unit = -1;
 
-    Place<STEP> c;                                                    // the step to compute
+    Place<STEP> c;                                              // the step to compute
     int at_c = e, unit_first = 0;                               // its number, and that of its unit's first step
     if (a < e) {
         c.b = steps.find(p, first_sm, a, &unit_first);
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
         at_c = unit_first + x;
     }
     if (at_c < e) {
-        Place<STEP> f = c;                                            // the next step to copy
+        Place<STEP> f = c;                                      // the next step to copy
         int at_f = at_c;
 
         // Table entries [base, base + 64) of sequence window_b, two a lane.  The second

@@ -22,20 +22,31 @@ struct NormParams {
     void* y;
     float* scales;                 // null: 16-bit output
     int64_t T, H, x_stride, res_stride;
-    int64_t group;                 // columns of one scale (H: one a row)
+    int64_t group, groups;         // columns of one scale (H: one a row), scales a row
+    int lanes_log2;                // groups of 16 to 256 columns: threads of one, eight columns each
     float eps;
 };
 
 template <bool MAX>
 __device__ __forceinline__ float join(float a, float b) { return MAX ? fmaxf(a, b) : a + b; }
 
-// Reduction over groups of `lanes` neighbouring lanes (a power of two).
+// Reduction over a warp.
 template <bool MAX>
-__device__ __forceinline__ float lane_reduce(float v, int lanes = 32) {
+__device__ __forceinline__ float lane_reduce(float v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        if (o < lanes) v = join<MAX>(v, __shfl_xor_sync(0xffffffffu, v, o));
+    for (int o = 16; o > 0; o >>= 1) v = join<MAX>(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
+}
+
+// The largest of each of V values over groups of 2^log2 neighbouring lanes.
+template <int V>
+__device__ __forceinline__ void group_max(float (&v)[V], int log2) {
+#pragma unroll
+    for (int k = 0; k < 5; ++k) {
+        if (k >= log2) break;
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = fmaxf(v[i], __shfl_xor_sync(0xffffffffu, v[i], 1 << k));
+    }
 }
 
 // Reduction over the threads of a row; every thread gets the result.  `sm` holds
@@ -131,7 +142,6 @@ __global__ void __launch_bounds__(norm_threads(V)) norm_rows_kernel(const NormPa
         }
     } else {
         const bool by_row = p.group == p.H;
-        const int lanes = by_row ? 32 : (int)(p.group / 8);       // threads of one scale
         float amax[V], top = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -144,13 +154,14 @@ __global__ void __launch_bounds__(norm_threads(V)) norm_rows_kernel(const NormPa
             top = fmaxf(top, amax[i]);
         }
         if (by_row) top = row_reduce<true>(top, sm[1]);
-        const int64_t groups = p.H / p.group;
+        else group_max<V>(amax, p.lanes_log2);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int c = i * blockDim.x + threadIdx.x;
-            const float s = e4m3_scale(by_row ? top : lane_reduce<true>(amax[i], lanes)), inv = e4m3_inverse(s);
+            const float s = e4m3_scale(by_row ? top : amax[i]), inv = e4m3_inverse(s);
             if (c >= pieces) continue;
-            if (by_row ? c == 0 : threadIdx.x % lanes == 0) p.scales[t * groups + (by_row ? 0 : c / lanes)] = s;
+            if (by_row ? c == 0 : (threadIdx.x & ((1 << p.lanes_log2) - 1)) == 0)
+                p.scales[t * p.groups + (by_row ? 0 : c >> p.lanes_log2)] = s;
             const F2 minus_s = make_f2(-s, -s), inv2 = make_f2(inv, inv);
             const uint32_t o0 = e4m3_codes(y[i][0], minus_s, inv2), o1 = e4m3_codes(y[i][1], minus_s, inv2);
             const uint32_t o2 = e4m3_codes(y[i][2], minus_s, inv2), o3 = e4m3_codes(y[i][3], minus_s, inv2);
@@ -278,13 +289,12 @@ __global__ void __launch_bounds__(1024) norm_any_kernel(const NormParams p) {
         for (int64_t i = threadIdx.x; i < p.H; i += blockDim.x) y[i] = e4m3_code(value(i), s, inv);
         return;
     }
-    const int64_t groups = p.H / p.group;              // a warp takes a group at a time
-    const int lane = threadIdx.x & 31;
-    for (int64_t g = threadIdx.x >> 5; g < groups; g += blockDim.x >> 5) {
+    const int lane = threadIdx.x & 31;                 // a warp takes a group at a time
+    for (int64_t g = threadIdx.x >> 5; g < p.groups; g += blockDim.x >> 5) {
         float amax = 0.f;
         for (int64_t i = g * p.group + lane; i < (g + 1) * p.group; i += 32) amax = fmaxf(amax, fabsf(value(i)));
         const float s = e4m3_scale(lane_reduce<true>(amax)), inv = e4m3_inverse(s);
-        if (lane == 0) p.scales[t * groups + g] = s;
+        if (lane == 0) p.scales[t * p.groups + g] = s;
         for (int64_t i = g * p.group + lane; i < (g + 1) * p.group; i += 32)
             y[i] = e4m3_code(value(i), s, inv);
     }
@@ -321,7 +331,7 @@ nvfp4_status launch_norm(const NormParams& p, bool f16, cudaStream_t stream) {
     if (rows) {
         // Rows that fill the GPU take several pieces a thread: loads in flight, few
         // threads to join and fewer scales' divisions (8192x8192: one 84.6 us, two 79.3,
-        // four 80.4; with E4M3 output 4096x5120: two 24.6, four 23.1, eight 36.7).  Few
+        // four 80.4; with E4M3 output 8192x8192: two 85, four 73.3).  Few
         // rows take as many threads as they have pieces, for the shortest way through one.
         int V = p.T <= sm_count() * 2 ? 1 : e4m3 ? 4 : 2;
         while (pieces > norm_threads(V) * V) V *= 2;
@@ -385,6 +395,7 @@ extern "C" nvfp4_status nvfp4_rms_norm(const void* X, int64_t x_stride, const vo
     p.x = (const uint16_t*)X; p.residual = (const uint16_t*)residual; p.weight = (const uint16_t*)weight;
     p.residual_out = (uint16_t*)residual_out; p.y = Y; p.scales = e4m3 ? scales : nullptr;
     p.T = T; p.H = H; p.x_stride = x_stride; p.res_stride = residual_stride;
-    p.group = group ? group : H; p.eps = eps;
+    p.group = group ? group : H; p.groups = H / p.group; p.eps = eps;
+    for (p.lanes_log2 = 0; group > 8 << p.lanes_log2;) ++p.lanes_log2;
     return launch_norm(p, f16 != 0, (cudaStream_t)stream);
 }
