@@ -401,14 +401,13 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
         // Table entries [base, base + 64) of sequence window_b, two a lane.  The second
         // half is loaded when the first is entered, long before it is needed.
         int near = 0, far = 0, base = 0, window_b = -1;
-        auto entry = [&](int t) { return p.cache.page_shift >= 0 ? t >> p.cache.page_shift : t / p.cache.page_size; };
         auto load_entries = [&](int i) {
-            return i <= entry(f.n - 1) ? p.block_table[f.b * p.table_stride + i] : 0;
+            return i <= p.cache.entry(f.n - 1) ? p.block_table[f.b * p.table_stride + i] : 0;
         };
         const int held_chunks = D * (E4M3 ? 1 : 2) / 16, r0 = lane / CH, c0 = lane % CH;
         auto copy = [&](int stage) {
             const uint32_t dst = ring_s + stage * S::kStage;
-            const int s0 = f.step * STEP, i0 = entry(max(s0, f.lo));
+            const int s0 = f.step * STEP, i0 = p.cache.entry(max(s0, f.lo));
             if (f.b != window_b || i0 < base || i0 >= base + 64) {
                 window_b = f.b;
                 base = i0;
@@ -420,7 +419,7 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
                 far = load_entries(base + 32 + lane);
             }
             // the page and place of token lane % STEP; those not held take a neighbour's
-            const int t = min(max(s0 + (lane & (STEP - 1)), f.lo), f.n - 1), i = entry(t);
+            const int t = min(max(s0 + (lane & (STEP - 1)), f.lo), f.n - 1), i = p.cache.entry(t);
             const int n0 = __shfl_sync(0xffffffffu, near, (i - base) & 31), n1 = __shfl_sync(0xffffffffu, far, (i - base) & 31);
             int page = i - base < 32 ? n0 : n1;
             if ((uint32_t)page >= (uint32_t)p.cache.num_pages) {

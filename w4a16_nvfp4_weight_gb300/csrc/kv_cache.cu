@@ -47,6 +47,8 @@ nvfp4_status check_cache(const char* fn, const nvfp4_kv_cache* c, CacheView* vie
     view->page_shift = -1;
     for (int i = 0; i <= 20; ++i)
         if (view->page_size == 1 << i) view->page_shift = i;
+    for (view->page_mul_shift = 0; 2 << view->page_mul_shift < view->page_size;) ++view->page_mul_shift;
+    view->page_mul = (uint32_t)(((1ull << (32 + view->page_mul_shift)) + c->page_size - 1) / c->page_size);
     view->e4m3 = e4m3;
     return NVFP4_OK;
 }

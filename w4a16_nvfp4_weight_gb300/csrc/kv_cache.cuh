@@ -17,12 +17,21 @@ struct CacheView {
     int64_t page_bytes, head_bytes, token_bytes;
     int page_size, heads, D;
     int page_shift;                // log2(page_size), or -1
+    uint32_t page_mul;             // where that is -1: 2^(32 + page_mul_shift) / page_size, rounded up
+    int page_mul_shift;
     bool e4m3;
+
+    // t / page_size for t < 2^31, by a product (Granlund and Montgomery, PLDI 1994): page_mul
+    // is above the quotient by less than page_size <= 2^(page_mul_shift + 1), in units of
+    // 2^-(32 + page_mul_shift) / page_size, which t < 2^31 cannot carry to the next integer.
+    __device__ int entry(int t) const {
+        return page_shift >= 0 ? t >> page_shift : (int)(__umulhi((uint32_t)t, page_mul) >> page_mul_shift);
+    }
 
     // Page and place of a slot below num_slots (a 64-bit division only where nothing shorter will do).
     __device__ void split(int64_t slot, int64_t* page, int* at) const {
         if (page_shift >= 0) *page = slot >> page_shift;
-        else if (num_slots <= INT32_MAX) *page = (int32_t)slot / page_size;
+        else if (num_slots <= INT32_MAX) *page = entry((int32_t)slot);
         else *page = slot / page_size;
         *at = (int)(slot - *page * page_size);
     }
