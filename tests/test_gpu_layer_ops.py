@@ -461,6 +461,21 @@ def test_paged_attention_strided_query_and_large_queries(kind):
                        nv.paged_attention(case[1].contiguous(), block_table=case[2], lengths=case[3], **case[0]))
 
 
+@pytest.mark.parametrize("kind", ["16", "e4m3"])
+@pytest.mark.parametrize("step", [0.02, 0.4, -0.4, 30.0])
+def test_paged_attention_of_scores_that_rise_or_fall_with_the_tokens(kind, step):
+    """The base of the exponentials lags behind a rising maximum, or never moves."""
+    c, q, table, lengths, slots = _attention_case([1500, 400, 17], 8, 2, 64, 16, "bf16", kind, 83)
+    q = torch.zeros_like(q)
+    q[:, :, 0] = 1.0
+    T = slots.numel()
+    k = torch.zeros(T, 2, 64, dtype=torch.bfloat16, device="cuda")
+    k[:, :, 0] = torch.cat([torch.arange(n) for n in lengths.tolist()]).cuda()[:, None] * step
+    v = _randn(_gen(84), (T, 2, 64), "bf16")
+    nv.rope_cache_write(k, k, v, slots, nv.rope_table(1, 0), slots=slots, **c)
+    _check_attention(c, q, table, lengths, slots, 16, "bf16", kind, scale=1.0)
+
+
 @pytest.mark.parametrize("all_zero", [True, False])
 def test_paged_attention_of_values_whose_scale_is_zero(all_zero):
     """Rows of zeros (a scale of 0 is no scale the write gives) weigh as others do."""

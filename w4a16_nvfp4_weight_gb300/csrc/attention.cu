@@ -3,7 +3,7 @@
 // For query head h of sequence b, with n = lengths[b] cached tokens:
 //     z_j = softmax_scale * q . k_j   for max(0, n - window) <= j < n,
 //     out = sum_j exp(z_j - lse) v_j,   lse = log sum_j exp(z_j),
-// in one pass over the cache: a running maximum m, l = sum exp(z - m) and
+// in one pass over the cache: a running base m near the maximum, l = sum exp(z - m) and
 // o = sum exp(z - m) v, all in 32 bits; two passes over different tokens join as
 //     m = max(m1, m2),  l = l1 exp(m1 - m) + l2 exp(m2 - m),  o likewise.
 // A row with no token gives out = 0 and lse = -infinity.
@@ -33,7 +33,7 @@
 // FP16 for FP16 and E4M3.  E4M3 codes are exact in FP16; a BF16 query meets them
 // as FP16 after a power of two that puts its largest element at 2^14 (elements
 // below 2^-28 of it lose bits).  The scale of a value row is multiplied into its weight,
-// whose running maximum is taken over z + log2(scale), so that it fits FP16.
+// whose base is taken over z + log2(scale), so that it fits FP16.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -49,6 +49,10 @@ namespace {
 
 constexpr int kRows = 16;          // tokens of an MMA; a step has one or two blocks of so many
 constexpr int kWholeUnit = 256;    // units of at most so many tokens are not split between blocks
+// Scores may pass the base of their exponentials, the largest score when it was taken, by
+// so many powers of two before a new one is taken: weights up to 2^4 lose nothing in 16
+// bits, and most steps need no maximum over the warp and no rescaling.
+constexpr float kSlack = 4.f;
 constexpr int kUnitCost = 4;       // steps' worth of time that the start and end of a unit take
 constexpr size_t kMaxSmem = 227 * 1024;
 
@@ -307,8 +311,10 @@ struct Numbering {
     // The sequence that holds number x < total, and its first number (a whole warp asks).
     __device__ __forceinline__ int find(const AttnParams& p, const int* sm, int x, int* first) const {
         int t = -1;
-#pragma unroll 4
-        for (int k = 0; k < WARPS * 32; k += 32) t += __popc(__ballot_sync(0xffffffffu, sm[k + (threadIdx.x & 31)] <= x));
+        for (int k = 0, c = 32; k < WARPS * 32 && c == 32; k += 32) {       // ascending: up to the first one above
+            c = __popc(__ballot_sync(0xffffffffu, sm[k + (threadIdx.x & 31)] <= x));
+            t += c;
+        }
         int b = t * per, at = sm[t];
         for (int n; per > 1 && x >= at + (n = numbers_of<STEP>(p, b)); ++b) at += n;
         *first = at;
@@ -594,60 +600,67 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
                     if (E4M3) {
                         k_by[tb][y] = lds_f32(ks_s + 2 * S::kTile + row * 4);
                         v_by[tb][y] = lds_f32(ks_s + 2 * S::kTile + (STEP + row) * 4);
-                        // a power of two above the scale: weights times scales stay below 1.  At least
-                        // 2^-99, above the least scale that is written: a scale of zero leaves l finite.
-                        lv[tb][y] = (float)max((int)((__float_as_uint(v_by[tb][y]) >> 23) & 255) - 126, -99);
+                        // a power of two above the scale: weights times scales stay below 2^kSlack.
+                        // At least 2^-95, so that scales next to zero leave l finite.
+                        lv[tb][y] = (float)max((int)((__float_as_uint(v_by[tb][y]) >> 23) & 255) - 126, -95);
                     }
                 }
-            uint32_t pf[TB][NT][2];
-            float keep[NT][2];
-            bool grown = false;
+            float top[NT][2];
+            bool above = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float s[TB][4], w[TB][4];
 #pragma unroll
                 for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        s[tb][x] = (NT == 1 ? z[tb][nt][x] + z2[tb][nt][x] : z[tb][nt][x]) * qs[nt][x & 1];
-                        if (E4M3) s[tb][x] *= k_by[tb][x >> 1];
-                        if (!held[tb][x >> 1]) s[tb][x] = -INFINITY;
+                        float& s = z[tb][nt][x];
+                        s = (NT == 1 ? s + z2[tb][nt][x] : s) * qs[nt][x & 1];
+                        if (E4M3) s *= k_by[tb][x >> 1];
+                        if (!held[tb][x >> 1]) s = -INFINITY;
                     }
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    float top = fmaxf(s[0][x] + lv[0][0], s[0][x + 2] + lv[0][1]);
-                    if constexpr (TB == 2) top = fmaxf(top, fmaxf(s[TB - 1][x] + lv[TB - 1][0], s[TB - 1][x + 2] + lv[TB - 1][1]));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                    const float to = fmaxf(m[nt][x], top);
-                    const float base = to == -INFINITY ? 0.f : to;
-                    keep[nt][x] = ex2(m[nt][x] - base);
-                    grown |= to > m[nt][x];
-                    m[nt][x] = to;
-                    float sum = 0.f;
-#pragma unroll
-                    for (int tb = 0; tb < TB; ++tb) {
-                        w[tb][x] = ex2(s[tb][x] - base);
-                        w[tb][x + 2] = ex2(s[tb][x + 2] - base);
-                        sum = tb == 0 ? w[tb][x] + w[tb][x + 2] : sum + (w[tb][x] + w[tb][x + 2]);
-                    }
-                    l[nt][x] = l[nt][x] * keep[nt][x] + sum;
-                }
-                // heads on the MMA's columns: transpose the 8x8 blocks
-#pragma unroll
-                for (int tb = 0; tb < TB; ++tb) {
-                    pf[tb][nt][0] = movmatrix(f32_to_act2<H>(w[tb][0] * v_by[tb][0], w[tb][1] * v_by[tb][0]));
-                    pf[tb][nt][1] = movmatrix(f32_to_act2<H>(w[tb][2] * v_by[tb][1], w[tb][3] * v_by[tb][1]));
+                    top[nt][x] = fmaxf(z[0][nt][x] + lv[0][0], z[0][nt][x + 2] + lv[0][1]);
+                    if constexpr (TB == 2)
+                        top[nt][x] = fmaxf(top[nt][x], fmaxf(z[TB - 1][nt][x] + lv[TB - 1][0], z[TB - 1][nt][x + 2] + lv[TB - 1][1]));
+                    above |= top[nt][x] > m[nt][x] + kSlack;
                 }
             }
-            if (__any_sync(0xffffffffu, grown)) {
+            if (__any_sync(0xffffffffu, above)) {               // a new base: seldom after the first steps
 #pragma unroll
-                for (int mt = 0; mt < KS; ++mt)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int x = 0; x < 2; ++x) {
+                        float to = top[nt][x];
+                        to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 4));
+                        to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 8));
+                        to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 16));
+                        to = fmaxf(m[nt][x], to);
+                        const float keep = ex2(m[nt][x] - (to == -INFINITY ? 0.f : to));
+                        m[nt][x] = to;
+                        l[nt][x] *= keep;
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) o[mt][nt][x] *= keep[nt][x & 1];
+                        for (int mt = 0; mt < KS; ++mt) {
+                            o[mt][nt][x] *= keep;
+                            o[mt][nt][x + 2] *= keep;
+                        }
+                    }
+            }
+            uint32_t pf[TB][NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float base[2] = {m[nt][0] == -INFINITY ? 0.f : m[nt][0], m[nt][1] == -INFINITY ? 0.f : m[nt][1]};
+#pragma unroll
+                for (int tb = 0; tb < TB; ++tb) {
+                    float w[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) w[x] = ex2(z[tb][nt][x] - base[x & 1]);
+                    l[nt][0] += w[0] + w[2];
+                    l[nt][1] += w[1] + w[3];
+                    // heads on the MMA's columns: transpose the 8x8 blocks
+                    pf[tb][nt][0] = movmatrix(f32_to_act2<H>(w[0] * v_by[tb][0], w[1] * v_by[tb][0]));
+                    pf[tb][nt][1] = movmatrix(f32_to_act2<H>(w[2] * v_by[tb][1], w[3] * v_by[tb][1]));
+                }
             }
 
             // ---- output of 16 dimensions (rows) x 8 heads at a time
