@@ -64,6 +64,9 @@ __device__ __forceinline__ float row_reduce(float v, float* sm) {
 
 // Threads of a row at most: V pieces a thread have to fit in the registers.
 constexpr int norm_threads(int V) { return V == 1 ? 1024 : 512; }
+// Blocks of so many that an SM holds at least, by 64 registers a thread for four pieces
+// (69 without the limit: 8192x8192 to E4M3 74.4 us, with it 71.7).
+constexpr int norm_blocks(int V) { return V == 4 ? 2 : 1; }
 
 // Rows of 16-byte pieces: a row's threads keep it in registers, V pieces of 8
 // elements each, so that it is read once.
@@ -71,10 +74,9 @@ constexpr int norm_threads(int V) { return V == 1 ? 1024 : 512; }
 // out), all loads issued before the first use, and the weights' (from L2) before
 // the one barrier of the sum: 8192x8192 in 79.2 us (6.8 TB/s), 4096x5120 to E4M3 in
 // 22.9 (6.4).  The E4M3 output is not far from its instructions' time: values are kept
-// for both of its passes, and computed in pairs.  Four pieces a thread keep to 64
-// registers, for 1024 threads an SM (69 without the limit: 23.5; 4096x16384 83.2, with it 79.6).
+// for both of its passes, and computed in pairs.
 template <bool F16, bool E4M3, int V>
-__global__ void __launch_bounds__(norm_threads(V), V == 4 ? 2 : 1) norm_rows_kernel(const NormParams p) {
+__global__ void __launch_bounds__(norm_threads(V), norm_blocks(V)) norm_rows_kernel(const NormParams p) {
     __shared__ float sm[2][32];
     pdl_wait_previous();
     pdl_launch_dependents();
@@ -306,7 +308,6 @@ template <bool F16>
 const void* rows_kernel(bool e4m3, int V) {
     switch (V) {
         case 1: return e4m3 ? (const void*)norm_rows_kernel<F16, true, 1> : (const void*)norm_rows_kernel<F16, false, 1>;
-        case 2: return e4m3 ? (const void*)norm_rows_kernel<F16, true, 2> : (const void*)norm_rows_kernel<F16, false, 2>;
         case 4: return e4m3 ? (const void*)norm_rows_kernel<F16, true, 4> : (const void*)norm_rows_kernel<F16, false, 4>;
         default: return e4m3 ? (const void*)norm_rows_kernel<F16, true, 8> : (const void*)norm_rows_kernel<F16, false, 8>;
     }
@@ -331,12 +332,12 @@ nvfp4_status launch_norm(const NormParams& p, bool f16, cudaStream_t stream) {
     const void* kernel = f16 ? (const void*)norm_any_kernel<true> : (const void*)norm_any_kernel<false>;
     dim3 block(p.H > 4096 ? 1024 : 256);
     if (rows) {
-        // Rows that fill the GPU take several pieces a thread: loads in flight, few
-        // threads to join and fewer scales' divisions (8192x8192: one 84.6 us, two 79.3,
-        // four 80.4; with E4M3 output 8192x8192: two 85, four 73.3).  Few
-        // rows take as many threads as they have pieces, for the shortest way through one.
-        int V = p.T <= sm_count() * 2 ? 1 : e4m3 ? 4 : 2;
-        while (pieces > norm_threads(V) * V) V *= 2;
+        // Rows that fill the GPU take four pieces a thread: loads in flight, few threads
+        // to join and few scales' quotients (8192x8192: one 84.6 us, two 78.5, four 78.9;
+        // 500x4096 two 3.5, four 3.0; 8192x8192 to E4M3 two 85, four 71.7).  Few rows take
+        // as many threads as they have pieces, for the shortest way through one.
+        int V = p.T <= sm_count() * 2 ? 1 : 4;
+        while (pieces > norm_threads(V) * V) V = V == 1 ? 4 : 8;
         block = dim3((unsigned)round_up(ceil_div(pieces, V), 32));
         kernel = f16 ? rows_kernel<true>(e4m3, V) : rows_kernel<false>(e4m3, V);
     } else if (p.group == p.H) {
