@@ -51,7 +51,8 @@ constexpr int kRows = 16;          // tokens of an MMA; a step has one or two bl
 constexpr int kWholeUnit = 256;    // units of at most so many tokens are not split between blocks
 // Scores may pass the base of their exponentials, the largest score when it was taken, by
 // so many powers of two before a new one is taken: weights up to 2^4 lose nothing in 16
-// bits, and most steps need no maximum over the warp and no rescaling.
+// bits, and most steps need no maximum over the warp and no rescaling (64 x 8192 E4M3
+// tokens, 16 query heads a key head: 237 us, without 244; of 256 and 16 bits 750, 765).
 constexpr float kSlack = 4.f;
 constexpr int kUnitCost = 4;       // steps' worth of time that the start and end of a unit take
 constexpr size_t kMaxSmem = 227 * 1024;
@@ -79,8 +80,8 @@ struct AttnParams {
 // block an SM) and steps in a warp's ring.  As many bytes in flight as shared
 // memory holds, and as many warps as that and the registers leave: steps of 4 KB
 // need sixteen to be computed as fast as they come.  E4M3 rows of 128 with two head
-// tiles take twelve warps and four steps each: 129 us for 16 x 16384 tokens, 96 query
-// and 8 key heads (BF16 query; eight warps and six steps: 138), 29.8 against 28.4 at 2048.
+// tiles take twelve warps and four steps each: 122 us for 16 x 16384 tokens, 96 query
+// and 8 key heads (BF16 query; eight warps and six steps: 130), 28.2 against 26.7 at 2048.
 constexpr int attn_warps(int row, int values) { return row > 256 ? 4 : row > 128 ? 8 : values >= 64 ? 12 : 16; }
 constexpr int attn_stages(int row, int values) { return row == 128 && values >= 64 ? 4 : 3; }
 
@@ -91,7 +92,7 @@ struct Shape {
     static constexpr int kChunks = kRow / 16;                   // 16-byte chunks a row
     // Blocks of 16 tokens a step: 2 KB leave most of a step's instructions to finding its
     // pages and to the softmax, which a second block shares (64 x 8192 tokens, 32 query
-    // and 8 key heads of 64: 100 us; one block 131).  Longer rows have no room for it.
+    // and 8 key heads of 64: 98 us; one block 129).  Longer rows have no room for it.
     static constexpr int kBlocks = kRow == 64 ? 2 : 1;
     static constexpr int kStep = kRows * kBlocks;
     static constexpr int kTile = kStep * kRow;
@@ -952,8 +953,8 @@ nvfp4_status launch_attention(AttnParams p, void* workspace, cudaStream_t stream
     if (most > INT32_MAX)
         return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s: %lld steps of tokens and heads in one call, above 2^31", fn, (long long)most);
     // Short units are not split between blocks: there is nothing to join after the
-    // kernel.  (8 sequences of 128 tokens 7.0 us and one launch against 8.0 and two; at
-    // 500 tokens, 31 steps, splitting wins, 9.2 against 10.4 us.)
+    // kernel.  (8 sequences of 128 tokens 6.2 us and one launch against 6.8 and two; at
+    // 500 tokens, 31 steps, splitting wins, 8.6 against 9.2 us.)
     int64_t tokens = (int64_t)p.width * p.cache.page_size;
     if (p.window > 0) tokens = std::min<int64_t>(tokens, (int64_t)p.window + S::kStep);
     p.whole_units = tokens <= kWholeUnit;
