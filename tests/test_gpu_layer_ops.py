@@ -613,3 +613,95 @@ def test_refusals():
     assert write(q=q[:0], k=kv[:0], v=kv[:0], pos=slots[:0], slots=slots[:0]).shape == (0, 8, 64)
     assert nv.cache_read(slots=slots[:0], **c)[0].shape == (0, 2, 64)
     gu.check_device_status()
+
+
+def _far_token_case(act, kind, gap, spread, at, n=40000, B=320, Hkv=8, D=64, page=64):
+    """One token `gap` above the rest in score, B sequences over the same pages: with as many
+    (sequence, head) units as warps, a warp has the far token and thousands of others.  The
+    far token's value is zero, from an E4M3 cache zero but for its first dimension."""
+    g = _gen(int(gap) * 10 + at % 7 + (kind == "e4m3"))
+    c = _make_cache(-(-n // page), Hkv, page, D, act, kind)
+    k = torch.zeros(n, Hkv, D, device="cuda")
+    k[:, :, 0] = spread * torch.randn(n, Hkv, generator=g, device="cuda")
+    k[at, :, 0] = gap
+    v = 1 + 0.1 * torch.randn(n, Hkv, D, generator=g, device="cuda")
+    v[at] = 0
+    if kind == "e4m3":
+        v[at, :, 0] = 100.0
+    else:
+        v *= 1e4
+    slots = torch.arange(n, device="cuda")
+    k, v = k.to(DT[act]), v.to(DT[act])
+    nv.rope_cache_write(k, k, v, slots, nv.rope_table(1, 0), slots=slots, **c)
+    q = torch.zeros(B, Hkv, D, dtype=DT[act], device="cuda")
+    q[:, :, 0] = 1
+    table = torch.arange(-(-n // page), dtype=torch.int32, device="cuda").expand(B, -1).contiguous()
+    out, lse = nv.paged_attention(q, block_table=table, lengths=torch.full((B,), n, dtype=torch.int32, device="cuda"),
+                                  softmax_scale=1.0, return_lse=True, **c)
+    gu.check_device_status()
+    return c, slots, q, out, lse
+
+
+@pytest.mark.parametrize("at", [0, 19999])
+@pytest.mark.parametrize("spread", [0, 1])
+@pytest.mark.parametrize("gap", [14, 17, 20, 24, 28])
+@pytest.mark.parametrize("act", ["f16", "bf16"])
+def test_paged_attention_beside_a_far_token_whose_value_is_zero(act, gap, spread, at):
+    """The weights of the others keep their bits: a weight that meets the values as FP16 is
+    off by 2^-11 of itself, or by 2^-25 of a step whose largest is 2^-7 at least; of 16 such and values
+    0.5 to 1.5 times their mean, 2^-12 of the step's sum.  In the far token's own step 2^-36 of
+    its weight is where FP16 ends.  BF16 weights are off by 2^-8.  Scores and sums in 32
+    bits: 2^-12."""
+    n = 40000
+    c, slots, q, out, lse = _far_token_case(act, "16", gap, spread, at)
+    k, v = _cached_values(c, "k", slots, 64), _cached_values(c, "v", slots, 64)
+    ref, ref_lse, mag = layer.attend(_np(q[0]), k, v, 1.0)
+    near = np.exp(np.minimum(k[at // 16 * 16:at // 16 * 16 + 16, :, 0] - gap, 0.0))      # [16, Hkv]
+    lost = np.einsum("th,thd->hd", np.minimum(near, 2.0 ** -36), np.abs(v[at // 16 * 16:at // 16 * 16 + 16]))
+    bound = U[act] * np.abs(ref) + TINY[act] + (U[act] + 2.0 ** -11) * mag + (lost if act == "f16" else 0)
+    err = np.abs(_np(out) - ref[None])
+    assert np.all(err <= bound[None]), (err / bound[None]).max()
+    assert np.all(np.abs(_np(lse) - ref_lse[None]) <= 2.0 ** -17 * (1 + np.abs(ref_lse[None])))
+
+
+@pytest.mark.parametrize("gap", [8, 14, 16, 17])
+@pytest.mark.parametrize("act", ["f16", "bf16"])
+def test_paged_attention_beside_a_far_token_in_e4m3(act, gap):
+    """A weight times its value row's scale, as FP16, is off by 2^-11 of itself or by 2^-25 where
+    the largest such product is 2^10 at least (2^11 over the scale rounded up to a power of two),
+    which its codes, at most 448, multiply."""
+    c, slots, q, out, lse = _far_token_case(act, "e4m3", gap, 0, 0)
+    k, v = _cached_values(c, "k", slots, 64), _cached_values(c, "v", slots, 64)
+    ref, ref_lse, mag = layer.attend(_np(q[0]), k, v, 1.0)
+    s = c["v_scale"].transpose(1, 2).reshape(-1, 8)[slots].double().cpu().numpy()        # [n, Hkv]
+    w = np.exp(k[:, :, 0] - k[:, :, 0].max(0))
+    under = 2.0 ** -35 * (w * s).max(0) / w.sum(0) * (np.abs(v) / s[..., None]).sum(0).max(-1)
+    bound = U[act] * np.abs(ref) + TINY[act] + (U["f16"] + 2.0 ** -12) * mag + under[:, None]
+    err = np.abs(_np(out) - ref[None])
+    assert np.all(err <= bound[None]), (err / bound[None]).max()
+    assert np.all(np.abs(_np(lse) - ref_lse[None]) <= 2.0 ** -17 * (1 + np.abs(ref_lse[None])))
+
+
+@pytest.mark.parametrize("act,kind,G,D", [("f16", "16", 1, 64), ("f16", "16", 4, 128), ("f16", "16", 12, 128),
+                                          ("f16", "16", 16, 256), ("f16", "e4m3", 12, 64), ("bf16", "e4m3", 3, 128)])
+def test_paged_attention_of_scores_that_fall_far_and_rise_again(act, kind, G, D):
+    """Scores in stretches up to 60 apart, other ones for each head, one stretch after another:
+    bases that fall, rise and fall again, and pieces of different bases joined.  Weights lost
+    beside the stretches far above them are below 2^-36 of the largest each."""
+    n = 9000
+    case = _attention_case([n, 700], G * 2, 2, D, 16, act, kind, 85)
+    c, q, table, lengths, slots = case
+    g = _gen(86)
+    T = slots.numel()
+    level = torch.tensor([-3.0, 20, -25, 30, -30, 29, 5, -20, 30, 11], device="cuda")
+    k = torch.zeros(T, 2, D, device="cuda")
+    t = torch.cat([torch.arange(m) for m in lengths.tolist()]).cuda()
+    for j in range(8):                                     # dimension j has the levels shifted by j
+        k[:, :, j] = (level[(t // 137 + j) % 10] + torch.randn(T, generator=g, device="cuda"))[:, None]
+    v = _randn(g, (T, 2, D), act)
+    q = torch.zeros_like(q)
+    for h in range(G * 2):
+        q[:, h, h % 8] = 1
+    k = k.to(DT[act])
+    nv.rope_cache_write(k, k, v, slots, nv.rope_table(1, 0), slots=slots, **c)
+    _check_attention(c, q, table, lengths, slots, 16, act, kind, scale=1.0)

@@ -5,7 +5,8 @@
 //     out = sum_j exp(z_j - lse) v_j,   lse = log sum_j exp(z_j),
 // in one pass over the cache: a running base m near the maximum, l = sum exp(z - m) and
 // o = sum exp(z - m) v, all in 32 bits; two passes over different tokens join as
-//     m = max(m1, m2),  l = l1 exp(m1 - m) + l2 exp(m2 - m),  o likewise.
+//     m = max(m1, m2),  l = l1 exp(m1 - m) + l2 exp(m2 - m),  o likewise,
+// whatever the distance of each base from its largest score.
 // A row with no token gives out = 0 and lse = -infinity.
 //
 // Bound by the cache's bytes (2 G / element size flop a byte, G query heads a
@@ -30,7 +31,8 @@
 //    small kernel, in the order of the tokens: the result does not depend on timing.
 // Roundings: the softmax weights meet the values in the MMA as 16 bits, BF16 for
 // a BF16 cache (a relative 2^-8 of each weight, while l keeps the 32-bit ones),
-// FP16 for FP16 and E4M3.  E4M3 codes are exact in FP16; a BF16 query meets them
+// FP16 for FP16 and E4M3, 2^11 larger, so that a weight keeps its 11 bits down to 2^-25 of the
+// largest (and below, where the values are FP16: the base follows).  E4M3 codes are exact in FP16; a BF16 query meets them
 // as FP16 after a power of two that puts its largest element at 2^14 (elements
 // below 2^-28 of it lose bits).  The scale of a value row is multiplied into its weight,
 // whose base is taken over z + log2(scale), so that it fits FP16.
@@ -49,11 +51,27 @@ namespace {
 
 constexpr int kRows = 16;          // tokens of an MMA; a step has one or two blocks of so many
 constexpr int kWholeUnit = 256;    // units of at most so many tokens are not split between blocks
-// Scores may pass the base of their exponentials, the largest score when it was taken, by
-// so many powers of two before a new one is taken: weights up to 2^4 lose nothing in 16
-// bits, and most steps need no maximum over the warp and no rescaling (64 x 8192 E4M3
-// tokens, 16 query heads a key head: 237 us, without 244; of 256 and 16 bits 750, 765).
+// Scores may pass the base of their exponentials by so many powers of two more than the
+// largest score did when it was taken, before a new one is taken: most steps need no
+// maximum over the warp and no rescaling (64 x 8192 E4M3 tokens, 16 query heads a key
+// head: 237 us, without 244; of 256 and 16 bits 750, 765).
 constexpr float kSlack = 4.f;
+// Weights that meet the values as FP16 are taken over a base 2^11 below the largest score:
+// up to 2^15 with the slack, FP16's range used upwards, since downwards it ends at 2^-14
+// (2^-24 with fewer bits) and l, in 32 bits, counts what is lost there.  BF16 has the
+// range of 32 bits and needs none.
+constexpr float kLift = 11.f;
+// The scales of value rows that enter the base are at least this power of two, so that a
+// row next to zero, whose weight may then be 2^(kSlack + kLift) over its scale, leaves l finite.
+constexpr int kLeastScale = -84;
+// With FP16 values the base also follows the scores down: a head whose weights are all
+// below 2^kLow in a step takes that step's largest for its base, as far as l stays below
+// 2^kMostSum.  A token far above the others with a value next to zero (the first of a long
+// text, often) would else press their weights out of FP16: 24 nats above 8192 equal ones
+// they came out 23 % too small.  (E4M3 values bring their scale into the base, and such a token
+// does not raise it.)
+constexpr float kLow = -7.f;
+constexpr int kMostSum = 80;
 constexpr int kUnitCost = 4;       // steps' worth of time that the start and end of a unit take
 constexpr size_t kMaxSmem = 227 * 1024;
 
@@ -337,6 +355,8 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
     using S = Shape<E4M3, DP, NT>;
     constexpr int W = S::kWarps, CH = S::kChunks, KS = DP / 16, ST = S::kStages, TB = S::kBlocks, STEP = S::kStep;
     constexpr bool H = F16 || E4M3;                             // FP16 operands in the MMAs
+    constexpr bool FALLS = F16 && !E4M3;                        // the base may fall, too
+    constexpr float LIFT = H ? kLift : 0.f;
     extern __shared__ __align__(1024) uint8_t ring_all[];
     __shared__ int first_sm[W * 32], sums[W];
     // Pieces of units, two a warp: the rest of a unit that an earlier warp began, and the last of the range.
@@ -601,13 +621,13 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
                     if (E4M3) {
                         k_by[tb][y] = lds_f32(ks_s + 2 * S::kTile + row * 4);
                         v_by[tb][y] = lds_f32(ks_s + 2 * S::kTile + (STEP + row) * 4);
-                        // a power of two above the scale: weights times scales stay below 2^kSlack.
-                        // At least 2^-95, so that scales next to zero leave l finite.
-                        lv[tb][y] = (float)max((int)((__float_as_uint(v_by[tb][y]) >> 23) & 255) - 126, -95);
+                        // a power of two above the scale: weights times scales stay below 2^(kSlack + kLift)
+                        lv[tb][y] = (float)max((int)((__float_as_uint(v_by[tb][y]) >> 23) & 255) - 126, kLeastScale);
                     }
                 }
             float top[NT][2];
             bool above = false;
+            uint32_t low = 0xffffffffu;                         // by column: no weight of this lane reaches 2^kLow
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -624,10 +644,19 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
                     top[nt][x] = fmaxf(z[0][nt][x] + lv[0][0], z[0][nt][x + 2] + lv[0][1]);
                     if constexpr (TB == 2)
                         top[nt][x] = fmaxf(top[nt][x], fmaxf(z[TB - 1][nt][x] + lv[TB - 1][0], z[TB - 1][nt][x + 2] + lv[TB - 1][1]));
-                    above |= top[nt][x] > m[nt][x] + kSlack;
+                    above |= top[nt][x] > m[nt][x] + (kSlack + LIFT);
+                    if (FALLS && !(top[nt][x] < m[nt][x] + kLow)) low &= ~(1u << (nt * 8 + x) << 2 * q4);
                 }
             }
-            if (__any_sync(0xffffffffu, above)) {               // a new base: seldom after the first steps
+            bool rises;
+            if constexpr (FALLS) {                              // both votes in one
+                low = __reduce_and_sync(0xffffffffu, above ? low & 0x7fffffffu : low);
+                rises = !(low >> 31);
+                low &= (1u << NT * 8) - 1;
+            } else {
+                rises = __any_sync(0xffffffffu, above);
+            }
+            if (rises) {                                        // a new base: seldom after the first steps
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -636,7 +665,7 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
                         to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 4));
                         to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 8));
                         to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 16));
-                        to = fmaxf(m[nt][x], to);
+                        to = fmaxf(m[nt][x], to - LIFT);
                         const float keep = ex2(m[nt][x] - (to == -INFINITY ? 0.f : to));
                         m[nt][x] = to;
                         l[nt][x] *= keep;
@@ -644,6 +673,32 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
                         for (int mt = 0; mt < KS; ++mt) {
                             o[mt][nt][x] *= keep;
                             o[mt][nt][x + 2] *= keep;
+                        }
+                    }
+            }
+            if (FALLS && low != 0) {                            // a lower one: about once a token that is far above
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        float to = top[nt][x], sum = l[nt][x];
+#pragma unroll
+                        for (int lanes = 4; lanes < 32; lanes <<= 1) {
+                            to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, lanes));
+                            sum = fmaxf(sum, __shfl_xor_sync(0xffffffffu, sum, lanes));
+                        }
+                        // whole powers of two, by which l and o lose nothing
+                        const int room = kMostSum + 126 - (int)(__float_as_uint(sum) >> 23);
+                        const int by = min((int)fminf(m[nt][x] - (to - LIFT), 100.f), room);
+                        if ((low >> (nt * 8 + x) >> 2 * q4 & 1) && by > 0) {
+                            const float up = __uint_as_float((uint32_t)(127 + by) << 23);
+                            m[nt][x] -= (float)by;
+                            l[nt][x] *= up;
+#pragma unroll
+                            for (int mt = 0; mt < KS; ++mt) {
+                                o[mt][nt][x] *= up;
+                                o[mt][nt][x + 2] *= up;
+                            }
                         }
                     }
             }
