@@ -626,8 +626,7 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
                     }
                 }
             float top[NT][2];
-            bool above = false;
-            uint32_t low = 0xffffffffu;                         // by column: no weight of this lane reaches 2^kLow
+            bool above = false, below = false;                  // a score far above its base; all of a head's far below it
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -644,19 +643,14 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
                     top[nt][x] = fmaxf(z[0][nt][x] + lv[0][0], z[0][nt][x + 2] + lv[0][1]);
                     if constexpr (TB == 2)
                         top[nt][x] = fmaxf(top[nt][x], fmaxf(z[TB - 1][nt][x] + lv[TB - 1][0], z[TB - 1][nt][x + 2] + lv[TB - 1][1]));
-                    above |= top[nt][x] > m[nt][x] + (kSlack + LIFT);
-                    if (FALLS && !(top[nt][x] < m[nt][x] + kLow)) low &= ~(1u << (nt * 8 + x) << 2 * q4);
+                    const float by = top[nt][x] - m[nt][x];
+                    above |= by > kSlack + LIFT;
+                    if (FALLS) below |= by < kLow;
                 }
             }
-            bool rises;
-            if constexpr (FALLS) {                              // both votes in one
-                low = __reduce_and_sync(0xffffffffu, above ? low & 0x7fffffffu : low);
-                rises = !(low >> 31);
-                low &= (1u << NT * 8) - 1;
-            } else {
-                rises = __any_sync(0xffffffffu, above);
-            }
-            if (rises) {                                        // a new base: seldom after the first steps
+            // a new base: seldom after the first steps (with both signs, one vote where there is none)
+            const bool moves = __any_sync(0xffffffffu, above || below);
+            if (FALLS ? moves && __any_sync(0xffffffffu, above) : moves) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -676,31 +670,41 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
                         }
                     }
             }
-            if (FALLS && low != 0) {                            // a lower one: about once a token that is far above
+            if (FALLS && moves) {                               // a lower one: about once a token far above the others
+                uint32_t low = 0;                               // by column: no weight of this lane reaches 2^kLow
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        float to = top[nt][x], sum = l[nt][x];
+                    for (int x = 0; x < 2; ++x) low |= (uint32_t)(top[nt][x] - m[nt][x] < kLow) << (nt * 2 + x);
+                // ... and of none of the eight lanes of the same heads
 #pragma unroll
-                        for (int lanes = 4; lanes < 32; lanes <<= 1) {
-                            to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, lanes));
-                            sum = fmaxf(sum, __shfl_xor_sync(0xffffffffu, sum, lanes));
-                        }
-                        // whole powers of two, by which l and o lose nothing
-                        const int room = kMostSum + 126 - (int)(__float_as_uint(sum) >> 23);
-                        const int by = min((int)fminf(m[nt][x] - (to - LIFT), 100.f), room);
-                        if ((low >> (nt * 8 + x) >> 2 * q4 & 1) && by > 0) {
-                            const float up = __uint_as_float((uint32_t)(127 + by) << 23);
-                            m[nt][x] -= (float)by;
-                            l[nt][x] *= up;
+                for (int lanes = 4; lanes < 32; lanes <<= 1) low &= __shfl_xor_sync(0xffffffffu, low, lanes);
+                if (__any_sync(0xffffffffu, low != 0)) {
 #pragma unroll
-                            for (int mt = 0; mt < KS; ++mt) {
-                                o[mt][nt][x] *= up;
-                                o[mt][nt][x + 2] *= up;
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            float to = top[nt][x], sum = l[nt][x];
+#pragma unroll
+                            for (int lanes = 4; lanes < 32; lanes <<= 1) {
+                                to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, lanes));
+                                sum = fmaxf(sum, __shfl_xor_sync(0xffffffffu, sum, lanes));
+                            }
+                            // whole powers of two, by which l and o lose nothing
+                            const int room = kMostSum + 126 - (int)(__float_as_uint(sum) >> 23);
+                            const int by = min((int)fminf(m[nt][x] - (to - LIFT), 100.f), room);
+                            if ((low >> (nt * 2 + x) & 1) && by > 0) {
+                                const float up = __uint_as_float((uint32_t)(127 + by) << 23);
+                                m[nt][x] -= (float)by;
+                                l[nt][x] *= up;
+#pragma unroll
+                                for (int mt = 0; mt < KS; ++mt) {
+                                    o[mt][nt][x] *= up;
+                                    o[mt][nt][x + 2] *= up;
+                                }
                             }
                         }
-                    }
+                }
             }
             uint32_t pf[TB][NT][2];
 #pragma unroll
