@@ -705,3 +705,53 @@ def test_paged_attention_of_scores_that_fall_far_and_rise_again(act, kind, G, D)
     k = k.to(DT[act])
     nv.rope_cache_write(k, k, v, slots, nv.rope_table(1, 0), slots=slots, **c)
     _check_attention(c, q, table, lengths, slots, 16, act, kind, scale=1.0)
+
+
+def _half_step(x, act):
+    """Half the distance of neighbouring 16-bit values at x."""
+    _, e = np.frexp(x)
+    least, bits = (-126, 8) if act == "bf16" else (-14, 11)
+    return np.exp2(np.maximum(e - 1, least).astype(float) - bits)
+
+
+@pytest.mark.parametrize("gap", [0.3, 0.55, 0.8])
+@pytest.mark.parametrize("G,D", [(1, 64), (12, 64), (4, 128), (16, 128), (2, 256)])
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+def test_paged_attention_weights_keep_their_bits_over_16_bit_caches(act, G, D, gap):
+    """One token in 16 has a higher score, all others equal weights, values of one sign: a
+    rounding of the weights to 16 bits would move every output alike, by up to 2^-9
+    (BF16) or 2^-12.  As two halves the weights are off by 2^-16 at most, sums in 32 bits over a few
+    dozen steps and the exponentials by 2^-16: the rest is the output's one rounding."""
+    c, q, table, lengths, slots = _attention_case([1500, 400, 17], G * 2, 2, D, 16, act, "16", 87)
+    T = slots.numel()
+    k = torch.zeros(T, 2, D, dtype=DT[act], device="cuda")
+    t = torch.cat([torch.arange(m) for m in lengths.tolist()]).cuda()
+    k[:, :, 0] = (t % 16 == 0)[:, None] * gap
+    v = (1.5 + 0.1 * torch.randn(T, 2, D, generator=_gen(88), device="cuda")).to(DT[act])
+    nv.rope_cache_write(k, k, v, slots, nv.rope_table(1, 0), slots=slots, **c)
+    q = torch.zeros_like(q)
+    q[:, :, 0] = 1
+    out = _np(nv.paged_attention(q, block_table=table, lengths=lengths, softmax_scale=1.0, **c))
+    gu.check_device_status()
+    at = 0
+    for b, n in enumerate(lengths.tolist()):
+        ref, _, mag = layer.attend(_np(q[b]), _np(k[at:at + n]), _np(v[at:at + n]), 1.0)
+        at += n
+        bound = _half_step(ref, act) + 2.0 ** -15 * mag
+        assert np.all(np.abs(out[b] - ref) <= bound), (b, (np.abs(out[b] - ref) / bound).max())
+
+
+@pytest.mark.parametrize("G,D", [(2, 64), (10, 128), (2, 256), (16, 256)])
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+def test_paged_attention_of_infinite_values_gives_infinities(act, G, D):
+    """Values of plus and minus infinity beside finite ones, at weights of every rounding."""
+    c, q, table, lengths, slots = _attention_case([300, 70], G * 2, 2, D, 16, act, "16", 89)
+    kv = nv.cache_read(slots=slots, **c)
+    v = kv[1].clone()
+    v[::7, :, 3] = float("inf")
+    v[5::11, :, 8] = float("-inf")
+    nv.rope_cache_write(kv[0], kv[0], v, slots, nv.rope_table(1, 0), slots=slots, **c)
+    out = nv.paged_attention(q, block_table=table, lengths=lengths, **c)
+    assert torch.all(out[:, :, 3] == float("inf")) and torch.all(out[:, :, 8] == float("-inf"))
+    rest = [d for d in range(D) if d not in (3, 8)]
+    assert torch.all(out[:, :, rest].isfinite())

@@ -30,12 +30,13 @@
 //    are joined per block in shared memory, and across blocks by a second
 //    small kernel, in the order of the tokens: the result does not depend on timing.
 // Roundings: the softmax weights meet the values in the MMA as 16 bits, BF16 for
-// a BF16 cache (a relative 2^-8 of each weight, while l keeps the 32-bit ones),
-// FP16 for FP16 and E4M3, 2^11 larger, so that a weight keeps its 11 bits down to 2^-25 of the
-// largest (and below, where the values are FP16: the base follows).  E4M3 codes are exact in FP16; a BF16 query meets them
-// as FP16 after a power of two that puts its largest element at 2^14 (elements
-// below 2^-28 of it lose bits).  The scale of a value row is multiplied into its weight,
-// whose base is taken over z + log2(scale), so that it fits FP16.
+// a BF16 cache, else FP16, and 16-bit values as two such halves (exact_weights below): a relative 2^-16 or
+// 2^-22 of each weight.  Where there is one, 2^-8 or 2^-11, while l keeps the 32-bit ones.  FP16 weights
+// are taken 2^11 larger, so that one keeps its 11 bits down to 2^-25 of the largest (and
+// below, where the values are FP16: the base follows).  E4M3 codes are exact in FP16; a
+// BF16 query meets them as FP16 after a power of two that puts its largest element at
+// 2^14 (elements below 2^-28 of it lose bits).  The scale of a value row is multiplied into
+// its weight, whose base is taken over z + log2(scale), so that it fits FP16.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -103,6 +104,19 @@ struct AttnParams {
 constexpr int attn_warps(int row, int values) { return row > 256 ? 4 : row > 128 ? 8 : values >= 64 ? 12 : 16; }
 constexpr int attn_stages(int row, int values) { return row == 128 && values >= 64 ? 4 : 3; }
 
+// 16-bit values are met by both halves of a weight, the larger one and what that left: the
+// output is then as near the formula as 32-bit weights would bring it (64 x 16384 tokens of BF16: 1.0
+// times the error of a plain form in 32 bits, with rounded weights 1.4).  Loads hide the
+// second product (331 us where one took 329; 32 x 16384 of 16 heads a key head 178.6 and 177.6)
+// but for 16 heads a key head of 256, whose four warps an SM wait for their products: 233
+// us with, 214 without; those keep rounded weights.  So do E4M3 values: they are off by
+// 2^-4 themselves, and the instances are short of instructions.
+constexpr bool exact_weights(bool e4m3, int values) { return !e4m3 && values <= 64; }
+// The larger half is a weight times this, rounded towards zero: what it leaves is above zero
+// then, in 16 bits too (down to 2^-14 in FP16), so that an infinite value gives an infinity, not a NaN.
+template <bool F16>
+constexpr float kMost = F16 ? 1.f - 0x1p-10f : 1.f - 0x1p-20f;
+
 // Shape of an instance: DP padded head size, NT tiles of 8 query heads.
 template <bool E4M3, int DP, int NT>
 struct Shape {
@@ -119,6 +133,7 @@ struct Shape {
     static constexpr int kStages = attn_stages(kRow, DP / 4 * NT);
     static constexpr int kRing = kStages * kStage;
     static constexpr size_t kSmem = (size_t)kWarps * kRing;
+    static constexpr bool kExact = exact_weights(E4M3, DP / 4 * NT);
     static constexpr int kHeads = 8 * NT;
     static constexpr int kPart = kHeads * (DP + 2);             // floats of a partial result: o, m, l
     static constexpr int kPitch = DP + 4;                       // floats from head to head in shared memory
@@ -357,6 +372,7 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
     constexpr bool H = F16 || E4M3;                             // FP16 operands in the MMAs
     constexpr bool FALLS = F16 && !E4M3;                        // the base may fall, too
     constexpr float LIFT = H ? kLift : 0.f;
+    constexpr bool REST = S::kExact;
     extern __shared__ __align__(1024) uint8_t ring_all[];
     __shared__ int first_sm[W * 32], sums[W];
     // Pieces of units, two a warp: the rest of a unit that an earlier warp began, and the last of the range.
@@ -706,7 +722,7 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
                         }
                 }
             }
-            uint32_t pf[TB][NT][2];
+            uint32_t pf[TB][NT][2], pr[TB][NT][2];              // weights, or (REST) their halves
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const float base[2] = {m[nt][0] == -INFINITY ? 0.f : m[nt][0], m[nt][1] == -INFINITY ? 0.f : m[nt][1]};
@@ -718,8 +734,18 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
                     l[nt][0] += w[0] + w[2];
                     l[nt][1] += w[1] + w[3];
                     // heads on the MMA's columns: transpose the 8x8 blocks
-                    pf[tb][nt][0] = movmatrix(f32_to_act2<H>(w[0] * v_by[tb][0], w[1] * v_by[tb][0]));
-                    pf[tb][nt][1] = movmatrix(f32_to_act2<H>(w[2] * v_by[tb][1], w[3] * v_by[tb][1]));
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const float a = w[2 * y], b = w[2 * y + 1];
+                        if constexpr (REST) {
+                            const uint32_t most = f32_to_act2_down<H>(a * kMost<H>, b * kMost<H>);
+                            const float2 u = act2_to_f32<H>(most);
+                            pf[tb][nt][y] = movmatrix(most);
+                            pr[tb][nt][y] = movmatrix(f32_to_act2<H>(a - u.x, b - u.y));
+                        } else {
+                            pf[tb][nt][y] = movmatrix(f32_to_act2<H>(a * v_by[tb][y], b * v_by[tb][y]));
+                        }
+                    }
                 }
             }
 
@@ -733,7 +759,10 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
                         uint32_t af[4];
                         ldmatrix4_trans(af, vs_s + row * S::kRow + value_chunk<E4M3, CH>(row, mt * 2 + ch) * 16);
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma_16816<H>(o[mt][nt], af, pf[tb][nt][0], pf[tb][nt][1]);
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma_16816<H>(o[mt][nt], af, pf[tb][nt][0], pf[tb][nt][1]);
+                            if constexpr (REST) mma_16816<H>(o[mt][nt], af, pr[tb][nt][0], pr[tb][nt][1]);
+                        }
                     }
                 } else {
                     // A lane takes the dimensions of chunk g (half a chunk of 64) of tokens 2 q4, 2 q4 + 1 and

@@ -43,6 +43,15 @@ __device__ __forceinline__ uint32_t f32_to_act2(float lo, float hi) {
     return d;
 }
 
+// The same rounded towards zero.
+template <bool F16>
+__device__ __forceinline__ uint32_t f32_to_act2_down(float lo, float hi) {
+    uint32_t d;
+    if (F16) asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    else asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
 // Two FP32 values rounded to E4M3 (nearest even, saturating at +-448, NaN kept).
 __device__ __forceinline__ uint16_t f32_to_e4m3x2(float lo, float hi) {
     uint16_t d;
