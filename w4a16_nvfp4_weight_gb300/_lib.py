@@ -123,6 +123,10 @@ def load_binding():
             raise RuntimeError(
                 f"Python module not built ({build_lib.BINDING} missing); run "
                 "`python -c 'import __graft_entry__ as g; g.build()'` first")
+        if build_lib.binding_abi_built() != build_lib._binding_abi():
+            raise RuntimeError(
+                f"Python module {build_lib.BINDING} was built for {build_lib.binding_abi_built()}, this is "
+                f"{build_lib._binding_abi()}; build again")
         loader = importlib.machinery.ExtensionFileLoader(name, build_lib.BINDING)
         module = importlib.util.module_from_spec(importlib.util.spec_from_file_location(name, build_lib.BINDING, loader=loader))
         loader.exec_module(module)
