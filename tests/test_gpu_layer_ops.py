@@ -755,3 +755,26 @@ def test_paged_attention_of_infinite_values_gives_infinities(act, G, D):
     assert torch.all(out[:, :, 3] == float("inf")) and torch.all(out[:, :, 8] == float("-inf"))
     rest = [d for d in range(D) if d not in (3, 8)]
     assert torch.all(out[:, :, rest].isfinite())
+
+
+# (head dim, heads a key head) -> warps a block of the instance that has more of them, 8 heads a tile
+WORKSPACE = [(64, 1, 16, 8), (64, 16, 16, 16), (128, 8, 16, 8), (128, 9, 12, 16), (256, 1, 8, 8), (256, 16, 8, 16), (200, 40, 8, 16)]
+
+
+@pytest.mark.parametrize("D,G,warps,heads", WORKSPACE)
+def test_paged_attention_workspace_is_what_the_kernels_use(D, G, warps, heads):
+    """A partial result a warp and two a block of one block an SM; the bytes behind them stay."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    padded = 64 if D <= 64 else 128 if D <= 128 else 256
+    size = nv.paged_attention_workspace_size(3, 2 * G, 2, D)
+    assert size == sms * (2 + warps) * heads * (padded + 2) * 4
+    if D % 16:
+        return
+    for kind in ("16", "e4m3"):
+        case = _attention_case([9000, 33, 4000], 2 * G, 2, D, 16, "bf16", kind, 91)
+        buf = torch.full((size + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+        _check_attention(*case, 16, "bf16", kind, workspace=buf[:size])
+        assert torch.all(buf[size:] == 0xA5)
+        with pytest.raises(nv.Nvfp4Error) as err:
+            nv.paged_attention(case[1], block_table=case[2], lengths=case[3], workspace=buf[:size - 1], **case[0])
+        assert err.value.status == 4

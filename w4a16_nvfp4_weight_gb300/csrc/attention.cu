@@ -140,9 +140,11 @@ struct Shape {
     static_assert(kSmem + 10240 <= kMaxSmem && kHeads * kPitch * 4 <= kRing && 8 * kPitch * 4 <= kStage, "ring");
 };
 
-// Partial results in the workspace: two a block, then one a warp.
-inline size_t workspace_for(int heads, int DP, int64_t sms) {
-    return (size_t)sms * (2 + 16) * heads * (DP + 2) * sizeof(float);      // at most 16 warps a block
+// Partial results in the workspace: two a block, then one a warp, of whichever cache
+// type has more warps (the E4M3 one, whose rows are shorter).
+inline size_t workspace_for(int NT, int DP, int64_t sms) {
+    const int warps = std::max(attn_warps(DP, DP / 4 * NT), attn_warps(2 * DP, DP / 4 * NT));
+    return (size_t)sms * (2 + warps) * 8 * NT * (DP + 2) * sizeof(float);
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -1096,8 +1098,7 @@ using namespace nvfp4;
 
 extern "C" size_t nvfp4_paged_attention_workspace(int64_t B, int64_t Hq, int64_t heads, int64_t head_dim) {
     if (B <= 0 || heads <= 0 || Hq <= 0 || Hq % heads != 0 || head_dim <= 0 || head_dim > kMaxHeadDim) return 0;
-    const int DP = padded_dim(head_dim), group = 8 * head_tiles(Hq / heads);
-    return workspace_for(group, DP, sm_count());
+    return workspace_for(head_tiles(Hq / heads), padded_dim(head_dim), sm_count());
 }
 
 extern "C" nvfp4_status nvfp4_paged_attention(const void* q, int64_t q_row_stride, int64_t q_head_stride,
