@@ -439,15 +439,15 @@ typedef enum { NVFP4_OUT_16 = 0, NVFP4_OUT_E4M3 = 1 } nvfp4_out_type;
  *  X, residual   device BF16 (FP16 with f16 = 1) [T, H], rows x_stride /
  *                residual_stride elements apart.
  *  weight        device [H], the same type.
- *  Y             device [T, H], dense: 16-bit, or uint8 E4M3 codes.  Must not
- *                overlap the inputs.
+ *  Y             device [T, H], dense: 16-bit, or uint8 E4M3 codes.
  *  scales        device FP32 [T, H / group] ([T, 1] with group 0); E4M3 only.
- *  residual_out  device [T, H], dense, with residual only: receives r.  It may be
- *                residual or X where that is dense (element for element in place).
+ *  residual_out  device [T, H], dense, with residual only: receives r.
  *  group         0, 16, 32, 64, 128 or 256, dividing H (0 for 16-bit output).
  * H in [1, 2^24], any width, stride and alignment; rows whose width, strides and
  * pointers are multiples of 16 bytes run on vector loads, others on 4- or 2-byte
- * ones.  T == 0 launches nothing.
+ * ones.  T == 0 launches nothing.  A 16-bit Y and residual_out may each be X or
+ * residual where that is dense (element for element in place); outputs that overlap
+ * inputs or each other in another way are refused.
  */
 nvfp4_status nvfp4_rms_norm(const void* X, int64_t x_stride, const void* residual, int64_t residual_stride,
                             const void* weight, int64_t T, int64_t H, float eps, int out_type, int64_t group,
@@ -487,8 +487,9 @@ typedef struct {
  *  sections      host int32 [axes]; NULL: one axis.  axes is 1 to 4.
  *  table         device FP32 [table_rows, rot], 16-byte aligned.
  *  slots         device int64 [T]: page * page_size + token, negative: not stored.
- *                No two tokens may share a slot.
- *  q_out         device [T, Hq, D], dense, RN of the rotated q (q itself if dense).
+ *                No two tokens may share a slot, nor k or v lie in rows that are written.
+ *  q_out         device [T, Hq, D], dense, RN of the rotated q.  It may be q where that is
+ *                dense; over any other input, or the cache, it is refused.
  * The cache gets RN(k), RN(v), or per token and head s = max(amax / 448, 2^-100)
  * and E4M3(x / s) of the FP32 values (NaN and infinities as in nvfp4_rms_norm).
  * A position outside the table leaves its elements as they are, a slot outside
@@ -505,7 +506,8 @@ nvfp4_status nvfp4_rope_cache_write(const void* q, int64_t q_token_stride, int64
 /*
  * Read cached rows back: k_out, v_out [T, heads, D] dense, 16-byte aligned, of
  * the slots (negative: zeros; outside the cache: zeros and NVFP4_ERR_BAD_INDEX
- * in the status word), RN(code * scale) from an E4M3 cache.
+ * in the status word), RN(code * scale) from an E4M3 cache.  Outputs over the
+ * cache, the slots or each other are refused.
  */
 nvfp4_status nvfp4_kv_cache_read(const nvfp4_kv_cache* cache, const int64_t* slots, int64_t T, int f16,
                                  void* k_out, void* v_out, void* stream);
@@ -521,7 +523,8 @@ nvfp4_status nvfp4_kv_cache_read(const nvfp4_kv_cache* cache, const int64_t* slo
  *                of tokens [i * page_size, (i + 1) * page_size).  Entries past a
  *                sequence's length are not read.
  *  lengths       device int32 [B].
- *  out           device [B, Hq, D], dense, 16-byte aligned.
+ *  out           device [B, Hq, D], dense, 16-byte aligned.  It may be q where that
+ *                is dense; out, lse and workspace over anything else are refused.
  *  lse           device FP32 [B, Hq] or NULL.
  *  workspace     device, >= nvfp4_paged_attention_workspace(...) bytes, 256-byte
  *                aligned.  Contents on entry do not matter.

@@ -778,3 +778,66 @@ def test_paged_attention_workspace_is_what_the_kernels_use(D, G, warps, heads):
         with pytest.raises(nv.Nvfp4Error) as err:
             nv.paged_attention(case[1], block_table=case[2], lengths=case[3], workspace=buf[:size - 1], **case[0])
         assert err.value.status == 4
+
+
+@pytest.mark.parametrize("T,H", [(64, 512), (700, 512), (64, 509), (3, 40008), (5, 20480), (400, 268)])
+def test_norm_in_place_of_its_inputs(T, H):
+    g = _gen(92)
+    x, r, w = _randn(g, (T, H)), _randn(g, (T, H)), _randn(g, (H,))
+    plain, (y, a) = nv.rms_norm(x, w), nv.rms_norm(x, w, residual=r)
+    x1 = x.clone()
+    assert nv.rms_norm(x1, w, out=x1) is x1 and torch.equal(x1, plain)
+    for names in (("x", None), ("r", None), ("x", "r"), ("r", "x"), ("r", "r2"), (None, "x")):
+        t = {"x": x.clone(), "r": r.clone(), None: None, "r2": torch.empty_like(r)}
+        got, added = nv.rms_norm(t["x"], w, residual=t["r"], out=t[names[0]], residual_out=t[names[1]])
+        assert torch.equal(got, y) and torch.equal(added, a)
+        assert names[0] is None or got is t[names[0]]
+        assert names[1] is None or added is t[names[1]]
+
+
+@pytest.mark.parametrize("lengths,Hq,Hkv,D,act,kind", [([70001], 8, 1, 128, "bf16", "16"), ([9000, 0, 33, 4000], 40, 2, 64, "f16", "e4m3"),
+                                                       ([120, 255, 1, 0], 16, 4, 128, "bf16", "e4m3"), ([30000, 5], 16, 1, 256, "f16", "16")])
+def test_paged_attention_in_place_of_its_query(lengths, Hq, Hkv, D, act, kind):
+    c, q, table, n, _ = _attention_case(lengths, Hq, Hkv, D, 16, act, kind, 93)
+    want = nv.paged_attention(q, block_table=table, lengths=n, **c)
+    got = nv.paged_attention(q, block_table=table, lengths=n, out=q, **c)
+    assert got is q and torch.equal(got.view(torch.int16), want.view(torch.int16))
+    gu.check_device_status()
+
+
+def test_outputs_beside_and_between_inputs_are_taken_and_over_them_refused():
+    g = _gen(94)
+    w, T, H = _randn(g, (256,)), 6, 256
+    pool = _randn(g, (4 * T * H,)).view(torch.bfloat16)
+
+    def refused(fn, *a, **kw):
+        with pytest.raises(nv.Nvfp4Error) as err:
+            fn(*a, **kw)
+        assert err.value.status == 1 and "overlap" in str(err.value)
+
+    x = pool[:T * H].view(T, H)
+    want = nv.rms_norm(x.clone(), w)
+    assert torch.equal(nv.rms_norm(x, w, out=pool[T * H:2 * T * H].view(T, H)), want)
+    refused(nv.rms_norm, x, w, out=pool[H:H + T * H].view(T, H))
+    refused(nv.rms_norm, x, w, residual=_randn(g, (T, H)), residual_out=pool[8:8 + T * H].view(T, H))
+    codes = pool.view(torch.uint8)[:T * H].view(E4M3).view(T, H)
+    refused(nv.rms_norm_e4m3, x, w, out=codes)
+    apart = pool.view(2, -1)[:, :H]                         # two rows far apart, the output between them
+    want = nv.rms_norm(apart.clone(), w)
+    assert torch.equal(nv.rms_norm(apart, w, out=pool[H:3 * H].view(2, H)), want)
+    c = _make_cache(4, 2, 16, 64, "bf16", "16", fill=0.0)
+    qkv = _randn(g, (3, 8, 64))
+    q, k, v = qkv[:, :4], qkv[:, 4:6], qkv[:, 6:]
+    slots, table = torch.arange(3, device="cuda"), nv.rope_table(8, 64)
+    refused(nv.rope_cache_write, q, k, v, slots, table, slots=slots, q_out=qkv.view(-1)[:3 * 4 * 64].view(3, 4, 64), **c)
+    refused(nv.rope_cache_write, q, k, v, slots, table, slots=slots, q_out=c["v_cache"].view(-1)[:3 * 4 * 64].view(3, 4, 64), **c)
+    one = [t[:1] for t in (q, k, v, slots)]                 # one token's heads are dense
+    assert nv.rope_cache_write(*one, table, slots=slots[:1], q_out=one[0], **c) is one[0]
+    out = torch.empty(2, 3, 2, 64, dtype=torch.bfloat16, device="cuda")
+    refused(nv.cache_read, slots=slots, k_out=out[0], v_out=out[0], **c)
+    refused(nv.cache_read, slots=slots, k_out=out[0], v_out=c["k_cache"].view(-1)[:3 * 2 * 64].view(3, 2, 64), **c)
+    nv.cache_read(slots=slots, k_out=out[0], v_out=out[1], **c)
+    bt, n = torch.zeros((3, 1), dtype=torch.int32, device="cuda"), torch.ones(3, dtype=torch.int32, device="cuda")
+    refused(nv.paged_attention, q.contiguous(), block_table=bt, lengths=n, out=c["k_cache"].view(-1)[:3 * 4 * 64].view(3, 4, 64), **c)
+    refused(nv.paged_attention, q, block_table=bt, lengths=n, out=qkv.view(-1)[:3 * 4 * 64].view(3, 4, 64), **c)
+    gu.check_device_status()

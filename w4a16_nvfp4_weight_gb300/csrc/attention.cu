@@ -1127,6 +1127,20 @@ extern "C" nvfp4_status nvfp4_paged_attention(const void* q, int64_t q_row_strid
     if (workspace_bytes < need || !workspace)
         return fail(NVFP4_ERR_WORKSPACE, "%s: workspace %zu bytes, needs %zu", fn, workspace_bytes, need);
     if (!aligned(workspace, 256)) return fail(NVFP4_ERR_ALIGNMENT, "%s: workspace must be 256-byte aligned", fn);
+    // out may be q: a unit's output is written once all of its steps are done, and no other unit reads its query.
+    const int64_t D = p.cache.D;
+    const Span o = dense_span("out", out, 2 * B * Hq * D), sums = dense_span("lse", lse, 4 * B * Hq), ws = dense_span("workspace", workspace, (int64_t)need);
+    const Span qs = strided_span("q", q, 2 * D, {{B, 2 * q_row_stride}, {Hq, 2 * q_head_stride}});
+    const bool in_place = q == out && (B == 1 || q_row_stride == Hq * D) && (Hq == 1 || q_head_stride == D);
+    if (!in_place && overlaps(o, qs))
+        return fail(NVFP4_ERR_INVALID_ARG, "%s: out overlaps q (it may be q itself where that is dense)", fn);
+    const Span pages = strided_span("block_table", block_table, 4 * table_width, {{B, 4 * table_stride}}), counts = dense_span("lengths", lengths, 4 * B);
+    if (const char* s = met(sums, {qs, o, ws})) return fail(NVFP4_ERR_INVALID_ARG, "%s: lse overlaps %s", fn, s);
+    if (const char* s = met(ws, {qs, o})) return fail(NVFP4_ERR_INVALID_ARG, "%s: workspace overlaps %s", fn, s);
+    for (const Span& to : {o, sums, ws}) {
+        if (const char* s = met(to, {pages, counts})) return fail(NVFP4_ERR_INVALID_ARG, "%s: %s overlaps %s", fn, to.name, s);
+        if (const char* part = met_cache(to, p.cache)) return fail(NVFP4_ERR_INVALID_ARG, "%s: %s overlaps %s", fn, to.name, part);
+    }
     p.status = device_status_ptr();
     if (!p.status) return fail(NVFP4_ERR_CUDA, "%s: no CUDA device", fn);
     p.q = (const uint16_t*)q; p.q_row = q_row_stride; p.q_head = q_head_stride;

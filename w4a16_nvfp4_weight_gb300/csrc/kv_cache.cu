@@ -480,6 +480,17 @@ extern "C" nvfp4_status nvfp4_rope_cache_write(const void* q, int64_t q_token_st
     }
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(table, 16) || !aligned(positions, 8) || !aligned(slots, 8))
         return fail(NVFP4_ERR_ALIGNMENT, "%s: q, k, v, q_out and table must be 16-byte aligned, positions and slots 8-byte", fn);
+    // q_out may be q: a thread reads both sides of its pairs before it writes them.
+    const Span to = dense_span("q_out", q_out, 2 * T * Hq * D);
+    const Span qs = strided_span("q", q, 2 * D, {{T, 2 * q_token_stride}, {Hq, 2 * q_head_stride}});
+    const bool in_place = q == q_out && (T == 1 || q_token_stride == Hq * D) && (Hq == 1 || q_head_stride == D);
+    if (!in_place && overlaps(to, qs)) return fail(NVFP4_ERR_INVALID_ARG, "%s: q_out overlaps q (it may be q itself where that is dense)", fn);
+    if (const char* in = met(to, {strided_span("k", k, 2 * D, {{T, 2 * k_token_stride}, {p.cache.heads, 2 * k_head_stride}}),
+                                  strided_span("v", v, 2 * D, {{T, 2 * v_token_stride}, {p.cache.heads, 2 * v_head_stride}}),
+                                  dense_span("positions", positions, 8 * axes * T), dense_span("slots", slots, 8 * T),
+                                  dense_span("table", table, 4 * table_rows * rot)}))
+        return fail(NVFP4_ERR_INVALID_ARG, "%s: q_out overlaps %s", fn, in);
+    if (const char* part = met_cache(to, p.cache)) return fail(NVFP4_ERR_INVALID_ARG, "%s: q_out overlaps %s", fn, part);
     if (no_device(&p.status)) return fail(NVFP4_ERR_CUDA, "%s: no CUDA device", fn);
     p.q = (const uint16_t*)q; p.k = (const uint16_t*)k; p.v = (const uint16_t*)v;
     p.q_token = q_token_stride; p.q_head = q_head_stride; p.k_token = k_token_stride; p.k_head = k_head_stride;
@@ -502,6 +513,13 @@ extern "C" nvfp4_status nvfp4_kv_cache_read(const nvfp4_kv_cache* cache, const i
     if (!slots || !k_out || !v_out) return fail(NVFP4_ERR_INVALID_ARG, "%s: null pointer", fn);
     if (!aligned(slots, 8) || !aligned(k_out, 16) || !aligned(v_out, 16))
         return fail(NVFP4_ERR_ALIGNMENT, "%s: slots must be 8-byte aligned, k_out and v_out 16-byte", fn);
+    const int64_t bytes = 2 * T * p.cache.heads * p.cache.D;
+    const Span ko = dense_span("k_out", k_out, bytes), vo = dense_span("v_out", v_out, bytes);
+    for (const Span& out : {ko, vo}) {
+        if (overlaps(out, dense_span("slots", slots, 8 * T))) return fail(NVFP4_ERR_INVALID_ARG, "%s: %s overlaps slots", fn, out.name);
+        if (const char* part = met_cache(out, p.cache)) return fail(NVFP4_ERR_INVALID_ARG, "%s: %s overlaps %s", fn, out.name, part);
+    }
+    if (overlaps(ko, vo)) return fail(NVFP4_ERR_INVALID_ARG, "%s: k_out overlaps v_out", fn);
     if (no_device(&p.status)) return fail(NVFP4_ERR_CUDA, "%s: no CUDA device", fn);
     p.slots = slots; p.k_out = (uint16_t*)k_out; p.v_out = (uint16_t*)v_out; p.T = T;
     cudaStream_t s = (cudaStream_t)stream;

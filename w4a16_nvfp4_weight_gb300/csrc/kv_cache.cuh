@@ -5,6 +5,7 @@
 #include <cstdint>
 
 #include "common.cuh"
+#include "overlap.cuh"
 
 namespace nvfp4 {
 
@@ -44,6 +45,19 @@ struct CacheView {
         return (page * heads + h) * page_size + at;
     }
 };
+
+// The cache's rows, keys or values, and scales.
+inline Span cache_span(const char* name, const CacheView& c, const void* rows) {
+    return strided_span(name, rows, (int64_t)c.D * (c.e4m3 ? 1 : 2), {{c.num_pages, c.page_bytes}, {c.heads, c.head_bytes}, {c.page_size, c.token_bytes}});
+}
+inline Span scale_span(const char* name, const CacheView& c, const float* scale) {
+    return dense_span(name, scale, 4 * c.num_slots * c.heads);
+}
+// The cache's part that `out` overlaps, or null.
+inline const char* met_cache(const Span& out, const CacheView& c) {
+    return met(out, {cache_span("the cache's keys", c, c.k), cache_span("the cache's values", c, c.v),
+                     scale_span("the cache's scales", c, c.k_scale), scale_span("the cache's scales", c, c.v_scale)});
+}
 
 // Checks `c` and fills `view`.
 nvfp4_status check_cache(const char* fn, const nvfp4_kv_cache* c, CacheView* view);

@@ -9,6 +9,7 @@
 
 #include "common.cuh"
 #include "numeric.cuh"
+#include "overlap.cuh"
 #include "ptx.cuh"
 
 namespace nvfp4 {
@@ -393,6 +394,18 @@ extern "C" nvfp4_status nvfp4_rms_norm(const void* X, int64_t x_stride, const vo
     if (!aligned(X, 2) || !aligned(weight, 2) || (!e4m3 && !aligned(Y, 2)) || !aligned(residual, 2) ||
         !aligned(residual_out, 2) || !aligned(scales, 4))
         return fail(NVFP4_ERR_ALIGNMENT, "%s: pointers must be aligned to their elements", fn);
+    // A thread reads its elements of X and residual before it writes them, so an output of
+    // their type may be one of them; anything else would be read by others after that.
+    const Span x = strided_span("X", X, 2 * H, {{T, 2 * x_stride}}), res = strided_span("residual", residual, 2 * H, {{T, 2 * residual_stride}});
+    const Span y = dense_span("Y", Y, T * H * (e4m3 ? 1 : 2)), sums = dense_span("residual_out", residual_out, 2 * T * H);
+    const Span by = dense_span("scales", e4m3 ? scales : nullptr, 4 * T * (group ? H / group : 1)), w = dense_span("weight", weight, 2 * H);
+    for (const Span& in : {x, res})
+        for (const Span& out : {y, sums})
+            if (overlaps(out, in) && !same_place(out, in))
+                return fail(NVFP4_ERR_INVALID_ARG, "%s: %s overlaps %s", fn, out.name, in.name);
+    if (const char* s = met(by, {x, res, w})) return fail(NVFP4_ERR_INVALID_ARG, "%s: scales overlap %s", fn, s);
+    if (const char* s = met(sums, {w, by})) return fail(NVFP4_ERR_INVALID_ARG, "%s: residual_out overlaps %s", fn, s);
+    if (const char* s = met(y, {w, by, sums})) return fail(NVFP4_ERR_INVALID_ARG, "%s: Y overlaps %s", fn, s);
     if (sm_count() <= 0 || device_status_ptr() == nullptr) return fail(NVFP4_ERR_CUDA, "%s: no CUDA device", fn);
     NormParams p{};
     p.x = (const uint16_t*)X; p.residual = (const uint16_t*)residual; p.weight = (const uint16_t*)weight;

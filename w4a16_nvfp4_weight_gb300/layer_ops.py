@@ -12,6 +12,9 @@ with rows of head_dim contiguous and on 16-byte boundaries, the same for both:
 views of one interleaved pool will do) in the activation type, or in
 torch.float8_e4m3fn with ``k_scale`` and ``v_scale`` float32 [pages, heads,
 page_size].  Slot s of a token is page * page_size + offset.
+
+An output over an input or another output is refused but where a function says that
+it may be that input itself.
 """
 
 import torch
@@ -34,7 +37,8 @@ _ops = _Unloaded()
 def rms_norm(x, weight, eps=1e-6, residual=None, residual_out=None, out=None):
     """y = RN(r * rsqrt(mean(r^2) + eps) * weight) over the rows of x [T, H] (any
     row stride), r = x, or RN(x + residual), which is returned too: y, or (y, r).
-    ``residual_out`` may be ``residual`` (contiguous) to add in place."""
+    ``out`` and ``residual_out`` may each be ``x`` or ``residual`` (contiguous), to
+    work in place."""
     return _ops.rms_norm(x, weight, eps, residual, residual_out, out, False, 0, None)
 
 
@@ -61,7 +65,7 @@ def rope_cache_write(q, k, v, positions, table, k_cache, v_cache, slots, k_scale
                      interleaved=False, q_out=None):
     """Rotate q [T, Hq, D] and k [T, Hkv, D], and store k and v [T, Hkv, D] in the
     cache rows of ``slots`` (int64 [T]; negative: not stored).  Returns the rotated
-    q [T, Hq, D].  q, k and v may be views of one projection's output (16-byte
+    q [T, Hq, D] (``q_out`` may be q where it is contiguous).  q, k and v may be views of one projection's output (16-byte
     aligned rows).  ``positions``: int64 [T], or [axes, T] with ``sections`` (a
     list with the number of frequencies of each axis, at most four) for positions
     with several axes.  ``table``: float32 [rows, rot] (rope_table); elements from
@@ -90,7 +94,8 @@ def paged_attention(q, k_cache, v_cache, block_table, lengths, k_scale=None, v_s
     cached tokens of each sequence (int32 [B]; the new token's own key and value are
     in the cache already), whose pages are block_table[b] (int32 [B, width]).  Hq is
     a multiple of the cache's heads.  ``softmax_scale`` defaults to D^-0.5;
-    ``window`` > 0 attends to the last ``window`` tokens only.  Returns out [B, Hq, D],
+    ``window`` > 0 attends to the last ``window`` tokens only.  Returns out [B, Hq, D]
+    (``out`` may be q where it is contiguous),
     with ``return_lse`` also the log-sum-exp of the scaled scores (float32 [B, Hq],
     natural log).  A sequence of length 0 gives zeros and -inf.  A length or page
     outside the table or the cache is taken as the nearest end or as page 0, and
