@@ -841,3 +841,34 @@ def test_outputs_beside_and_between_inputs_are_taken_and_over_them_refused():
     refused(nv.paged_attention, q.contiguous(), block_table=bt, lengths=n, out=c["k_cache"].view(-1)[:3 * 4 * 64].view(3, 4, 64), **c)
     refused(nv.paged_attention, q, block_table=bt, lengths=n, out=qkv.view(-1)[:3 * 4 * 64].view(3, 4, 64), **c)
     gu.check_device_status()
+
+
+@pytest.mark.parametrize("heads,page,pages", [(1, 16, 5), (2, 1, 30), (1, 1, 30), (2, 32, 1), (1, 32, 1)])
+@pytest.mark.parametrize("kind", ["16", "e4m3"])
+def test_cache_strides_of_dimensions_of_one_element_do_not_matter(heads, page, pages, kind):
+    """Keys laid out [pages, heads, page, D] and values [pages, page, heads, D]: the same places
+    where there is one head or one token a page, whatever strides torch gives that dimension."""
+    D, n = 64, 25
+    a = _make_cache(pages, heads, page, D, "bf16", kind)
+    b = dict(a, k_cache=a["k_cache"].clone() if kind == "16" else a["k_cache"].view(torch.uint8).clone().view(E4M3))
+    b["v_cache"] = _make_cache(pages, heads, page, D, "bf16", kind, layout="nhd")["v_cache"]
+    shape = a["k_cache"].shape
+    odd = [s if m > 1 else 8 * i + 3 for i, (s, m) in enumerate(zip(a["k_cache"].stride(), shape))]
+    c = dict(b, v_cache=torch.as_strided(b["v_cache"], shape, b["v_cache"].stride()),
+             k_cache=torch.as_strided(b["k_cache"].clone() if kind == "16" else b["k_cache"].view(torch.uint8).clone().view(E4M3), shape, odd))
+    for t in (b, c):
+        t.update({s: a[s].clone() for s in ("k_scale", "v_scale") if s in a})
+    if heads > 1 and page > 1:
+        b["v_cache"] = c["v_cache"] = torch.empty_like(a["v_cache"])
+    g = _gen(95)
+    q, k, v = _randn(g, (n, 4, D)), _randn(g, (n, heads, D)), _randn(g, (n, heads, D))
+    slots, table = torch.arange(n, device="cuda"), nv.rope_table(n, D)
+    bt = torch.arange(-(-n // page), dtype=torch.int32, device="cuda")[None]
+    got = []
+    for t in (a, b, c):
+        turned = nv.rope_cache_write(q, k, v, slots, table, slots=slots, **t)
+        rows = nv.cache_read(slots=slots, dtype=torch.bfloat16, **t)
+        got.append((turned, *rows, nv.paged_attention(q[:1], block_table=bt, lengths=slots[-1:].int(), **t)))
+    for other in got[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(got[0], other))
+    gu.check_device_status()

@@ -146,7 +146,15 @@ nvfp4_kv_cache cache_of(const Call& c, PyObject* k_cache, PyObject* v_cache, PyO
     const auto shape = k.sizes();
     c.check(k, "k_cache", e4m3 ? at::kFloat8_e4m3fn : c.act, shape, false);
     c.check(v, "v_cache", k.scalar_type(), shape, false);
-    if (v.strides() != k.strides())
+    // A dimension of one element has no step: any stride there stands for that of dense rows.
+    int64_t strides[3], dense = shape[3];
+    bool same = true;
+    for (int i = 2; i >= 0; --i) {
+        strides[i] = shape[i] == 1 ? dense : k.stride(i);
+        same = same && (shape[i] == 1 || v.stride(i) == k.stride(i));
+        dense = strides[i] * shape[i];
+    }
+    if (!same)
         refuse(1, "k_cache and v_cache must have the same strides, got " + shape_text(k.strides()) + " and " + shape_text(v.strides()));
     const at::Tensor* ks = tensor_or_none(k_scale, "k_scale");
     const at::Tensor* vs = tensor_or_none(v_scale, "v_scale");
@@ -162,7 +170,7 @@ nvfp4_kv_cache cache_of(const Call& c, PyObject* k_cache, PyObject* v_cache, PyO
     d.k_scale = e4m3 ? (float*)ks->data_ptr() : nullptr;
     d.v_scale = e4m3 ? (float*)vs->data_ptr() : nullptr;
     d.num_pages = shape[0]; d.heads = shape[1]; d.page_size = shape[2]; d.head_dim = shape[3];
-    d.page_stride = k.stride(0); d.head_stride = k.stride(1); d.token_stride = k.stride(2);
+    d.page_stride = strides[0]; d.head_stride = strides[1]; d.token_stride = strides[2];
     d.type = e4m3 ? NVFP4_CACHE_E4M3 : NVFP4_CACHE_16;
     return d;
 }
