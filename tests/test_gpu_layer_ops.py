@@ -872,3 +872,28 @@ def test_cache_strides_of_dimensions_of_one_element_do_not_matter(heads, page, p
     for other in got[1:]:
         assert all(torch.equal(x, y) for x, y in zip(got[0], other))
     gu.check_device_status()
+
+
+@pytest.mark.parametrize("T,H,group", [(400, 5120, 128), (400, 5120, 16), (400, 16384, 256), (400, 2304, 64),       # four pieces, several warps a row
+                                       (3, 16392, 0), (320, 16392, 0), (2, 20480, 32), (400, 20480, 128), (330, 32768, 0), (2, 32768, 256)])
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+def test_norm_e4m3_of_many_and_of_wide_rows(T, H, group, act):
+    test_norm_e4m3(T, H, group, act)
+
+
+@pytest.mark.parametrize("T,H", [(1, 16392), (320, 16392), (7, 20480), (400, 20480), (310, 32768), (2, 32768)])
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+def test_norm_of_wide_rows(T, H, act):
+    g = _gen(T + H)
+    x, w, r = _randn(g, (T, H), act), _randn(g, (H,), act), _randn(g, (T, H), act)
+    _close16(nv.rms_norm(x, w, eps=1e-5), layer.rms_norm(_np(x), _np(w), 1e-5), act)
+    y, added = nv.rms_norm(x, w, residual=r)
+    assert torch.equal(added, (x.float() + r.float()).to(DT[act]))
+    _close16(y, layer.rms_norm(_np(added), _np(w), 1e-6), act)
+
+
+@pytest.mark.parametrize("kind", ["16", "e4m3"])
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+@pytest.mark.parametrize("T,Hq,Hkv,D,rot,sections", [(3000, 8, 2, 80, 40, None), (2900, 9, 3, 112, 56, [10, 9, 9]), (1500, 24, 1, 256, 136, [1, 67])])
+def test_rope_interleaved_in_pieces_of_four_with_many_heads_a_thread(T, Hq, Hkv, D, rot, sections, act, kind):
+    test_rope_cache_write_and_read(T, Hq, Hkv, D, rot, 16, sections, True, act, kind, "hnd")
