@@ -492,8 +492,8 @@ typedef struct {
  *                dense; over any other input, or the cache, it is refused.
  * The cache gets RN(k), RN(v), or per token and head s = max(amax / 448, 2^-100)
  * and E4M3(x / s) of the FP32 values (NaN and infinities as in nvfp4_rms_norm).
- * A position outside the table leaves its elements as they are, a slot outside
- * the cache is not written; both record NVFP4_ERR_BAD_INDEX in the status word.
+ * A position outside the table is taken as an angle of zero (c = 1, s = 0), a slot
+ * outside the cache is not written; both record NVFP4_ERR_BAD_INDEX in the status word.
  */
 nvfp4_status nvfp4_rope_cache_write(const void* q, int64_t q_token_stride, int64_t q_head_stride,
                                     const void* k, int64_t k_token_stride, int64_t k_head_stride,

@@ -55,7 +55,7 @@ constexpr int kWholeUnit = 256;    // units of at most so many tokens are not sp
 // Scores may pass the base of their exponentials by so many powers of two more than the
 // largest score did when it was taken, before a new one is taken: most steps need no
 // maximum over the warp and no rescaling (64 x 8192 E4M3 tokens, 16 query heads a key
-// head: 237 us, without 244; of 256 and 16 bits 750, 765).
+// head: 235 us, without 244; 16 x 16384 of 256 and 16 bits 215, 229).
 constexpr float kSlack = 4.f;
 // Weights that meet the values as FP16 are taken over a base 2^11 below the largest score:
 // up to 2^15 with the slack, FP16's range used upwards, since downwards it ends at 2^-14
@@ -69,8 +69,9 @@ constexpr int kLeastScale = -84;
 // below 2^kLow in a step takes that step's largest for its base, as far as l stays below
 // 2^kMostSum.  A token far above the others with a value next to zero (the first of a long
 // text, often) would else press their weights out of FP16: 24 nats above 8192 equal ones
-// they came out 23 % too small.  (E4M3 values bring their scale into the base, and such a token
-// does not raise it.)
+// they came out 23 % too small.  The votes cost up to 2 %, of 16 heads a key head of 256 3 % (221
+// us, 214 without).  (E4M3 values bring their scale into the base, and such a token does not
+// raise it; what else is lost there, below 2^-36 of the largest weight, is less than their codes' steps.)
 constexpr float kLow = -7.f;
 constexpr int kMostSum = 80;
 constexpr int kUnitCost = 4;       // steps' worth of time that the start and end of a unit take
@@ -99,17 +100,19 @@ struct AttnParams {
 // block an SM) and steps in a warp's ring.  As many bytes in flight as shared
 // memory holds, and as many warps as that and the registers leave: steps of 4 KB
 // need sixteen to be computed as fast as they come.  E4M3 rows of 128 with two head
-// tiles take twelve warps and four steps each: 122 us for 16 x 16384 tokens, 96 query
-// and 8 key heads (BF16 query; eight warps and six steps: 130), 28.2 against 26.7 at 2048.
+// tiles take twelve warps and four steps each: 121 us for 16 x 16384 tokens, 96 query
+// and 8 key heads (eight warps and six steps: 130).  Short contexts lose by it: at 4096
+// tokens 42.4 against 41.9, at 2048 27.9 against 26.5, one sequence of 1000 10.7 against 9.8.
 constexpr int attn_warps(int row, int values) { return row > 256 ? 4 : row > 128 ? 8 : values >= 64 ? 12 : 16; }
 constexpr int attn_stages(int row, int values) { return row == 128 && values >= 64 ? 4 : 3; }
 
 // 16-bit values are met by both halves of a weight, the larger one and what that left: the
 // output is then as near the formula as 32-bit weights would bring it (64 x 16384 tokens of BF16: 1.0
 // times the error of a plain form in 32 bits, with rounded weights 1.4).  Loads hide the
-// second product (331 us where one took 329; 32 x 16384 of 16 heads a key head 178.6 and 177.6)
-// but for 16 heads a key head of 256, whose four warps an SM wait for their products: 233
-// us with, 214 without; those keep rounded weights.  So do E4M3 values: they are off by
+// second product (64 x 16384 of BF16 326 us with and without, of FP16 329 and 327; 32 x 16384 of
+// 16 heads a key head 177.6 and 175.3; 1 x 1000 7.05 and 6.98) but for 16 heads a key head of
+// 256, whose four warps an SM wait for their products: 233 us with, 214 without; those keep
+// rounded weights.  So do E4M3 values: they are off by
 // 2^-4 themselves, and the instances are short of instructions.
 constexpr bool exact_weights(bool e4m3, int values) { return !e4m3 && values <= 64; }
 // The larger half is a weight times this, rounded towards zero: what it leaves is above zero
@@ -124,7 +127,8 @@ struct Shape {
     static constexpr int kChunks = kRow / 16;                   // 16-byte chunks a row
     // Blocks of 16 tokens a step: 2 KB leave most of a step's instructions to finding its
     // pages and to the softmax, which a second block shares (64 x 8192 tokens, 32 query
-    // and 8 key heads of 64: 98 us; one block 129).  Longer rows have no room for it.
+    // and 8 key heads of 64: 99 us, one block 131; 16 x 2048 13.5 and 14.8; one sequence of
+    // 1000 7.9 and 7.4).  Longer rows have no room for it.
     static constexpr int kBlocks = kRow == 64 ? 2 : 1;
     static constexpr int kStep = kRows * kBlocks;
     static constexpr int kTile = kStep * kRow;
@@ -1043,8 +1047,8 @@ nvfp4_status launch_attention(AttnParams p, void* workspace, cudaStream_t stream
     if (most > INT32_MAX)
         return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s: %lld steps of tokens and heads in one call, above 2^31", fn, (long long)most);
     // Short units are not split between blocks: there is nothing to join after the
-    // kernel.  (8 sequences of 128 tokens 6.2 us and one launch against 6.8 and two; at
-    // 500 tokens, 31 steps, splitting wins, 8.6 against 9.2 us.)
+    // kernel.  (8 sequences of 128 tokens 6.3 us and one launch against 6.8 and two, of
+    // 256 7.3 and 7.9; at 500 tokens, 32 steps, splitting wins, 8.8 against 9.5 us.)
     int64_t tokens = (int64_t)p.width * p.cache.page_size;
     if (p.window > 0) tokens = std::min<int64_t>(tokens, (int64_t)p.window + S::kStep);
     p.whole_units = tokens <= kWholeUnit;

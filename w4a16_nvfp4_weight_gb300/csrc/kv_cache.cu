@@ -173,7 +173,7 @@ __device__ __forceinline__ void store_words(void* to, const uint32_t* w) {
 // pieces as they are.  PE is 8 where rot allows it, else 4.  L threads a head (a
 // power of two), `per` heads a token at a time, `tokens` a block of at most kRopeThreads.
 // Bound by memory (q, k, v in, q and the cache rows out) and not far from it by
-// instructions: 20.5 us (5.8 TB/s) for 4096 tokens of 40 + 2 * 8 heads of 128
+// instructions: 20.4 us (5.9 TB/s) for 4096 tokens of 40 + 2 * 8 heads of 128
 // with three axes, where a piece of 8 a thread with its mate's by shuffle (176
 // instructions a warp for two heads) took 30.  The rows of U heads are loaded first;
 // then the block fetches its tokens' cosines and sines into shared memory, a
@@ -364,7 +364,7 @@ nvfp4_status launch_rope(RopeParams p, bool f16, bool inter, cudaStream_t stream
     int log2_L = 0;
     while ((2 * PE << log2_L) < p.D) ++log2_L;
     const int L = 1 << log2_L;
-    // Many tokens: four heads a thread, all in flight (4096 tokens of 40 + 2 * 8 heads: 20.9
+    // Many tokens: four heads a thread, all in flight (4096 tokens of 40 + 2 * 8 heads: 20.4
     // us; three 26.6, two 24.6).  Few tokens: one head a thread over as many blocks
     // as that takes, for the shortest way through.
     const bool one = p.T * heads * L <= (int64_t)sm_count() * 1024;

@@ -334,9 +334,10 @@ nvfp4_status launch_norm(const NormParams& p, bool f16, cudaStream_t stream) {
     dim3 block(p.H > 4096 ? 1024 : 256);
     if (rows) {
         // Rows that fill the GPU take four pieces a thread: loads in flight, few threads
-        // to join and few scales' quotients (8192x8192: one 84.6 us, two 78.5, four 78.9;
-        // 500x4096 two 3.5, four 3.0; 8192x8192 to E4M3 two 85, four 71.7).  Few rows take
-        // as many threads as they have pieces, for the shortest way through one.
+        // to join and few scales' quotients (8192x8192: one 84.9 us, four 79.1; 500x4096 3.12
+        // and 2.95; 8192x8192 to E4M3 91.5 and 71.5).  Few rows take as many threads as they
+        // have pieces: that is for narrow ones (1x1024 1.41 us with one, 1.49 with four; to
+        // E4M3 with groups of 128 1.56 and 1.90); wide ones lose by it (1x8192 2.31 and 2.01).
         int V = p.T <= sm_count() * 2 ? 1 : 4;
         while (pieces > norm_threads(V) * V) V = V == 1 ? 4 : 8;
         block = dim3((unsigned)round_up(ceil_div(pieces, V), 32));

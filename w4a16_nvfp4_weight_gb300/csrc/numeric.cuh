@@ -89,7 +89,7 @@ __device__ __forceinline__ float e4m3_inverse(float s) {
     return y;
 }
 
-// Two 32-bit values an instruction.
+// Two 32-bit values: products and fused ones take one instruction for both.
 struct F2 { uint64_t v; };
 __device__ __forceinline__ F2 make_f2(float lo, float hi) {
     F2 r;

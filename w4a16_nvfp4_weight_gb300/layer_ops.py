@@ -71,7 +71,7 @@ def rope_cache_write(q, k, v, positions, table, k_cache, v_cache, slots, k_scale
     with several axes.  ``table``: float32 [rows, rot] (rope_table); elements from
     rot on are not rotated.  Pairs are (i, i + rot/2), or (2i, 2i + 1) when
     ``interleaved``.  Two tokens must not share a slot.  A position outside the
-    table leaves its elements unrotated, a slot outside the cache is not written,
+    table turns its elements by an angle of zero, a slot outside the cache is not written,
     and device_status() then reports 8."""
     return _ops.rope_cache_write(q, k, v, positions, table, k_cache, v_cache, slots, k_scale, v_scale, sections, interleaved,
                                  q_out)
