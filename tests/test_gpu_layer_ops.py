@@ -897,3 +897,29 @@ def test_norm_of_wide_rows(T, H, act):
 @pytest.mark.parametrize("T,Hq,Hkv,D,rot,sections", [(3000, 8, 2, 80, 40, None), (2900, 9, 3, 112, 56, [10, 9, 9]), (1500, 24, 1, 256, 136, [1, 67])])
 def test_rope_interleaved_in_pieces_of_four_with_many_heads_a_thread(T, Hq, Hkv, D, rot, sections, act, kind):
     test_rope_cache_write_and_read(T, Hq, Hkv, D, rot, 16, sections, True, act, kind, "hnd")
+
+
+@pytest.mark.parametrize("gap", [0.3, 0.55, 0.8])
+@pytest.mark.parametrize("G,D", [(1, 64), (4, 128), (8, 128), (2, 256)])
+def test_paged_attention_weights_keep_their_bits_over_e4m3_caches(G, D, gap):
+    """As over 16-bit caches, of an FP16 output (BF16's rounding is eight times that of the weights):
+    rows of one scale, so that a rounding of weight times scale would move every output alike."""
+    c, q, table, lengths, slots = _attention_case([1500, 400, 17], G * 2, 2, D, 16, "f16", "e4m3", 96)
+    T = slots.numel()
+    k = torch.zeros(T, 2, D, dtype=torch.float16, device="cuda")
+    t = torch.cat([torch.arange(m) for m in lengths.tolist()]).cuda()
+    k[:, :, 0] = (t % 16 == 0)[:, None] * gap
+    v = (1.5 + 0.1 * torch.randn(T, 2, D, generator=_gen(97), device="cuda")).clamp(0, 1.9).half()
+    v[:, :, 5] = 2.0
+    nv.rope_cache_write(k, k, v, slots, nv.rope_table(1, 0), slots=slots, **c)
+    q = torch.zeros_like(q)
+    q[:, :, 0] = 1
+    out = _np(nv.paged_attention(q, block_table=table, lengths=lengths, softmax_scale=1.0, **c))
+    gu.check_device_status()
+    kk, vv = _cached_values(c, "k", slots, 16), _cached_values(c, "v", slots, 16)
+    at = 0
+    for b, n in enumerate(lengths.tolist()):
+        ref, _, mag = layer.attend(_np(q[b]), kk[at:at + n], vv[at:at + n], 1.0)
+        at += n
+        bound = _half_step(ref, "f16") + 2.0 ** -15 * mag
+        assert np.all(np.abs(out[b] - ref) <= bound), (b, (np.abs(out[b] - ref) / bound).max())

@@ -30,8 +30,9 @@
 //    are joined per block in shared memory, and across blocks by a second
 //    small kernel, in the order of the tokens: the result does not depend on timing.
 // Roundings: the softmax weights meet the values in the MMA as 16 bits, BF16 for
-// a BF16 cache, else FP16, and 16-bit values as two such halves (exact_weights below): a relative 2^-16 or
-// 2^-22 of each weight.  Where there is one, 2^-8 or 2^-11, while l keeps the 32-bit ones.  FP16 weights
+// a BF16 cache, else FP16, and but for two shapes that exact_weights below excepts as two such
+// halves wherever one rounding would show in the output: a relative 2^-16 or 2^-21 of each weight,
+// where there is one half 2^-8 or 2^-11, while l keeps the 32-bit ones.  FP16 weights
 // are taken 2^11 larger, so that one keeps its 11 bits down to 2^-25 of the largest (and
 // below, where the values are FP16: the base follows).  E4M3 codes are exact in FP16; a
 // BF16 query meets them as FP16 after a power of two that puts its largest element at
@@ -106,15 +107,16 @@ struct AttnParams {
 constexpr int attn_warps(int row, int values) { return row > 256 ? 4 : row > 128 ? 8 : values >= 64 ? 12 : 16; }
 constexpr int attn_stages(int row, int values) { return row == 128 && values >= 64 ? 4 : 3; }
 
-// 16-bit values are met by both halves of a weight, the larger one and what that left: the
-// output is then as near the formula as 32-bit weights would bring it (64 x 16384 tokens of BF16: 1.0
-// times the error of a plain form in 32 bits, with rounded weights 1.4).  Loads hide the
-// second product (64 x 16384 of BF16 326 us with and without, of FP16 329 and 327; 32 x 16384 of
-// 16 heads a key head 177.6 and 175.3; 1 x 1000 7.05 and 6.98) but for 16 heads a key head of
-// 256, whose four warps an SM wait for their products: 233 us with, 214 without; those keep
-// rounded weights.  So do E4M3 values: they are off by
-// 2^-4 themselves, and the instances are short of instructions.
-constexpr bool exact_weights(bool e4m3, int values) { return !e4m3 && values <= 64; }
+// Where a weight rounded as its values are would show beside the output's own rounding (16-bit
+// values; E4M3 ones with an FP16 output, whose weights are FP16), the values are met by both
+// halves of it, the larger one and what that left: the output is then as near the formula as
+// 32-bit weights would bring it (64 x 16384 tokens of BF16: 1.0 times the error of a plain form
+// in 32 bits, with rounded weights 1.4).  Loads hide the second product: 64 x 16384 of
+// BF16 326 us with and without, of FP16 329 and 327; 32 x 16384 of 16 heads a key head 177.6 and
+// 175.3; 1 x 1000 7.05 and 6.98; E4M3 16 x 4096 19.5 and 18.9, 64 x 8192 179 and 185.
+// Not where two tiles of heads wait for their products: 16 heads a key head of 256 in 16 bits
+// 233 us with, 214 without; E4M3 96 on 8 heads 130 and 113.  Those keep rounded weights.
+constexpr bool exact_weights(bool f16, bool e4m3, int DP, int NT) { return e4m3 ? f16 && NT == 1 : DP / 4 * NT <= 64; }
 // The larger half is a weight times this, rounded towards zero: what it leaves is above zero
 // then, in 16 bits too (down to 2^-14 in FP16), so that an infinite value gives an infinity, not a NaN.
 template <bool F16>
@@ -137,7 +139,8 @@ struct Shape {
     static constexpr int kStages = attn_stages(kRow, DP / 4 * NT);
     static constexpr int kRing = kStages * kStage;
     static constexpr size_t kSmem = (size_t)kWarps * kRing;
-    static constexpr bool kExact = exact_weights(E4M3, DP / 4 * NT);
+    template <bool F16>
+    static constexpr bool kExact = exact_weights(F16, E4M3, DP, NT);
     static constexpr int kHeads = 8 * NT;
     static constexpr int kPart = kHeads * (DP + 2);             // floats of a partial result: o, m, l
     static constexpr int kPitch = DP + 4;                       // floats from head to head in shared memory
@@ -378,7 +381,7 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
     constexpr bool H = F16 || E4M3;                             // FP16 operands in the MMAs
     constexpr bool FALLS = F16 && !E4M3;                        // the base may fall, too
     constexpr float LIFT = H ? kLift : 0.f;
-    constexpr bool REST = S::kExact;
+    constexpr bool REST = S::template kExact<F16>;
     extern __shared__ __align__(1024) uint8_t ring_all[];
     __shared__ int first_sm[W * 32], sums[W];
     // Pieces of units, two a warp: the rest of a unit that an earlier warp began, and the last of the range.
@@ -742,14 +745,14 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
                     // heads on the MMA's columns: transpose the 8x8 blocks
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        const float a = w[2 * y], b = w[2 * y + 1];
+                        const float a = w[2 * y] * v_by[tb][y], b = w[2 * y + 1] * v_by[tb][y];
                         if constexpr (REST) {
                             const uint32_t most = f32_to_act2_down<H>(a * kMost<H>, b * kMost<H>);
                             const float2 u = act2_to_f32<H>(most);
                             pf[tb][nt][y] = movmatrix(most);
                             pr[tb][nt][y] = movmatrix(f32_to_act2<H>(a - u.x, b - u.y));
                         } else {
-                            pf[tb][nt][y] = movmatrix(f32_to_act2<H>(a * v_by[tb][y], b * v_by[tb][y]));
+                            pf[tb][nt][y] = movmatrix(f32_to_act2<H>(a, b));
                         }
                     }
                 }
@@ -797,8 +800,10 @@ __global__ void __launch_bounds__(Shape<E4M3, DP, NT>::kWarps * 32, 1) attend_ke
                                 const uint32_t af[4] = {e4m3x2_to_f16x2((uint16_t)lo), e4m3x2_to_f16x2((uint16_t)(lo >> 16)),
                                                         e4m3x2_to_f16x2((uint16_t)hi), e4m3x2_to_f16x2((uint16_t)(hi >> 16))};
 #pragma unroll
-                                for (int nt = 0; nt < NT; ++nt)
+                                for (int nt = 0; nt < NT; ++nt) {
                                     mma_16816<H>(o[j * 8 + w * 2 + half][nt], af, pf[tb][nt][0], pf[tb][nt][1]);
+                                    if constexpr (REST) mma_16816<H>(o[j * 8 + w * 2 + half][nt], af, pr[tb][nt][0], pr[tb][nt][1]);
+                                }
                             }
                     }
                 }
