@@ -542,6 +542,117 @@ nvfp4_status nvfp4_paged_attention(const void* q, int64_t q_row_stride, int64_t 
                                    void* out, float* lse, void* workspace, size_t workspace_bytes,
                                    void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* What differs from request to request: pages, adapters, the next token      */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * Page tables of a batch, on the device.  Request b has lengths[b] tokens in the pages
+ * block_table[b][0 .. ceil(lengths[b] / page_size)), and gets new_tokens[b] more, rows
+ * starts[b] to starts[b + 1] of the batch.  Pages that these need are taken from the top
+ * of the stack free_pages[0 .. *free_count), in the order of the requests, and entered in
+ * the table.  Row i of request b's new tokens has
+ *     position = lengths[b] + i,
+ *     slot = block_table[b][position / page_size] * page_size + position % page_size,
+ * as nvfp4_rope_cache_write and nvfp4_kv_cache_read take them.
+ * A request is not served where its new length does not fit its row of the table, its rows end
+ * behind `rows`, or its pages and those asked for before it are more than the stack
+ * holds: it keeps its length (lengths_out[b] == lengths[b]), and its rows have slot -1.
+ * Rows behind the last token have position 0, slot -1 and request -1.
+ *  lengths, new_tokens  device int32 [B].  B is at most 16384.
+ *  block_table   device int32 [B, table_width], rows table_stride apart; new pages are
+ *                written, nothing else.
+ *  free_pages    device int32 [num_free]; free_count device int32 [1].
+ *  positions, slots  device int64 [rows]; request device int32 [rows]; starts device
+ *                int32 [B + 1] (at most `rows`).
+ *  lengths_out   device int32 [B], may be lengths; free_count_out device int32 [1], may be
+ *                free_count.
+ *  row_lengths   device int32 [rows] or NULL: position + 1, 0 where the slot is -1.
+ *  row_tables    device int32 [rows, table_width] or NULL (needs row_lengths): the pages of
+ *                the row's request up to that length, then zeros -- with row_lengths what
+ *                nvfp4_paged_attention takes for several new tokens of one request.
+ * A negative length or number of new tokens (that request is not served) and a count
+ * outside [0, num_free] (taken as the nearest end) record NVFP4_ERR_BAD_INDEX in the status
+ * word.  Other outputs over inputs or each other are refused.
+ */
+nvfp4_status nvfp4_extend_tables(const int32_t* lengths, const int32_t* new_tokens, int64_t B, int32_t* block_table,
+                                 int64_t table_stride, int64_t table_width, const int32_t* free_pages, int64_t num_free,
+                                 const int32_t* free_count, int64_t page_size, int64_t rows, int64_t* positions,
+                                 int64_t* slots, int32_t* request, int32_t* starts, int32_t* lengths_out,
+                                 int32_t* free_count_out, int32_t* row_tables, int32_t* row_lengths, void* stream);
+
+/*
+ * Shorten requests to min(lengths, keep) tokens (0: ended; fewer than it has: drafts that
+ * were not accepted) and put the pages behind that on the stack, in the order of the
+ * requests and of their pages.  Tensors as above; the table is only read, and its
+ * entries stay.  A negative length or keep (that request stays as it is), pages behind the table's
+ * width or the stack's end (dropped) and a count outside [0, num_free] record
+ * NVFP4_ERR_BAD_INDEX in the status word.
+ */
+nvfp4_status nvfp4_trim_tables(const int32_t* lengths, const int32_t* keep, int64_t B, const int32_t* block_table,
+                               int64_t table_stride, int64_t table_width, int32_t* free_pages, int64_t num_free,
+                               const int32_t* free_count, int64_t page_size, int32_t* lengths_out, int32_t* free_count_out,
+                               void* stream);
+
+/*
+ * Low-rank adapters of many requests at once, beside a projection that all share:
+ *     out_t = RN(y_t + scales[a] * B[a] (A[a] x_t)),  a = adapters[t];  a < 0: out_t = y_t.
+ * The rows of an adapter need not lie side by side.  A x is held in 32 bits and meets B as two
+ * 16-bit halves, so the one rounding is that of the output.
+ *  y, x          device BF16 (FP16 with f16 = 1) [T, N] and [T, K], rows y_stride / x_stride
+ *                elements apart; any alignment (16-byte rows run on vector loads).
+ *  A, B          device [num_adapters, r, K] and [num_adapters, N, r], the same type, dense.  An
+ *                adapter of a smaller rank is padded with zeros.
+ *  scales        device FP32 [num_adapters], or NULL: 1.
+ *  adapters      device int32 [T].  One that is not below num_adapters counts as none and records
+ *                NVFP4_ERR_BAD_INDEX in the status word.
+ *  out           device [T, N], dense.  It may be y where that is dense; over anything else
+ *                it is refused.
+ *  workspace     device, >= nvfp4_lora_workspace(...) bytes, 256-byte aligned.  Contents on
+ *                entry do not matter.
+ * r is at most 256, num_adapters at most 4096.  T == 0 or N == 0 launches nothing.  Repeated
+ * calls on the same inputs give the same bits.
+ */
+size_t nvfp4_lora_workspace(int64_t T, int64_t num_adapters, int64_t r, int64_t K);
+nvfp4_status nvfp4_lora_add(const void* y, int64_t y_stride, const void* x, int64_t x_stride, const void* A, const void* B,
+                            const float* scales, const int32_t* adapters, int64_t T, int64_t num_adapters, int64_t r, int64_t K,
+                            int64_t N, int f16, void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Type of a row of logits. */
+typedef enum { NVFP4_LOGITS_BF16 = 0, NVFP4_LOGITS_F16 = 1, NVFP4_LOGITS_F32 = 2 } nvfp4_logits_type;
+
+/* How to draw: device arrays with a value a row, or NULL and one value for all rows. */
+typedef struct {
+    const float* temperature;
+    const int32_t* top_k;
+    const float* top_p;
+    const float* min_p;
+    float temperature_all;
+    int32_t top_k_all;
+    float top_p_all, min_p_all;
+} nvfp4_sampling;
+
+/*
+ * Draw a token of each row.  With w_i = exp((l_i - max l) / temperature), kept are
+ *  - the top_k largest logits (0 or less: all), equal ones ranked by index,
+ *  - of these the shortest prefix, in that order, with at least top_p of their mass (1 or
+ *    more: all; at least one),
+ *  - of these those with w_i >= min_p (0 or less: all; the largest logits stay),
+ * and the token is the first kept one, by index, at which the running sum of w passes u
+ * times the sum over all kept.  A temperature that is not above zero: the largest logit,
+ * the first of equal ones.  NaN and -infinity are never drawn; where there is nothing
+ * else the token is -1 (log-probability -infinity).  Logits of +infinity share the draw.
+ *  logits        device [B, V], rows row_stride elements apart, any alignment; V at most 2^20.
+ *  u             device FP32 [B], in [0, 1) (below: 0, above: the last kept token).
+ *  how           host; its arrays are device arrays of B values.
+ *  tokens        device int64 [B].
+ *  logprobs      device FP32 [B] or NULL: log of the token's share of the kept mass.
+ * Weights are whole numbers of 2^-43, right to about 2^-32 of their value; their sums are exact,
+ * so the result does not depend on how the work is split.
+ */
+nvfp4_status nvfp4_sample(const void* logits, int64_t row_stride, int type, int64_t B, int64_t V, const float* u,
+                          const nvfp4_sampling* how, int64_t* tokens, float* logprobs, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -29,6 +29,7 @@ Modules:
 * ``formats``  -- E2M1 / E4M3 decoding, global-scale inversion, BF16 rounding.
 * ``dense``    -- dequantization, AWQ activation scaling, the GEMM.
 * ``moe``      -- top-k routing, permutation tables, FC1+SwiGLU, FC2, combine.
+* ``batch``    -- page tables and slots, adapters, the draw of a token.
 * ``layer``    -- RMS norm, E4M3 rows, rotary positions, attention of one token.
 
 Parity status of every function is stated in its docstring; every function is
@@ -36,4 +37,4 @@ pinned by ``tests/test_oracle_*.py`` against worked values, closed forms,
 library routines or brute force on tiny inputs.
 """
 
-from . import formats, dense, layer, moe  # noqa: F401
+from . import batch, formats, dense, layer, moe  # noqa: F401

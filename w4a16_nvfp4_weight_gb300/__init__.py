@@ -11,7 +11,8 @@ in the library's CUDA kernels; there is no Python or CPU fallback.
     y = gemm(x_fp16, w)                       # FP16 activations: FP16 weights and output
 
 and, between the linears (layer_ops): rms_norm, rms_norm_e4m3, rope_cache_write,
-cache_read and paged_attention.
+cache_read and paged_attention; and for the requests of a batch (batch_ops):
+extend_tables, trim_tables, lora_add and sample.
 
 The activation dtype (torch.bfloat16 or torch.float16) selects the entry
 point (nvfp4_w4a16_gemm or nvfp4_w4a16_gemm_f16, and likewise for the MoE
@@ -24,6 +25,7 @@ import torch
 
 from . import _lib
 from ._lib import Nvfp4Error
+from .batch_ops import extend_tables, lora_add, lora_workspace_size, sample, trim_tables
 from .layer_ops import (cache_read, paged_attention, paged_attention_workspace_size, rms_norm, rms_norm_e4m3,
                         rope_cache_write, rope_table)
 
@@ -33,6 +35,7 @@ __all__ = ["Nvfp4Error", "NVFP4Weight", "repack", "repack_size", "swizzled_scale
            "mlp", "mlp_workspace_size",
            "rms_norm", "rms_norm_e4m3", "rope_table", "rope_cache_write", "cache_read",
            "paged_attention", "paged_attention_workspace_size",
+           "extend_tables", "trim_tables", "lora_add", "lora_workspace_size", "sample",
            "device_status",
            "abi_version"]
 

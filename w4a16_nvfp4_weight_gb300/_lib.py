@@ -26,6 +26,12 @@ class KVCache(ctypes.Structure):
                 ("page_stride", c_i64), ("head_stride", c_i64), ("token_stride", c_i64), ("type", c_i64)]
 
 
+class Sampling(ctypes.Structure):
+    """nvfp4_sampling of the header."""
+    _fields_ = [("temperature", c_vp), ("top_k", c_vp), ("top_p", c_vp), ("min_p", c_vp), ("temperature_all", c_float),
+                ("top_k_all", ctypes.c_int32), ("top_p_all", c_float), ("min_p_all", c_float)]
+
+
 c_cache = ctypes.POINTER(KVCache)
 
 # name -> (restype, argtypes), mirroring include/nvfp4_w4a16.h
@@ -68,6 +74,12 @@ SIGNATURES = {
     "nvfp4_paged_attention_workspace": (c_size, [c_i64, c_i64, c_i64, c_i64]),
     "nvfp4_paged_attention": (c_int, [c_vp, c_i64, c_i64, c_cache, c_vp, c_i64, c_i64, c_vp, c_i64, c_i64, c_float,
                                       c_i64, c_int, c_vp, c_vp, c_vp, c_size, c_vp]),
+    "nvfp4_extend_tables": (c_int, [c_vp, c_vp, c_i64, c_vp, c_i64, c_i64, c_vp, c_i64, c_vp, c_i64, c_i64] + [c_vp] * 9),
+    "nvfp4_trim_tables": (c_int, [c_vp, c_vp, c_i64, c_vp, c_i64, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_vp]),
+    "nvfp4_lora_workspace": (c_size, [c_i64, c_i64, c_i64, c_i64]),
+    "nvfp4_lora_add": (c_int, [c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_i64, c_i64, c_int,
+                               c_vp, c_vp, c_size, c_vp]),
+    "nvfp4_sample": (c_int, [c_vp, c_i64, c_int, c_i64, c_i64, c_vp, ctypes.POINTER(Sampling), c_vp, c_vp, c_vp]),
 }
 
 STATUS_NAMES = {

@@ -1,5 +1,5 @@
-// Python entry points of the operators between the linears (layer_ops.py names
-// and documents them): argument checks, outputs and workspaces from torch's
+// Python entry points of the operators between the linears and around a batch
+// (layer_ops.py and batch_ops.py name and document them): argument checks, outputs and workspaces from torch's
 // allocator, then the C ABI of include/nvfp4_w4a16.h on the current stream.
 //
 // These calls are short (a decode step makes a few hundred of them), and a
@@ -8,6 +8,7 @@
 // the call about 6 with its launches.
 #include <Python.h>
 
+#include <algorithm>
 #include <cmath>
 #include <initializer_list>
 #include <limits>
@@ -339,6 +340,141 @@ PyObject* paged_attention(PyObject* const* a) {
     return with_lse ? result({out, lse}) : result({out});
 }
 
+// The requests' lengths, block table and stack of free pages of a call.
+struct Pool {
+    const at::Tensor *lengths, *table, *pages, *count;
+    int64_t B, width, page;
+
+    Pool(const Call& c, const at::Tensor& n, PyObject* table_, PyObject* pages_, PyObject* count_, PyObject* page_) {
+        if (n.dim() != 1) refuse(2, "lengths must be [B], got " + shape_text(n.sizes()));
+        B = n.size(0);
+        lengths = &c.check(n, "lengths", at::kInt, {B});
+        table = &tensor(table_, "block_table");
+        if (table->dim() != 2) refuse(2, "block_table must be a tensor [B, width]");
+        width = table->size(1);
+        c.check(*table, "block_table", at::kInt, {B, width}, false);
+        pages = &tensor(pages_, "free_pages");
+        if (pages->dim() != 1) refuse(2, "free_pages must be a tensor [P]");
+        c.check(*pages, "free_pages", at::kInt, pages->sizes());
+        count = &c.check(tensor(count_, "free_count"), "free_count", at::kInt, {1});
+        page = integer(page_, "page_size");
+    }
+};
+
+// (lengths, new_tokens, block_table, free_pages, free_count, page_size, rows, row_tables, in_place)
+PyObject* extend_tables(PyObject* const* a) {
+    const at::Tensor& n = tensor(a[0], "lengths");
+    Call c(n, "lengths", false);
+    const Pool pool(c, n, a[2], a[3], a[4], a[5]);
+    const at::Tensor& m = c.check(tensor(a[1], "new_tokens"), "new_tokens", at::kInt, {pool.B});
+    const int64_t rows = integer(a[6], "rows");
+    if (rows < 0) refuse(1, "rows must not be negative, got " + std::to_string(rows));
+    const int tables = PyObject_IsTrue(a[7]), in_place = PyObject_IsTrue(a[8]);
+    if (tables < 0 || in_place < 0) throw PythonError{};
+    at::Tensor positions = c.output(Py_None, "", at::kLong, {rows}), slots = c.output(Py_None, "", at::kLong, {rows});
+    at::Tensor request = c.output(Py_None, "", at::kInt, {rows}), starts = c.output(Py_None, "", at::kInt, {pool.B + 1});
+    at::Tensor lengths = in_place ? n : c.output(Py_None, "", at::kInt, {pool.B});
+    at::Tensor count = in_place ? *pool.count : c.output(Py_None, "", at::kInt, {1});
+    at::Tensor row_tables, row_lengths;
+    if (tables) {
+        row_tables = c.output(Py_None, "", at::kInt, {rows, pool.width});
+        row_lengths = c.output(Py_None, "", at::kInt, {rows});
+    }
+    done(nvfp4_extend_tables((const int32_t*)n.data_ptr(), (const int32_t*)m.data_ptr(), pool.B, (int32_t*)pool.table->data_ptr(), step(*pool.table, 0),
+                             pool.width, (const int32_t*)pool.pages->data_ptr(), pool.pages->numel(), (const int32_t*)pool.count->data_ptr(),
+                             pool.page, rows, (int64_t*)positions.data_ptr(), (int64_t*)slots.data_ptr(), (int32_t*)request.data_ptr(),
+                             (int32_t*)starts.data_ptr(), (int32_t*)lengths.data_ptr(), (int32_t*)count.data_ptr(),
+                             tables ? (int32_t*)row_tables.data_ptr() : nullptr, tables ? (int32_t*)row_lengths.data_ptr() : nullptr, c.stream()));
+    if (tables) return result({positions, slots, request, starts, lengths, count, row_tables, row_lengths});
+    return result({positions, slots, request, starts, lengths, count});
+}
+
+// (lengths, keep, block_table, free_pages, free_count, page_size, in_place)
+PyObject* trim_tables(PyObject* const* a) {
+    const at::Tensor& n = tensor(a[0], "lengths");
+    Call c(n, "lengths", false);
+    const Pool pool(c, n, a[2], a[3], a[4], a[5]);
+    const at::Tensor& keep = c.check(tensor(a[1], "keep"), "keep", at::kInt, {pool.B});
+    const int in_place = PyObject_IsTrue(a[6]);
+    if (in_place < 0) throw PythonError{};
+    at::Tensor lengths = in_place ? n : c.output(Py_None, "", at::kInt, {pool.B});
+    at::Tensor count = in_place ? *pool.count : c.output(Py_None, "", at::kInt, {1});
+    done(nvfp4_trim_tables((const int32_t*)n.data_ptr(), (const int32_t*)keep.data_ptr(), pool.B, (const int32_t*)pool.table->data_ptr(),
+                           step(*pool.table, 0), pool.width, (int32_t*)pool.pages->data_ptr(), pool.pages->numel(),
+                           (const int32_t*)pool.count->data_ptr(), pool.page, (int32_t*)lengths.data_ptr(), (int32_t*)count.data_ptr(), c.stream()));
+    return result({lengths, count});
+}
+
+// (y, x, a, b, adapters, scales, out, workspace)
+PyObject* lora_add(PyObject* const* a) {
+    const at::Tensor& y = tensor(a[0], "y");
+    Call c(y, "y");
+    if (y.dim() != 2) refuse(2, "y must be [T, N], got " + shape_text(y.sizes()));
+    c.rows(y, "y");
+    const int64_t T = y.size(0), N = y.size(1);
+    const at::Tensor &x = tensor(a[1], "x"), &down = tensor(a[2], "a"), &up = tensor(a[3], "b");
+    if (down.dim() != 3) refuse(2, "a must be [adapters, r, K], got " + shape_text(down.sizes()));
+    const int64_t n = down.size(0), r = down.size(1), K = down.size(2);
+    c.check(down, "a", c.act, down.sizes());
+    c.check(up, "b", c.act, {n, N, r});
+    c.check(x, "x", c.act, {T, K}, false);
+    const at::Tensor& ids = c.check(tensor(a[4], "adapters"), "adapters", at::kInt, {T});
+    const at::Tensor* scales = tensor_or_none(a[5], "scales");
+    if (scales) c.check(*scales, "scales", at::kFloat, {n});
+    at::Tensor out = c.output(a[6], "out", c.act, y.sizes());
+    size_t ws_bytes = nvfp4_lora_workspace(T, n, r, K);
+    void* ws = nullptr;
+    c10::DataPtr held;                                          // given back after the launches, in stream order
+    if (const at::Tensor* t = tensor_or_none(a[7], "workspace")) {
+        c.check(*t, "workspace", at::kByte, t->sizes());
+        ws = t->data_ptr();
+        ws_bytes = (size_t)t->numel();
+    } else if (ws_bytes) {
+        held = c10::cuda::CUDACachingAllocator::get()->allocate(ws_bytes);
+        ws = held.get();
+    }
+    done(nvfp4_lora_add(y.data_ptr(), step(y, 0), x.data_ptr(), step(x, 0), down.data_ptr(), up.data_ptr(),
+                        scales ? (const float*)scales->data_ptr() : nullptr, (const int32_t*)ids.data_ptr(), T, n, r, K, N, c.f16, out.data_ptr(),
+                        ws, ws_bytes, c.stream()));
+    return result({out});
+}
+
+// (logits, u, temperature, top_k, top_p, min_p, return_logprob, out, logprob)
+PyObject* sample(PyObject* const* a) {
+    const at::Tensor& logits = tensor(a[0], "logits");
+    Call c(logits, "logits", false);
+    const auto t = logits.scalar_type();
+    if (t != at::kBFloat16 && t != at::kHalf && t != at::kFloat)
+        refuse(1, "logits must be torch.bfloat16, torch.float16 or torch.float32, got " + type_text(t));
+    if (logits.dim() != 2) refuse(2, "logits must be [B, V], got " + shape_text(logits.sizes()));
+    c.rows(logits, "logits");
+    const int64_t B = logits.size(0), V = logits.size(1);
+    const at::Tensor& u = c.check(tensor(a[1], "u"), "u", at::kFloat, {B});
+    nvfp4_sampling how{};
+    // A tensor [B], or one number for all rows.
+    const auto setting = [&](PyObject* o, Name name, const float** each, float* all) {
+        if (THPVariable_Check(o)) *each = (const float*)c.check(THPVariable_Unpack(o), name, at::kFloat, {B}).data_ptr();
+        else *all = real(o, name);
+    };
+    setting(a[2], "temperature", &how.temperature, &how.temperature_all);
+    setting(a[4], "top_p", &how.top_p, &how.top_p_all);
+    setting(a[5], "min_p", &how.min_p, &how.min_p_all);
+    if (THPVariable_Check(a[3])) {
+        how.top_k = (const int32_t*)c.check(THPVariable_Unpack(a[3]), "top_k", at::kInt, {B}).data_ptr();
+    } else {
+        const int64_t k = integer(a[3], "top_k");
+        how.top_k_all = (int32_t)std::min<int64_t>(std::max<int64_t>(k, 0), std::numeric_limits<int32_t>::max());
+    }
+    const int with_logprob = PyObject_IsTrue(a[6]);
+    if (with_logprob < 0) throw PythonError{};
+    at::Tensor out = c.output(a[7], "out", at::kLong, {B}), logprob;
+    if (with_logprob || a[8] != Py_None) logprob = c.output(a[8], "logprob", at::kFloat, {B});
+    done(nvfp4_sample(logits.data_ptr(), step(logits, 0), t == at::kBFloat16 ? NVFP4_LOGITS_BF16 : t == at::kHalf ? NVFP4_LOGITS_F16 : NVFP4_LOGITS_F32,
+                      B, V, (const float*)u.data_ptr(), &how, (int64_t*)out.data_ptr(), logprob.defined() ? (float*)logprob.data_ptr() : nullptr,
+                      c.stream()));
+    return with_logprob ? result({out, logprob}) : result({out});
+}
+
 // Argument count, and every C++ exception as a Python one.
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -383,6 +519,10 @@ PyMethodDef methods[] = {
     ENTRY(rope_cache_write, 13),
     ENTRY(cache_read, 8),
     ENTRY(paged_attention, 13),
+    ENTRY(extend_tables, 9),
+    ENTRY(trim_tables, 7),
+    ENTRY(lora_add, 8),
+    ENTRY(sample, 9),
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_nvfp4_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -1,0 +1,30 @@
+// One launch, with clusters where asked, that may begin while the kernel before it
+// in the stream ends (the kernels wait for it themselves, pdl_wait_previous).
+#pragma once
+
+#include "common.cuh"
+
+namespace nvfp4 {
+
+inline nvfp4_status launch_kernel(const void* kernel, dim3 grid, dim3 block, size_t smem, unsigned cluster, void** args,
+                                  cudaStream_t stream, const char* fn) {
+    if (smem > 48 * 1024)
+        if (nvfp4_status st = check_cuda(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem), fn)) return st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return check_cuda(cudaLaunchKernelExC(&cfg, kernel, args), fn);
+}
+
+}  // namespace nvfp4

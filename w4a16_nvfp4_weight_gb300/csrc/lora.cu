@@ -1,0 +1,436 @@
+// Low-rank adapters of many requests at once, beside a projection that all share:
+//     out_t = RN(y_t + s_a B_a (A_a x_t)),  a = adapters[t]  (a < 0: out_t = y_t).
+// x, y, A and B are 16-bit; A x and its sums are held in 32 bits and meet B as two 16-bit halves
+// (2^-16 of a value for BF16, 2^-21 for FP16 or better), so the output is rounded once.
+//
+// Three launches.  Rows are grouped by adapter into items of up to 16 or 64 rows of one
+// adapter (rows of a request need not lie side by side).  The down kernel multiplies
+// an item's rows with A, the long axis K split over blocks and warps; the up kernel adds
+// the splits' sums in their order (no atomics: the same bits every time), multiplies with
+// B and adds y.  Both products are mma.sync m16n8k16: at rank r they do r flop for each
+// byte of x or y that they read or write, far below what would need tcgen05, and the
+// operands go straight from memory to registers: an order of k that is the same for both operands
+// lets a thread load 16 bytes of each row, and an order of the columns 16 bytes of y.
+#include <algorithm>
+
+#include "common.cuh"
+#include "launch.cuh"
+#include "numeric.cuh"
+#include "overlap.cuh"
+#include "ptx.cuh"
+#include "stream_mma.cuh"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kMaxAdapters = 4096;
+constexpr int kMaxRank = 256;
+constexpr int kDownWarps = 4;
+constexpr int kUpWarps = 4;
+constexpr int kMaxSplits = 16;
+
+struct Item { int32_t adapter, first, rows, pad; };      // rows order[first .. first + rows)
+
+struct LoraParams {
+    const uint16_t *x, *a, *b, *y;
+    const int32_t* adapters;
+    const float* scales;                   // null: 1
+    uint16_t* out;
+    int64_t T, K, N, x_stride, y_stride;
+    int n, r, rp;                          // adapters, rank, rank rounded up to 16
+    int splits, k_split;                   // of K, and its elements a split (a multiple of 32)
+    int rows_item;                         // 16 or 64
+    int copy_rest;                         // rows without an adapter are copied
+    int32_t* num_items;
+    Item* items;
+    int32_t* order;                        // [T] rows by adapter
+    float* low;                            // [splits, T, rp] A x, in that order of rows
+    int* status;
+};
+
+// Rows by adapter, and items of them.  One block.
+__global__ void __launch_bounds__(1024) lora_group_kernel(const LoraParams p) {
+    extern __shared__ int32_t sm_groups[];
+    __shared__ int32_t warp_sum[2][32];
+    int32_t* count = sm_groups;            // [n + 1] rows of each adapter; the last: without one
+    int32_t* place = count + p.n + 1;      // [n + 1] where the next of them goes
+    pdl_wait_previous();
+    pdl_launch_dependents();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, groups = p.n + 1;
+    for (int g = tid; g < groups; g += blockDim.x) count[g] = 0;
+    __syncthreads();
+    const auto group_of = [&](int64_t t) {
+        const int a = p.adapters[t];
+        return a < 0 || a >= p.n ? p.n : a;
+    };
+    for (int64_t t = tid; t < p.T; t += blockDim.x) {
+        if (p.adapters[t] >= p.n) record_status(p.status, NVFP4_ERR_BAD_INDEX);
+        atomicAdd(&count[group_of(t)], 1);
+    }
+    __syncthreads();
+    // Exclusive sums of rows and items over the groups, a run of groups a thread.
+    const int per = (groups + blockDim.x - 1) / blockDim.x, g0 = min(tid * per, groups), g1 = min(g0 + per, groups);
+    int rows = 0, items = 0;
+    for (int g = g0; g < g1; ++g) {
+        rows += count[g];
+        items += (count[g] + p.rows_item - 1) / p.rows_item;
+    }
+    int r = rows, i = items;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, r, o), v = __shfl_up_sync(0xffffffffu, i, o);
+        if (lane >= o) {
+            r += u;
+            i += v;
+        }
+    }
+    if (lane == 31) {
+        warp_sum[0][warp] = r;
+        warp_sum[1][warp] = i;
+    }
+    __syncthreads();
+    r -= rows;
+    i -= items;
+    for (int w = 0; w < warp; ++w) {
+        r += warp_sum[0][w];
+        i += warp_sum[1][w];
+    }
+    for (int g = g0; g < g1; ++g) {
+        place[g] = r;
+        const int adapter = g == p.n ? -1 : g;
+        for (int at = 0; at < count[g]; at += p.rows_item)
+            p.items[i++] = Item{adapter, r + at, min(p.rows_item, count[g] - at), 0};
+        r += count[g];
+    }
+    if (tid == blockDim.x - 1) *p.num_items = i;            // the threads past the last group hold the sum, too
+    __syncthreads();
+    for (int64_t t = tid; t < p.T; t += blockDim.x) p.order[atomicAdd(&place[group_of(t)], 1)] = (int32_t)t;
+}
+
+// Eight 16-bit elements, zero where they are outside; VEC: all or none, 16-byte aligned.
+template <bool VEC>
+__device__ __forceinline__ uint4 eight(const uint16_t* p, int64_t left) {
+    if (VEC) return left > 0 ? *(const uint4*)p : make_uint4(0, 0, 0, 0);
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < left) w[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// One item's rows times 8 * NT rows of A over one split of K.  A warp takes 32 k of a step:
+// four lanes 16 bytes each of one row.
+template <bool F16, int MT, int NT, bool VEC>
+__global__ void __launch_bounds__(kDownWarps * 32) lora_down_kernel(const LoraParams p) {
+    constexpr int kRows = 16 * MT, kCols = 8 * NT;
+    __shared__ float sm[kDownWarps][kRows][kCols + 4];
+    pdl_wait_previous();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+    const int items = *p.num_items;
+    const int split = blockIdx.y, col0 = blockIdx.z * kCols;
+    const int64_t k_begin = (int64_t)split * p.k_split, k_end = min(k_begin + p.k_split, p.K);
+    for (int it = blockIdx.x; it < items; it += gridDim.x) {
+        const Item item = p.items[it];
+        if (item.adapter < 0) continue;
+        const uint16_t* xr[MT][2];
+        bool held[MT][2];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int row = m * 16 + h * 8 + g;
+                held[m][h] = row < item.rows;
+                xr[m][h] = p.x + (held[m][h] ? p.order[item.first + row] : 0) * p.x_stride;
+            }
+        const uint16_t* a = p.a + ((int64_t)item.adapter * p.r + col0 + g) * p.K;
+        float acc[MT][NT][4] = {};
+        constexpr int U = MT == 1 ? 4 : 1;
+        for (int64_t k0 = k_begin + warp * 32; k0 < k_end; k0 += kDownWarps * 32 * U) {
+            uint4 xv[U][MT][2], av[U][NT];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t k = k0 + u * kDownWarps * 32 + q * 8, left = k_end - k;
+#pragma unroll
+                for (int j = 0; j < NT; ++j) av[u][j] = col0 + j * 8 + g < p.r ? eight<VEC>(a + (int64_t)j * 8 * p.K + k, left) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) xv[u][m][h] = held[m][h] ? eight<VEC>(xr[m][h] + k, left) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const uint32_t lo[4] = {xv[u][m][0].x, xv[u][m][1].x, xv[u][m][0].y, xv[u][m][1].y};
+                    const uint32_t hi[4] = {xv[u][m][0].z, xv[u][m][1].z, xv[u][m][0].w, xv[u][m][1].w};
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        mma_16816<F16>(acc[m][j], lo, av[u][j].x, av[u][j].y);
+                        mma_16816<F16>(acc[m][j], hi, av[u][j].z, av[u][j].w);
+                    }
+                }
+        }
+        __syncthreads();                                    // the last item's sums are read
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    *(float2*)&sm[warp][m * 16 + h * 8 + g][j * 8 + q * 2] = make_float2(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
+        __syncthreads();
+        for (int i = threadIdx.x; i < kRows * kCols; i += kDownWarps * 32) {
+            const int row = i / kCols, c = i % kCols;
+            if (row >= item.rows || col0 + c >= p.rp) continue;
+            float v = sm[0][row][c];
+#pragma unroll
+            for (int w = 1; w < kDownWarps; ++w) v += sm[w][row][c];
+            p.low[((int64_t)split * p.T + item.first + row) * p.rp + col0 + c] = v;
+        }
+    }
+}
+
+// Four elements of a row of B, zero from `left` on; VEC: all or none, 8-byte aligned.
+template <bool VEC>
+__device__ __forceinline__ uint2 four(const uint16_t* p, int left) {
+    if (VEC) return left > 0 ? *(const uint2*)p : make_uint2(0, 0);
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < left) w[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
+    return make_uint2(w[0], w[1]);
+}
+
+// One item's rows of A x times B, and y, over a range of N.  A warp takes 32 columns of a step;
+// tile j of four holds columns 8 (c / 2) + 2 j + c % 2, so that a lane's eight outputs of a
+// row lie side by side.
+template <bool F16, int MT, bool VEC_B, bool VEC_Y>
+__global__ void __launch_bounds__(kUpWarps * 32) lora_up_kernel(const LoraParams p, const int cols_block) {
+    constexpr int kRows = 16 * MT;
+    extern __shared__ __align__(16) uint8_t sm_up[];
+    const int pitch = p.rp + 4;                             // halves of A x as fragments read them: 16 bits
+    uint32_t* sm_hi = (uint32_t*)sm_up;                     // [kRows][pitch / 2]
+    uint32_t* sm_lo = sm_hi + kRows * (pitch / 2);
+    float* sm_scale = (float*)(sm_lo + kRows * (pitch / 2));   // [kRows]
+    pdl_wait_previous();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+    const int items = *p.num_items;
+    const int64_t n_begin = (int64_t)blockIdx.x * cols_block, n_end = min(n_begin + cols_block, p.N);
+    for (int it = blockIdx.y; it < items; it += gridDim.y) {
+        const Item item = p.items[it];
+        if (item.adapter < 0 && !p.copy_rest) continue;
+        const int steps = item.adapter < 0 ? 0 : p.rp / 16;
+        __syncthreads();
+        // The splits' sums in order, as two halves.  FP16 holds them times the power of two that
+        // puts a row's largest below 2, which the end takes back.
+        if (steps)
+            for (int row = warp; row < kRows; row += kUpWarps) {
+                float v[kMaxRank / 64][2], most = 0.f;
+#pragma unroll
+                for (int j = 0; j < kMaxRank / 64; ++j) {
+                    const int c = (j * 32 + lane) * 2;
+                    float2 s = make_float2(0.f, 0.f);
+                    if (row < item.rows && c < p.rp)
+                        for (int sp = 0; sp < p.splits; ++sp) {
+                            const float2 u = *(const float2*)(p.low + ((int64_t)sp * p.T + item.first + row) * p.rp + c);
+                            s.x += u.x;
+                            s.y += u.y;
+                        }
+                    v[j][0] = s.x;
+                    v[j][1] = s.y;
+                    most = fmaxf(most, fmaxf(fabsf(s.x), fabsf(s.y)));
+                }
+                float down = 1.f, up = 1.f;
+                if (F16) {
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+                    if (most > 0x1p-100f && most < INFINITY) {
+                        const uint32_t e = __float_as_uint(most) & 0x7f800000u;
+                        up = __uint_as_float(e);
+                        down = __uint_as_float(0x7f000000u - e);        // 2^-exponent
+                    }
+                }
+                if (lane == 0) sm_scale[row] = up * (p.scales ? p.scales[item.adapter] : 1.f);
+#pragma unroll
+                for (int j = 0; j < kMaxRank / 64; ++j) {
+                    const int c = (j * 32 + lane) * 2;
+                    if (c >= p.rp) break;
+                    const float a = v[j][0] * down, b = v[j][1] * down;
+                    const uint32_t hi = f32_to_act2<F16>(a, b);
+                    const float2 back = act2_to_f32<F16>(hi);
+                    // An infinity (or one that the type cannot hold) is its own first half.
+                    const float la = fabsf(back.x) < INFINITY ? a - back.x : 0.f, lb = fabsf(back.y) < INFINITY ? b - back.y : 0.f;
+                    sm_hi[row * (pitch / 2) + c / 2] = hi;
+                    sm_lo[row * (pitch / 2) + c / 2] = f32_to_act2<F16>(la, lb);
+                }
+            }
+        __syncthreads();
+        const uint16_t* b = p.b + (int64_t)max(item.adapter, 0) * p.N * p.r;
+        for (int64_t n0 = n_begin + warp * 32; n0 < n_end; n0 += kUpWarps * 32) {
+            float acc[MT][4][4] = {};
+            for (int st = 0; st < steps; ++st) {
+                uint2 bv[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int64_t n = n0 + 8 * (g >> 1) + 2 * j + (g & 1);
+                    bv[j] = n < n_end ? four<VEC_B>(b + n * p.r + st * 16 + q * 4, p.r - st * 16 - q * 4) : make_uint2(0, 0);
+                }
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const int at = (m * 16 + g) * (pitch / 2) + st * 8 + q * 2, at8 = at + 8 * (pitch / 2);
+                    const uint2 h0 = *(const uint2*)(sm_hi + at), h1 = *(const uint2*)(sm_hi + at8);
+                    const uint2 l0 = *(const uint2*)(sm_lo + at), l1 = *(const uint2*)(sm_lo + at8);
+                    const uint32_t hi[4] = {h0.x, h1.x, h0.y, h1.y}, lo[4] = {l0.x, l1.x, l0.y, l1.y};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        mma_16816<F16>(acc[m][j], hi, bv[j].x, bv[j].y);
+                        mma_16816<F16>(acc[m][j], lo, bv[j].x, bv[j].y);
+                    }
+                }
+            }
+            const int64_t n = n0 + q * 8;
+            if (n >= n_end) continue;
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int row = m * 16 + h * 8 + g;
+                    if (row >= item.rows) continue;
+                    const int64_t t = p.order[item.first + row];
+                    const float s = steps ? sm_scale[row] : 0.f;
+                    const uint4 yv = eight<VEC_Y>(p.y + t * p.y_stride + n, n_end - n);
+                    uint32_t w[4] = {yv.x, yv.y, yv.z, yv.w};
+                    if (steps)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 u = act2_to_f32<F16>(w[j]);
+                            w[j] = f32_to_act2<F16>(fmaf(s, acc[m][j][2 * h], u.x), fmaf(s, acc[m][j][2 * h + 1], u.y));
+                        }
+                    uint16_t* out = p.out + t * p.N + n;
+                    if (VEC_Y) {
+                        *(uint4*)out = make_uint4(w[0], w[1], w[2], w[3]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (n + i < n_end) out[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+                    }
+                }
+        }
+    }
+}
+
+// How a call of these sizes is cut up.
+struct LoraPlan {
+    int rows_item, splits, k_split, nt;
+    int64_t items;                         // at most
+    size_t bytes, order_at, low_at;
+};
+
+LoraPlan plan_lora(int64_t T, int64_t n, int64_t r, int64_t K) {
+    LoraPlan pl{};
+    pl.rows_item = T >= 64 * (n + 1) ? 64 : 16;
+    pl.items = std::min(T, T / pl.rows_item + n + 1);
+    pl.nt = r <= 8 ? 1 : r <= 16 ? 2 : 4;
+    const int64_t blocks = pl.items * ceil_div(r, pl.nt * 8);
+    int64_t splits = ceil_div(4 * (int64_t)sm_count(), blocks);
+    splits = std::min<int64_t>({splits, kMaxSplits, ceil_div(K, kDownWarps * 64)});
+    pl.k_split = (int)round_up(ceil_div(K, std::max<int64_t>(splits, 1)), 32);
+    pl.splits = (int)ceil_div(K, pl.k_split);
+    pl.order_at = 256 + (size_t)round_up(sizeof(Item) * pl.items, 256);
+    pl.low_at = pl.order_at + (size_t)round_up(4 * T, 256);
+    pl.bytes = pl.low_at + (size_t)round_up(4 * pl.splits * T * round_up(r, 16), 256);
+    return pl;
+}
+
+template <bool F16, int MT, bool VEC>
+const void* down_kernel(int nt) {
+    return nt == 1 ? (const void*)lora_down_kernel<F16, MT, 1, VEC> : nt == 2 ? (const void*)lora_down_kernel<F16, MT, 2, VEC>
+                                                                             : (const void*)lora_down_kernel<F16, MT, 4, VEC>;
+}
+
+template <bool F16>
+const void* down_kernel(int rows, int nt, bool vec) {
+    if (rows == 16) return vec ? down_kernel<F16, 1, true>(nt) : down_kernel<F16, 1, false>(nt);
+    return vec ? down_kernel<F16, 4, true>(nt) : down_kernel<F16, 4, false>(nt);
+}
+
+template <bool F16, int MT>
+const void* up_kernel(bool vec_b, bool vec_y) {
+    if (vec_b) return vec_y ? (const void*)lora_up_kernel<F16, MT, true, true> : (const void*)lora_up_kernel<F16, MT, true, false>;
+    return vec_y ? (const void*)lora_up_kernel<F16, MT, false, true> : (const void*)lora_up_kernel<F16, MT, false, false>;
+}
+
+nvfp4_status check_sizes(const char* fn, int64_t T, int64_t n, int64_t r, int64_t K, int64_t N) {
+    if (T < 0 || N < 0 || n < 0) return fail(NVFP4_ERR_INVALID_ARG, "%s: negative size T=%lld N=%lld adapters=%lld", fn, (long long)T, (long long)N, (long long)n);
+    if (r < 1 || r > kMaxRank) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s: rank %lld must be in [1, %d]", fn, (long long)r, kMaxRank);
+    if (n > kMaxAdapters) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s: %lld adapters, at most %d", fn, (long long)n, kMaxAdapters);
+    if (K < 1 || K > (1 << 24) || N > (1 << 24) || T > (1 << 24))
+        return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s: T=%lld, K=%lld and N=%lld must be at most 2^24, K positive", fn, (long long)T, (long long)K, (long long)N);
+    return NVFP4_OK;
+}
+
+}  // namespace
+}  // namespace nvfp4
+
+using namespace nvfp4;
+
+extern "C" size_t nvfp4_lora_workspace(int64_t T, int64_t adapters, int64_t r, int64_t K) {
+    if (check_sizes("nvfp4_lora_workspace", T, adapters, r, K, 0) != NVFP4_OK || T == 0) return 0;
+    return plan_lora(T, adapters, r, K).bytes;
+}
+
+extern "C" nvfp4_status nvfp4_lora_add(const void* y, int64_t y_stride, const void* x, int64_t x_stride, const void* A, const void* B,
+                                       const float* scales, const int32_t* adapters, int64_t T, int64_t num_adapters, int64_t r, int64_t K,
+                                       int64_t N, int f16, void* out, void* workspace, size_t workspace_bytes, void* stream) {
+    const char* fn = "nvfp4_lora_add";
+    if (nvfp4_status st = check_sizes(fn, T, num_adapters, r, K, N)) return st;
+    if (f16 != 0 && f16 != 1) return fail(NVFP4_ERR_INVALID_ARG, "%s: f16=%d must be 0 or 1", fn, f16);
+    if (x_stride < 0 || y_stride < 0) return fail(NVFP4_ERR_INVALID_ARG, "%s: negative stride", fn);
+    if (T == 0 || N == 0) return NVFP4_OK;
+    if (!y || !x || !adapters || !out || (num_adapters > 0 && (!A || !B))) return fail(NVFP4_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (!aligned(y, 2) || !aligned(x, 2) || !aligned(A, 2) || !aligned(B, 2) || !aligned(out, 2) || !aligned(adapters, 4) || !aligned(scales, 4))
+        return fail(NVFP4_ERR_ALIGNMENT, "%s: pointers must be aligned to their elements", fn);
+    const LoraPlan pl = plan_lora(T, num_adapters, r, K);
+    if (!workspace || workspace_bytes < pl.bytes) return fail(NVFP4_ERR_WORKSPACE, "%s: workspace %zu bytes, needs %zu", fn, workspace ? workspace_bytes : 0, pl.bytes);
+    if (!aligned(workspace, 256)) return fail(NVFP4_ERR_ALIGNMENT, "%s: workspace must be 256-byte aligned", fn);
+    const Span to = dense_span("out", out, 2 * T * N), ws = dense_span("workspace", workspace, (int64_t)pl.bytes);
+    const Span ys = strided_span("y", y, 2 * N, {{T, 2 * y_stride}}), xs = strided_span("x", x, 2 * K, {{T, 2 * x_stride}});
+    const Span as = dense_span("a", A, 2 * num_adapters * r * K), bs = dense_span("b", B, 2 * num_adapters * N * r);
+    const Span ids = dense_span("adapters", adapters, 4 * T), ss = dense_span("scales", scales, 4 * num_adapters);
+    if (overlaps(to, ys) && !same_place(to, ys)) return fail(NVFP4_ERR_INVALID_ARG, "%s: out overlaps y (it may be y itself where that is dense)", fn);
+    if (const char* s = met(to, {xs, as, bs, ids, ss, ws})) return fail(NVFP4_ERR_INVALID_ARG, "%s: out overlaps %s", fn, s);
+    if (const char* s = met(ws, {ys, xs, as, bs, ids, ss})) return fail(NVFP4_ERR_INVALID_ARG, "%s: workspace overlaps %s", fn, s);
+    LoraParams p{};
+    p.status = device_status_ptr();
+    if (!p.status) return fail(NVFP4_ERR_CUDA, "%s: no CUDA device", fn);
+    uint8_t* w = (uint8_t*)workspace;
+    p.x = (const uint16_t*)x; p.a = (const uint16_t*)A; p.b = (const uint16_t*)B; p.y = (const uint16_t*)y;
+    p.adapters = adapters; p.scales = scales; p.out = (uint16_t*)out;
+    p.T = T; p.K = K; p.N = N; p.x_stride = x_stride; p.y_stride = y_stride;
+    p.n = (int)num_adapters; p.r = (int)r; p.rp = (int)round_up(r, 16);
+    p.splits = pl.splits; p.k_split = pl.k_split; p.rows_item = pl.rows_item; p.copy_rest = out != y;
+    p.num_items = (int32_t*)w; p.items = (Item*)(w + 256); p.order = (int32_t*)(w + pl.order_at); p.low = (float*)(w + pl.low_at);
+    cudaStream_t s = (cudaStream_t)stream;
+    void* args[] = {&p};
+    if (nvfp4_status st = launch_kernel((const void*)lora_group_kernel, dim3(1), dim3(1024), 8 * (p.n + 1), 1, args, s, fn)) return st;
+    const bool vec_x = K % 8 == 0 && x_stride % 8 == 0 && aligned(x, 16) && aligned(A, 16);
+    const bool vec_b = r % 4 == 0 && aligned(B, 8);
+    const bool vec_y = N % 8 == 0 && y_stride % 8 == 0 && aligned(y, 16) && aligned(out, 16);
+    if (num_adapters > 0) {
+        const void* kernel = f16 ? down_kernel<true>(pl.rows_item, pl.nt, vec_x) : down_kernel<false>(pl.rows_item, pl.nt, vec_x);
+        const dim3 grid((unsigned)std::min<int64_t>(pl.items, 65535), (unsigned)pl.splits, (unsigned)ceil_div(p.rp, pl.nt * 8));
+        if (nvfp4_status st = launch_kernel(kernel, grid, dim3(kDownWarps * 32), 0, 1, args, s, fn)) return st;
+    }
+    const void* kernel = pl.rows_item == 16 ? (f16 ? up_kernel<true, 1>(vec_b, vec_y) : up_kernel<false, 1>(vec_b, vec_y))
+                                            : (f16 ? up_kernel<true, 4>(vec_b, vec_y) : up_kernel<false, 4>(vec_b, vec_y));
+    // Columns of a block: enough of them that the sums over splits are not read too often, few
+    // enough to fill the SMs.
+    int cols = kUpWarps * 32 * 4;
+    while (cols > kUpWarps * 32 && ceil_div(N, cols) * pl.items < 4 * (int64_t)sm_count()) cols /= 2;
+    const size_t smem = (size_t)pl.rows_item * ((p.rp + 4) * 4 + 4);
+    void* up_args[] = {&p, &cols};
+    return launch_kernel(kernel, dim3((unsigned)ceil_div(N, cols), (unsigned)std::min<int64_t>(pl.items, 65535)), dim3(kUpWarps * 32), smem, 1,
+                         up_args, s, fn);
+}
