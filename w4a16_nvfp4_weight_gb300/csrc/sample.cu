@@ -29,7 +29,6 @@ constexpr int kList = 1024;                // values sorted at most
 constexpr int kMaxCluster = 8;
 constexpr int kOneLog2 = 43;               // a weight of one is 2^43: 2^20 of them sum inside 63 bits
 constexpr int64_t kMaxVocabulary = 1 << 20;
-constexpr size_t kHeldBytes = 84 * 1024;   // of a block's logits in shared memory: two blocks an SM
 
 // 2^30 * 2^(j / 512), from the series of exp.
 struct Exp2Table {
@@ -84,15 +83,20 @@ struct NearScale {
     }
     __device__ __forceinline__ float tidy(float l) const { return fmaxf(l, low); }       // NaN, too
     __device__ __forceinline__ bool counts(float l) const { return l > low; }
-    // Bin of the first histogram, 20 for each factor of two; never falls as l falls.
-    __device__ __forceinline__ int bin(float l) const {
-        return __float_as_int(fmaf(l, -20.f * ch, (kWhole + 1.f) + rintf(20.f * mh))) - kWholeBits;
-    }
+    // Place below the largest in 512ths of a factor of two, as the low bits of a float: kWholeBits at
+    // the largest, falling with l (each rounding keeps order).
+    __device__ __forceinline__ int place(float l) const { return __float_as_int(fmaf(l, ch * 512.f, kWhole - mh * 512.f)); }
+    __device__ __forceinline__ int bin(float l) const { return (kWholeBits >> 5) - (place(l) >> 5); }
     __device__ __forceinline__ float log_weight(float l) const { return fmaf(l, cl, fmaf(l, ch, -mh)) * 0.693147180559945f; }
+    // A weight as w * 2^(13 - s), w in [2^30, 2^31) and s = (kWholeBits >> 9) - (n >> 9).
+    struct Weight {
+        uint32_t w;
+        int n;
+    };
     // 2^(l ch + l cl - mh): the nearest 512th by table, in 2^-30; the rest, below 2^-10 (and 2^-12
-    // for l cl), by three terms of exp's series, good to 2^-33 of the whole.  The rest itself is
+    // for l cl), by three terms of exp's series, good to 2^-31 of the whole.  The rest itself is
     // exact but for its last bit: mh plus a 512th has no rounding.
-    __device__ __forceinline__ void weights(float la, float lb, const uint2* table, uint64_t& wa, uint64_t& wb) const {
+    __device__ __forceinline__ void weights(float la, float lb, const uint2* table, Weight& wa, Weight& wb) const {
         const F2 l = make_f2(la, lb);
         const F2 whole = fma2(l, make_f2(ch * 512.f, ch * 512.f), make_f2(kWhole - mh * 512.f, kWhole - mh * 512.f));
         const F2 k = fma2(whole, make_f2(1.f, 1.f), make_f2(-kWhole, -kWhole));
@@ -102,22 +106,34 @@ struct NearScale {
         const F2 p = mul2(rest, fma2(rest, fma2(rest, make_f2(kLn2 * kLn2 * kLn2 / 6, kLn2 * kLn2 * kLn2 / 6), make_f2(kLn2 * kLn2 / 2, kLn2 * kLn2 / 2)),
                                      make_f2(kLn2, kLn2)));
         const float2 n = both(whole);
-        const int na = __float_as_int(n.x), nb = __float_as_int(n.y);
-        const uint2 ea = table[na & 511], eb = table[nb & 511];
+        wa.n = __float_as_int(n.x);
+        wb.n = __float_as_int(n.y);
+        const uint2 ea = table[wa.n & 511], eb = table[wb.n & 511];
         const float2 v = both(fma2(make_f2(__uint_as_float(ea.y), __uint_as_float(eb.y)), p, make_f2(kWhole, kWhole)));
-        wa = shifted(ea.x + __float_as_uint(v.x), (kWholeBits >> 9) - (na >> 9));
-        wb = shifted(eb.x + __float_as_uint(v.y), (kWholeBits >> 9) - (nb >> 9));
+        wa.w = ea.x + __float_as_uint(v.x);
+        wb.w = eb.x + __float_as_uint(v.y);
     }
-    // w * 2^(13 - s), to the nearest whole number.
-    __device__ __forceinline__ static uint64_t shifted(uint32_t w, int s) {
-        const int d = s - (kOneLog2 - 30);                          // below 13 the product is whole
-        if (d <= 0) return (uint64_t)w << -d;
-        return ((w >> min(d - 1, 31)) + 1) >> 1;
+    __device__ __forceinline__ static uint32_t power(int e) {      // 2^e, zero outside [0, 31]
+        uint32_t v;
+        asm("shl.b32 %0, 1, %1;" : "=r"(v) : "r"(e));
+        return v;
     }
+    // w * 2^(13 - s) to the nearest whole number: up to s = 13 a product, then the high word of one;
+    // either power is zero where the other is not.
+    __device__ __forceinline__ static uint32_t small(const Weight& x) {
+        const uint32_t m = power((x.n >> 9) + (45 - (kWholeBits >> 9)));
+        return (uint32_t)(((uint64_t)x.w * m + 0x80000000u) >> 32);
+    }
+    __device__ __forceinline__ static uint64_t value(const Weight& x) {
+        return (uint64_t)x.w * power((x.n >> 9) + (13 - (kWholeBits >> 9))) + small(x);
+    }
+    // Bin, and the weight within its factor of two to 15 bits.
+    __device__ __forceinline__ static int bin_of(const Weight& x) { return (kWholeBits >> 5) - (x.n >> 5); }
+    __device__ __forceinline__ static uint32_t rough(const Weight& x) { return x.w >> 16; }
     __device__ __forceinline__ uint64_t weight(float l, const uint2* table) const {
-        uint64_t a, b;
+        Weight a, b;
         weights(l, l, table, a, b);
-        return a;
+        return value(a);
     }
 };
 
@@ -141,17 +157,30 @@ struct FarScale {
     __device__ __forceinline__ float tidy(float l) const { return fmaxf(l, -INFINITY); }
     __device__ __forceinline__ bool counts(float l) const { return place(l) > -47.0; }
     __device__ __forceinline__ double place(float l) const { return far_place(c, top, l); }
-    __device__ __forceinline__ int bin(float l) const { return (int)(fmax(place(l), -47.0) * -20.0); }
+    __device__ __forceinline__ int bin(float l) const { return bin_at(place(l)); }
+    __device__ __forceinline__ static int bin_at(double x) { return -(int)floor(fmax(x, -47.0) * 16.0); }
     __device__ __forceinline__ float log_weight(float l) const { return (float)(place(l) * 0.69314718055994530942); }
     __device__ __forceinline__ uint64_t weight(float l, const uint2*) const {
         return far_weight(place(l));
     }
-    __device__ __forceinline__ void weights(float la, float lb, const uint2* table, uint64_t& wa, uint64_t& wb) const {
-        wa = weight(la, table);
-        wb = weight(lb, table);
+    struct Weight {
+        uint64_t w;
+        int bin;
+    };
+    __device__ __forceinline__ void weights(float la, float lb, const uint2*, Weight& wa, Weight& wb) const {
+        const double a = place(la), b = place(lb);
+        wa = Weight{far_weight(a), bin_at(a)};
+        wb = Weight{far_weight(b), bin_at(b)};
+    }
+    __device__ __forceinline__ static uint64_t value(const Weight& x) { return x.w; }
+    __device__ __forceinline__ static int bin_of(const Weight& x) { return x.bin; }
+    // As above: a bin's octave begins right behind its factor of two.
+    __device__ __forceinline__ static uint32_t rough(const Weight& x) {
+        const int up = ((x.bin + 15) >> 4) - (kOneLog2 - 14);
+        return (uint32_t)(up >= 0 ? x.w << up : x.w >> -up);
     }
 };
-constexpr int kDeadBin = 20 * (kOneLog2 + 1) + 2;          // what lies in bins from here on weighs nothing
+constexpr int kDeadBin = 16 * (kOneLog2 + 3);              // what lies in bins from here on weighs nothing
 
 // Floats as whole numbers in the same order, the two zeros as one.
 __device__ __forceinline__ uint32_t order_key(float l) {
@@ -183,20 +212,21 @@ __device__ __forceinline__ uint64_t part_of(float f, uint64_t s, bool up) {
 enum { kTypeBf16, kTypeF16, kTypeF32 };
 
 // The row's virtual elements, in 16-byte pieces: element 0 is on a boundary of eight elements.
-// HELD: a block's part stays in shared memory, each lane's pieces where that lane finds them.
-template <int TYPE, bool HELD>
+template <int TYPE>
 struct Row {
     static constexpr int kSize = TYPE == kTypeF32 ? 4 : 2;
     static constexpr int kPieces = kSize / 2;              // of eight elements
     const uint8_t* base;
-    uint8_t* held;
     int first, end;                        // virtual elements that are the row's
 
-    __device__ __forceinline__ Row(const void* logits, int64_t offset, int V, uint8_t* held_) : held(held_) {
+    __device__ __forceinline__ Row(const void* logits, int64_t offset, int V) {
         const uint8_t* p = (const uint8_t*)logits + offset * kSize;
         first = (int)(((uintptr_t)p & (8 * kSize - 1)) / kSize);
         base = p - first * kSize;
         end = first + V;
+    }
+    __device__ __forceinline__ float one(int j) const {
+        return TYPE == kTypeF32 ? ((const float*)base)[j] : act_to_f32<TYPE == kTypeF16>(((const uint16_t*)base)[j]);
     }
     // Elements j to j + 7 (j a multiple of 8) from memory, -infinity outside the row.
     __device__ __forceinline__ void load(int j, uint4 (&v)[kPieces]) const {
@@ -240,20 +270,6 @@ struct Row {
             }
         }
     }
-    __device__ __forceinline__ uint4* place(int step) const {
-        return (uint4*)held + (step * kSampleWarps + (threadIdx.x >> 5)) * kPieces * 32 + (threadIdx.x & 31);
-    }
-    // Elements j to j + 7, this lane's of step `step`.
-    __device__ __forceinline__ void eight(int j, int step, float (&l)[8]) const {
-        uint4 v[kPieces];
-        if (HELD) {
-#pragma unroll
-            for (int k = 0; k < kPieces; ++k) v[k] = place(step)[k * 32];
-        } else {
-            load(j, v);
-        }
-        widen(v, l);
-    }
 };
 
 // Where the kept tokens of a row end: every logit above `value`, and of those equal to it the
@@ -266,14 +282,15 @@ struct Cut {
 
 struct Shared {
     uint2 table[512];
-    uint32_t count[kBins], lo[kBins], hi[kBins];           // a mass is lo + 2^32 hi
+    uint32_t count[kBins], lo[kBins], hi[kBins];           // an exact mass is lo + 2^32 hi
+    uint64_t pairs[kList];                 // logits with their indices, of a row with few candidates
     uint32_t list[2][kList];               // values of a bin, as keys: of this block; of the whole row
-    uint32_t listed[2];                    // of the two lists that a row may need
-    int64_t scan[2][kSampleWarps];
+    uint32_t listed, paired, few[kMaxCluster];
+    uint64_t scan[2][kSampleWarps];
     uint64_t found[4];
-    float best[kMaxCluster];               // pushed here by every block of the row
+    float best[kMaxCluster];               // pushed here by every block of the row, as the next ones
     int best_at[kMaxCluster];
-    uint64_t mass[kMaxCluster];
+    uint64_t total[kMaxCluster], above[kMaxCluster], mass[kMaxCluster];
     uint32_t ties[kMaxCluster];
     float warp_best[kSampleWarps];
     int warp_at[kSampleWarps];
@@ -307,6 +324,11 @@ __device__ __forceinline__ void push_u32(void* p, uint32_t rank, uint32_t v) {
 __device__ __forceinline__ void push_u64(void* p, uint32_t rank, uint64_t v) {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(map_rank(smem_u32(p), rank)), "l"(v) : "memory");
 }
+__device__ __forceinline__ uint32_t remote_add(void* p, uint32_t rank, uint32_t v) {
+    uint32_t old;
+    asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(map_rank(smem_u32(p), rank)), "r"(v) : "memory");
+    return old;
+}
 __device__ __forceinline__ void cluster_sync() {
     __syncwarp();
     cluster_arrive();
@@ -330,27 +352,44 @@ __device__ __forceinline__ T warp_below(T v, int lane) {          // sum over lo
     return x - v;
 }
 
-// Sums over the threads below this one, of a count and a mass; returns the whole mass.
-__device__ __forceinline__ uint64_t block_below(uint64_t& count, uint64_t& mass, Shared& sm) {
+// Sum over the threads below this one; `all`: over all of them.
+__device__ __forceinline__ uint64_t block_below(uint64_t v, uint64_t (&sm)[kSampleWarps], uint64_t* all) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t c = warp_below((uint32_t)count, lane);
-    const uint64_t m = warp_below(mass, lane);
-    if (lane == 31) {
-        sm.scan[0][warp] = c + count;
-        sm.scan[1][warp] = m + mass;
-    }
+    const uint64_t x = warp_below(v, lane);
+    if (lane == 31) sm[warp] = x + v;
     __syncthreads();
-    uint64_t cs = 0, ms = 0, all = 0;
+    uint64_t below = 0, sum = 0;
 #pragma unroll
     for (int w = 0; w < kSampleWarps; ++w) {
-        if (w == warp) ms = all;
-        if (w < warp) cs += sm.scan[0][w];
-        all += sm.scan[1][w];
+        if (w == warp) below = sum;
+        sum += sm[w];
     }
     __syncthreads();
-    count = c + cs;
-    mass = m + ms;
-    return all;
+    *all = sum;
+    return x + below;
+}
+
+// `size` (a power of two, at most 2 * kSampleThreads) values from the largest down, in place; up to
+// 64 by one warp, the others skip it.
+template <class T>
+__device__ __forceinline__ void sort_down(T* v, int size) {
+    const int i = threadIdx.x;
+    const bool small = size <= 64;
+    if (!small || i < 32)
+        for (int k = 2; k <= size; k *= 2)
+            for (int s = k / 2; s > 0; s /= 2) {
+                if (i < size / 2) {
+                    const int a = 2 * i - (i & (s - 1)), b = a + s;
+                    const T x = v[a], y = v[b];
+                    if ((x < y) == ((a & k) == 0)) {
+                        v[a] = y;
+                        v[b] = x;
+                    }
+                }
+                // A warp's pairs lie in 64 values of its own up to 32 apart.
+                if (small || (s <= 32 && (s > 1 || k < 64))) __syncwarp();
+                else __syncthreads();
+            }
 }
 
 __device__ __forceinline__ void add_mass(Shared& sm, int bin, uint64_t w) {
@@ -361,47 +400,53 @@ __device__ __forceinline__ void add_mass(Shared& sm, int bin, uint64_t w) {
 
 constexpr int kOwnBins = kBins / kSampleThreads;           // bins of a thread when they are summed
 
-template <int TYPE, bool HELD, class SCALE>
+// A bin where a running sum reaches a target: what it holds, and what goes before it.
+struct Reached {
+    int bin;
+    uint64_t here, before;
+};
+
+template <int TYPE, class SCALE>
 struct Sampler {
+    using Weight = typename SCALE::Weight;
     Shared& sm;
-    const Row<TYPE, HELD>& row;
+    const Row<TYPE>& row;
     const uint32_t rank, ranks;
     const int j0, j1;                      // virtual elements of this warp
     const SCALE& scale;
 
-    // f(first virtual index, eight logits) over this warp's elements, in index order over lanes.
+    // f(eight logits, their largest, the first's index) over this warp's elements.
     template <class F>
     __device__ __forceinline__ void each(F f) const {
-        int step = 0;
-        for (int j = j0 + (threadIdx.x & 31) * 8; j < j1; j += 256, ++step) {
+        int j = j0 + (threadIdx.x & 31) * 8;
+        if (j >= j1) return;
+        uint4 next[Row<TYPE>::kPieces];                     // a load ahead
+        row.load(j, next);
+        for (; j < j1; j += 256) {
             float l[8];
-            row.eight(j, step, l);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) l[i] = scale.tidy(l[i]);
-            f(j, l);
+            row.widen(next, l);
+            if (j + 256 < j1) row.load(j + 256, next);
+            f(l, scale.tidy(fmaxf(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])), fmaxf(fmaxf(l[4], l[5]), fmaxf(l[6], l[7])))), j);
         }
+    }
+    __device__ __forceinline__ void tidy(float (&l)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) l[i] = scale.tidy(l[i]);
     }
 
-    // Counts and masses of the whole row's bins after every block has made its own.
-    __device__ __forceinline__ void gather(bool by_count, bool by_mass, uint64_t (&count)[kOwnBins], uint64_t (&mass)[kOwnBins]) {
-        static_assert(kOwnBins == 2, "read in pairs");
-        cluster_sync();
-        uint64_t hi[kOwnBins] = {0, 0};
-        count[0] = count[1] = mass[0] = mass[1] = 0;
-        if (by_count) read(sm.count, count);
-        if (by_mass) {
-            read(sm.lo, mass);
-            read(sm.hi, hi);
-            mass[0] += hi[0] << 32;
-            mass[1] += hi[1] << 32;
-        }
+    __device__ __forceinline__ void clear() {
+        cluster_sync();                                     // all have read the last histogram
+        for (int i = threadIdx.x; i < kBins; i += kSampleThreads) sm.count[i] = sm.lo[i] = sm.hi[i] = 0;
+        __syncthreads();
     }
-    // Sums of this thread's two bins over the blocks.
+    // Sums of this thread's two bins over the blocks, after a barrier of them.
     __device__ __forceinline__ void read(const uint32_t (&bins)[kBins], uint64_t (&sum)[kOwnBins]) const {
+        static_assert(kOwnBins == 2, "read in pairs");
         uint2 v[kMaxCluster];
         const uint32_t at = smem_u32(&bins[threadIdx.x * 2]);
 #pragma unroll
         for (uint32_t r = 0; r < kMaxCluster; ++r) v[r] = r < ranks ? remote_u32x2(map_rank(at, r)) : make_uint2(0, 0);
+        sum[0] = sum[1] = 0;
 #pragma unroll
         for (uint32_t r = 0; r < kMaxCluster; ++r) {
             sum[0] += v[r].x;
@@ -409,33 +454,98 @@ struct Sampler {
         }
     }
 
-    // Histogram of the row's logits by their place, of counts and masses as asked.
-    __device__ __forceinline__ void histogram(bool by_count, bool by_mass, uint64_t (&count)[kOwnBins], uint64_t (&mass)[kOwnBins]) {
-        each([&](int, const float (&l)[8]) {
+    // Counts of the lanes' largest logits.
+    __device__ __forceinline__ void count_lanes(float most, uint64_t (&count)[kOwnBins]) {
+        most = scale.tidy(most);
+        if (scale.counts(most)) atomicAdd(&sm.count[scale.bin(most)], 1u);
+        cluster_sync();
+        read(sm.count, count);
+    }
+    // Counts of all logits of the row.
+    __device__ __noinline__ void count_all(uint64_t (&count)[kOwnBins]) {
+        clear();
+        each([&](float (&l)[8], float, int) {
+            tidy(l);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (scale.counts(l[i])) atomicAdd(&sm.count[scale.bin(l[i])], 1u);
+        });
+        cluster_sync();
+        read(sm.count, count);
+    }
+
+    // The row's mass, exactly, and that of each bin but for up to 2^-14 of it: to 15 bits of each weight
+    // one addition in shared memory does, and the bin in question is known but for its neighbours.
+    __device__ __forceinline__ uint64_t weigh_bins(uint64_t (&mass)[kOwnBins]) {
+        uint64_t sum = 0;
+        each([&](float (&l)[8], float, int) {
+            tidy(l);
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
-                uint64_t w[2] = {0, 0};
-                if (by_mass) scale.weights(l[i], l[i + 1], sm.table, w[0], w[1]);
+                Weight w[2];
+                scale.weights(l[i], l[i + 1], sm.table, w[0], w[1]);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    if (!scale.counts(l[i + k])) continue;
-                    const int b = scale.bin(l[i + k]);
-                    if (by_count) atomicAdd(&sm.count[b], 1u);
-                    if (by_mass) add_mass(sm, b, w[k]);
+                    sum += SCALE::value(w[k]);
+                    if (scale.counts(l[i + k])) atomicAdd(&sm.count[SCALE::bin_of(w[k])], SCALE::rough(w[k]));
                 }
             }
         });
-        gather(by_count, by_mass, count, mass);
+        push_block_sum(sum, sm.total);
+        cluster_sync();
+        read(sm.count, mass);
+#pragma unroll
+        for (int k = 0; k < kOwnBins; ++k) {
+            const int down = (((int)threadIdx.x * kOwnBins + k + 15) >> 4) - (kOneLog2 - 14);
+            if (mass[k]) mass[k] = max(down > 0 ? mass[k] >> down : mass[k] << -down, (uint64_t)1);
+        }
+        sum = 0;
+        for (uint32_t r = 0; r < ranks; ++r) sum += sm.total[r];
+        return sum;
+    }
+    // This block's sum to its place in every block's `to`; a barrier of the blocks has to follow.
+    __device__ __forceinline__ void push_block_sum(uint64_t v, uint64_t (&to)[kMaxCluster]) {
+        v = warp_sum(v);
+        if ((threadIdx.x & 31) == 0) sm.warp_mass[threadIdx.x >> 5] = v;
+        __syncthreads();
+        if (threadIdx.x < ranks) {
+            uint64_t m = 0;
+#pragma unroll
+            for (int w = 0; w < kSampleWarps; ++w) m += sm.warp_mass[w];
+            push_u64(&to[rank], threadIdx.x, m);
+        }
     }
 
-    // The same of one bin's logits whose keys begin with the `bits` bits `known`, by their next
-    // `take` bits, the largest first.
-    __device__ __noinline__ void digits(int bin, uint32_t known, uint32_t bits, uint32_t take, bool by_mass, uint64_t (&count)[kOwnBins],
-                                           uint64_t (&mass)[kOwnBins]) {
-        cluster_sync();                                     // all have read the last histogram
-        for (int i = threadIdx.x; i < kBins; i += kSampleThreads) sm.count[i] = sm.lo[i] = sm.hi[i] = 0;
+    // The bin in which the running sum reaches the target; bin -1 where it never does.
+    __device__ __forceinline__ Reached reach(const uint64_t (&v)[kOwnBins], uint64_t target, uint64_t* all) {
+        uint64_t mine = 0;
+#pragma unroll
+        for (int k = 0; k < kOwnBins; ++k) mine += v[k];
+        if (threadIdx.x == 0) sm.found[0] = ~0ull;
+        uint64_t sum = block_below(mine, sm.scan[0], all);
+#pragma unroll
+        for (int k = 0; k < kOwnBins; ++k) {
+            if (sum < target && target <= sum + v[k]) {
+                sm.found[0] = threadIdx.x * kOwnBins + k;
+                sm.found[1] = v[k];
+                sm.found[2] = sum;
+            }
+            sum += v[k];
+        }
         __syncthreads();
-        each([&](int, const float (&l)[8]) {
+        const Reached r{(int)sm.found[0], sm.found[1], sm.found[2]};
+        __syncthreads();
+        return r;
+    }
+
+    // Exact counts and masses of one bin's logits whose keys begin with the `bits` bits `known`, by
+    // their next `take` bits, the largest first.
+    __device__ __forceinline__ void digits(int bin, uint32_t known, uint32_t bits, uint32_t take, bool by_mass, uint64_t (&count)[kOwnBins],
+                                           uint64_t (&mass)[kOwnBins]) {
+        clear();
+        each([&](float (&l)[8], float most, int) {
+            if (scale.bin(most) > bin) return;
+            tidy(l);
 #pragma unroll 1
             for (int i = 0; i < 8; ++i) {
                 const uint32_t k = order_key(l[i]);
@@ -445,207 +555,297 @@ struct Sampler {
                 if (by_mass) add_mass(sm, d, scale.weight(l[i], sm.table));
             }
         });
-        gather(true, by_mass, count, mass);
-    }
-
-    // The bin in which `count` or `mass` reaches the target; false where the sum never does.
-    // Leaves the bin, its count, and the count and mass before it in `out`.
-    __device__ __forceinline__ bool bin_of(const uint64_t (&count)[kOwnBins], const uint64_t (&mass)[kOwnBins], bool by_mass, uint64_t target,
-                                           uint64_t (&out)[4]) {
-        uint64_t c = 0, m = 0;
-#pragma unroll
-        for (int k = 0; k < kOwnBins; ++k) {
-            c += count[k];
-            m += mass[k];
+        cluster_sync();
+        read(sm.count, count);
+        mass[0] = mass[1] = 0;
+        if (by_mass) {
+            uint64_t hi[kOwnBins];
+            read(sm.lo, mass);
+            read(sm.hi, hi);
+            mass[0] += hi[0] << 32;
+            mass[1] += hi[1] << 32;
         }
-        if (threadIdx.x == 0) sm.found[0] = ~0ull;
-        block_below(c, m, sm);
-#pragma unroll
-        for (int k = 0; k < kOwnBins; ++k) {
-            const uint64_t before = by_mass ? m : c, here = by_mass ? mass[k] : count[k];
-            if (before < target && target <= before + here) {
-                sm.found[0] = threadIdx.x * kOwnBins + k;
-                sm.found[1] = count[k];
-                sm.found[2] = c;
-                sm.found[3] = m;
-            }
-            c += count[k];
-            m += mass[k];
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < 4; ++k) out[k] = sm.found[k];
-        __syncthreads();
-        return out[0] != ~0ull;
     }
-
-    // The cut at which the count or the mass of the logits, from the largest down, reaches the
-    // target, which lies in `bin` of the first histogram.  `which` list: the row's first or second.
-    __device__ __noinline__ Cut cut_in(uint64_t (&bin)[4], bool by_mass, bool with_mass, uint64_t target, int which) {
-        uint32_t known = 0, bits = 0;                       // leading bits of the keys in question
-        const int b0 = (int)bin[0];
-        while (bin[1] > kList && bits < 32) {
-            // More values than can be sorted: their keys' next bits, 10, 10, 10 and 2 of them.
+    // The cut in a bin of more values than are sorted: key bits, 10, 10, 10 and 2 of them.  `want` is counted
+    // from the bin's first value on; false where the bin's mass does not reach it.
+    __device__ __noinline__ bool cut_by_digits(int bin, bool by_mass, bool with_mass, uint64_t want, Cut& cut) {
+        uint32_t known = 0;
+        uint64_t count_before = 0, mass_before = 0;
+        for (uint32_t bits = 0; bits < 32;) {
             const uint32_t take = min(32 - bits, 10u);
-            uint64_t count[kOwnBins], mass[kOwnBins];
-            const uint64_t count0 = bin[2], mass0 = bin[3];
-            digits(b0, known, bits, take, with_mass, count, mass);
-            bin_of(count, mass, by_mass, target - (by_mass ? mass0 : count0), bin);
-            known = (known << take) | ((1u << take) - 1 - (uint32_t)bin[0]);
-            bits += take;
-            bin[2] += count0;
-            bin[3] += mass0;
-        }
-        Cut cut;
-        if (bits == 32) {                                   // all values left are equal
-            cut.value = key_value(known);
-            cut.above = bin[3];
-            cut.each = scale.weight(cut.value, sm.table);
-            cut.ties = (uint32_t)(by_mass ? (target - bin[3] + cut.each - 1) / cut.each : target - bin[2]);
-            return cut;
-        }
-        // The bin's keys, from every block.
-        if (which) {
-            __syncthreads();
-            cluster_sync();                                 // all have read the first list
-        }
-        each([&](int, const float (&l)[8]) {
+            uint64_t count[kOwnBins], mass[kOwnBins], all;
+            digits(bin, known, bits, take, with_mass, count, mass);
+            const Reached r = reach(by_mass ? mass : count, want - (by_mass ? mass_before : count_before), &all);
+            if (r.bin < 0) return false;                    // in the first round, if any
+            // What goes before the digit in the other measure.
+            uint64_t other = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (!scale.counts(l[i]) || scale.bin(l[i]) != b0) continue;
-                const uint32_t k = order_key(l[i]);
-                if (bits && k >> (32 - bits) != known) continue;
-                sm.list[0][atomicAdd(&sm.listed[which], 1u)] = k;
+            for (int k = 0; k < kOwnBins; ++k)
+                if ((int)threadIdx.x * kOwnBins + k < r.bin) other += by_mass ? count[k] : mass[k];
+            block_below(other, sm.scan[1], &all);
+            count_before += by_mass ? all : r.before;
+            mass_before += by_mass ? r.before : all;
+            known = (known << take) | ((1u << take) - 1 - (uint32_t)r.bin);
+            bits += take;
+        }
+        cut.value = key_value(known);
+        cut.above = mass_before;
+        cut.each = scale.weight(cut.value, sm.table);
+        cut.ties = (uint32_t)(by_mass ? (want - mass_before + cut.each - 1) / cut.each : want - count_before);
+        return true;
+    }
+
+    // The cut in `bin`, where the count (or, with `by_mass`, the mass) of all logits from the largest down
+    // reaches the target; `before` (known for counts) goes before the bin.  By mass the bin may
+    // turn out to be a neighbour: 1 where it is a later one, -1 where an earlier one, else 0.
+    __device__ __noinline__ int cut_in(int bin, bool by_mass, bool with_mass, uint64_t target, uint64_t before, bool again, Cut& cut) {
+        if (again) cluster_sync();                          // all have read the last list
+        if (threadIdx.x == 0) sm.listed = 0;
+        __syncthreads();
+        uint64_t above = 0;
+        each([&](float (&l)[8], float most, int) {
+            if (scale.bin(most) > bin) return;
+            tidy(l);
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                Weight w[2];
+                if (with_mass) scale.weights(l[i], l[i + 1], sm.table, w[0], w[1]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int b = scale.bin(l[i + k]);
+                    if (with_mass && b < bin) above += SCALE::value(w[k]);
+                    if (b != bin || !scale.counts(l[i + k])) continue;
+                    const uint32_t at = atomicAdd(&sm.listed, 1u);
+                    if (at < kList) sm.list[0][at] = order_key(l[i + k]);
+                }
             }
         });
+        push_block_sum(above, sm.above);
         cluster_sync();
-        const uint64_t want = target - (by_mass ? bin[3] : bin[2]);
-        int n = 0;
-        const auto weight_of = [&](uint32_t k) { return scale.weight(key_value(k), sm.table); };
-        if (bin[1] <= 32) {
-            // A value a lane, in every warp alike: what goes before each, and the one that reaches the target.
-            const int lane = threadIdx.x & 31;
-            uint32_t key = 0;
-            for (uint32_t r = 0; r < ranks; ++r) {
-                const int m = (int)remote_u32(&sm.listed[which], r);
-                if (lane >= n && lane < n + m) key = remote_u32(&sm.list[0][lane - n], r);
-                n += m;
-            }
-            const uint64_t w = lane < n && with_mass ? weight_of(key) : 0;
-            uint32_t c = 0, greater = 0;                    // before it: larger ones, and equal ones of lower lanes
-            uint64_t m = 0, above = 0;
-            for (int o = 0; o < n; ++o) {
-                const uint32_t k = __shfl_sync(0xffffffffu, key, o);
-                const uint64_t v = __shfl_sync(0xffffffffu, w, o);
-                const bool over = k > key, ahead = over || (k == key && o < lane);
-                c += ahead;
-                greater += over;
-                m += ahead ? v : 0;
-                above += over ? v : 0;
-            }
-            const uint64_t before = by_mass ? m : c, here = by_mass ? w : 1;
-            const uint32_t reaches = __ballot_sync(0xffffffffu, lane < n && before < want && want <= before + here);
-            const int at = __ffs(reaches) - 1;
-            cut.value = key_value(__shfl_sync(0xffffffffu, key, at));
-            cut.above = bin[3] + __shfl_sync(0xffffffffu, above, at);
-            cut.each = __shfl_sync(0xffffffffu, w, at);
-            cut.ties = (uint32_t)(by_mass ? (target - cut.above + cut.each - 1) / cut.each : want - __shfl_sync(0xffffffffu, greater, at));
-            return cut;
+        above = 0;
+        for (uint32_t r = 0; r < ranks; ++r) above += sm.above[r];
+        if (by_mass) before = above;
+        if (target <= before) return -1;
+        const uint64_t want = target - before;
+        uint32_t held[kMaxCluster], n = 0;
+#pragma unroll
+        for (uint32_t r = 0; r < kMaxCluster; ++r) held[r] = r < ranks ? remote_u32(&sm.listed, r) : 0;
+#pragma unroll
+        for (uint32_t r = 0; r < kMaxCluster; ++r) n += held[r];
+        if (n > kList) {
+            if (!cut_by_digits(bin, by_mass, with_mass, want, cut)) return 1;
+            cut.above += above;
+            return 0;
         }
-        for (uint32_t r = 0; r < ranks; ++r) {
-            const int m = (int)remote_u32(&sm.listed[which], r);
-            for (int i = threadIdx.x; i < m; i += kSampleThreads) sm.list[1][n + i] = remote_u32(&sm.list[0][i], r);
-            n += m;
+        uint32_t from = 0;
+#pragma unroll
+        for (uint32_t r = 0; r < kMaxCluster; ++r) {
+            for (uint32_t i = threadIdx.x; i < held[r]; i += kSampleThreads) sm.list[1][from + i] = remote_u32(&sm.list[0][i], r);
+            from += held[r];
         }
-        int size = 64;
+        uint32_t size = 2;
         while (size < n) size *= 2;
-        for (int i = n + threadIdx.x; i < size; i += kSampleThreads) sm.list[1][i] = 0;      // below every key
+        for (uint32_t i = n + threadIdx.x; i < size; i += kSampleThreads) sm.list[1][i] = 0;      // below every key
+        if (threadIdx.x == 0) sm.found[0] = 0;
         __syncthreads();
-        for (int k = 2; k <= size; k *= 2)                  // from the largest down, in place
-            for (int s = k / 2; s > 0; s /= 2) {
-                const int i = threadIdx.x;
-                if (i < size / 2) {
-                    const int a = 2 * i - (i & (s - 1)), b = a + s;
-                    const uint32_t x = sm.list[1][a], y = sm.list[1][b];
-                    if ((x < y) == ((a & k) == 0)) {
-                        sm.list[1][a] = y;
-                        sm.list[1][b] = x;
-                    }
-                }
-                __syncthreads();
-            }
+        sort_down(sm.list[1], (int)size);
+        __syncthreads();
         // The value where the target is reached, then what lies above it.
-        const int i = threadIdx.x * 2;
-        uint64_t w[2] = {0, 0};
-        for (int k = 0; k < 2; ++k)
+        const uint32_t i = threadIdx.x * 2;
+        const auto weight_of = [&](uint32_t k) { return scale.weight(key_value(k), sm.table); };
+        uint64_t w[2] = {0, 0}, all;
+        for (uint32_t k = 0; k < 2; ++k)
             if (i + k < n && with_mass) w[k] = weight_of(sm.list[1][i + k]);
-        uint64_t c = (i < n) + (i + 1 < n), m = w[0] + w[1];
-        block_below(c, m, sm);
-        for (int k = 0; k < 2; ++k)
+        const uint64_t m = block_below(w[0] + w[1], sm.scan[0], &all);
+        for (uint32_t k = 0; k < 2; ++k)
             if (i + k < n) {
-                const uint64_t before = by_mass ? m + (k ? w[0] : 0) : c + k, here = by_mass ? w[k] : 1;
-                if (before < want && want <= before + here) sm.found[0] = sm.list[1][i + k];
+                const uint64_t ahead = by_mass ? m + (k ? w[0] : 0) : i + k, here = by_mass ? w[k] : 1;
+                if (ahead < want && want <= ahead + here) sm.found[0] = sm.list[1][i + k];
             }
         __syncthreads();
         const uint32_t key = (uint32_t)sm.found[0];
-        for (int k = 0; k < 2; ++k) {                       // its first place in the list
-            const int at = i + k;
+        __syncthreads();                                    // all have read it
+        if (key == 0) return 1;
+        for (uint32_t k = 0; k < 2; ++k) {                  // its first place in the list
+            const uint32_t at = i + k;
             if (at < n && sm.list[1][at] == key && (at == 0 || sm.list[1][at - 1] != key)) {
-                sm.found[1] = c + k;
+                sm.found[1] = at;
                 sm.found[2] = m + (k ? w[0] : 0);
             }
         }
         __syncthreads();
         cut.value = key_value(key);
-        cut.above = bin[3] + sm.found[2];
+        cut.above = above + sm.found[2];
         cut.each = weight_of(key);
         cut.ties = (uint32_t)(by_mass ? (target - cut.above + cut.each - 1) / cut.each : want - sm.found[1]);
         __syncthreads();
-        return cut;
+        return 0;
+    }
+
+    // The row's logits up to the bin `last`, which the top_k largest are among, as the candidates of the
+    // first block; false where they are more than it sorts.
+    __device__ __forceinline__ bool collect(int last) {
+        if (threadIdx.x == 0) sm.listed = 0;
+        __syncthreads();
+        each([&](float (&l)[8], float most, int j) {
+            if (scale.bin(most) > last) return;             // bins rise as logits fall
+            tidy(l);
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i)
+                if (scale.bin(l[i]) <= last && scale.counts(l[i])) {
+                    atomicAdd(&sm.listed, 1u);
+                    const uint32_t at = remote_add(&sm.paired, 0, 1);
+                    if (at < kList) push_u64(&sm.pairs[at], 0, (uint64_t)order_key(l[i]) << 32 | (uint32_t)~(j + i - row.first));
+                }
+        });
+        __syncthreads();
+        if (threadIdx.x < ranks) push_u32(&sm.few[rank], threadIdx.x, sm.listed);
+        cluster_sync();
+        uint32_t n = 0;
+        for (uint32_t r = 0; r < ranks; ++r) n += sm.few[r];
+        return n <= kList;
+    }
+    // A draw from them.  Sorted by value, then by index, they give the kept ones; sorted by index the token.
+    __device__ __noinline__ void draw_of_few(const SampleParams& p, int64_t b, float best, int top_k, float top_p, float min_p) {
+        if (rank != 0) return;
+        const uint32_t n = sm.paired;
+        uint32_t size = 2;
+        while (size < n) size *= 2;
+        const bool small = size <= 64;                      // one warp does it all
+        if (small && threadIdx.x >= 32) return;
+        const auto sync = [&] {
+            if (small) __syncwarp();
+            else __syncthreads();
+        };
+        const auto below = [&](uint64_t v, uint64_t* all) {
+            if (!small) return block_below(v, sm.scan[0], all);
+            const uint64_t x = warp_below(v, threadIdx.x);
+            *all = __shfl_sync(0xffffffffu, x + v, 31);
+            return x;
+        };
+        for (uint32_t i = n + threadIdx.x; i < size; i += small ? 32 : kSampleThreads) sm.pairs[i] = 0;
+        sync();
+        sort_down(sm.pairs, (int)size);
+        sync();
+        const uint32_t i = threadIdx.x * 2;
+        uint64_t w[2] = {0, 0}, all;
+        float l[2] = {0.f, 0.f};
+        if (i < size) {
+            l[0] = key_value((uint32_t)(sm.pairs[i] >> 32));
+            l[1] = key_value((uint32_t)(sm.pairs[i + 1] >> 32));
+            Weight x[2];
+            scale.weights(l[0], l[1], sm.table, x[0], x[1]);
+            for (uint32_t k = 0; k < 2; ++k) w[k] = i + k < min(n, (uint32_t)top_k) ? SCALE::value(x[k]) : 0;
+        }
+        if (top_p < 1.f) {
+            uint64_t m = below(w[0] + w[1], &all);
+            const uint64_t target = max(part_of(top_p, all, true), (uint64_t)1);
+            for (uint32_t k = 0; k < 2; ++k) {              // what begins at or behind the target is not kept
+                const uint64_t here = w[k];
+                if (m >= target) w[k] = 0;
+                m += here;
+            }
+        }
+        const uint64_t least = least_weight(min_p, best);
+        sync();
+        for (uint32_t k = 0; k < 2; ++k)
+            if (i < size) {
+                if (w[k] < least && l[k] != best) w[k] = 0;
+                // By index: the largest first, and its complement in order.  Weights have 44 bits, indices 20.
+                sm.pairs[i + k] = (uint64_t)(0xfffffu & (uint32_t)sm.pairs[i + k]) << 44 | w[k];
+            }
+        sync();
+        sort_down(sm.pairs, (int)size);
+        sync();
+        constexpr uint64_t kWeightBits = (1ull << 44) - 1;
+        w[0] = i < size ? sm.pairs[i] & kWeightBits : 0;
+        w[1] = i < size ? sm.pairs[i + 1] & kWeightBits : 0;
+        uint64_t m = below(w[0] + w[1], &all);
+        const float u = p.u[b];
+        const uint64_t target = u < 1.f ? part_of(u, all, false) : all - 1;
+        for (uint32_t k = 0; k < 2; ++k) {
+            if (target >= m && target < m + w[k]) {
+                const int at = 0xfffff - (int)(sm.pairs[i + k] >> 44);
+                p.tokens[b] = at;
+                if (p.logprobs) p.logprobs[b] = log_share(row.one(at + row.first), w[k], all);
+            }
+            m += w[k];
+        }
+    }
+
+    __device__ __forceinline__ uint64_t least_weight(float min_p, float best) const {
+        return min_p > 0.f ? min_p < 1.f ? part_of(min_p, scale.weight(best, sm.table), true) : ~0ull : 0;
     }
 
     // From the largest logit to the token.
-    __device__ __forceinline__ void draw(const SampleParams& p, int64_t b, float best, int top_k, float top_p, float min_p) {
+    __device__ __forceinline__ void draw(const SampleParams& p, int64_t b, float best, float most, int top_k, float top_p, float min_p) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         Cut cut{-INFINITY, 0, 0, 0};                        // everything
         const bool by_k = top_k > 0 && top_k < p.V, by_p = top_p < 1.f;
-        if (by_k || by_p) {
-            uint64_t count[kOwnBins], mass[kOwnBins], bin[4], total = ~0ull;
-            histogram(true, by_p, count, mass);
-            if (by_k && bin_of(count, mass, false, (uint64_t)top_k, bin) && bin[0] < kDeadBin) {
-                cut = cut_in(bin, false, by_p, (uint64_t)top_k, 0);
+        uint64_t bins[kOwnBins], total = 0, all;
+        if (by_k) {
+            // As many lanes as top_k have a logit of this bin or above, so the top_k largest are there, too.
+            count_lanes(most, bins);
+            Reached r = reach(bins, (uint64_t)top_k, &all);
+            if (r.bin >= 0 && r.bin < kDeadBin && collect(r.bin)) return draw_of_few(p, b, best, top_k, top_p, min_p);
+            count_all(bins);
+            r = reach(bins, (uint64_t)top_k, &all);
+            if (r.bin >= 0 && r.bin < kDeadBin) {
+                cut_in(r.bin, false, by_p, (uint64_t)top_k, r.before, false, cut);
                 total = cut.above + cut.ties * cut.each;
             }
-            if (by_p) {
-                if (total == ~0ull) {
-                    uint64_t c = 0, m = 0;
-#pragma unroll
-                    for (int k = 0; k < kOwnBins; ++k) m += mass[k];
-                    total = block_below(c, m, sm);
-                }
-                const uint64_t target = max(part_of(top_p, total, true), (uint64_t)1);
-                if (bin_of(count, mass, true, target, bin)) cut = cut_in(bin, true, true, target, 1);
+            if (by_p) clear();
+        }
+        if (by_p) {
+            const uint64_t whole = weigh_bins(bins);
+            if (total == 0) total = whole;
+            const uint64_t target = max(part_of(top_p, total, true), (uint64_t)1);
+            reach(bins, 1, &all);
+            // Weights to 15 bits, rounded down: half of what that leaves out goes off the target.
+            uint64_t rough = min(max(target - (target >> 15), (uint64_t)1), all);
+            for (int round = 0; round < kBins; ++round) {              // one, or two where the target is next to a bin's border
+                const Reached r = reach(bins, rough, &all);
+                const int side = cut_in(r.bin, true, true, target, 0, by_k || round, cut);
+                if (side == 0) break;
+                rough = side < 0 ? r.before : r.before + r.here + 1;       // the next bin with anything in it
             }
         }
 
         // Mass of what is kept, over warps, blocks and the row; equal values at the cut count by index.
-        const uint64_t least = min_p > 0.f ? min_p < 1.f ? part_of(min_p, scale.weight(best, sm.table), true) : ~0ull : 0;
+        const uint64_t least = least_weight(min_p, best);
         const auto kept = [&](float l, uint64_t w) -> uint64_t { return w >= least || l == best ? w : 0; };
         const auto kept_weight = [&](float l) -> uint64_t { return kept(l, scale.weight(l, sm.table)); };
         cut.each = cut.value == -INFINITY ? 0 : kept_weight(cut.value);
         uint64_t mass = 0;
         uint32_t ties = 0;
-        each([&](int, const float (&l)[8]) {
+        if (cut.value == -INFINITY && least == 0) {
+            each([&](float (&l)[8], float, int) {
+                tidy(l);
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                if (l[i] > cut.value || l[i + 1] > cut.value) {
-                    uint64_t w[2];
+                for (int i = 0; i < 8; i += 2) {
+                    Weight w[2];
                     scale.weights(l[i], l[i + 1], sm.table, w[0], w[1]);
-                    mass += (l[i] > cut.value ? kept(l[i], w[0]) : 0) + (l[i + 1] > cut.value ? kept(l[i + 1], w[1]) : 0);
+                    mass += SCALE::value(w[0]);
+                    mass += SCALE::value(w[1]);
                 }
-                ties += (l[i] == cut.value) + (l[i + 1] == cut.value);
-            }
-        });
+            });
+        } else {
+            each([&](float (&l)[8], float most, int) {
+                if (most < cut.value) return;
+                tidy(l);
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    if (fmaxf(l[i], l[i + 1]) < cut.value) continue;
+                    Weight w[2];
+                    scale.weights(l[i], l[i + 1], sm.table, w[0], w[1]);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        if (l[i + k] > cut.value) mass += kept(l[i + k], SCALE::value(w[k]));
+                        ties += l[i + k] == cut.value;
+                    }
+                }
+            });
+        }
         mass = warp_sum(mass);
         ties = warp_sum(ties);
         if (lane == 0) {
@@ -685,13 +885,14 @@ struct Sampler {
         }
         // The warp that holds the running mass's passage goes through its values again.
         if (target < before || target >= before + with_ties(mass, seen, ties)) return;
-        int step = 0;
-        for (int j = j0 + lane * 8; j - lane * 8 < j1; j += 256, ++step) {
+        for (int j = j0 + lane * 8; j - lane * 8 < j1; j += 256) {
             float l[8];
             uint64_t w[8], m = 0;
             uint32_t n = 0;
             if (j < j1) {
-                row.eight(j, step, l);
+                uint4 v[Row<TYPE>::kPieces];
+                row.load(j, v);
+                row.widen(v, l);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     l[i] = scale.tidy(l[i]);
@@ -704,6 +905,7 @@ struct Sampler {
             const uint64_t mine = with_ties(m, at, n);
             uint64_t sum = before + warp_below(mine, lane);
             if (target >= sum && target < sum + mine) {
+#pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const uint64_t here = l[i] == cut.value ? (at++ < cut.ties ? cut.each : 0) : w[i];
                     if (target >= sum && target < sum + here) {
@@ -719,16 +921,15 @@ struct Sampler {
     }
 
     // log(w / whole): near one by what is missing, from 2^24 units on by the quotient, else by the place.
-    __device__ __forceinline__ float log_share(float l, uint64_t w, uint64_t whole) const {
+    __device__ __noinline__ float log_share(float l, uint64_t w, uint64_t whole) const {
         if (w > whole / 2) return log1pf(-((float)(whole - w) / (float)whole));
         if (w >= 1u << 24) return logf((float)w / (float)whole);
         return scale.log_weight(l) - logf((float)whole * (1.f / (float)(1ull << kOneLog2)));
     }
 };
 
-template <int TYPE, bool HELD>
+template <int TYPE>
 __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleParams p) {
-    extern __shared__ __align__(16) uint8_t sm_held[];
     __shared__ Shared sm;
     cluster_arrive();                                       // that every block of the row runs: before the first push
     const uint32_t rank = cluster_rank(), ranks = cluster_ranks();
@@ -736,32 +937,29 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleP
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     sm.table[threadIdx.x] = table_entry(kExp2.v[threadIdx.x]);
     for (int i = threadIdx.x; i < kBins; i += kSampleThreads) sm.count[i] = sm.lo[i] = sm.hi[i] = 0;
-    if (threadIdx.x < 2) sm.listed[threadIdx.x] = 0;
+    if (threadIdx.x == 0) sm.paired = 0;
     pdl_wait_previous();
     pdl_launch_dependents();
     const float temperature = p.how.temperature ? p.how.temperature[b] : p.how.temperature_all;
     const bool greedy = !(temperature > 0.f);
     const int top_k = p.how.top_k ? p.how.top_k[b] : p.how.top_k_all;
     const float top_p = p.how.top_p ? p.how.top_p[b] : p.how.top_p_all, min_p = p.how.min_p ? p.how.min_p[b] : p.how.min_p_all;
-    const Row<TYPE, HELD> row(p.logits, b * p.stride, p.V, sm_held);
+    const Row<TYPE> row(p.logits, b * p.stride, p.V);
     const int64_t start = ((int64_t)rank * kSampleWarps + warp) * p.chunk;
     const int j0 = (int)min(start, (int64_t)row.end), j1 = (int)min(start + p.chunk, (int64_t)row.end);
 
-    // The largest logit, the first of equal ones; four loads in flight.
-    constexpr int U = 4 / Row<TYPE, HELD>::kPieces;
+    // The largest logit, the first of equal ones; eight loads in flight.
+    constexpr int U = 8 / Row<TYPE>::kPieces;
     float best = -INFINITY;
-    int best_at = INT32_MAX, step = 0;
-    for (int j = j0 + lane * 8; j < j1; j += 256 * U, step += U) {
-        uint4 v[U][Row<TYPE, HELD>::kPieces];
+    int best_at = INT32_MAX;
+    for (int j = j0 + lane * 8; j < j1; j += 256 * U) {
+        uint4 v[U][Row<TYPE>::kPieces];
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (j + u * 256 < j1) row.load(j + u * 256, v[u]);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (j + u * 256 >= j1) break;
-            if (HELD)
-#pragma unroll
-                for (int k = 0; k < Row<TYPE, HELD>::kPieces; ++k) row.place(step + u)[k * 32] = v[u][k];
             float l[8];
             row.widen(v[u], l);
             float m = fmaxf(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])), fmaxf(fmaxf(l[4], l[5]), fmaxf(l[6], l[7])));
@@ -775,6 +973,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleP
             }
         }
     }
+    const float most = best;                                // of this lane
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const float other = __shfl_xor_sync(0xffffffffu, best, o);
@@ -819,16 +1018,13 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleP
     }
     NearScale near;
     if (near.set(best, temperature)) {
-        Sampler<TYPE, HELD, NearScale>{sm, row, rank, ranks, j0, j1, near}.draw(p, b, best, top_k, top_p, min_p);
+        Sampler<TYPE, NearScale>{sm, row, rank, ranks, j0, j1, near}.draw(p, b, best, most, top_k, top_p, min_p);
     } else {
         FarScale far;
         far.set(best, temperature);
-        Sampler<TYPE, HELD, FarScale>{sm, row, rank, ranks, j0, j1, far}.draw(p, b, best, top_k, top_p, min_p);
+        Sampler<TYPE, FarScale>{sm, row, rank, ranks, j0, j1, far}.draw(p, b, best, most, top_k, top_p, min_p);
     }
 }
-
-template <int TYPE>
-const void* sample_kernel_of(bool held) { return held ? (const void*)sample_kernel<TYPE, true> : (const void*)sample_kernel<TYPE, false>; }
 
 }  // namespace
 }  // namespace nvfp4
@@ -857,18 +1053,14 @@ extern "C" nvfp4_status nvfp4_sample(const void* logits, int64_t row_stride, int
             return fail(NVFP4_ERR_INVALID_ARG, "%s: %s overlaps %s", fn, out.name, s);
     if (overlaps(t, lp)) return fail(NVFP4_ERR_INVALID_ARG, "%s: logprobs overlap tokens", fn);
     if (!device_status_ptr()) return fail(NVFP4_ERR_CUDA, "%s: no CUDA device", fn);
-    // Blocks of a row: enough of them to fill the SMs with two each, none with less than 4096 logits;
-    // more where a block's part then stays in shared memory beside another block's.
-    const auto part = [&](unsigned ranks) { return round_up(ceil_div(ceil_div(V + 7, ranks), kSampleWarps), 8); };      // of a warp
-    const auto bytes = [&](unsigned ranks) { return (size_t)ceil_div(part(ranks), 256) * 256 * kSampleWarps * size; };
+    // Blocks of a row: enough of them for every SM, none with less than 4096 logits.
     unsigned ranks = 1;
-    while (ranks < kMaxCluster && ((B * ranks < sm_count() && V / (2 * ranks) >= 4096) || bytes(ranks) > kHeldBytes)) ranks *= 2;
-    const bool held = bytes(ranks) <= kHeldBytes;
+    while (ranks < kMaxCluster && B * ranks < sm_count() && V / (2 * ranks) >= 4096) ranks *= 2;
     SampleParams p{};
     p.logits = logits; p.stride = row_stride; p.u = u; p.how = *how; p.tokens = tokens; p.logprobs = logprobs;
-    p.V = (int)V; p.chunk = (int)part(ranks);
-    const void* kernel = type == NVFP4_LOGITS_BF16 ? sample_kernel_of<kTypeBf16>(held)
-                       : type == NVFP4_LOGITS_F16 ? sample_kernel_of<kTypeF16>(held) : sample_kernel_of<kTypeF32>(held);
+    p.V = (int)V; p.chunk = (int)round_up(ceil_div(ceil_div(V + 7, ranks), kSampleWarps), 8);
+    const void* kernel = type == NVFP4_LOGITS_BF16 ? (const void*)sample_kernel<kTypeBf16>
+                       : type == NVFP4_LOGITS_F16 ? (const void*)sample_kernel<kTypeF16> : (const void*)sample_kernel<kTypeF32>;
     void* args[] = {&p};
-    return launch_kernel(kernel, dim3((unsigned)(B * ranks)), dim3(kSampleThreads), held ? bytes(ranks) : 0, ranks, args, (cudaStream_t)stream, fn);
+    return launch_kernel(kernel, dim3((unsigned)(B * ranks)), dim3(kSampleThreads), 0, ranks, args, (cudaStream_t)stream, fn);
 }
