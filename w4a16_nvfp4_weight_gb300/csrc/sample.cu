@@ -27,6 +27,7 @@ constexpr int kSampleWarps = kSampleThreads / 32;
 constexpr int kBins = 1024;                // of the histogram
 constexpr int kList = 1024;                // values sorted at most
 constexpr int kMaxCluster = 8;
+constexpr int kStages = 4;                 // steps of a warp in flight or in use
 constexpr int kOneLog2 = 43;               // a weight of one is 2^43: 2^20 of them sum inside 63 bits
 constexpr int64_t kMaxVocabulary = 1 << 20;
 
@@ -55,7 +56,7 @@ struct SampleParams {
     nvfp4_sampling how;
     int64_t* tokens;
     float* logprobs;
-    int V, chunk;                          // chunk: virtual elements of a warp, a multiple of 8
+    int V, chunk;                          // chunk: virtual elements of a warp, a multiple of 256
 };
 
 // A number whose last bit is worth one: added to a float below 2^22, it leaves the nearest
@@ -211,11 +212,15 @@ __device__ __forceinline__ uint64_t part_of(float f, uint64_t s, bool up) {
 
 enum { kTypeBf16, kTypeF16, kTypeF32 };
 
-// The row's virtual elements, in 16-byte pieces: element 0 is on a boundary of eight elements.
+// The row's virtual elements, in 16-byte pieces: element 0 is on a boundary of eight elements.  A warp
+// takes them in steps of 256, each piece of a step (one of eight elements a lane, or two of four) as 512
+// bytes side by side.
 template <int TYPE>
 struct Row {
     static constexpr int kSize = TYPE == kTypeF32 ? 4 : 2;
-    static constexpr int kPieces = kSize / 2;              // of eight elements
+    static constexpr int kPieces = kSize / 2, kPer = 8 / kPieces;
+    static constexpr int kStageBytes = 512 * kPieces;
+    static constexpr int kRingBytes = kSampleWarps * kStages * kStageBytes;
     const uint8_t* base;
     int first, end;                        // virtual elements that are the row's
 
@@ -228,23 +233,18 @@ struct Row {
     __device__ __forceinline__ float one(int j) const {
         return TYPE == kTypeF32 ? ((const float*)base)[j] : act_to_f32<TYPE == kTypeF16>(((const uint16_t*)base)[j]);
     }
-    // Elements j to j + 7 (j a multiple of 8) from memory, -infinity outside the row.
-    __device__ __forceinline__ void load(int j, uint4 (&v)[kPieces]) const {
-        if (j >= first && j + 8 <= end) {
+    // Where element i of the eight lies that a lane has of the step at `at`.
+    __device__ __forceinline__ static int index(int at, int i) { return at + i / kPer * 32 * kPer + (threadIdx.x & 31) * kPer + i % kPer; }
+
+    // The piece from element j on, -infinity outside the row.
+    __device__ __forceinline__ uint4 load(int j) const {
+        if (j >= first && j + kPer <= end) return *(const uint4*)(base + (int64_t)j * kSize);
+        uint32_t w[4];
 #pragma unroll
-            for (int k = 0; k < kPieces; ++k) v[k] = ((const uint4*)(base + (int64_t)j * kSize))[k];
-            return;
-        }
-        if (TYPE == kTypeF32) {
-            uint32_t w[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = j + i >= first && j + i < end ? ((const uint32_t*)base)[j + i] : 0xff800000u;
-            v[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            v[kPieces - 1] = make_uint4(w[4], w[5], w[6], w[7]);
-        } else {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 4; ++i) {
+            if (TYPE == kTypeF32) {
+                w[i] = j + i >= first && j + i < end ? ((const uint32_t*)base)[j + i] : 0xff800000u;
+            } else {
                 uint32_t h[2];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
@@ -253,8 +253,17 @@ struct Row {
                 }
                 w[i] = h[0] | h[1] << 16;
             }
-            v[0] = make_uint4(w[0], w[1], w[2], w[3]);
         }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // The same, to shared memory: asynchronous but at the row's ends.
+    __device__ __forceinline__ void copy(int j, uint32_t to) const {
+        if (j >= first && j + kPer <= end) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(base + (int64_t)j * kSize) : "memory");
+            return;
+        }
+        const uint4 v = load(j);
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
     }
     __device__ __forceinline__ static void widen(const uint4 (&v)[kPieces], float (&l)[8]) {
         const uint32_t* w = (const uint32_t*)v;
@@ -269,6 +278,38 @@ struct Row {
                 l[2 * i + 1] = x.y;
             }
         }
+    }
+    // f(eight logits, the step's first element) over the elements j0 to j1 (multiples of 256 after j0, or the
+    // row's end) of a warp, three steps ahead of it on their way.  A lane reads what it copied.
+    template <class F>
+    __device__ __forceinline__ void each(int j0, int j1, uint32_t ring, F f) const {
+        ring += (threadIdx.x >> 5) * kStages * kStageBytes + (threadIdx.x & 31) * 16;
+        const auto stage = [&](int at, int s) {
+            if (at < j1)
+#pragma unroll
+                for (int k = 0; k < kPieces; ++k) copy(index(at, k * kPer), ring + s * kStageBytes + k * 512);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+#pragma unroll
+        for (int s = 0; s < kStages - 1; ++s) stage(j0 + s * 256, s);
+        int s = 0;
+        for (int at = j0; at < j1; at += 256) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+            uint4 v[kPieces];
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k)
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[k].x), "=r"(v[k].y), "=r"(v[k].z), "=r"(v[k].w)
+                             : "r"(ring + s * kStageBytes + k * 512) : "memory");
+            float l[8];
+            widen(v, l);
+            stage(at + (kStages - 1) * 256, (s + kStages - 1) % kStages);
+            s = (s + 1) % kStages;
+            f(l, at);
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+    __device__ __forceinline__ static float largest(const float (&l)[8]) {
+        return fmaxf(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])), fmaxf(fmaxf(l[4], l[5]), fmaxf(l[6], l[7])));
     }
 };
 
@@ -400,6 +441,12 @@ __device__ __forceinline__ void add_mass(Shared& sm, int bin, uint64_t w) {
 
 constexpr int kOwnBins = kBins / kSampleThreads;           // bins of a thread when they are summed
 
+struct Bins {                              // of one thread
+    uint64_t of[kOwnBins];
+    __device__ __forceinline__ uint64_t& operator[](int k) { return of[k]; }
+    __device__ __forceinline__ const uint64_t& operator[](int k) const { return of[k]; }
+};
+
 // A bin where a running sum reaches a target: what it holds, and what goes before it.
 struct Reached {
     int bin;
@@ -410,24 +457,16 @@ template <int TYPE, class SCALE>
 struct Sampler {
     using Weight = typename SCALE::Weight;
     Shared& sm;
-    const Row<TYPE>& row;
-    const uint32_t rank, ranks;
-    const int j0, j1;                      // virtual elements of this warp
-    const SCALE& scale;
+    Row<TYPE> row;
+    uint32_t ring;                         // shared address of the warps' stages
+    uint32_t rank, ranks;
+    int j0, j1;                            // virtual elements of this warp
+    SCALE scale;
 
-    // f(eight logits, their largest, the first's index) over this warp's elements.
+    // f(eight logits, their largest, the step's first element) over this warp's elements.
     template <class F>
     __device__ __forceinline__ void each(F f) const {
-        int j = j0 + (threadIdx.x & 31) * 8;
-        if (j >= j1) return;
-        uint4 next[Row<TYPE>::kPieces];                     // a load ahead
-        row.load(j, next);
-        for (; j < j1; j += 256) {
-            float l[8];
-            row.widen(next, l);
-            if (j + 256 < j1) row.load(j + 256, next);
-            f(l, scale.tidy(fmaxf(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])), fmaxf(fmaxf(l[4], l[5]), fmaxf(l[6], l[7])))), j);
-        }
+        row.each(j0, j1, ring, [&](float (&l)[8], int j) { f(l, scale.tidy(Row<TYPE>::largest(l)), j); });
     }
     __device__ __forceinline__ void tidy(float (&l)[8]) const {
 #pragma unroll
@@ -440,7 +479,7 @@ struct Sampler {
         __syncthreads();
     }
     // Sums of this thread's two bins over the blocks, after a barrier of them.
-    __device__ __forceinline__ void read(const uint32_t (&bins)[kBins], uint64_t (&sum)[kOwnBins]) const {
+    __device__ __forceinline__ void read(const uint32_t (&bins)[kBins], Bins& sum) const {
         static_assert(kOwnBins == 2, "read in pairs");
         uint2 v[kMaxCluster];
         const uint32_t at = smem_u32(&bins[threadIdx.x * 2]);
@@ -455,15 +494,20 @@ struct Sampler {
     }
 
     // Counts of the lanes' largest logits.
-    __device__ __forceinline__ void count_lanes(float most, uint64_t (&count)[kOwnBins]) {
+    __device__ __forceinline__ void count_lanes(float most, Bins& count) {
         most = scale.tidy(most);
         if (scale.counts(most)) atomicAdd(&sm.count[scale.bin(most)], 1u);
         cluster_sync();
         read(sm.count, count);
     }
     // Counts of all logits of the row.
-    __device__ __noinline__ void count_all(uint64_t (&count)[kOwnBins]) {
-        clear();
+    __device__ __noinline__ static Bins count_all(Sampler s) {
+        s.clear();
+        Bins count;
+        s.count(count);
+        return count;
+    }
+    __device__ __forceinline__ void count(Bins& count) const {
         each([&](float (&l)[8], float, int) {
             tidy(l);
 #pragma unroll
@@ -476,7 +520,7 @@ struct Sampler {
 
     // The row's mass, exactly, and that of each bin but for up to 2^-14 of it: to 15 bits of each weight
     // one addition in shared memory does, and the bin in question is known but for its neighbours.
-    __device__ __forceinline__ uint64_t weigh_bins(uint64_t (&mass)[kOwnBins]) {
+    __device__ __forceinline__ uint64_t weigh_bins(Bins& mass) {
         uint64_t sum = 0;
         each([&](float (&l)[8], float, int) {
             tidy(l);
@@ -517,7 +561,7 @@ struct Sampler {
     }
 
     // The bin in which the running sum reaches the target; bin -1 where it never does.
-    __device__ __forceinline__ Reached reach(const uint64_t (&v)[kOwnBins], uint64_t target, uint64_t* all) {
+    __device__ __forceinline__ Reached reach(const Bins& v, uint64_t target, uint64_t* all) {
         uint64_t mine = 0;
 #pragma unroll
         for (int k = 0; k < kOwnBins; ++k) mine += v[k];
@@ -540,8 +584,8 @@ struct Sampler {
 
     // Exact counts and masses of one bin's logits whose keys begin with the `bits` bits `known`, by
     // their next `take` bits, the largest first.
-    __device__ __forceinline__ void digits(int bin, uint32_t known, uint32_t bits, uint32_t take, bool by_mass, uint64_t (&count)[kOwnBins],
-                                           uint64_t (&mass)[kOwnBins]) {
+    __device__ __forceinline__ void digits(int bin, uint32_t known, uint32_t bits, uint32_t take, bool by_mass, Bins& count,
+                                           Bins& mass) {
         clear();
         each([&](float (&l)[8], float most, int) {
             if (scale.bin(most) > bin) return;
@@ -559,7 +603,7 @@ struct Sampler {
         read(sm.count, count);
         mass[0] = mass[1] = 0;
         if (by_mass) {
-            uint64_t hi[kOwnBins];
+            Bins hi;
             read(sm.lo, mass);
             read(sm.hi, hi);
             mass[0] += hi[0] << 32;
@@ -568,12 +612,22 @@ struct Sampler {
     }
     // The cut in a bin of more values than are sorted: key bits, 10, 10, 10 and 2 of them.  `want` is counted
     // from the bin's first value on; false where the bin's mass does not reach it.
-    __device__ __noinline__ bool cut_by_digits(int bin, bool by_mass, bool with_mass, uint64_t want, Cut& cut) {
+    struct Ended {
+        Cut cut;
+        int side;                          // the target lies in an earlier bin (-1), here, in a later one
+    };
+    __device__ __noinline__ static Ended cut_by_digits(Sampler s, int bin, bool by_mass, bool with_mass, uint64_t want) {
+        Ended e;
+        e.side = s.digits_cut(bin, by_mass, with_mass, want, e.cut) ? 0 : 1;
+        return e;
+    }
+    __device__ __forceinline__ bool digits_cut(int bin, bool by_mass, bool with_mass, uint64_t want, Cut& cut) {
         uint32_t known = 0;
         uint64_t count_before = 0, mass_before = 0;
         for (uint32_t bits = 0; bits < 32;) {
             const uint32_t take = min(32 - bits, 10u);
-            uint64_t count[kOwnBins], mass[kOwnBins], all;
+            Bins count, mass;
+            uint64_t all;
             digits(bin, known, bits, take, with_mass, count, mass);
             const Reached r = reach(by_mass ? mass : count, want - (by_mass ? mass_before : count_before), &all);
             if (r.bin < 0) return false;                    // in the first round, if any
@@ -598,7 +652,12 @@ struct Sampler {
     // The cut in `bin`, where the count (or, with `by_mass`, the mass) of all logits from the largest down
     // reaches the target; `before` (known for counts) goes before the bin.  By mass the bin may
     // turn out to be a neighbour: 1 where it is a later one, -1 where an earlier one, else 0.
-    __device__ __noinline__ int cut_in(int bin, bool by_mass, bool with_mass, uint64_t target, uint64_t before, bool again, Cut& cut) {
+    __device__ __noinline__ static Ended cut_by_count(Sampler s, int bin, bool with_mass, uint64_t target, uint64_t before) {
+        Ended e;
+        e.side = s.cut_in(bin, false, with_mass, target, before, false, e.cut);
+        return e;
+    }
+    __device__ __forceinline__ int cut_in(int bin, bool by_mass, bool with_mass, uint64_t target, uint64_t before, bool again, Cut& cut) {
         if (again) cluster_sync();                          // all have read the last list
         if (threadIdx.x == 0) sm.listed = 0;
         __syncthreads();
@@ -633,9 +692,10 @@ struct Sampler {
 #pragma unroll
         for (uint32_t r = 0; r < kMaxCluster; ++r) n += held[r];
         if (n > kList) {
-            if (!cut_by_digits(bin, by_mass, with_mass, want, cut)) return 1;
+            const Ended e = cut_by_digits(*this, bin, by_mass, with_mass, want);
+            cut = e.cut;
             cut.above += above;
-            return 0;
+            return e.side;
         }
         uint32_t from = 0;
 #pragma unroll
@@ -695,7 +755,7 @@ struct Sampler {
                 if (scale.bin(l[i]) <= last && scale.counts(l[i])) {
                     atomicAdd(&sm.listed, 1u);
                     const uint32_t at = remote_add(&sm.paired, 0, 1);
-                    if (at < kList) push_u64(&sm.pairs[at], 0, (uint64_t)order_key(l[i]) << 32 | (uint32_t)~(j + i - row.first));
+                    if (at < kList) push_u64(&sm.pairs[at], 0, (uint64_t)order_key(l[i]) << 32 | (uint32_t)~(Row<TYPE>::index(j, i) - row.first));
                 }
         });
         __syncthreads();
@@ -706,7 +766,7 @@ struct Sampler {
         return n <= kList;
     }
     // A draw from them.  Sorted by value, then by index, they give the kept ones; sorted by index the token.
-    __device__ __noinline__ void draw_of_few(const SampleParams& p, int64_t b, float best, int top_k, float top_p, float min_p) {
+    __device__ __forceinline__ void draw_of_few(const SampleParams& p, int64_t b, float best, int top_k, float top_p, float min_p) {
         if (rank != 0) return;
         const uint32_t n = sm.paired;
         uint32_t size = 2;
@@ -778,20 +838,24 @@ struct Sampler {
     }
 
     // From the largest logit to the token.
+    __device__ __noinline__ static void draw_far(Sampler s, const SampleParams& p, int64_t b, float best, float most, int top_k, float top_p, float min_p) {
+        s.draw(p, b, best, most, top_k, top_p, min_p);
+    }
     __device__ __forceinline__ void draw(const SampleParams& p, int64_t b, float best, float most, int top_k, float top_p, float min_p) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         Cut cut{-INFINITY, 0, 0, 0};                        // everything
         const bool by_k = top_k > 0 && top_k < p.V, by_p = top_p < 1.f;
-        uint64_t bins[kOwnBins], total = 0, all;
+        Bins bins;
+        uint64_t total = 0, all;
         if (by_k) {
             // As many lanes as top_k have a logit of this bin or above, so the top_k largest are there, too.
             count_lanes(most, bins);
             Reached r = reach(bins, (uint64_t)top_k, &all);
             if (r.bin >= 0 && r.bin < kDeadBin && collect(r.bin)) return draw_of_few(p, b, best, top_k, top_p, min_p);
-            count_all(bins);
+            bins = count_all(*this);
             r = reach(bins, (uint64_t)top_k, &all);
             if (r.bin >= 0 && r.bin < kDeadBin) {
-                cut_in(r.bin, false, by_p, (uint64_t)top_k, r.before, false, cut);
+                cut = cut_by_count(*this, r.bin, by_p, (uint64_t)top_k, r.before).cut;
                 total = cut.above + cut.ties * cut.each;
             }
             if (by_p) clear();
@@ -885,31 +949,29 @@ struct Sampler {
         }
         // The warp that holds the running mass's passage goes through its values again.
         if (target < before || target >= before + with_ties(mass, seen, ties)) return;
-        for (int j = j0 + lane * 8; j - lane * 8 < j1; j += 256) {
+        constexpr int kPer = Row<TYPE>::kPer;
+        for (int at = j0; at < j1; at += 32 * kPer) {       // in index order: a piece a lane
+            const uint4 v[2] = {row.load(at + lane * kPer), make_uint4(0, 0, 0, 0)};
             float l[8];
-            uint64_t w[8], m = 0;
+            uint64_t w[kPer], m = 0;
             uint32_t n = 0;
-            if (j < j1) {
-                uint4 v[Row<TYPE>::kPieces];
-                row.load(j, v);
-                row.widen(v, l);
+            Row<TYPE>::widen(*(const uint4(*)[Row<TYPE>::kPieces])v, l);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    l[i] = scale.tidy(l[i]);
-                    w[i] = l[i] > cut.value ? kept_weight(l[i]) : 0;
-                    m += w[i];
-                    n += l[i] == cut.value;
-                }
+            for (int i = 0; i < kPer; ++i) {
+                l[i] = scale.tidy(l[i]);
+                w[i] = l[i] > cut.value ? kept_weight(l[i]) : 0;
+                m += w[i];
+                n += l[i] == cut.value;
             }
-            uint32_t at = seen + warp_below(n, lane);
-            const uint64_t mine = with_ties(m, at, n);
+            uint32_t tie = seen + warp_below(n, lane);
+            const uint64_t mine = with_ties(m, tie, n);
             uint64_t sum = before + warp_below(mine, lane);
             if (target >= sum && target < sum + mine) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint64_t here = l[i] == cut.value ? (at++ < cut.ties ? cut.each : 0) : w[i];
+                for (int i = 0; i < kPer; ++i) {
+                    const uint64_t here = l[i] == cut.value ? (tie++ < cut.ties ? cut.each : 0) : w[i];
                     if (target >= sum && target < sum + here) {
-                        p.tokens[b] = j + i - row.first;
+                        p.tokens[b] = at + lane * kPer + i - row.first;
                         if (p.logprobs) p.logprobs[b] = log_share(l[i], here, whole);
                     }
                     sum += here;
@@ -921,7 +983,7 @@ struct Sampler {
     }
 
     // log(w / whole): near one by what is missing, from 2^24 units on by the quotient, else by the place.
-    __device__ __noinline__ float log_share(float l, uint64_t w, uint64_t whole) const {
+    __device__ __forceinline__ float log_share(float l, uint64_t w, uint64_t whole) const {
         if (w > whole / 2) return log1pf(-((float)(whole - w) / (float)whole));
         if (w >= 1u << 24) return logf((float)w / (float)whole);
         return scale.log_weight(l) - logf((float)whole * (1.f / (float)(1ull << kOneLog2)));
@@ -930,7 +992,9 @@ struct Sampler {
 
 template <int TYPE>
 __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleParams p) {
+    extern __shared__ __align__(16) uint8_t sm_ring[];
     __shared__ Shared sm;
+    const uint32_t ring = smem_u32(sm_ring);
     cluster_arrive();                                       // that every block of the row runs: before the first push
     const uint32_t rank = cluster_rank(), ranks = cluster_ranks();
     const int64_t b = blockIdx.x / ranks;
@@ -948,31 +1012,20 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleP
     const int64_t start = ((int64_t)rank * kSampleWarps + warp) * p.chunk;
     const int j0 = (int)min(start, (int64_t)row.end), j1 = (int)min(start + p.chunk, (int64_t)row.end);
 
-    // The largest logit, the first of equal ones; eight loads in flight.
-    constexpr int U = 8 / Row<TYPE>::kPieces;
+    // The largest logit, the first of equal ones.
     float best = -INFINITY;
     int best_at = INT32_MAX;
-    for (int j = j0 + lane * 8; j < j1; j += 256 * U) {
-        uint4 v[U][Row<TYPE>::kPieces];
+    row.each(j0, j1, ring, [&](const float (&l)[8], int j) {
+        const float m = Row<TYPE>::largest(l);
+        if (m > best) {                                     // NaN is neither
+            best = m;
+            if (greedy) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (j + u * 256 < j1) row.load(j + u * 256, v[u]);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (j + u * 256 >= j1) break;
-            float l[8];
-            row.widen(v[u], l);
-            float m = fmaxf(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])), fmaxf(fmaxf(l[4], l[5]), fmaxf(l[6], l[7])));
-            if (m > best) {                                 // NaN is neither
-                best = m;
-                if (greedy) {
-#pragma unroll
-                    for (int i = 7; i >= 0; --i)
-                        if (l[i] == m) best_at = j + u * 256 + i;
-                }
+                for (int i = 7; i >= 0; --i)
+                    if (l[i] == m) best_at = Row<TYPE>::index(j, i);
             }
         }
-    }
+    });
     const float most = best;                                // of this lane
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -1018,11 +1071,12 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleP
     }
     NearScale near;
     if (near.set(best, temperature)) {
-        Sampler<TYPE, NearScale>{sm, row, rank, ranks, j0, j1, near}.draw(p, b, best, most, top_k, top_p, min_p);
+        Sampler<TYPE, NearScale>{sm, row, ring, rank, ranks, j0, j1, near}.draw(p, b, best, most, top_k, top_p, min_p);
     } else {
         FarScale far;
         far.set(best, temperature);
-        Sampler<TYPE, FarScale>{sm, row, rank, ranks, j0, j1, far}.draw(p, b, best, most, top_k, top_p, min_p);
+        const Sampler<TYPE, FarScale> s{sm, row, ring, rank, ranks, j0, j1, far};
+        Sampler<TYPE, FarScale>::draw_far(s, p, b, best, most, top_k, top_p, min_p);
     }
 }
 
@@ -1058,9 +1112,9 @@ extern "C" nvfp4_status nvfp4_sample(const void* logits, int64_t row_stride, int
     while (ranks < kMaxCluster && B * ranks < sm_count() && V / (2 * ranks) >= 4096) ranks *= 2;
     SampleParams p{};
     p.logits = logits; p.stride = row_stride; p.u = u; p.how = *how; p.tokens = tokens; p.logprobs = logprobs;
-    p.V = (int)V; p.chunk = (int)round_up(ceil_div(ceil_div(V + 7, ranks), kSampleWarps), 8);
+    p.V = (int)V; p.chunk = (int)round_up(ceil_div(ceil_div(V + 7, ranks), kSampleWarps), 256);
     const void* kernel = type == NVFP4_LOGITS_BF16 ? (const void*)sample_kernel<kTypeBf16>
                        : type == NVFP4_LOGITS_F16 ? (const void*)sample_kernel<kTypeF16> : (const void*)sample_kernel<kTypeF32>;
     void* args[] = {&p};
-    return launch_kernel(kernel, dim3((unsigned)(B * ranks)), dim3(kSampleThreads), 0, ranks, args, (cudaStream_t)stream, fn);
+    return launch_kernel(kernel, dim3((unsigned)(B * ranks)), dim3(kSampleThreads), type == NVFP4_LOGITS_F32 ? Row<kTypeF32>::kRingBytes : Row<kTypeBf16>::kRingBytes, ranks, args, (cudaStream_t)stream, fn);
 }
