@@ -67,6 +67,28 @@ constexpr int kWholeBits = 0x4B400000;
 // Entry of the table: 2^30 * 2^(j / 512) less kWholeBits, and as a float.
 __device__ __forceinline__ uint2 table_entry(uint32_t v) { return make_uint2(v - (uint32_t)kWholeBits, __float_as_uint((float)v)); }
 
+// A weight of w * 2^(13 - s) units, w in [2^30, 2^31]: s factors of two below the largest.  n - kWholeBits is its
+// place in 512ths of a factor of two, rounded; s and the bin go by its leading bits.
+struct Weight {
+    uint32_t w;
+    int n;
+
+    // The bins cut a factor of two into 16, and each belongs to one s.
+    __device__ __forceinline__ int bin() const { return (kWholeBits >> 5) - (n >> 5); }
+    __device__ __forceinline__ static uint32_t power(int e) {      // 2^e, zero outside [0, 31]
+        uint32_t v;
+        asm("shl.b32 %0, 1, %1;" : "=r"(v) : "r"(e));
+        return v;
+    }
+    // To the nearest whole number: up to s = 13 a product, then the high word of one; either power is
+    // zero where the other is not.
+    __device__ __forceinline__ uint64_t units() const {
+        const uint32_t down = power((n >> 9) + (45 - (kWholeBits >> 9)));
+        return (uint64_t)w * power((n >> 9) + (13 - (kWholeBits >> 9))) + (uint32_t)(((uint64_t)w * down + 0x80000000u) >> 32);
+    }
+};
+__device__ __forceinline__ int shift_of_bin(int bin) { return ((bin + 15) >> 4) - 13; }        // s - 13
+
 // Weights of a row's logits as whole numbers, and places below the largest, in 32 bits; times
 // 2^(rounding of mh), which is the same for the whole row and falls out of every ratio.
 struct NearScale {
@@ -89,11 +111,6 @@ struct NearScale {
     __device__ __forceinline__ int place(float l) const { return __float_as_int(fmaf(l, ch * 512.f, kWhole - mh * 512.f)); }
     __device__ __forceinline__ int bin(float l) const { return (kWholeBits >> 5) - (place(l) >> 5); }
     __device__ __forceinline__ float log_weight(float l) const { return fmaf(l, cl, fmaf(l, ch, -mh)) * 0.693147180559945f; }
-    // A weight as w * 2^(13 - s), w in [2^30, 2^31) and s = (kWholeBits >> 9) - (n >> 9).
-    struct Weight {
-        uint32_t w;
-        int n;
-    };
     // 2^(l ch + l cl - mh): the nearest 512th by table, in 2^-30; the rest, below 2^-10 (and 2^-12
     // for l cl), by three terms of exp's series, good to 2^-31 of the whole.  The rest itself is
     // exact but for its last bit: mh plus a 512th has no rounding.
@@ -114,27 +131,10 @@ struct NearScale {
         wa.w = ea.x + __float_as_uint(v.x);
         wb.w = eb.x + __float_as_uint(v.y);
     }
-    __device__ __forceinline__ static uint32_t power(int e) {      // 2^e, zero outside [0, 31]
-        uint32_t v;
-        asm("shl.b32 %0, 1, %1;" : "=r"(v) : "r"(e));
-        return v;
-    }
-    // w * 2^(13 - s) to the nearest whole number: up to s = 13 a product, then the high word of one;
-    // either power is zero where the other is not.
-    __device__ __forceinline__ static uint32_t small(const Weight& x) {
-        const uint32_t m = power((x.n >> 9) + (45 - (kWholeBits >> 9)));
-        return (uint32_t)(((uint64_t)x.w * m + 0x80000000u) >> 32);
-    }
-    __device__ __forceinline__ static uint64_t value(const Weight& x) {
-        return (uint64_t)x.w * power((x.n >> 9) + (13 - (kWholeBits >> 9))) + small(x);
-    }
-    // Bin, and the weight within its factor of two to 15 bits.
-    __device__ __forceinline__ static int bin_of(const Weight& x) { return (kWholeBits >> 5) - (x.n >> 5); }
-    __device__ __forceinline__ static uint32_t rough(const Weight& x) { return x.w >> 16; }
-    __device__ __forceinline__ uint64_t weight(float l, const uint2* table) const {
+    __device__ __forceinline__ Weight weight(float l, const uint2* table) const {
         Weight a, b;
         weights(l, l, table, a, b);
-        return value(a);
+        return a;
     }
 };
 
@@ -142,10 +142,12 @@ struct NearScale {
 // infinity): 64-bit floating point, an exponential each.
 __device__ __noinline__ double far_place(double c, float top, float l) {
     if (l == top) return 0.0;
-    return l == -INFINITY ? -INFINITY : ((double)l - (double)top) * c;             // zero times infinity: not counted
+    const double x = l == -INFINITY ? -INFINITY : ((double)l - (double)top) * c;   // zero times infinity: far below
+    return fmax(x, -47.0);
 }
-__device__ __noinline__ uint64_t far_weight(double x) {
-    return x > -47.0 ? (uint64_t)__double2ll_rn(exp2(x) * (double)(1ull << kOneLog2)) : 0;
+__device__ __noinline__ Weight far_weight(double x) {
+    const int k = (int)floor(x * 512.0);
+    return Weight{(uint32_t)__double2ll_rn(exp2(x - (double)(k >> 9)) * 1073741824.0), kWholeBits + k};
 }
 struct FarScale {
     double c;
@@ -156,29 +158,13 @@ struct FarScale {
         c = 1.4426950408889634074 / (double)t;
     }
     __device__ __forceinline__ float tidy(float l) const { return fmaxf(l, -INFINITY); }
-    __device__ __forceinline__ bool counts(float l) const { return place(l) > -47.0; }
-    __device__ __forceinline__ double place(float l) const { return far_place(c, top, l); }
-    __device__ __forceinline__ int bin(float l) const { return bin_at(place(l)); }
-    __device__ __forceinline__ static int bin_at(double x) { return -(int)floor(fmax(x, -47.0) * 16.0); }
-    __device__ __forceinline__ float log_weight(float l) const { return (float)(place(l) * 0.69314718055994530942); }
-    __device__ __forceinline__ uint64_t weight(float l, const uint2*) const {
-        return far_weight(place(l));
-    }
-    struct Weight {
-        uint64_t w;
-        int bin;
-    };
-    __device__ __forceinline__ void weights(float la, float lb, const uint2*, Weight& wa, Weight& wb) const {
-        const double a = place(la), b = place(lb);
-        wa = Weight{far_weight(a), bin_at(a)};
-        wb = Weight{far_weight(b), bin_at(b)};
-    }
-    __device__ __forceinline__ static uint64_t value(const Weight& x) { return x.w; }
-    __device__ __forceinline__ static int bin_of(const Weight& x) { return x.bin; }
-    // As above: a bin's octave begins right behind its factor of two.
-    __device__ __forceinline__ static uint32_t rough(const Weight& x) {
-        const int up = ((x.bin + 15) >> 4) - (kOneLog2 - 14);
-        return (uint32_t)(up >= 0 ? x.w << up : x.w >> -up);
+    __device__ __forceinline__ bool counts(float l) const { return far_place(c, top, l) > -47.0; }
+    __device__ __forceinline__ int bin(float l) const { return -((int)floor(far_place(c, top, l) * 512.0) >> 5); }
+    __device__ __forceinline__ float log_weight(float l) const { return (float)(far_place(c, top, l) * 0.69314718055994530942); }
+    __device__ __forceinline__ Weight weight(float l, const uint2*) const { return far_weight(far_place(c, top, l)); }
+    __device__ __forceinline__ void weights(float la, float lb, const uint2* table, Weight& wa, Weight& wb) const {
+        wa = weight(la, table);
+        wb = weight(lb, table);
     }
 };
 constexpr int kDeadBin = 16 * (kOneLog2 + 3);              // what lies in bins from here on weighs nothing
@@ -314,16 +300,15 @@ struct Row {
 };
 
 // Where the kept tokens of a row end: every logit above `value`, and of those equal to it the
-// first `ties`, by index.  `above` is the mass of the former, `each` the weight of the latter.
+// first `ties`, by index.
 struct Cut {
     float value;
     uint32_t ties;
-    uint64_t above, each;
 };
 
 struct Shared {
     uint2 table[512];
-    uint32_t count[kBins], lo[kBins], hi[kBins];           // an exact mass is lo + 2^32 hi
+    uint32_t count[kBins], lo[kBins], hi[kBins];
     uint64_t pairs[kList];                 // logits with their indices, of a row with few candidates
     uint32_t list[2][kList];               // values of a bin, as keys: of this block; of the whole row
     uint32_t listed, paired, few[kMaxCluster];
@@ -331,7 +316,7 @@ struct Shared {
     uint64_t found[4];
     float best[kMaxCluster];               // pushed here by every block of the row, as the next ones
     int best_at[kMaxCluster];
-    uint64_t total[kMaxCluster], above[kMaxCluster], mass[kMaxCluster];
+    uint64_t mass[kMaxCluster];
     uint32_t ties[kMaxCluster];
     float warp_best[kSampleWarps];
     int warp_at[kSampleWarps];
@@ -433,12 +418,6 @@ __device__ __forceinline__ void sort_down(T* v, int size) {
             }
 }
 
-__device__ __forceinline__ void add_mass(Shared& sm, int bin, uint64_t w) {
-    const uint32_t low = (uint32_t)w, old = atomicAdd(&sm.lo[bin], low);
-    const uint32_t up = (uint32_t)(w >> 32) + (old + low < old);
-    if (up) atomicAdd(&sm.hi[bin], up);
-}
-
 constexpr int kOwnBins = kBins / kSampleThreads;           // bins of a thread when they are summed
 
 struct Bins {                              // of one thread
@@ -455,12 +434,12 @@ struct Reached {
 
 template <int TYPE, class SCALE>
 struct Sampler {
-    using Weight = typename SCALE::Weight;
     Shared& sm;
     Row<TYPE> row;
     uint32_t ring;                         // shared address of the warps' stages
     uint32_t rank, ranks;
     int j0, j1;                            // virtual elements of this warp
+    bool large;                            // more than 2^16 of a block
     SCALE scale;
 
     // f(eight logits, their largest, the step's first element) over this warp's elements.
@@ -518,45 +497,47 @@ struct Sampler {
         read(sm.count, count);
     }
 
-    // The row's mass, exactly, and that of each bin but for up to 2^-14 of it: to 15 bits of each weight
-    // one addition in shared memory does, and the bin in question is known but for its neighbours.
-    __device__ __forceinline__ uint64_t weigh_bins(Bins& mass) {
-        uint64_t sum = 0;
-        each([&](float (&l)[8], float, int) {
+    // A weight's share of a sum: its high and its low 16 bits apart, so that neither sum leaves 32 bits
+    // (up to 2^16 logits a block) and nothing has to come back from shared memory; larger blocks carry.
+    __device__ __forceinline__ void add(int at, uint32_t w) {
+        if (!large) {
+            atomicAdd(&sm.hi[at], w >> 16);
+            atomicAdd(&sm.lo[at], w & 0xffffu);
+        } else if (atomicAdd(&sm.lo[at], w) + w < w) {
+            atomicAdd(&sm.hi[at], 1u);
+        }
+    }
+    __device__ __forceinline__ void read_sums(Bins& sum) const {
+        Bins lo;
+        read(sm.hi, sum);
+        read(sm.lo, lo);
+#pragma unroll
+        for (int k = 0; k < kOwnBins; ++k) sum[k] = (sum[k] << (large ? 32 : 16)) + lo[k];
+    }
+    // Mass of the row's bins, of what is up to `cut`, in units.  (Whole units of a bin, not of its weights:
+    // where a unit is more than a weight's last bit the one differs from the other in that.)
+    __device__ __forceinline__ void weigh_bins(const Cut& cut, Bins& mass) {
+        const bool all = cut.value == -INFINITY;
+        each([&](float (&l)[8], float most, int) {
+            if (most < cut.value) return;
             tidy(l);
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
                 Weight w[2];
                 scale.weights(l[i], l[i + 1], sm.table, w[0], w[1]);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    sum += SCALE::value(w[k]);
-                    if (scale.counts(l[i + k])) atomicAdd(&sm.count[SCALE::bin_of(w[k])], SCALE::rough(w[k]));
-                }
+                for (int k = 0; k < 2; ++k)
+                    if (scale.counts(l[i + k]) && (all || l[i + k] > cut.value)) add(w[k].bin(), w[k].w);
             }
         });
-        push_block_sum(sum, sm.total);
         cluster_sync();
-        read(sm.count, mass);
+        read_sums(mass);
+        const Weight last = all ? Weight{0, kWholeBits} : scale.weight(cut.value, sm.table);
 #pragma unroll
         for (int k = 0; k < kOwnBins; ++k) {
-            const int down = (((int)threadIdx.x * kOwnBins + k + 15) >> 4) - (kOneLog2 - 14);
-            if (mass[k]) mass[k] = max(down > 0 ? mass[k] >> down : mass[k] << -down, (uint64_t)1);
-        }
-        sum = 0;
-        for (uint32_t r = 0; r < ranks; ++r) sum += sm.total[r];
-        return sum;
-    }
-    // This block's sum to its place in every block's `to`; a barrier of the blocks has to follow.
-    __device__ __forceinline__ void push_block_sum(uint64_t v, uint64_t (&to)[kMaxCluster]) {
-        v = warp_sum(v);
-        if ((threadIdx.x & 31) == 0) sm.warp_mass[threadIdx.x >> 5] = v;
-        __syncthreads();
-        if (threadIdx.x < ranks) {
-            uint64_t m = 0;
-#pragma unroll
-            for (int w = 0; w < kSampleWarps; ++w) m += sm.warp_mass[w];
-            push_u64(&to[rank], threadIdx.x, m);
+            const int b = (int)threadIdx.x * kOwnBins + k, down = shift_of_bin(b);
+            if (!all && b == last.bin()) mass[k] += (uint64_t)cut.ties * last.w;
+            mass[k] = down > 0 ? mass[k] >> down : mass[k] << -down;
         }
     }
 
@@ -582,121 +563,67 @@ struct Sampler {
         return r;
     }
 
-    // Exact counts and masses of one bin's logits whose keys begin with the `bits` bits `known`, by
-    // their next `take` bits, the largest first.
-    __device__ __forceinline__ void digits(int bin, uint32_t known, uint32_t bits, uint32_t take, bool by_mass, Bins& count,
-                                           Bins& mass) {
+    // Counts, or sums of w, of one bin's logits whose keys begin with the `bits` bits `known`, by their next
+    // `take` bits, the largest first.
+    __device__ __forceinline__ void digits(int bin, uint32_t known, uint32_t bits, uint32_t take, bool by_mass, Bins& sum) {
         clear();
         each([&](float (&l)[8], float most, int) {
             if (scale.bin(most) > bin) return;
             tidy(l);
-#pragma unroll 1
+#pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const uint32_t k = order_key(l[i]);
                 if (!scale.counts(l[i]) || scale.bin(l[i]) != bin || (bits && k >> (32 - bits) != known)) continue;
                 const int d = (int)((1u << take) - 1 - ((k >> (32 - bits - take)) & ((1u << take) - 1)));
-                atomicAdd(&sm.count[d], 1u);
-                if (by_mass) add_mass(sm, d, scale.weight(l[i], sm.table));
+                if (by_mass) add(d, scale.weight(l[i], sm.table).w);
+                else atomicAdd(&sm.count[d], 1u);
             }
         });
         cluster_sync();
-        read(sm.count, count);
-        mass[0] = mass[1] = 0;
-        if (by_mass) {
-            Bins hi;
-            read(sm.lo, mass);
-            read(sm.hi, hi);
-            mass[0] += hi[0] << 32;
-            mass[1] += hi[1] << 32;
-        }
+        if (by_mass) read_sums(sum);
+        else read(sm.count, sum);
     }
-    // The cut in a bin of more values than are sorted: key bits, 10, 10, 10 and 2 of them.  `want` is counted
-    // from the bin's first value on; false where the bin's mass does not reach it.
-    struct Ended {
-        Cut cut;
-        int side;                          // the target lies in an earlier bin (-1), here, in a later one
-    };
-    __device__ __noinline__ static Ended cut_by_digits(Sampler s, int bin, bool by_mass, bool with_mass, uint64_t want) {
-        Ended e;
-        e.side = s.digits_cut(bin, by_mass, with_mass, want, e.cut) ? 0 : 1;
-        return e;
-    }
-    __device__ __forceinline__ bool digits_cut(int bin, bool by_mass, bool with_mass, uint64_t want, Cut& cut) {
+    // The cut in a bin of more values than are sorted: key bits, 10, 10, 10 and 2 of them.
+    __device__ __noinline__ static Cut cut_by_digits(Sampler s, int bin, bool by_mass, uint64_t want) {
         uint32_t known = 0;
-        uint64_t count_before = 0, mass_before = 0;
         for (uint32_t bits = 0; bits < 32;) {
             const uint32_t take = min(32 - bits, 10u);
-            Bins count, mass;
+            Bins sum;
             uint64_t all;
-            digits(bin, known, bits, take, with_mass, count, mass);
-            const Reached r = reach(by_mass ? mass : count, want - (by_mass ? mass_before : count_before), &all);
-            if (r.bin < 0) return false;                    // in the first round, if any
-            // What goes before the digit in the other measure.
-            uint64_t other = 0;
-#pragma unroll
-            for (int k = 0; k < kOwnBins; ++k)
-                if ((int)threadIdx.x * kOwnBins + k < r.bin) other += by_mass ? count[k] : mass[k];
-            block_below(other, sm.scan[1], &all);
-            count_before += by_mass ? all : r.before;
-            mass_before += by_mass ? r.before : all;
+            s.digits(bin, known, bits, take, by_mass, sum);
+            const Reached r = s.reach(sum, want, &all);
+            want -= r.before;
             known = (known << take) | ((1u << take) - 1 - (uint32_t)r.bin);
             bits += take;
         }
-        cut.value = key_value(known);
-        cut.above = mass_before;
-        cut.each = scale.weight(cut.value, sm.table);
-        cut.ties = (uint32_t)(by_mass ? (want - mass_before + cut.each - 1) / cut.each : want - count_before);
-        return true;
+        const float value = key_value(known);
+        const uint32_t each = by_mass ? s.scale.weight(value, s.sm.table).w : 1;
+        return Cut{value, (uint32_t)((want + each - 1) / each)};
     }
 
-    // The cut in `bin`, where the count (or, with `by_mass`, the mass) of all logits from the largest down
-    // reaches the target; `before` (known for counts) goes before the bin.  By mass the bin may
-    // turn out to be a neighbour: 1 where it is a later one, -1 where an earlier one, else 0.
-    __device__ __noinline__ static Ended cut_by_count(Sampler s, int bin, bool with_mass, uint64_t target, uint64_t before) {
-        Ended e;
-        e.side = s.cut_in(bin, false, with_mass, target, before, false, e.cut);
-        return e;
-    }
-    __device__ __forceinline__ int cut_in(int bin, bool by_mass, bool with_mass, uint64_t target, uint64_t before, bool again, Cut& cut) {
-        if (again) cluster_sync();                          // all have read the last list
+    // The cut in `bin`, where the count (or, with `by_mass`, the sum of w) of its logits from the largest
+    // down reaches `want`.
+    __device__ __noinline__ static Cut cut_in(Sampler s, int bin, bool by_mass, uint64_t want) { return s.cut(bin, by_mass, want); }
+    __device__ __forceinline__ Cut cut(int bin, bool by_mass, uint64_t want) {
         if (threadIdx.x == 0) sm.listed = 0;
         __syncthreads();
-        uint64_t above = 0;
         each([&](float (&l)[8], float most, int) {
-            if (scale.bin(most) > bin) return;
+            if (scale.bin(most) > bin) return;              // bins rise as logits fall
             tidy(l);
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                Weight w[2];
-                if (with_mass) scale.weights(l[i], l[i + 1], sm.table, w[0], w[1]);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int b = scale.bin(l[i + k]);
-                    if (with_mass && b < bin) above += SCALE::value(w[k]);
-                    if (b != bin || !scale.counts(l[i + k])) continue;
-                    const uint32_t at = atomicAdd(&sm.listed, 1u);
-                    if (at < kList) sm.list[0][at] = order_key(l[i + k]);
-                }
+            for (int i = 0; i < 8; ++i) {
+                if (scale.bin(l[i]) != bin || !scale.counts(l[i])) continue;
+                const uint32_t at = atomicAdd(&sm.listed, 1u);
+                if (at < kList) sm.list[0][at] = order_key(l[i]);
             }
         });
-        push_block_sum(above, sm.above);
         cluster_sync();
-        above = 0;
-        for (uint32_t r = 0; r < ranks; ++r) above += sm.above[r];
-        if (by_mass) before = above;
-        if (target <= before) return -1;
-        const uint64_t want = target - before;
         uint32_t held[kMaxCluster], n = 0;
 #pragma unroll
         for (uint32_t r = 0; r < kMaxCluster; ++r) held[r] = r < ranks ? remote_u32(&sm.listed, r) : 0;
 #pragma unroll
         for (uint32_t r = 0; r < kMaxCluster; ++r) n += held[r];
-        if (n > kList) {
-            const Ended e = cut_by_digits(*this, bin, by_mass, with_mass, want);
-            cut = e.cut;
-            cut.above += above;
-            return e.side;
-        }
+        if (n > kList) return cut_by_digits(*this, bin, by_mass, want);
         uint32_t from = 0;
 #pragma unroll
         for (uint32_t r = 0; r < kMaxCluster; ++r) {
@@ -706,40 +633,33 @@ struct Sampler {
         uint32_t size = 2;
         while (size < n) size *= 2;
         for (uint32_t i = n + threadIdx.x; i < size; i += kSampleThreads) sm.list[1][i] = 0;      // below every key
-        if (threadIdx.x == 0) sm.found[0] = 0;
         __syncthreads();
         sort_down(sm.list[1], (int)size);
         __syncthreads();
         // The value where the target is reached, then what lies above it.
         const uint32_t i = threadIdx.x * 2;
-        const auto weight_of = [&](uint32_t k) { return scale.weight(key_value(k), sm.table); };
+        const auto weight_of = [&](uint32_t k) { return scale.weight(key_value(k), sm.table).w; };
         uint64_t w[2] = {0, 0}, all;
         for (uint32_t k = 0; k < 2; ++k)
-            if (i + k < n && with_mass) w[k] = weight_of(sm.list[1][i + k]);
+            if (i + k < n) w[k] = by_mass ? weight_of(sm.list[1][i + k]) : 1;
         const uint64_t m = block_below(w[0] + w[1], sm.scan[0], &all);
-        for (uint32_t k = 0; k < 2; ++k)
-            if (i + k < n) {
-                const uint64_t ahead = by_mass ? m + (k ? w[0] : 0) : i + k, here = by_mass ? w[k] : 1;
-                if (ahead < want && want <= ahead + here) sm.found[0] = sm.list[1][i + k];
-            }
+        for (uint32_t k = 0; k < 2; ++k) {
+            const uint64_t ahead = m + (k ? w[0] : 0);
+            if (ahead < want && want <= ahead + w[k]) sm.found[0] = sm.list[1][i + k];
+        }
         __syncthreads();
         const uint32_t key = (uint32_t)sm.found[0];
-        __syncthreads();                                    // all have read it
-        if (key == 0) return 1;
         for (uint32_t k = 0; k < 2; ++k) {                  // its first place in the list
             const uint32_t at = i + k;
             if (at < n && sm.list[1][at] == key && (at == 0 || sm.list[1][at - 1] != key)) {
-                sm.found[1] = at;
-                sm.found[2] = m + (k ? w[0] : 0);
+                sm.found[1] = m + (k ? w[0] : 0);
+                sm.found[2] = w[k];
             }
         }
         __syncthreads();
-        cut.value = key_value(key);
-        cut.above = above + sm.found[2];
-        cut.each = weight_of(key);
-        cut.ties = (uint32_t)(by_mass ? (target - cut.above + cut.each - 1) / cut.each : want - sm.found[1]);
+        const uint64_t above = sm.found[1], each = sm.found[2];
         __syncthreads();
-        return 0;
+        return Cut{key_value(key), (uint32_t)((want - above + each - 1) / each)};
     }
 
     // The row's logits up to the bin `last`, which the top_k largest are among, as the candidates of the
@@ -795,7 +715,7 @@ struct Sampler {
             l[1] = key_value((uint32_t)(sm.pairs[i + 1] >> 32));
             Weight x[2];
             scale.weights(l[0], l[1], sm.table, x[0], x[1]);
-            for (uint32_t k = 0; k < 2; ++k) w[k] = i + k < min(n, (uint32_t)top_k) ? SCALE::value(x[k]) : 0;
+            for (uint32_t k = 0; k < 2; ++k) w[k] = i + k < min(n, (uint32_t)top_k) ? x[k].units() : 0;
         }
         if (top_p < 1.f) {
             uint64_t m = below(w[0] + w[1], &all);
@@ -834,7 +754,7 @@ struct Sampler {
     }
 
     __device__ __forceinline__ uint64_t least_weight(float min_p, float best) const {
-        return min_p > 0.f ? min_p < 1.f ? part_of(min_p, scale.weight(best, sm.table), true) : ~0ull : 0;
+        return min_p > 0.f ? min_p < 1.f ? part_of(min_p, scale.weight(best, sm.table).units(), true) : ~0ull : 0;
     }
 
     // From the largest logit to the token.
@@ -843,10 +763,10 @@ struct Sampler {
     }
     __device__ __forceinline__ void draw(const SampleParams& p, int64_t b, float best, float most, int top_k, float top_p, float min_p) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        Cut cut{-INFINITY, 0, 0, 0};                        // everything
+        Cut cut{-INFINITY, 0};                              // everything
         const bool by_k = top_k > 0 && top_k < p.V, by_p = top_p < 1.f;
         Bins bins;
-        uint64_t total = 0, all;
+        uint64_t all;
         if (by_k) {
             // As many lanes as top_k have a logit of this bin or above, so the top_k largest are there, too.
             count_lanes(most, bins);
@@ -854,32 +774,25 @@ struct Sampler {
             if (r.bin >= 0 && r.bin < kDeadBin && collect(r.bin)) return draw_of_few(p, b, best, top_k, top_p, min_p);
             bins = count_all(*this);
             r = reach(bins, (uint64_t)top_k, &all);
-            if (r.bin >= 0 && r.bin < kDeadBin) {
-                cut = cut_by_count(*this, r.bin, by_p, (uint64_t)top_k, r.before).cut;
-                total = cut.above + cut.ties * cut.each;
-            }
+            if (r.bin >= 0 && r.bin < kDeadBin) cut = cut_in(*this, r.bin, false, (uint64_t)top_k - r.before);
             if (by_p) clear();
         }
         if (by_p) {
-            const uint64_t whole = weigh_bins(bins);
-            if (total == 0) total = whole;
-            const uint64_t target = max(part_of(top_p, total, true), (uint64_t)1);
-            reach(bins, 1, &all);
-            // Weights to 15 bits, rounded down: half of what that leaves out goes off the target.
-            uint64_t rough = min(max(target - (target >> 15), (uint64_t)1), all);
-            for (int round = 0; round < kBins; ++round) {              // one, or two where the target is next to a bin's border
-                const Reached r = reach(bins, rough, &all);
-                const int side = cut_in(r.bin, true, true, target, 0, by_k || round, cut);
-                if (side == 0) break;
-                rough = side < 0 ? r.before : r.before + r.here + 1;       // the next bin with anything in it
-            }
+            weigh_bins(cut, bins);
+            block_below(bins[0] + bins[1], sm.scan[0], &all);
+            const uint64_t target = max(part_of(top_p, all, true), (uint64_t)1);
+            const Reached r = reach(bins, target, &all);
+            // From units to w, up: as much as makes a bin's units reach it.
+            const int down = shift_of_bin(r.bin);
+            const uint64_t want = target - r.before;
+            cut = cut_in(*this, r.bin, true, down > 0 ? want << down : (want + (1ull << -down) - 1) >> -down);
         }
 
         // Mass of what is kept, over warps, blocks and the row; equal values at the cut count by index.
         const uint64_t least = least_weight(min_p, best);
         const auto kept = [&](float l, uint64_t w) -> uint64_t { return w >= least || l == best ? w : 0; };
-        const auto kept_weight = [&](float l) -> uint64_t { return kept(l, scale.weight(l, sm.table)); };
-        cut.each = cut.value == -INFINITY ? 0 : kept_weight(cut.value);
+        const auto kept_weight = [&](float l) -> uint64_t { return kept(l, scale.weight(l, sm.table).units()); };
+        const uint64_t tie_weight = cut.value == -INFINITY ? 0 : kept_weight(cut.value);
         uint64_t mass = 0;
         uint32_t ties = 0;
         if (cut.value == -INFINITY && least == 0) {
@@ -889,8 +802,8 @@ struct Sampler {
                 for (int i = 0; i < 8; i += 2) {
                     Weight w[2];
                     scale.weights(l[i], l[i + 1], sm.table, w[0], w[1]);
-                    mass += SCALE::value(w[0]);
-                    mass += SCALE::value(w[1]);
+                    mass += w[0].units();
+                    mass += w[1].units();
                 }
             });
         } else {
@@ -904,7 +817,7 @@ struct Sampler {
                     scale.weights(l[i], l[i + 1], sm.table, w[0], w[1]);
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        if (l[i + k] > cut.value) mass += kept(l[i + k], SCALE::value(w[k]));
+                        if (l[i + k] > cut.value) mass += kept(l[i + k], w[k].units());
                         ties += l[i + k] == cut.value;
                     }
                 }
@@ -929,7 +842,7 @@ struct Sampler {
         }
         cluster_sync();
         // Mass of m above the cut and the t-th to (t + n)-th values equal to it.
-        const auto with_ties = [&](uint64_t m, uint32_t t, uint32_t n) { return m + (min(t + n, cut.ties) - min(t, cut.ties)) * cut.each; };
+        const auto with_ties = [&](uint64_t m, uint32_t t, uint32_t n) { return m + (min(t + n, cut.ties) - min(t, cut.ties)) * tie_weight; };
         uint64_t whole = 0, before = 0;
         uint32_t seen = 0, seen_before = 0;
         for (uint32_t r = 0; r < ranks; ++r) {
@@ -969,7 +882,7 @@ struct Sampler {
             if (target >= sum && target < sum + mine) {
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) {
-                    const uint64_t here = l[i] == cut.value ? (tie++ < cut.ties ? cut.each : 0) : w[i];
+                    const uint64_t here = l[i] == cut.value ? (tie++ < cut.ties ? tie_weight : 0) : w[i];
                     if (target >= sum && target < sum + here) {
                         p.tokens[b] = at + lane * kPer + i - row.first;
                         if (p.logprobs) p.logprobs[b] = log_share(l[i], here, whole);
@@ -1071,11 +984,11 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleP
     }
     NearScale near;
     if (near.set(best, temperature)) {
-        Sampler<TYPE, NearScale>{sm, row, ring, rank, ranks, j0, j1, near}.draw(p, b, best, most, top_k, top_p, min_p);
+        Sampler<TYPE, NearScale>{sm, row, ring, rank, ranks, j0, j1, p.chunk > 65536 / kSampleWarps, near}.draw(p, b, best, most, top_k, top_p, min_p);
     } else {
         FarScale far;
         far.set(best, temperature);
-        const Sampler<TYPE, FarScale> s{sm, row, ring, rank, ranks, j0, j1, far};
+        const Sampler<TYPE, FarScale> s{sm, row, ring, rank, ranks, j0, j1, p.chunk > 65536 / kSampleWarps, far};
         Sampler<TYPE, FarScale>::draw_far(s, p, b, best, most, top_k, top_p, min_p);
     }
 }
@@ -1107,12 +1020,14 @@ extern "C" nvfp4_status nvfp4_sample(const void* logits, int64_t row_stride, int
             return fail(NVFP4_ERR_INVALID_ARG, "%s: %s overlaps %s", fn, out.name, s);
     if (overlaps(t, lp)) return fail(NVFP4_ERR_INVALID_ARG, "%s: logprobs overlap tokens", fn);
     if (!device_status_ptr()) return fail(NVFP4_ERR_CUDA, "%s: no CUDA device", fn);
-    // Blocks of a row: enough of them for every SM, none with less than 4096 logits.
+    // Blocks of a row: enough of them for every SM, none with less than 4096 logits, or more than 65536
+    // where that can be.
+    const auto chunk = [&](unsigned ranks) { return round_up(ceil_div(ceil_div(V + 7, ranks), kSampleWarps), 256); };
     unsigned ranks = 1;
-    while (ranks < kMaxCluster && B * ranks < sm_count() && V / (2 * ranks) >= 4096) ranks *= 2;
+    while (ranks < kMaxCluster && ((B * ranks < sm_count() && V / (2 * ranks) >= 4096) || chunk(ranks) > 65536 / kSampleWarps)) ranks *= 2;
     SampleParams p{};
     p.logits = logits; p.stride = row_stride; p.u = u; p.how = *how; p.tokens = tokens; p.logprobs = logprobs;
-    p.V = (int)V; p.chunk = (int)round_up(ceil_div(ceil_div(V + 7, ranks), kSampleWarps), 256);
+    p.V = (int)V; p.chunk = (int)chunk(ranks);
     const void* kernel = type == NVFP4_LOGITS_BF16 ? (const void*)sample_kernel<kTypeBf16>
                        : type == NVFP4_LOGITS_F16 ? (const void*)sample_kernel<kTypeF16> : (const void*)sample_kernel<kTypeF32>;
     void* args[] = {&p};
