@@ -25,9 +25,9 @@ namespace {
 
 constexpr int kMaxAdapters = 4096;
 constexpr int kMaxRank = 256;
-constexpr int kDownWarps = 4;
-constexpr int kUpWarps = 4;
+constexpr int kLoraThreads = 128;
 constexpr int kMaxSplits = 16;
+constexpr int kSelfRows = kLoraThreads;    // up to so many rows every block finds its item for itself
 
 struct Item { int32_t adapter, first, rows, pad; };      // rows order[first .. first + rows)
 
@@ -41,14 +41,15 @@ struct LoraParams {
     int splits, k_split;                   // of K, and its elements a split (a multiple of 32)
     int rows_item;                         // 16 or 64
     int copy_rest;                         // rows without an adapter are copied
-    int32_t* num_items;
+    int32_t* num_items;                    // null: every block finds its item for itself
     Item* items;
     int32_t* order;                        // [T] rows by adapter
-    float* low;                            // [splits, T, rp] A x, in that order of rows
+    float* low;                            // [splits, T, rp] A x
     int* status;
 };
 
-// Rows by adapter, and items of them.  One block.
+// Rows by adapter, and items of them.  One block; eight rows a thread at a time, and one addition
+// for neighbours of the same adapter (8192 rows 13.2 us with an addition and a load a row).
 __global__ void __launch_bounds__(1024) lora_group_kernel(const LoraParams p) {
     extern __shared__ int32_t sm_groups[];
     __shared__ int32_t warp_sum[2][32];
@@ -59,13 +60,28 @@ __global__ void __launch_bounds__(1024) lora_group_kernel(const LoraParams p) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, groups = p.n + 1;
     for (int g = tid; g < groups; g += blockDim.x) count[g] = 0;
     __syncthreads();
-    const auto group_of = [&](int64_t t) {
-        const int a = p.adapters[t];
-        return a < 0 || a >= p.n ? p.n : a;
+    constexpr int kEach = 8;
+    const int64_t round = (int64_t)blockDim.x * kEach;
+    int group[kEach];
+    const auto read = [&](int64_t t0) {                     // of this round; -1 behind the last row
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int64_t t = t0 + i * blockDim.x + tid;
+            group[i] = t < p.T ? p.adapters[t] : INT32_MIN;
+        }
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            if (group[i] >= p.n) record_status(p.status, NVFP4_ERR_BAD_INDEX);
+            group[i] = group[i] == INT32_MIN && t0 + i * blockDim.x + tid >= p.T ? -1 : group[i] < 0 || group[i] >= p.n ? p.n : group[i];
+        }
     };
-    for (int64_t t = tid; t < p.T; t += blockDim.x) {
-        if (p.adapters[t] >= p.n) record_status(p.status, NVFP4_ERR_BAD_INDEX);
-        atomicAdd(&count[group_of(t)], 1);
+    for (int64_t t0 = 0; t0 < p.T; t0 += round) {
+        read(t0);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const uint32_t same = __match_any_sync(0xffffffffu, group[i]);
+            if (group[i] >= 0 && lane == __ffs(same) - 1) atomicAdd(&count[group[i]], __popc(same));
+        }
     }
     __syncthreads();
     // Exclusive sums of rows and items over the groups, a run of groups a thread.
@@ -104,8 +120,71 @@ __global__ void __launch_bounds__(1024) lora_group_kernel(const LoraParams p) {
     }
     if (tid == blockDim.x - 1) *p.num_items = i;            // the threads past the last group hold the sum, too
     __syncthreads();
-    for (int64_t t = tid; t < p.T; t += blockDim.x) p.order[atomicAdd(&place[group_of(t)], 1)] = (int32_t)t;
+    for (int64_t t0 = 0; t0 < p.T; t0 += round) {
+        if (p.T > round) read(t0);                          // else they are still here
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const uint32_t same = __match_any_sync(0xffffffffu, group[i]);
+            const int leader = __ffs(same) - 1;
+            int at = 0;
+            if (group[i] >= 0 && lane == leader) at = atomicAdd(&place[group[i]], __popc(same));
+            at = __shfl_sync(0xffffffffu, at, leader) + __popc(same & ((1u << lane) - 1));
+            if (group[i] >= 0) p.order[at] = (int32_t)(t0 + i * blockDim.x + tid);
+        }
+    }
 }
+
+// The rows of a block's item.
+template <int ROWS>
+struct ItemRows {
+    int32_t row[ROWS];
+    int32_t ids[kSelfRows];
+    int32_t warp_starts[kLoraThreads / 32];
+    int32_t adapter, first;
+
+    // Item `it`, its adapter and number of rows; false where there is none.  Of the few rows that have no list,
+    // each 16th of an adapter begins an item, in the order of the rows.
+    __device__ __forceinline__ bool find(const LoraParams& p, int it, int* adapter_out, int* rows_out) {
+        const int tid = threadIdx.x;
+        if (p.num_items) {
+            if (it >= *p.num_items) return false;
+            const Item item = p.items[it];
+            *adapter_out = item.adapter;
+            *rows_out = item.rows;
+            if (tid < item.rows) row[tid] = p.order[item.first + tid];
+            __syncthreads();
+            return true;
+        }
+        int id = INT32_MIN;                                 // behind the last row
+        if (tid < p.T) {
+            id = p.adapters[tid];
+            if (id >= p.n && it == 0) record_status(p.status, NVFP4_ERR_BAD_INDEX);
+            if (id < 0 || id >= p.n) id = -1;
+        }
+        ids[tid] = id;
+        if (tid == 0) first = -1;
+        __syncthreads();
+        int rank = 0;
+        for (int t = 0; t < (int)p.T; ++t) rank += t < tid && ids[t] == id;
+        const bool starts = id >= (p.copy_rest ? -1 : 0) && rank % ROWS == 0;
+        const uint32_t mine = __ballot_sync(0xffffffffu, starts);
+        if ((tid & 31) == 0) warp_starts[tid >> 5] = __popc(mine);
+        __syncthreads();
+        int index = __popc(mine & ((1u << (tid & 31)) - 1));
+        for (int w = 0; w < tid >> 5; ++w) index += warp_starts[w];
+        if (starts && index == it) {
+            adapter = id;
+            first = rank;
+        }
+        __syncthreads();
+        if (first < 0) return false;
+        const bool in = id == adapter && rank >= first && rank < first + ROWS;
+        if (in) row[rank - first] = tid;
+        *adapter_out = adapter;
+        *rows_out = __syncthreads_count(in);
+        return true;
+    }
+};
 
 // Eight 16-bit elements, zero where they are outside; VEC: all or none, 16-byte aligned.
 template <bool VEC>
@@ -118,76 +197,81 @@ __device__ __forceinline__ uint4 eight(const uint16_t* p, int64_t left) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One item's rows times 8 * NT rows of A over one split of K.  A warp takes 32 k of a step:
-// four lanes 16 bytes each of one row.
-template <bool F16, int MT, int NT, bool VEC>
-__global__ void __launch_bounds__(kDownWarps * 32) lora_down_kernel(const LoraParams p) {
-    constexpr int kRows = 16 * MT, kCols = 8 * NT;
-    __shared__ float sm[kDownWarps][kRows][kCols + 4];
+// One item's rows times 8 * NT rows of A over one split of K.  A warp takes MT * 16 rows and 32 k of a
+// step, four lanes 16 bytes each of a row; RW warps take the rows, and the others of four the next k.
+// Rows of 64 share their A through L1.
+template <bool F16, int RW, int MT, int NT, bool VEC>
+__global__ void __launch_bounds__(kLoraThreads) lora_down_kernel(const LoraParams p) {
+    constexpr int kRows = 16 * MT * RW, kCols = 8 * NT, kKWarps = kLoraThreads / 32 / RW;
+    __shared__ float sm[kKWarps][kRows][kCols + 4];
+    __shared__ ItemRows<kRows> item;
     pdl_wait_previous();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
-    const int items = *p.num_items;
+    const int row_warp = warp % RW, k_warp = warp / RW;
     const int split = blockIdx.y, col0 = blockIdx.z * kCols;
+    int adapter, rows;
+    if (!item.find(p, blockIdx.x, &adapter, &rows) || adapter < 0) return;
     const int64_t k_begin = (int64_t)split * p.k_split, k_end = min(k_begin + p.k_split, p.K);
-    for (int it = blockIdx.x; it < items; it += gridDim.x) {
-        const Item item = p.items[it];
-        if (item.adapter < 0) continue;
-        const uint16_t* xr[MT][2];
-        bool held[MT][2];
+    const uint16_t* xr[MT][2];
+    bool held[MT][2];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int row = m * 16 + h * 8 + g;
-                held[m][h] = row < item.rows;
-                xr[m][h] = p.x + (held[m][h] ? p.order[item.first + row] : 0) * p.x_stride;
-            }
-        const uint16_t* a = p.a + ((int64_t)item.adapter * p.r + col0 + g) * p.K;
-        float acc[MT][NT][4] = {};
-        constexpr int U = MT == 1 ? 4 : 1;
-        for (int64_t k0 = k_begin + warp * 32; k0 < k_end; k0 += kDownWarps * 32 * U) {
-            uint4 xv[U][MT][2], av[U][NT];
+        for (int h = 0; h < 2; ++h) {
+            const int row = (row_warp * MT + m) * 16 + h * 8 + g;
+            held[m][h] = row < rows;
+            xr[m][h] = p.x + (held[m][h] ? item.row[row] : 0) * p.x_stride;
+        }
+    const uint16_t* a = p.a + ((int64_t)adapter * p.r + col0 + g) * p.K;
+    float acc[MT][NT][4] = {};
+    constexpr int U = MT * 2 + NT <= 4 ? 4 : MT * 2 + NT <= 6 ? 2 : 1;         // steps whose loads go out together
+    for (int64_t k0 = k_begin + k_warp * 32; k0 < k_end; k0 += kKWarps * 32 * U) {
+        uint4 xv[U][MT][2], av[U][NT];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int64_t k = k0 + u * kDownWarps * 32 + q * 8, left = k_end - k;
+        for (int u = 0; u < U; ++u) {
+            const int64_t k = k0 + u * kKWarps * 32 + q * 8, left = k_end - k;
 #pragma unroll
-                for (int j = 0; j < NT; ++j) av[u][j] = col0 + j * 8 + g < p.r ? eight<VEC>(a + (int64_t)j * 8 * p.K + k, left) : make_uint4(0, 0, 0, 0);
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
+                for (int h = 0; h < 2; ++h) xv[u][m][h] = held[m][h] ? eight<VEC>(xr[m][h] + k, left) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) xv[u][m][h] = held[m][h] ? eight<VEC>(xr[m][h] + k, left) : make_uint4(0, 0, 0, 0);
-            }
+            for (int j = 0; j < NT; ++j) av[u][j] = col0 + j * 8 + g < p.r ? eight<VEC>(a + (int64_t)j * 8 * p.K + k, left) : make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    const uint32_t lo[4] = {xv[u][m][0].x, xv[u][m][1].x, xv[u][m][0].y, xv[u][m][1].y};
-                    const uint32_t hi[4] = {xv[u][m][0].z, xv[u][m][1].z, xv[u][m][0].w, xv[u][m][1].w};
+            for (int m = 0; m < MT; ++m) {
+                const uint32_t lo[4] = {xv[u][m][0].x, xv[u][m][1].x, xv[u][m][0].y, xv[u][m][1].y};
+                const uint32_t hi[4] = {xv[u][m][0].z, xv[u][m][1].z, xv[u][m][0].w, xv[u][m][1].w};
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        mma_16816<F16>(acc[m][j], lo, av[u][j].x, av[u][j].y);
-                        mma_16816<F16>(acc[m][j], hi, av[u][j].z, av[u][j].w);
-                    }
+                for (int j = 0; j < NT; ++j) {
+                    mma_16816<F16>(acc[m][j], lo, av[u][j].x, av[u][j].y);
+                    mma_16816<F16>(acc[m][j], hi, av[u][j].z, av[u][j].w);
                 }
+            }
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                *(float2*)&sm[k_warp][(row_warp * MT + m) * 16 + h * 8 + g][j * 8 + q * 2] = make_float2(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
+    __syncthreads();
+    for (int i = threadIdx.x; i < kRows * kCols / 4; i += kLoraThreads) {
+        const int row = i / (kCols / 4), c = i % (kCols / 4) * 4;
+        if (row >= rows || col0 + c >= p.rp) continue;
+        float4 v = *(const float4*)&sm[0][row][c];
+#pragma unroll
+        for (int w = 1; w < kKWarps; ++w) {
+            const float4 u = *(const float4*)&sm[w][row][c];
+            v.x += u.x;
+            v.y += u.y;
+            v.z += u.z;
+            v.w += u.w;
         }
-        __syncthreads();                                    // the last item's sums are read
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    *(float2*)&sm[warp][m * 16 + h * 8 + g][j * 8 + q * 2] = make_float2(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
-        __syncthreads();
-        for (int i = threadIdx.x; i < kRows * kCols; i += kDownWarps * 32) {
-            const int row = i / kCols, c = i % kCols;
-            if (row >= item.rows || col0 + c >= p.rp) continue;
-            float v = sm[0][row][c];
-#pragma unroll
-            for (int w = 1; w < kDownWarps; ++w) v += sm[w][row][c];
-            p.low[((int64_t)split * p.T + item.first + row) * p.rp + col0 + c] = v;
-        }
+        *(float4*)(p.low + ((int64_t)split * p.T + item.row[row]) * p.rp + col0 + c) = v;
     }
 }
 
@@ -202,113 +286,140 @@ __device__ __forceinline__ uint2 four(const uint16_t* p, int left) {
     return make_uint2(w[0], w[1]);
 }
 
-// One item's rows of A x times B, and y, over a range of N.  A warp takes 32 columns of a step;
-// tile j of four holds columns 8 (c / 2) + 2 j + c % 2, so that a lane's eight outputs of a
-// row lie side by side.
-template <bool F16, int MT, bool VEC_B, bool VEC_Y>
-__global__ void __launch_bounds__(kUpWarps * 32) lora_up_kernel(const LoraParams p, const int cols_block) {
-    constexpr int kRows = 16 * MT;
+// One item's rows of A x times B, and y, over a range of N.  A warp takes MT * 16 rows and CU * 32 columns
+// of a step, whose y it asks for first; tile j of four holds columns 8 (c / 2) + 2 j + c % 2, so that a
+// lane's eight outputs of a row lie side by side.
+template <bool F16, int RW, int MT, int CU, bool VEC_B, bool VEC_Y>
+__global__ void __launch_bounds__(kLoraThreads) lora_up_kernel(const LoraParams p, const int cols_block) {
+    constexpr int kRows = 16 * MT * RW, kColWarps = kLoraThreads / 32 / RW;
     extern __shared__ __align__(16) uint8_t sm_up[];
-    const int pitch = p.rp + 4;                             // halves of A x as fragments read them: 16 bits
-    uint32_t* sm_hi = (uint32_t*)sm_up;                     // [kRows][pitch / 2]
-    uint32_t* sm_lo = sm_hi + kRows * (pitch / 2);
-    float* sm_scale = (float*)(sm_lo + kRows * (pitch / 2));   // [kRows]
+    __shared__ ItemRows<kRows> item;
+    __shared__ float sm_scale[kRows];
+    const int pitch = p.rp / 2 + 4;                         // words of two values; a fragment's reads meet no bank twice
+    uint32_t* sm_hi = (uint32_t*)sm_up;                     // [kRows][pitch] halves of A x
+    uint32_t* sm_lo = sm_hi + kRows * pitch;
     pdl_wait_previous();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
-    const int items = *p.num_items;
-    const int64_t n_begin = (int64_t)blockIdx.x * cols_block, n_end = min(n_begin + cols_block, p.N);
-    for (int it = blockIdx.y; it < items; it += gridDim.y) {
-        const Item item = p.items[it];
-        if (item.adapter < 0 && !p.copy_rest) continue;
-        const int steps = item.adapter < 0 ? 0 : p.rp / 16;
-        __syncthreads();
-        // The splits' sums in order, as two halves.  FP16 holds them times the power of two that
-        // puts a row's largest below 2, which the end takes back.
-        if (steps)
-            for (int row = warp; row < kRows; row += kUpWarps) {
-                float v[kMaxRank / 64][2], most = 0.f;
-#pragma unroll
-                for (int j = 0; j < kMaxRank / 64; ++j) {
-                    const int c = (j * 32 + lane) * 2;
-                    float2 s = make_float2(0.f, 0.f);
-                    if (row < item.rows && c < p.rp)
-                        for (int sp = 0; sp < p.splits; ++sp) {
-                            const float2 u = *(const float2*)(p.low + ((int64_t)sp * p.T + item.first + row) * p.rp + c);
-                            s.x += u.x;
-                            s.y += u.y;
-                        }
-                    v[j][0] = s.x;
-                    v[j][1] = s.y;
-                    most = fmaxf(most, fmaxf(fabsf(s.x), fabsf(s.y)));
-                }
-                float down = 1.f, up = 1.f;
-                if (F16) {
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-                    if (most > 0x1p-100f && most < INFINITY) {
-                        const uint32_t e = __float_as_uint(most) & 0x7f800000u;
-                        up = __uint_as_float(e);
-                        down = __uint_as_float(0x7f000000u - e);        // 2^-exponent
+    int adapter, rows;
+    if (!item.find(p, blockIdx.x, &adapter, &rows) || (adapter < 0 && !p.copy_rest)) return;
+    const int64_t n_begin = (int64_t)blockIdx.y * cols_block, n_end = min(n_begin + cols_block, p.N);
+    const int steps = adapter < 0 ? 0 : p.rp / 16;
+    // The splits' sums in order, as two halves: four rows a warp at a time, eight lanes each.  FP16 holds
+    // them times the power of two that puts a row's largest below 2, which the end takes back.
+    if (steps)
+        for (int row = warp * 4 + (lane >> 3); row < kRows; row += kLoraThreads / 8) {
+            const bool held = row < rows;
+            const float* low = p.low + (int64_t)(held ? item.row[row] : 0) * p.rp + (lane & 7) * 2;
+            const int64_t apart = p.T * p.rp;
+            const auto sum = [&](int c) {                   // of a pair
+                float2 v = make_float2(0.f, 0.f);
+                if (held)
+#pragma unroll 4
+                    for (int sp = 0; sp < p.splits; ++sp) {
+                        const float2 u = *(const float2*)(low + sp * apart + c);
+                        v.x += u.x;
+                        v.y += u.y;
                     }
+                return v;
+            };
+            float down = 1.f, up = 1.f;
+            if (F16) {
+                float most = 0.f;
+                for (int c = 0; c < p.rp; c += 16) {
+                    const float2 v = sum(c);
+                    most = fmaxf(most, fmaxf(fabsf(v.x), fabsf(v.y)));
                 }
-                if (lane == 0) sm_scale[row] = up * (p.scales ? p.scales[item.adapter] : 1.f);
 #pragma unroll
-                for (int j = 0; j < kMaxRank / 64; ++j) {
-                    const int c = (j * 32 + lane) * 2;
-                    if (c >= p.rp) break;
-                    const float a = v[j][0] * down, b = v[j][1] * down;
-                    const uint32_t hi = f32_to_act2<F16>(a, b);
-                    const float2 back = act2_to_f32<F16>(hi);
-                    // An infinity (or one that the type cannot hold) is its own first half.
-                    const float la = fabsf(back.x) < INFINITY ? a - back.x : 0.f, lb = fabsf(back.y) < INFINITY ? b - back.y : 0.f;
-                    sm_hi[row * (pitch / 2) + c / 2] = hi;
-                    sm_lo[row * (pitch / 2) + c / 2] = f32_to_act2<F16>(la, lb);
+                for (int o = 4; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+                if (most > 0x1p-100f && most < INFINITY) {
+                    const uint32_t e = __float_as_uint(most) & 0x7f800000u;
+                    up = __uint_as_float(e);
+                    down = __uint_as_float(0x7f000000u - e);            // 2^-exponent
                 }
             }
-        __syncthreads();
-        const uint16_t* b = p.b + (int64_t)max(item.adapter, 0) * p.N * p.r;
-        for (int64_t n0 = n_begin + warp * 32; n0 < n_end; n0 += kUpWarps * 32) {
-            float acc[MT][4][4] = {};
-            for (int st = 0; st < steps; ++st) {
-                uint2 bv[4];
+            if ((lane & 7) == 0) sm_scale[row] = up * (p.scales ? p.scales[adapter] : 1.f);
+#pragma unroll 2
+            for (int c = 0; c < p.rp; c += 16) {
+                const float2 v = sum(c);
+                const float a = v.x * down, b = v.y * down;
+                const uint32_t hi = f32_to_act2<F16>(a, b);
+                const float2 back = act2_to_f32<F16>(hi);
+                // An infinity (or one that the type cannot hold) is its own first half.
+                const float la = fabsf(back.x) < INFINITY ? a - back.x : 0.f, lb = fabsf(back.y) < INFINITY ? b - back.y : 0.f;
+                sm_hi[row * pitch + c / 2 + (lane & 7)] = hi;
+                sm_lo[row * pitch + c / 2 + (lane & 7)] = f32_to_act2<F16>(la, lb);
+            }
+        }
+    __syncthreads();
+    const int row_warp = warp % RW, col_warp = warp / RW;
+    if (row_warp * MT * 16 >= rows) return;
+    int64_t t[MT][2];                                       // rows, -1 behind the last
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int row = (row_warp * MT + m) * 16 + h * 8 + g;
+            t[m][h] = row < rows ? item.row[row] : -1;
+        }
+    const uint16_t* b = p.b + (int64_t)max(adapter, 0) * p.N * p.r;
+    const uint32_t *hi0 = sm_hi + (row_warp * MT * 16 + g) * pitch + q * 2, *lo0 = sm_lo + (row_warp * MT * 16 + g) * pitch + q * 2;
+    for (int64_t n0 = n_begin + col_warp * 32 * CU; n0 < n_end; n0 += kColWarps * 32 * CU) {
+        uint4 yv[CU][MT][2];
+#pragma unroll
+        for (int u = 0; u < CU; ++u)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int64_t n = n0 + u * 32 + q * 8;
+                    yv[u][m][h] = t[m][h] >= 0 ? eight<VEC_Y>(p.y + t[m][h] * p.y_stride + n, n_end - n) : make_uint4(0, 0, 0, 0);
+                }
+        float acc[CU][MT][4][4] = {};
+#pragma unroll 2
+        for (int st = 0; st < steps; ++st) {
+            uint2 bv[CU][4];
+#pragma unroll
+            for (int u = 0; u < CU; ++u)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int64_t n = n0 + 8 * (g >> 1) + 2 * j + (g & 1);
-                    bv[j] = n < n_end ? four<VEC_B>(b + n * p.r + st * 16 + q * 4, p.r - st * 16 - q * 4) : make_uint2(0, 0);
+                    const int64_t n = n0 + u * 32 + 8 * (g >> 1) + 2 * j + (g & 1);
+                    bv[u][j] = n < n_end ? four<VEC_B>(b + n * p.r + st * 16 + q * 4, p.r - st * 16 - q * 4) : make_uint2(0, 0);
                 }
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    const int at = (m * 16 + g) * (pitch / 2) + st * 8 + q * 2, at8 = at + 8 * (pitch / 2);
-                    const uint2 h0 = *(const uint2*)(sm_hi + at), h1 = *(const uint2*)(sm_hi + at8);
-                    const uint2 l0 = *(const uint2*)(sm_lo + at), l1 = *(const uint2*)(sm_lo + at8);
-                    const uint32_t hi[4] = {h0.x, h1.x, h0.y, h1.y}, lo[4] = {l0.x, l1.x, l0.y, l1.y};
+            for (int m = 0; m < MT; ++m) {
+                const int at = m * 16 * pitch + st * 8, at8 = at + 8 * pitch;
+                const uint2 h0 = *(const uint2*)(hi0 + at), h1 = *(const uint2*)(hi0 + at8);
+                const uint2 l0 = *(const uint2*)(lo0 + at), l1 = *(const uint2*)(lo0 + at8);
+                const uint32_t hi[4] = {h0.x, h1.x, h0.y, h1.y}, lo[4] = {l0.x, l1.x, l0.y, l1.y};
+#pragma unroll
+                for (int u = 0; u < CU; ++u)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        mma_16816<F16>(acc[m][j], hi, bv[j].x, bv[j].y);
-                        mma_16816<F16>(acc[m][j], lo, bv[j].x, bv[j].y);
+                        mma_16816<F16>(acc[u][m][j], hi, bv[u][j].x, bv[u][j].y);
+                        mma_16816<F16>(acc[u][m][j], lo, bv[u][j].x, bv[u][j].y);
                     }
-                }
             }
-            const int64_t n = n0 + q * 8;
+        }
+#pragma unroll
+        for (int u = 0; u < CU; ++u) {
+            const int64_t n = n0 + u * 32 + q * 8;
             if (n >= n_end) continue;
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int row = m * 16 + h * 8 + g;
-                    if (row >= item.rows) continue;
-                    const int64_t t = p.order[item.first + row];
-                    const float s = steps ? sm_scale[row] : 0.f;
-                    const uint4 yv = eight<VEC_Y>(p.y + t * p.y_stride + n, n_end - n);
-                    uint32_t w[4] = {yv.x, yv.y, yv.z, yv.w};
-                    if (steps)
+                    if (t[m][h] < 0) continue;
+                    uint32_t w[4] = {yv[u][m][h].x, yv[u][m][h].y, yv[u][m][h].z, yv[u][m][h].w};
+                    if (steps) {
+                        const float s = sm_scale[(row_warp * MT + m) * 16 + h * 8 + g];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const float2 u = act2_to_f32<F16>(w[j]);
-                            w[j] = f32_to_act2<F16>(fmaf(s, acc[m][j][2 * h], u.x), fmaf(s, acc[m][j][2 * h + 1], u.y));
+                            const float2 v = act2_to_f32<F16>(w[j]);
+                            w[j] = f32_to_act2<F16>(fmaf(s, acc[u][m][j][2 * h], v.x), fmaf(s, acc[u][m][j][2 * h + 1], v.y));
                         }
-                    uint16_t* out = p.out + t * p.N + n;
+                    }
+                    uint16_t* out = p.out + t[m][h] * p.N + n;
                     if (VEC_Y) {
                         *(uint4*)out = make_uint4(w[0], w[1], w[2], w[3]);
                     } else {
@@ -324,6 +435,7 @@ __global__ void __launch_bounds__(kUpWarps * 32) lora_up_kernel(const LoraParams
 // How a call of these sizes is cut up.
 struct LoraPlan {
     int rows_item, splits, k_split, nt;
+    bool listed;                           // items from the grouping kernel
     int64_t items;                         // at most
     size_t bytes, order_at, low_at;
 };
@@ -331,35 +443,38 @@ struct LoraPlan {
 LoraPlan plan_lora(int64_t T, int64_t n, int64_t r, int64_t K) {
     LoraPlan pl{};
     pl.rows_item = T >= 64 * (n + 1) ? 64 : 16;
+    pl.listed = T > kSelfRows;
     pl.items = std::min(T, T / pl.rows_item + n + 1);
-    pl.nt = r <= 8 ? 1 : r <= 16 ? 2 : 4;
+    pl.nt = r <= 8 ? 1 : r <= 16 ? 2 : r <= 32 ? 4 : 8;
     const int64_t blocks = pl.items * ceil_div(r, pl.nt * 8);
-    int64_t splits = ceil_div(4 * (int64_t)sm_count(), blocks);
-    splits = std::min<int64_t>({splits, kMaxSplits, ceil_div(K, kDownWarps * 64)});
+    int64_t splits = ceil_div(3 * (int64_t)sm_count(), blocks);
+    splits = std::min<int64_t>({splits, kMaxSplits, ceil_div(K, 256)});
     pl.k_split = (int)round_up(ceil_div(K, std::max<int64_t>(splits, 1)), 32);
     pl.splits = (int)ceil_div(K, pl.k_split);
-    pl.order_at = 256 + (size_t)round_up(sizeof(Item) * pl.items, 256);
-    pl.low_at = pl.order_at + (size_t)round_up(4 * T, 256);
+    pl.order_at = 256 + (pl.listed ? (size_t)round_up(sizeof(Item) * pl.items, 256) : 0);
+    pl.low_at = pl.order_at + (pl.listed ? (size_t)round_up(4 * T, 256) : 0);
     pl.bytes = pl.low_at + (size_t)round_up(4 * pl.splits * T * round_up(r, 16), 256);
     return pl;
 }
 
-template <bool F16, int MT, bool VEC>
+template <bool F16, int RW, int MT, bool VEC>
 const void* down_kernel(int nt) {
-    return nt == 1 ? (const void*)lora_down_kernel<F16, MT, 1, VEC> : nt == 2 ? (const void*)lora_down_kernel<F16, MT, 2, VEC>
-                                                                             : (const void*)lora_down_kernel<F16, MT, 4, VEC>;
+    return nt == 1   ? (const void*)lora_down_kernel<F16, RW, MT, 1, VEC>
+           : nt == 2 ? (const void*)lora_down_kernel<F16, RW, MT, 2, VEC>
+           : nt == 4 ? (const void*)lora_down_kernel<F16, RW, MT, 4, VEC>
+                     : (const void*)lora_down_kernel<F16, RW, MT, 8, VEC>;
 }
 
 template <bool F16>
 const void* down_kernel(int rows, int nt, bool vec) {
-    if (rows == 16) return vec ? down_kernel<F16, 1, true>(nt) : down_kernel<F16, 1, false>(nt);
-    return vec ? down_kernel<F16, 4, true>(nt) : down_kernel<F16, 4, false>(nt);
+    if (rows == 16) return vec ? down_kernel<F16, 1, 1, true>(nt) : down_kernel<F16, 1, 1, false>(nt);
+    return vec ? down_kernel<F16, 2, 2, true>(nt) : down_kernel<F16, 2, 2, false>(nt);
 }
 
-template <bool F16, int MT>
+template <bool F16, int RW, int MT, int CU>
 const void* up_kernel(bool vec_b, bool vec_y) {
-    if (vec_b) return vec_y ? (const void*)lora_up_kernel<F16, MT, true, true> : (const void*)lora_up_kernel<F16, MT, true, false>;
-    return vec_y ? (const void*)lora_up_kernel<F16, MT, false, true> : (const void*)lora_up_kernel<F16, MT, false, false>;
+    if (vec_b) return vec_y ? (const void*)lora_up_kernel<F16, RW, MT, CU, true, true> : (const void*)lora_up_kernel<F16, RW, MT, CU, true, false>;
+    return vec_y ? (const void*)lora_up_kernel<F16, RW, MT, CU, false, true> : (const void*)lora_up_kernel<F16, RW, MT, CU, false, false>;
 }
 
 nvfp4_status check_sizes(const char* fn, int64_t T, int64_t n, int64_t r, int64_t K, int64_t N) {
@@ -414,23 +529,28 @@ extern "C" nvfp4_status nvfp4_lora_add(const void* y, int64_t y_stride, const vo
     p.num_items = (int32_t*)w; p.items = (Item*)(w + 256); p.order = (int32_t*)(w + pl.order_at); p.low = (float*)(w + pl.low_at);
     cudaStream_t s = (cudaStream_t)stream;
     void* args[] = {&p};
-    if (nvfp4_status st = launch_kernel((const void*)lora_group_kernel, dim3(1), dim3(1024), 8 * (p.n + 1), 1, args, s, fn)) return st;
+    if (pl.listed) {
+        if (nvfp4_status st = launch_kernel((const void*)lora_group_kernel, dim3(1), dim3(1024), 8 * (p.n + 1), 1, args, s, fn)) return st;
+    } else {
+        p.num_items = nullptr;
+    }
     const bool vec_x = K % 8 == 0 && x_stride % 8 == 0 && aligned(x, 16) && aligned(A, 16);
     const bool vec_b = r % 4 == 0 && aligned(B, 8);
     const bool vec_y = N % 8 == 0 && y_stride % 8 == 0 && aligned(y, 16) && aligned(out, 16);
     if (num_adapters > 0) {
         const void* kernel = f16 ? down_kernel<true>(pl.rows_item, pl.nt, vec_x) : down_kernel<false>(pl.rows_item, pl.nt, vec_x);
-        const dim3 grid((unsigned)std::min<int64_t>(pl.items, 65535), (unsigned)pl.splits, (unsigned)ceil_div(p.rp, pl.nt * 8));
-        if (nvfp4_status st = launch_kernel(kernel, grid, dim3(kDownWarps * 32), 0, 1, args, s, fn)) return st;
+        const dim3 grid((unsigned)pl.items, (unsigned)pl.splits, (unsigned)ceil_div(p.rp, pl.nt * 8));
+        if (nvfp4_status st = launch_kernel(kernel, grid, dim3(kLoraThreads), 0, 1, args, s, fn)) return st;
     }
-    const void* kernel = pl.rows_item == 16 ? (f16 ? up_kernel<true, 1>(vec_b, vec_y) : up_kernel<false, 1>(vec_b, vec_y))
-                                            : (f16 ? up_kernel<true, 4>(vec_b, vec_y) : up_kernel<false, 4>(vec_b, vec_y));
-    // Columns of a block: enough of them that the sums over splits are not read too often, few
-    // enough to fill the SMs.
-    int cols = kUpWarps * 32 * 4;
-    while (cols > kUpWarps * 32 && ceil_div(N, cols) * pl.items < 4 * (int64_t)sm_count()) cols /= 2;
-    const size_t smem = (size_t)pl.rows_item * ((p.rp + 4) * 4 + 4);
-    void* up_args[] = {&p, &cols};
-    return launch_kernel(kernel, dim3((unsigned)ceil_div(N, cols), (unsigned)std::min<int64_t>(pl.items, 65535)), dim3(kUpWarps * 32), smem, 1,
-                         up_args, s, fn);
+    const void* kernel = pl.rows_item == 16 ? (f16 ? up_kernel<true, 1, 1, 2>(vec_b, vec_y) : up_kernel<false, 1, 1, 2>(vec_b, vec_y))
+                                            : (f16 ? up_kernel<true, 2, 2, 2>(vec_b, vec_y) : up_kernel<false, 2, 2, 2>(vec_b, vec_y));
+    // Columns of a block: as many steps of its warps as leave four blocks an SM, so that the sums over
+    // splits are not read too often.
+    const int step = pl.rows_item == 16 ? 256 : 128;
+    int64_t cols = step;
+    while (cols < N && (ceil_div(N, 2 * cols) * pl.items >= 4 * (int64_t)sm_count() || ceil_div(N, cols) > 65535)) cols *= 2;
+    int cols_block = (int)cols;
+    const size_t smem = (size_t)pl.rows_item * (p.rp / 2 + 4) * 8;
+    void* up_args[] = {&p, &cols_block};
+    return launch_kernel(kernel, dim3((unsigned)pl.items, (unsigned)ceil_div(N, cols)), dim3(kLoraThreads), smem, 1, up_args, s, fn);
 }
