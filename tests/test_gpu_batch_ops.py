@@ -341,8 +341,11 @@ def test_lora_zero_padded_ranks_and_adapters_of_one_matrix():
     y, x, a, b, ids, s = _lora_case(40, 128, 64, 32, 3, "bf16", 4)
     a[:, 20:] = 0
     b[:, :, 20:] = 0
+    # Ranks of 20 and 32 sum their products in groups of 16 and 32, so the same real number is rounded after
+    # 32-bit sums of another order: each lies within the bound above of it, and two such are two bounds apart.
     small = nv.lora_add(y, x, a[:, :20].contiguous(), b[:, :, :20].contiguous(), ids, scales=s)
-    assert torch.equal(small, nv.lora_add(y, x, a, b, ids, scales=s))
+    _close_lora(small, y, x, a, b, ids, s, "bf16")
+    _close_lora(nv.lora_add(y, x, a, b, ids, scales=s), y, x, a, b, ids, s, "bf16")
 
 
 def test_lora_workspace_stream_and_graph():

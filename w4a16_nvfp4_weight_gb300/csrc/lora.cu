@@ -12,6 +12,7 @@
 // operands go straight from memory to registers: an order of k that is the same for both operands
 // lets a thread load 16 bytes of each row, and an order of the columns 16 bytes of y.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "launch.cuh"
@@ -275,27 +276,128 @@ __global__ void __launch_bounds__(kLoraThreads) lora_down_kernel(const LoraParam
     }
 }
 
-// Four elements of a row of B, zero from `left` on; VEC: all or none, 8-byte aligned.
-template <bool VEC>
-__device__ __forceinline__ uint2 four(const uint16_t* p, int left) {
-    if (VEC) return left > 0 ? *(const uint2*)p : make_uint2(0, 0);
-    uint32_t w[2] = {0, 0};
+constexpr int kRingStages = 4;
+
+// The same for items of 64 rows and 16-byte rows: stages of 64 k of x and A through a ring in shared memory
+// (cp.async, three in flight; straight to registers the loads of a step waited for the products before
+// it: 8192 rows of 4096, rank 64, 42 us).  Two warps by two: 32 rows and 32 of the 64 k each.  The four
+// 16-byte pieces of a lane group lie in the halves of a 128-byte row by turns, so eight lanes meet no bank twice.
+template <bool F16, int NT>
+__global__ void __launch_bounds__(kLoraThreads) lora_down_ring_kernel(const LoraParams p) {
+    constexpr int kRows = 64, kCols = 8 * NT, kStage = (kRows + kCols) * 128;
+    extern __shared__ __align__(128) uint8_t sm_ring[];
+    __shared__ ItemRows<kRows> item;
+    pdl_wait_previous();
+    pdl_launch_dependents();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+    const int split = blockIdx.y, col0 = blockIdx.z * kCols;
+    int adapter, rows;
+    if (!item.find(p, blockIdx.x, &adapter, &rows) || adapter < 0) return;
+    const int k_begin = split * p.k_split, k_end = min(k_begin + p.k_split, (int)p.K);
+    const uint32_t ring = smem_u32(sm_ring);
+    // A thread copies piece tid % 8 of rows tid / 8, + 16 and so on; zeros behind the rows, columns and K.
+    const int piece = tid & 7, row0 = tid >> 3;
+    const uint32_t to = ring + row0 * 128 + (piece ^ (row0 & 1) * 4) * 16;
+    const uint16_t *from_x[4], *from_a[(kCols + 15) / 16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (i < left) w[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
-    return make_uint2(w[0], w[1]);
+    for (int i = 0; i < 4; ++i) from_x[i] = p.x + (row0 + i * 16 < rows ? item.row[row0 + i * 16] : 0) * p.x_stride + piece * 8;
+#pragma unroll
+    for (int i = 0; i < (kCols + 15) / 16; ++i) {
+        const int c = col0 + row0 + i * 16;
+        from_a[i] = p.a + ((int64_t)adapter * p.r + (c < p.r ? c : 0)) * p.K + piece * 8;
+    }
+    const auto copy = [&](uint32_t dst, const uint16_t* src, bool held) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(held ? 16 : 0) : "memory");
+    };
+    const auto stage = [&](int k0, int s) {
+        if (k0 < k_end) {
+            const bool in = k0 + piece * 8 < k_end;
+            const int k = in ? k0 : 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) copy(to + s * kStage + i * 16 * 128, from_x[i] + k, in && row0 + i * 16 < rows);
+#pragma unroll
+            for (int i = 0; i < (kCols + 15) / 16; ++i)
+                if (row0 + i * 16 < kCols) copy(to + s * kStage + (kRows + i * 16) * 128, from_a[i] + k, in && col0 + row0 + i * 16 < p.r);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    const int row_warp = warp & 1, k_warp = warp >> 1;
+    float acc[2][NT][4] = {};
+#pragma unroll
+    for (int s = 0; s < kRingStages - 1; ++s) stage(k_begin + s * 64, s);
+    int s = 0;
+    for (int k0 = k_begin; k0 < k_end; k0 += 64) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kRingStages - 2) : "memory");
+        __syncthreads();                                    // this stage is there, and the last one is read
+        stage(k0 + (kRingStages - 1) * 64, (s + kRingStages - 1) % kRingStages);
+        const uint8_t* at = sm_ring + s * kStage + ((k_warp * 4 + q) ^ (g & 1) * 4) * 16 + g * 128;
+        uint4 xv[2][2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) xv[m][h] = *(const uint4*)(at + ((row_warp * 2 + m) * 16 + h * 8) * 128);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const uint4 av = *(const uint4*)(at + (kRows + j * 8) * 128);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const uint32_t lo[4] = {xv[m][0].x, xv[m][1].x, xv[m][0].y, xv[m][1].y};
+                const uint32_t hi[4] = {xv[m][0].z, xv[m][1].z, xv[m][0].w, xv[m][1].w};
+                mma_16816<F16>(acc[m][j], lo, av.x, av.y);
+                mma_16816<F16>(acc[m][j], hi, av.z, av.w);
+            }
+        }
+        s = (s + 1) % kRingStages;
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    float* sums = (float*)sm_ring;                          // [2][kRows][kCols + 4]
+    constexpr int kPitch = kCols + 4;
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                *(float2*)&sums[(k_warp * kRows + (row_warp * 2 + m) * 16 + h * 8 + g) * kPitch + j * 8 + q * 2] = make_float2(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
+    __syncthreads();
+    for (int i = tid; i < kRows * kCols / 4; i += kLoraThreads) {
+        const int row = i / (kCols / 4), c = i % (kCols / 4) * 4;
+        if (row >= rows || col0 + c >= p.rp) continue;
+        const float4 u = *(const float4*)&sums[row * kPitch + c], v = *(const float4*)&sums[(kRows + row) * kPitch + c];
+        *(float4*)(p.low + ((int64_t)split * p.T + item.row[row]) * p.rp + col0 + c) = make_float4(u.x + v.x, u.y + v.y, u.z + v.z, u.w + v.w);
+    }
+}
+
+// 2 * KP elements of a row of B, zero from `left` on; VEC: all or none, on boundaries of as many.
+template <int KP, bool VEC>
+__device__ __forceinline__ void part(const uint16_t* p, int left, uint32_t (&w)[KP]) {
+    if (VEC && KP == 4) {
+        const uint4 v = left > 0 ? *(const uint4*)p : make_uint4(0, 0, 0, 0);
+        w[0] = v.x; w[1] = v.y; w[KP - 2] = v.z; w[KP - 1] = v.w;
+    } else if (VEC) {
+        const uint2 v = left > 0 ? *(const uint2*)p : make_uint2(0, 0);
+        w[0] = v.x; w[1] = v.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < KP; ++i) w[i] = 0;
+#pragma unroll
+        for (int i = 0; i < 2 * KP; ++i)
+            if (i < left) w[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
+    }
 }
 
 // One item's rows of A x times B, and y, over a range of N.  A warp takes MT * 16 rows and CU * 32 columns
 // of a step, whose y it asks for first; tile j of four holds columns 8 (c / 2) + 2 j + c % 2, so that a
-// lane's eight outputs of a row lie side by side.
-template <bool F16, int RW, int MT, int CU, bool VEC_B, bool VEC_Y>
+// lane's eight outputs of a row lie side by side.  A lane takes KP words of a row of B: four k for
+// each 16, or (KP = 4) eight for each 32.
+template <bool F16, int RW, int MT, int CU, int KP, bool VEC_B, bool VEC_Y>
 __global__ void __launch_bounds__(kLoraThreads) lora_up_kernel(const LoraParams p, const int cols_block) {
     constexpr int kRows = 16 * MT * RW, kColWarps = kLoraThreads / 32 / RW;
     extern __shared__ __align__(16) uint8_t sm_up[];
     __shared__ ItemRows<kRows> item;
     __shared__ float sm_scale[kRows];
-    const int pitch = p.rp / 2 + 4;                         // words of two values; a fragment's reads meet no bank twice
+    const int pitch = p.rp / 2 + 4;                         // words of two values
     uint32_t* sm_hi = (uint32_t*)sm_up;                     // [kRows][pitch] halves of A x
     uint32_t* sm_lo = sm_hi + kRows * pitch;
     pdl_wait_previous();
@@ -304,7 +406,7 @@ __global__ void __launch_bounds__(kLoraThreads) lora_up_kernel(const LoraParams 
     int adapter, rows;
     if (!item.find(p, blockIdx.x, &adapter, &rows) || (adapter < 0 && !p.copy_rest)) return;
     const int64_t n_begin = (int64_t)blockIdx.y * cols_block, n_end = min(n_begin + cols_block, p.N);
-    const int steps = adapter < 0 ? 0 : p.rp / 16;
+    const int steps = adapter < 0 ? 0 : p.rp / (8 * KP);
     // The splits' sums in order, as two halves: four rows a warp at a time, eight lanes each.  FP16 holds
     // them times the power of two that puts a row's largest below 2, which the end takes back.
     if (steps)
@@ -362,9 +464,17 @@ __global__ void __launch_bounds__(kLoraThreads) lora_up_kernel(const LoraParams 
             const int row = (row_warp * MT + m) * 16 + h * 8 + g;
             t[m][h] = row < rows ? item.row[row] : -1;
         }
-    const uint16_t* b = p.b + (int64_t)max(adapter, 0) * p.N * p.r;
-    const uint32_t *hi0 = sm_hi + (row_warp * MT * 16 + g) * pitch + q * 2, *lo0 = sm_lo + (row_warp * MT * 16 + g) * pitch + q * 2;
-    for (int64_t n0 = n_begin + col_warp * 32 * CU; n0 < n_end; n0 += kColWarps * 32 * CU) {
+    const uint16_t* b = p.b + (int64_t)max(adapter, 0) * p.N * p.r + q * 2 * KP;
+    const uint32_t *hi0 = sm_hi + (row_warp * MT * 16 + g) * pitch + q * KP, *lo0 = sm_lo + (row_warp * MT * 16 + g) * pitch + q * KP;
+    float scale[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) scale[m][h] = steps ? sm_scale[(row_warp * MT + m) * 16 + h * 8 + g] : 0.f;
+    const int r = p.r, first = 8 * (g >> 1) + (g & 1);
+    // FULL: all columns of the step are there.
+    const auto step = [&](int64_t n0, auto full) {
+        constexpr bool FULL = decltype(full)::value;
         uint4 yv[CU][MT][2];
 #pragma unroll
         for (int u = 0; u < CU; ++u)
@@ -373,52 +483,60 @@ __global__ void __launch_bounds__(kLoraThreads) lora_up_kernel(const LoraParams 
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int64_t n = n0 + u * 32 + q * 8;
-                    yv[u][m][h] = t[m][h] >= 0 ? eight<VEC_Y>(p.y + t[m][h] * p.y_stride + n, n_end - n) : make_uint4(0, 0, 0, 0);
+                    yv[u][m][h] = make_uint4(0, 0, 0, 0);
+                    if (t[m][h] >= 0) yv[u][m][h] = eight<VEC_Y>(p.y + t[m][h] * p.y_stride + n, FULL ? 8 : n_end - n);
                 }
         float acc[CU][MT][4][4] = {};
+        const uint16_t* bn = b + (n0 + first) * r;
 #pragma unroll 2
         for (int st = 0; st < steps; ++st) {
-            uint2 bv[CU][4];
+            uint32_t bv[CU][4][KP];
+            const int left = r - st * 8 * KP - q * 2 * KP;
 #pragma unroll
             for (int u = 0; u < CU; ++u)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int64_t n = n0 + u * 32 + 8 * (g >> 1) + 2 * j + (g & 1);
-                    bv[u][j] = n < n_end ? four<VEC_B>(b + n * p.r + st * 16 + q * 4, p.r - st * 16 - q * 4) : make_uint2(0, 0);
-                }
+                for (int j = 0; j < 4; ++j)
+                    part<KP, VEC_B>(bn + (u * 32 + 2 * j) * r + st * 8 * KP, FULL || n0 + first + u * 32 + 2 * j < n_end ? left : 0, bv[u][j]);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                const int at = m * 16 * pitch + st * 8, at8 = at + 8 * pitch;
-                const uint2 h0 = *(const uint2*)(hi0 + at), h1 = *(const uint2*)(hi0 + at8);
-                const uint2 l0 = *(const uint2*)(lo0 + at), l1 = *(const uint2*)(lo0 + at8);
-                const uint32_t hi[4] = {h0.x, h1.x, h0.y, h1.y}, lo[4] = {l0.x, l1.x, l0.y, l1.y};
+                const int at = m * 16 * pitch + st * 4 * KP, at8 = at + 8 * pitch;
+                uint32_t h0[KP], h1[KP], l0[KP], l1[KP];
+                if (KP == 4) {
+                    *(uint4*)h0 = *(const uint4*)(hi0 + at); *(uint4*)h1 = *(const uint4*)(hi0 + at8);
+                    *(uint4*)l0 = *(const uint4*)(lo0 + at); *(uint4*)l1 = *(const uint4*)(lo0 + at8);
+                } else {
+                    *(uint2*)h0 = *(const uint2*)(hi0 + at); *(uint2*)h1 = *(const uint2*)(hi0 + at8);
+                    *(uint2*)l0 = *(const uint2*)(lo0 + at); *(uint2*)l1 = *(const uint2*)(lo0 + at8);
+                }
 #pragma unroll
-                for (int u = 0; u < CU; ++u)
+                for (int k = 0; k < KP; k += 2) {
+                    const uint32_t hi[4] = {h0[k], h1[k], h0[k + 1], h1[k + 1]}, lo[4] = {l0[k], l1[k], l0[k + 1], l1[k + 1]};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        mma_16816<F16>(acc[u][m][j], hi, bv[u][j].x, bv[u][j].y);
-                        mma_16816<F16>(acc[u][m][j], lo, bv[u][j].x, bv[u][j].y);
-                    }
+                    for (int u = 0; u < CU; ++u)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            mma_16816<F16>(acc[u][m][j], hi, bv[u][j][k], bv[u][j][k + 1]);
+                            mma_16816<F16>(acc[u][m][j], lo, bv[u][j][k], bv[u][j][k + 1]);
+                        }
+                }
             }
         }
 #pragma unroll
         for (int u = 0; u < CU; ++u) {
             const int64_t n = n0 + u * 32 + q * 8;
-            if (n >= n_end) continue;
+            if (!FULL && n >= n_end) continue;
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     if (t[m][h] < 0) continue;
                     uint32_t w[4] = {yv[u][m][h].x, yv[u][m][h].y, yv[u][m][h].z, yv[u][m][h].w};
-                    if (steps) {
-                        const float s = sm_scale[(row_warp * MT + m) * 16 + h * 8 + g];
+                    if (steps)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const float2 v = act2_to_f32<F16>(w[j]);
-                            w[j] = f32_to_act2<F16>(fmaf(s, acc[u][m][j][2 * h], v.x), fmaf(s, acc[u][m][j][2 * h + 1], v.y));
+                            w[j] = f32_to_act2<F16>(fmaf(scale[m][h], acc[u][m][j][2 * h], v.x), fmaf(scale[m][h], acc[u][m][j][2 * h + 1], v.y));
                         }
-                    }
                     uint16_t* out = p.out + t[m][h] * p.N + n;
                     if (VEC_Y) {
                         *(uint4*)out = make_uint4(w[0], w[1], w[2], w[3]);
@@ -429,6 +547,10 @@ __global__ void __launch_bounds__(kLoraThreads) lora_up_kernel(const LoraParams 
                     }
                 }
         }
+    };
+    for (int64_t n0 = n_begin + col_warp * 32 * CU; n0 < n_end; n0 += kColWarps * 32 * CU) {
+        if (n0 + 32 * CU <= n_end) step(n0, std::true_type{});
+        else step(n0, std::false_type{});
     }
 }
 
@@ -468,13 +590,23 @@ const void* down_kernel(int nt) {
 template <bool F16>
 const void* down_kernel(int rows, int nt, bool vec) {
     if (rows == 16) return vec ? down_kernel<F16, 1, 1, true>(nt) : down_kernel<F16, 1, 1, false>(nt);
-    return vec ? down_kernel<F16, 2, 2, true>(nt) : down_kernel<F16, 2, 2, false>(nt);
+    return down_kernel<F16, 2, 2, false>(nt);               // with vector loads: ring_kernel
 }
 
+template <bool F16>
+const void* ring_kernel(int nt) {
+    return nt == 1   ? (const void*)lora_down_ring_kernel<F16, 1>
+           : nt == 2 ? (const void*)lora_down_ring_kernel<F16, 2>
+           : nt == 4 ? (const void*)lora_down_ring_kernel<F16, 4>
+                     : (const void*)lora_down_ring_kernel<F16, 8>;
+}
+
+// wide: B in 16-byte pieces of eight k.  (Without vector loads there is one form of each.)
 template <bool F16, int RW, int MT, int CU>
-const void* up_kernel(bool vec_b, bool vec_y) {
-    if (vec_b) return vec_y ? (const void*)lora_up_kernel<F16, RW, MT, CU, true, true> : (const void*)lora_up_kernel<F16, RW, MT, CU, true, false>;
-    return vec_y ? (const void*)lora_up_kernel<F16, RW, MT, CU, false, true> : (const void*)lora_up_kernel<F16, RW, MT, CU, false, false>;
+const void* up_kernel(bool wide, bool vec_b, bool vec_y) {
+    if (!vec_b) return vec_y ? (const void*)lora_up_kernel<F16, RW, MT, CU, 2, false, true> : (const void*)lora_up_kernel<F16, RW, MT, CU, 2, false, false>;
+    if (wide) return vec_y ? (const void*)lora_up_kernel<F16, RW, MT, CU, 4, true, true> : (const void*)lora_up_kernel<F16, RW, MT, CU, 4, true, false>;
+    return vec_y ? (const void*)lora_up_kernel<F16, RW, MT, CU, 2, true, true> : (const void*)lora_up_kernel<F16, RW, MT, CU, 2, true, false>;
 }
 
 nvfp4_status check_sizes(const char* fn, int64_t T, int64_t n, int64_t r, int64_t K, int64_t N) {
@@ -535,18 +667,21 @@ extern "C" nvfp4_status nvfp4_lora_add(const void* y, int64_t y_stride, const vo
         p.num_items = nullptr;
     }
     const bool vec_x = K % 8 == 0 && x_stride % 8 == 0 && aligned(x, 16) && aligned(A, 16);
-    const bool vec_b = r % 4 == 0 && aligned(B, 8);
+    const bool vec_b = r % 4 == 0 && aligned(B, 8), wide = p.rp % 32 == 0 && r % 8 == 0 && aligned(B, 16);
     const bool vec_y = N % 8 == 0 && y_stride % 8 == 0 && aligned(y, 16) && aligned(out, 16);
     if (num_adapters > 0) {
-        const void* kernel = f16 ? down_kernel<true>(pl.rows_item, pl.nt, vec_x) : down_kernel<false>(pl.rows_item, pl.nt, vec_x);
+        const bool ring = vec_x && pl.rows_item == 64;
+        const void* kernel = ring ? (f16 ? ring_kernel<true>(pl.nt) : ring_kernel<false>(pl.nt))
+                                  : (f16 ? down_kernel<true>(pl.rows_item, pl.nt, vec_x) : down_kernel<false>(pl.rows_item, pl.nt, vec_x));
         const dim3 grid((unsigned)pl.items, (unsigned)pl.splits, (unsigned)ceil_div(p.rp, pl.nt * 8));
-        if (nvfp4_status st = launch_kernel(kernel, grid, dim3(kLoraThreads), 0, 1, args, s, fn)) return st;
+        const size_t smem = ring ? kRingStages * (64 + 8 * pl.nt) * 128 : 0;
+        if (nvfp4_status st = launch_kernel(kernel, grid, dim3(kLoraThreads), smem, 1, args, s, fn)) return st;
     }
-    const void* kernel = pl.rows_item == 16 ? (f16 ? up_kernel<true, 1, 1, 2>(vec_b, vec_y) : up_kernel<false, 1, 1, 2>(vec_b, vec_y))
-                                            : (f16 ? up_kernel<true, 2, 2, 2>(vec_b, vec_y) : up_kernel<false, 2, 2, 2>(vec_b, vec_y));
+    const void* kernel = pl.rows_item == 16 ? (f16 ? up_kernel<true, 1, 1, 2>(wide, vec_b, vec_y) : up_kernel<false, 1, 1, 2>(wide, vec_b, vec_y))
+                                            : (f16 ? up_kernel<true, 2, 2, 1>(wide, vec_b, vec_y) : up_kernel<false, 2, 2, 1>(wide, vec_b, vec_y));
     // Columns of a block: as many steps of its warps as leave four blocks an SM, so that the sums over
     // splits are not read too often.
-    const int step = pl.rows_item == 16 ? 256 : 128;
+    const int step = pl.rows_item == 16 ? 256 : 64;
     int64_t cols = step;
     while (cols < N && (ceil_div(N, 2 * cols) * pl.items >= 4 * (int64_t)sm_count() || ceil_div(N, cols) > 65535)) cols *= 2;
     int cols_block = (int)cols;
