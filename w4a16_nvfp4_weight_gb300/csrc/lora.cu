@@ -12,7 +12,6 @@
 // operands go straight from memory to registers: an order of k that is the same for both operands
 // lets a thread load 16 bytes of each row, and an order of the columns 16 bytes of y.
 #include <algorithm>
-#include <type_traits>
 
 #include "common.cuh"
 #include "launch.cuh"
@@ -387,6 +386,198 @@ __device__ __forceinline__ void part(const uint16_t* p, int left, uint32_t (&w)[
     }
 }
 
+// A x of an item's rows, the splits' sums in order, as two 16-bit halves in shared memory: four rows a warp at
+// a time, eight lanes each.  FP16 holds them times the power of two that puts a row's largest below 2,
+// which the end takes back.
+template <bool F16>
+__device__ __forceinline__ void sum_splits(const LoraParams& p, const int32_t* order, int adapter, int rows, int all, int pitch, uint32_t* sm_hi,
+                                           uint32_t* sm_lo, float* sm_scale) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int row = warp * 4 + (lane >> 3); row < all; row += kLoraThreads / 8) {
+        const bool held = row < rows;
+        const float* low = p.low + (int64_t)(held ? order[row] : 0) * p.rp;
+        const int64_t apart = p.T * p.rp;
+        const auto sum = [&](int c) {                   // of four
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (held && c < p.rp) {
+                const float* at = low + c;
+#pragma unroll 4
+                for (int sp = 0; sp < p.splits; ++sp, at += apart) {
+                    const float4 u = *(const float4*)at;
+                    v.x += u.x;
+                    v.y += u.y;
+                    v.z += u.z;
+                    v.w += u.w;
+                }
+            }
+            return v;
+        };
+        float down = 1.f, up = 1.f;
+        if (F16) {
+            float most = 0.f;
+            for (int c = (lane & 7) * 4; c < p.rp; c += 32) {
+                const float4 v = sum(c);
+                most = fmaxf(most, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+            }
+            __syncwarp();
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+            if (most > 0x1p-100f && most < INFINITY) {
+                const uint32_t e = __float_as_uint(most) & 0x7f800000u;
+                up = __uint_as_float(e);
+                down = __uint_as_float(0x7f000000u - e);            // 2^-exponent
+            }
+        }
+        if ((lane & 7) == 0) sm_scale[row] = up * (p.scales ? p.scales[adapter] : 1.f);
+        const auto halves = [&](float a, float b, uint32_t* hi, uint32_t* lo) {
+            *hi = f32_to_act2<F16>(a, b);
+            const float2 back = act2_to_f32<F16>(*hi);
+            // An infinity (or one that the type cannot hold) is its own first half.
+            *lo = f32_to_act2<F16>(fabsf(back.x) < INFINITY ? a - back.x : 0.f, fabsf(back.y) < INFINITY ? b - back.y : 0.f);
+        };
+        for (int c = (lane & 7) * 4; c < p.rp; c += 32) {
+            const float4 v = sum(c);
+            uint2 hi, lo;
+            halves(v.x * down, v.y * down, &hi.x, &lo.x);
+            halves(v.z * down, v.w * down, &hi.y, &lo.y);
+            *(uint2*)(sm_hi + row * pitch + c / 2) = hi;
+            *(uint2*)(sm_lo + row * pitch + c / 2) = lo;
+        }
+    }
+}
+
+constexpr int kUpStages = 3;
+
+// One item's 64 rows of A x times B, and y, over a range of N: stages of 64 columns of B and y through a
+// ring in shared memory (with loads to registers a step ahead, 8192 rows, 4096 columns, rank 64: 75 us).
+// Two warps by two: 32 rows and 32 columns each.  Tile j of four holds columns 8 (c / 2) + 2 j + c % 2, so
+// that a lane's eight outputs of a row lie side by side: the 16 bytes of y that it copies itself.  A lane
+// takes KP words of a row of B: four k for each 16, or (KP = 4) eight for each 32.
+template <bool F16, int KP>
+__global__ void __launch_bounds__(kLoraThreads, 3) lora_up_ring_kernel(const LoraParams p, const int cols_block) {
+    constexpr int kRows = 64, kStep = 64, kYBytes = kRows * kStep * 2;
+    extern __shared__ __align__(128) uint8_t sm_up[];
+    __shared__ ItemRows<kRows> item;
+    __shared__ float sm_scale[kRows];
+    const int pitch = p.rp / 2 + 4;                         // words of two values
+    const int b_bytes = kStep * p.r * 2;
+    uint8_t* sm_y = sm_up;                                  // [kUpStages][kLoraThreads][4] pieces of 16 bytes
+    uint8_t* sm_b = sm_y + kUpStages * kYBytes;             // [kUpStages][kStep][r]
+    uint32_t* sm_hi = (uint32_t*)(sm_b + kUpStages * b_bytes);      // [kRows][pitch] halves of A x
+    uint32_t* sm_lo = sm_hi + kRows * pitch;
+    pdl_wait_previous();
+    pdl_launch_dependents();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+    int adapter, rows;
+    if (!item.find(p, blockIdx.x, &adapter, &rows) || (adapter < 0 && !p.copy_rest)) return;
+    const int64_t n_begin = (int64_t)blockIdx.y * cols_block, n_end = min(n_begin + cols_block, p.N);
+    const int steps = adapter < 0 ? 0 : p.rp / (8 * KP);
+    const int row_warp = warp & 1, col_warp = warp >> 1;
+    bool held[2][2];
+    const uint16_t* y[2][2];
+    uint16_t* out[2][2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int row = (row_warp * 2 + m) * 16 + h * 8 + g;
+            held[m][h] = row < rows;
+            const int64_t t = held[m][h] ? item.row[row] : 0;
+            y[m][h] = p.y + t * p.y_stride + col_warp * 32 + q * 8;
+            out[m][h] = p.out + t * p.N + col_warp * 32 + q * 8;
+        }
+    const uint16_t* b = p.b + (int64_t)max(adapter, 0) * p.N * p.r;
+    const uint32_t y0 = smem_u32(sm_y) + tid * 16, b0 = smem_u32(sm_b);
+    // Rows of 128 bytes and their multiples: the four pieces of a lane group lie in the halves of 128 bytes by turns.
+    const int turn = p.r % 64 == 0 ? 4 : 0, pieces = p.r / 8;
+    const auto stage = [&](int64_t n0, int s) {
+        const int64_t left = n_end - n0;
+        if (left > 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (held[i >> 1][i & 1] && left > col_warp * 32 + q * 8)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(y0 + s * kYBytes + i * kLoraThreads * 16),
+                                 "l"(y[i >> 1][i & 1] + n0) : "memory");
+            if (steps) {
+                const int all = (int)min(left, (int64_t)kStep) * pieces;
+                const uint16_t* from = b + n0 * p.r;
+                for (int i = tid; i < all; i += kLoraThreads) {
+                    const int row = i / pieces, to = i ^ (row & 1) * turn;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(b0 + s * b_bytes + to * 16), "l"(from + i * 8) : "memory");
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int s = 0; s < kUpStages - 1; ++s) stage(n_begin + s * kStep, s);
+    if (steps) sum_splits<F16>(p, item.row, adapter, rows, kRows, pitch, sm_hi, sm_lo, sm_scale);
+    __syncthreads();
+    const uint32_t *hi0 = sm_hi + (row_warp * 32 + g) * pitch + q * KP, *lo0 = sm_lo + (row_warp * 32 + g) * pitch + q * KP;
+    float scale[2][2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) scale[m][h] = steps ? sm_scale[(row_warp * 2 + m) * 16 + h * 8 + g] : 0.f;
+    const int first = col_warp * 32 + 8 * (g >> 1) + (g & 1), odd = (g & 1) * turn * 16;     // of a row's pieces: 64 bytes on, or back
+    int s = 0;
+    for (int64_t n0 = n_begin; n0 < n_end; n0 += kStep) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kUpStages - 2) : "memory");
+        __syncthreads();                                    // this stage is there, and the last one is read
+        stage(n0 + (kUpStages - 1) * kStep, (s + kUpStages - 1) % kUpStages);
+        const uint8_t* bs = sm_b + s * b_bytes + first * p.r * 2;
+        float acc[2][4][4] = {};
+#pragma unroll 2
+        for (int st = 0; st < steps; ++st) {
+            const bool in = st * 8 * KP + q * 2 * KP < p.r;
+            const int at_b = (st * 8 * KP + q * 2 * KP) * 2 ^ odd;
+            uint32_t bv[4][KP];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (KP == 4) *(uint4*)bv[j] = in ? *(const uint4*)(bs + 2 * j * p.r * 2 + at_b) : make_uint4(0, 0, 0, 0);
+                else *(uint2*)bv[j] = in ? *(const uint2*)(bs + 2 * j * p.r * 2 + at_b) : make_uint2(0, 0);
+            }
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const int at = m * 16 * pitch + st * 4 * KP, at8 = at + 8 * pitch;
+                uint32_t h0[KP], h1[KP], l0[KP], l1[KP];
+                if (KP == 4) {
+                    *(uint4*)h0 = *(const uint4*)(hi0 + at); *(uint4*)h1 = *(const uint4*)(hi0 + at8);
+                    *(uint4*)l0 = *(const uint4*)(lo0 + at); *(uint4*)l1 = *(const uint4*)(lo0 + at8);
+                } else {
+                    *(uint2*)h0 = *(const uint2*)(hi0 + at); *(uint2*)h1 = *(const uint2*)(hi0 + at8);
+                    *(uint2*)l0 = *(const uint2*)(lo0 + at); *(uint2*)l1 = *(const uint2*)(lo0 + at8);
+                }
+#pragma unroll
+                for (int k = 0; k < KP; k += 2) {
+                    const uint32_t hi[4] = {h0[k], h1[k], h0[k + 1], h1[k + 1]}, lo[4] = {l0[k], l1[k], l0[k + 1], l1[k + 1]};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mma_16816<F16>(acc[m][j], hi, bv[j][k], bv[j][k + 1]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mma_16816<F16>(acc[m][j], lo, bv[j][k], bv[j][k + 1]);
+                }
+            }
+        }
+        if (n_end - n0 > col_warp * 32 + q * 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int m = i >> 1, h = i & 1;
+                if (!held[m][h]) continue;
+                const uint4 v = *(const uint4*)(sm_y + s * kYBytes + (i * kLoraThreads + tid) * 16);
+                uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                if (steps)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 u = act2_to_f32<F16>(w[j]);
+                        w[j] = f32_to_act2<F16>(fmaf(scale[m][h], acc[m][j][2 * h], u.x), fmaf(scale[m][h], acc[m][j][2 * h + 1], u.y));
+                    }
+                *(uint4*)(out[m][h] + n0) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        s = (s + 1) % kUpStages;
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
 // One item's rows of A x times B, and y, over a range of N.  A warp takes MT * 16 rows and CU * 32 columns
 // of a step, whose y it asks for first; tile j of four holds columns 8 (c / 2) + 2 j + c % 2, so that a
 // lane's eight outputs of a row lie side by side.  A lane takes KP words of a row of B: four k for
@@ -407,62 +598,22 @@ __global__ void __launch_bounds__(kLoraThreads) lora_up_kernel(const LoraParams 
     if (!item.find(p, blockIdx.x, &adapter, &rows) || (adapter < 0 && !p.copy_rest)) return;
     const int64_t n_begin = (int64_t)blockIdx.y * cols_block, n_end = min(n_begin + cols_block, p.N);
     const int steps = adapter < 0 ? 0 : p.rp / (8 * KP);
-    // The splits' sums in order, as two halves: four rows a warp at a time, eight lanes each.  FP16 holds
-    // them times the power of two that puts a row's largest below 2, which the end takes back.
-    if (steps)
-        for (int row = warp * 4 + (lane >> 3); row < kRows; row += kLoraThreads / 8) {
-            const bool held = row < rows;
-            const float* low = p.low + (int64_t)(held ? item.row[row] : 0) * p.rp + (lane & 7) * 2;
-            const int64_t apart = p.T * p.rp;
-            const auto sum = [&](int c) {                   // of a pair
-                float2 v = make_float2(0.f, 0.f);
-                if (held)
-#pragma unroll 4
-                    for (int sp = 0; sp < p.splits; ++sp) {
-                        const float2 u = *(const float2*)(low + sp * apart + c);
-                        v.x += u.x;
-                        v.y += u.y;
-                    }
-                return v;
-            };
-            float down = 1.f, up = 1.f;
-            if (F16) {
-                float most = 0.f;
-                for (int c = 0; c < p.rp; c += 16) {
-                    const float2 v = sum(c);
-                    most = fmaxf(most, fmaxf(fabsf(v.x), fabsf(v.y)));
-                }
-#pragma unroll
-                for (int o = 4; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-                if (most > 0x1p-100f && most < INFINITY) {
-                    const uint32_t e = __float_as_uint(most) & 0x7f800000u;
-                    up = __uint_as_float(e);
-                    down = __uint_as_float(0x7f000000u - e);            // 2^-exponent
-                }
-            }
-            if ((lane & 7) == 0) sm_scale[row] = up * (p.scales ? p.scales[adapter] : 1.f);
-#pragma unroll 2
-            for (int c = 0; c < p.rp; c += 16) {
-                const float2 v = sum(c);
-                const float a = v.x * down, b = v.y * down;
-                const uint32_t hi = f32_to_act2<F16>(a, b);
-                const float2 back = act2_to_f32<F16>(hi);
-                // An infinity (or one that the type cannot hold) is its own first half.
-                const float la = fabsf(back.x) < INFINITY ? a - back.x : 0.f, lb = fabsf(back.y) < INFINITY ? b - back.y : 0.f;
-                sm_hi[row * pitch + c / 2 + (lane & 7)] = hi;
-                sm_lo[row * pitch + c / 2 + (lane & 7)] = f32_to_act2<F16>(la, lb);
-            }
-        }
+    if (steps) sum_splits<F16>(p, item.row, adapter, rows, kRows, pitch, sm_hi, sm_lo, sm_scale);
     __syncthreads();
     const int row_warp = warp % RW, col_warp = warp / RW;
     if (row_warp * MT * 16 >= rows) return;
-    int64_t t[MT][2];                                       // rows, -1 behind the last
+    bool held[MT][2];
+    const uint16_t* y[MT][2];
+    uint16_t* out[MT][2];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int row = (row_warp * MT + m) * 16 + h * 8 + g;
-            t[m][h] = row < rows ? item.row[row] : -1;
+            held[m][h] = row < rows;
+            const int64_t t = held[m][h] ? item.row[row] : 0;
+            y[m][h] = p.y + t * p.y_stride + q * 8;
+            out[m][h] = p.out + t * p.N + q * 8;
         }
     const uint16_t* b = p.b + (int64_t)max(adapter, 0) * p.N * p.r + q * 2 * KP;
     const uint32_t *hi0 = sm_hi + (row_warp * MT * 16 + g) * pitch + q * KP, *lo0 = sm_lo + (row_warp * MT * 16 + g) * pitch + q * KP;
@@ -472,31 +623,51 @@ __global__ void __launch_bounds__(kLoraThreads) lora_up_kernel(const LoraParams 
 #pragma unroll
         for (int h = 0; h < 2; ++h) scale[m][h] = steps ? sm_scale[(row_warp * MT + m) * 16 + h * 8 + g] : 0.f;
     const int r = p.r, first = 8 * (g >> 1) + (g & 1);
-    // FULL: all columns of the step are there.
-    const auto step = [&](int64_t n0, auto full) {
-        constexpr bool FULL = decltype(full)::value;
-        uint4 yv[CU][MT][2];
+    // y of the step at n0.  `whole`: all of its columns are there.
+    const auto ask = [&](int64_t n0, bool whole, uint4 (&v)[CU][MT][2]) {
 #pragma unroll
         for (int u = 0; u < CU; ++u)
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int64_t n = n0 + u * 32 + q * 8;
-                    yv[u][m][h] = make_uint4(0, 0, 0, 0);
-                    if (t[m][h] >= 0) yv[u][m][h] = eight<VEC_Y>(p.y + t[m][h] * p.y_stride + n, FULL ? 8 : n_end - n);
+                    v[u][m][h] = make_uint4(0, 0, 0, 0);
+                    if (held[m][h]) v[u][m][h] = eight<VEC_Y>(y[m][h] + n0 + u * 32, whole ? 8 : n_end - n0 - u * 32 - q * 8);
                 }
+    };
+    constexpr int kStep = 32 * CU;
+    uint4 next[CU][MT][2];
+    int64_t n0 = n_begin + col_warp * kStep;
+    if (n0 < n_end) ask(n0, n0 + kStep <= n_end, next);
+    for (; n0 < n_end; n0 += kColWarps * kStep) {
+        const bool whole = n0 + kStep <= n_end;
+        uint4 now[CU][MT][2];
+#pragma unroll
+        for (int u = 0; u < CU; ++u)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) now[u][m][h] = next[u][m][h];
+        const int64_t n1 = n0 + kColWarps * kStep;
+        if (n1 < n_end) ask(n1, n1 + kStep <= n_end, next);
         float acc[CU][MT][4][4] = {};
         const uint16_t* bn = b + (n0 + first) * r;
 #pragma unroll 2
         for (int st = 0; st < steps; ++st) {
             uint32_t bv[CU][4][KP];
             const int left = r - st * 8 * KP - q * 2 * KP;
+            if (whole) {
 #pragma unroll
-            for (int u = 0; u < CU; ++u)
+                for (int u = 0; u < CU; ++u)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    part<KP, VEC_B>(bn + (u * 32 + 2 * j) * r + st * 8 * KP, FULL || n0 + first + u * 32 + 2 * j < n_end ? left : 0, bv[u][j]);
+                    for (int j = 0; j < 4; ++j) part<KP, VEC_B>(bn + (u * 32 + 2 * j) * r + st * 8 * KP, left, bv[u][j]);
+            } else {
+#pragma unroll
+                for (int u = 0; u < CU; ++u)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        part<KP, VEC_B>(bn + (u * 32 + 2 * j) * r + st * 8 * KP, n0 + first + u * 32 + 2 * j < n_end ? left : 0, bv[u][j]);
+            }
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 const int at = m * 16 * pitch + st * 4 * KP, at8 = at + 8 * pitch;
@@ -523,34 +694,30 @@ __global__ void __launch_bounds__(kLoraThreads) lora_up_kernel(const LoraParams 
         }
 #pragma unroll
         for (int u = 0; u < CU; ++u) {
-            const int64_t n = n0 + u * 32 + q * 8;
-            if (!FULL && n >= n_end) continue;
+            const int64_t left = n_end - n0 - u * 32 - q * 8;
+            if (left <= 0) continue;
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    if (t[m][h] < 0) continue;
-                    uint32_t w[4] = {yv[u][m][h].x, yv[u][m][h].y, yv[u][m][h].z, yv[u][m][h].w};
+                    if (!held[m][h]) continue;
+                    uint32_t w[4] = {now[u][m][h].x, now[u][m][h].y, now[u][m][h].z, now[u][m][h].w};
                     if (steps)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const float2 v = act2_to_f32<F16>(w[j]);
                             w[j] = f32_to_act2<F16>(fmaf(scale[m][h], acc[u][m][j][2 * h], v.x), fmaf(scale[m][h], acc[u][m][j][2 * h + 1], v.y));
                         }
-                    uint16_t* out = p.out + t[m][h] * p.N + n;
+                    uint16_t* to = out[m][h] + n0 + u * 32;
                     if (VEC_Y) {
-                        *(uint4*)out = make_uint4(w[0], w[1], w[2], w[3]);
+                        *(uint4*)to = make_uint4(w[0], w[1], w[2], w[3]);
                     } else {
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            if (n + i < n_end) out[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+                            if (i < left) to[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
                     }
                 }
         }
-    };
-    for (int64_t n0 = n_begin + col_warp * 32 * CU; n0 < n_end; n0 += kColWarps * 32 * CU) {
-        if (n0 + 32 * CU <= n_end) step(n0, std::true_type{});
-        else step(n0, std::false_type{});
     }
 }
 
@@ -569,7 +736,7 @@ LoraPlan plan_lora(int64_t T, int64_t n, int64_t r, int64_t K) {
     pl.items = std::min(T, T / pl.rows_item + n + 1);
     pl.nt = r <= 8 ? 1 : r <= 16 ? 2 : r <= 32 ? 4 : 8;
     const int64_t blocks = pl.items * ceil_div(r, pl.nt * 8);
-    int64_t splits = ceil_div(3 * (int64_t)sm_count(), blocks);
+    int64_t splits = std::max<int64_t>(1, 3 * (int64_t)sm_count() / blocks);
     splits = std::min<int64_t>({splits, kMaxSplits, ceil_div(K, 256)});
     pl.k_split = (int)round_up(ceil_div(K, std::max<int64_t>(splits, 1)), 32);
     pl.splits = (int)ceil_div(K, pl.k_split);
@@ -677,15 +844,23 @@ extern "C" nvfp4_status nvfp4_lora_add(const void* y, int64_t y_stride, const vo
         const size_t smem = ring ? kRingStages * (64 + 8 * pl.nt) * 128 : 0;
         if (nvfp4_status st = launch_kernel(kernel, grid, dim3(kLoraThreads), smem, 1, args, s, fn)) return st;
     }
-    const void* kernel = pl.rows_item == 16 ? (f16 ? up_kernel<true, 1, 1, 2>(wide, vec_b, vec_y) : up_kernel<false, 1, 1, 2>(wide, vec_b, vec_y))
-                                            : (f16 ? up_kernel<true, 2, 2, 1>(wide, vec_b, vec_y) : up_kernel<false, 2, 2, 1>(wide, vec_b, vec_y));
+    // The ring of a large rank does not leave room for two blocks an SM, so it goes up to 128 (rank 256: 147 KB).
+    const bool up_ring = pl.rows_item == 64 && vec_y && vec_b && r % 8 == 0 && r <= 128 && aligned(B, 16);
+    const void* kernel;
+    if (up_ring) {
+        kernel = wide ? (f16 ? (const void*)lora_up_ring_kernel<true, 4> : (const void*)lora_up_ring_kernel<false, 4>)
+                      : (f16 ? (const void*)lora_up_ring_kernel<true, 2> : (const void*)lora_up_ring_kernel<false, 2>);
+    } else {
+        kernel = pl.rows_item == 16 ? (f16 ? up_kernel<true, 1, 1, 2>(wide, vec_b, vec_y) : up_kernel<false, 1, 1, 2>(wide, vec_b, vec_y))
+                                    : (f16 ? up_kernel<true, 2, 2, 1>(wide, vec_b, vec_y) : up_kernel<false, 2, 2, 1>(wide, vec_b, vec_y));
+    }
     // Columns of a block: as many steps of its warps as leave four blocks an SM, so that the sums over
     // splits are not read too often.
     const int step = pl.rows_item == 16 ? 256 : 64;
     int64_t cols = step;
     while (cols < N && (ceil_div(N, 2 * cols) * pl.items >= 4 * (int64_t)sm_count() || ceil_div(N, cols) > 65535)) cols *= 2;
     int cols_block = (int)cols;
-    const size_t smem = (size_t)pl.rows_item * (p.rp / 2 + 4) * 8;
+    const size_t smem = (size_t)pl.rows_item * (p.rp / 2 + 4) * 8 + (up_ring ? (size_t)kUpStages * 64 * (128 + 2 * r) : 0);
     void* up_args[] = {&p, &cols_block};
     return launch_kernel(kernel, dim3((unsigned)pl.items, (unsigned)ceil_div(N, cols)), dim3(kLoraThreads), smem, 1, up_args, s, fn);
 }
