@@ -37,7 +37,7 @@ struct LoraParams {
     const float* scales;                   // null: 1
     uint16_t* out;
     int64_t T, K, N, x_stride, y_stride;
-    int n, r, rp;                          // adapters, rank, rank rounded up to 16
+    int n, r, rp;                          // adapters, rank, padded_rank(r)
     int splits, k_split;                   // of K, and its elements a split (a multiple of 32)
     int rows_item;                         // 16 or 64
     int copy_rest;                         // rows without an adapter are copied
@@ -451,11 +451,13 @@ constexpr int kUpStages = 3;
 // One item's 64 rows of A x times B, and y, over a range of N: stages of 64 columns of B and y through a
 // ring in shared memory (with loads to registers a step ahead, 8192 rows, 4096 columns, rank 64: 75 us).
 // Two warps by two: 32 rows and 32 columns each.  Tile j of four holds columns 8 (c / 2) + 2 j + c % 2, so
-// that a lane's eight outputs of a row lie side by side: the 16 bytes of y that it copies itself.  A lane
-// takes KP words of a row of B: four k for each 16, or (KP = 4) eight for each 32.
-template <bool F16, int KP>
+// that a lane's eight outputs of a row lie side by side: the 16 bytes of y that it copies itself.  KS: 16s
+// of the rank, or 8 for any number of them.  EXACT: it is a multiple of a step's k.
+template <bool F16, int KS, bool EXACT>
 __global__ void __launch_bounds__(kLoraThreads, 3) lora_up_ring_kernel(const LoraParams p, const int cols_block) {
     constexpr int kRows = 64, kStep = 64, kYBytes = kRows * kStep * 2;
+    constexpr int KP = KS == 1 ? 2 : 4;
+    constexpr bool kHeld = KS <= 4;
     extern __shared__ __align__(128) uint8_t sm_up[];
     __shared__ ItemRows<kRows> item;
     __shared__ float sm_scale[kRows];
@@ -489,7 +491,7 @@ __global__ void __launch_bounds__(kLoraThreads, 3) lora_up_ring_kernel(const Lor
     const uint16_t* b = p.b + (int64_t)max(adapter, 0) * p.N * p.r;
     const uint32_t y0 = smem_u32(sm_y) + tid * 16, b0 = smem_u32(sm_b);
     // Rows of 128 bytes and their multiples: the four pieces of a lane group lie in the halves of 128 bytes by turns.
-    const int turn = p.r % 64 == 0 ? 4 : 0, pieces = p.r / 8;
+    const int turn = p.r % 64 == 0 ? 4 : 0, row_bit = p.r == 128 ? 4 : 3, pieces = p.r / 8;
     const auto stage = [&](int64_t n0, int s) {
         const int64_t left = n_end - n0;
         if (left > 0) {
@@ -502,7 +504,7 @@ __global__ void __launch_bounds__(kLoraThreads, 3) lora_up_ring_kernel(const Lor
                 const int all = (int)min(left, (int64_t)kStep) * pieces;
                 const uint16_t* from = b + n0 * p.r;
                 for (int i = tid; i < all; i += kLoraThreads) {
-                    const int row = i / pieces, to = i ^ (row & 1) * turn;
+                    const int to = i ^ (i >> row_bit & 1) * turn;
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(b0 + s * b_bytes + to * 16), "l"(from + i * 8) : "memory");
                 }
             }
@@ -514,6 +516,28 @@ __global__ void __launch_bounds__(kLoraThreads, 3) lora_up_ring_kernel(const Lor
     if (steps) sum_splits<F16>(p, item.row, adapter, rows, kRows, pitch, sm_hi, sm_lo, sm_scale);
     __syncthreads();
     const uint32_t *hi0 = sm_hi + (row_warp * 32 + g) * pitch + q * KP, *lo0 = sm_lo + (row_warp * 32 + g) * pitch + q * KP;
+    // Halves of A x of a lane's rows: words w and w + 1 of step st are the k of one product.
+    const auto low_words = [&](const uint32_t* from, int m, int st, uint32_t (&w0)[KP], uint32_t (&w1)[KP]) {
+        const int at = m * 16 * pitch + st * 4 * KP, at8 = at + 8 * pitch;
+        if (KP == 4) {
+            *(uint4*)w0 = *(const uint4*)(from + at);
+            *(uint4*)w1 = *(const uint4*)(from + at8);
+        } else {
+            *(uint2*)w0 = *(const uint2*)(from + at);
+            *(uint2*)w1 = *(const uint2*)(from + at8);
+        }
+    };
+    // They are the same for all columns: up to rank 64 they stay in registers.
+    constexpr int kHeldSteps = kHeld ? KS * 2 / KP : 1;
+    uint32_t kept[2][2][kHeldSteps][2][KP];                 // [half][m][step][row or row + 8]
+    if (kHeld && steps)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int st = 0; st < kHeldSteps; ++st) {
+                low_words(hi0, m, st, kept[0][m][st][0], kept[0][m][st][1]);
+                low_words(lo0, m, st, kept[1][m][st][0], kept[1][m][st][1]);
+            }
     float scale[2][2];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
@@ -527,9 +551,8 @@ __global__ void __launch_bounds__(kLoraThreads, 3) lora_up_ring_kernel(const Lor
         stage(n0 + (kUpStages - 1) * kStep, (s + kUpStages - 1) % kUpStages);
         const uint8_t* bs = sm_b + s * b_bytes + first * p.r * 2;
         float acc[2][4][4] = {};
-#pragma unroll 2
-        for (int st = 0; st < steps; ++st) {
-            const bool in = st * 8 * KP + q * 2 * KP < p.r;
+        const auto products = [&](int st, const auto& words) {
+            const bool in = EXACT || st * 8 * KP + q * 2 * KP < p.r;
             const int at_b = (st * 8 * KP + q * 2 * KP) * 2 ^ odd;
             uint32_t bv[4][KP];
 #pragma unroll
@@ -538,25 +561,33 @@ __global__ void __launch_bounds__(kLoraThreads, 3) lora_up_ring_kernel(const Lor
                 else *(uint2*)bv[j] = in ? *(const uint2*)(bs + 2 * j * p.r * 2 + at_b) : make_uint2(0, 0);
             }
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const int at = m * 16 * pitch + st * 4 * KP, at8 = at + 8 * pitch;
-                uint32_t h0[KP], h1[KP], l0[KP], l1[KP];
-                if (KP == 4) {
-                    *(uint4*)h0 = *(const uint4*)(hi0 + at); *(uint4*)h1 = *(const uint4*)(hi0 + at8);
-                    *(uint4*)l0 = *(const uint4*)(lo0 + at); *(uint4*)l1 = *(const uint4*)(lo0 + at8);
-                } else {
-                    *(uint2*)h0 = *(const uint2*)(hi0 + at); *(uint2*)h1 = *(const uint2*)(hi0 + at8);
-                    *(uint2*)l0 = *(const uint2*)(lo0 + at); *(uint2*)l1 = *(const uint2*)(lo0 + at8);
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    uint32_t w0[KP], w1[KP];
+                    words(half, m, w0, w1);
+#pragma unroll
+                    for (int k = 0; k < KP; k += 2) {
+                        const uint32_t a[4] = {w0[k], w1[k], w0[k + 1], w1[k + 1]};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) mma_16816<F16>(acc[m][j], a, bv[j][k], bv[j][k + 1]);
+                    }
                 }
+        };
+        if (kHeld) {
+            if (steps)
 #pragma unroll
-                for (int k = 0; k < KP; k += 2) {
-                    const uint32_t hi[4] = {h0[k], h1[k], h0[k + 1], h1[k + 1]}, lo[4] = {l0[k], l1[k], l0[k + 1], l1[k + 1]};
+                for (int st = 0; st < kHeldSteps; ++st)
+                    products(st, [&](int half, int m, uint32_t (&w0)[KP], uint32_t (&w1)[KP]) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) mma_16816<F16>(acc[m][j], hi, bv[j][k], bv[j][k + 1]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) mma_16816<F16>(acc[m][j], lo, bv[j][k], bv[j][k + 1]);
-                }
-            }
+                        for (int k = 0; k < KP; ++k) {
+                            w0[k] = kept[half][m][st][0][k];
+                            w1[k] = kept[half][m][st][1][k];
+                        }
+                    });
+        } else {
+            for (int st = 0; st < steps; ++st)
+                products(st, [&](int half, int m, uint32_t (&w0)[KP], uint32_t (&w1)[KP]) { low_words(half ? lo0 : hi0, m, st, w0, w1); });
         }
         if (n_end - n0 > col_warp * 32 + q * 8)
 #pragma unroll
@@ -721,6 +752,9 @@ __global__ void __launch_bounds__(kLoraThreads) lora_up_kernel(const LoraParams 
     }
 }
 
+// The rank that A x is held with: whole steps of the products, zeros behind r.
+int64_t padded_rank(int64_t r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : round_up(r, 32); }
+
 // How a call of these sizes is cut up.
 struct LoraPlan {
     int rows_item, splits, k_split, nt;
@@ -742,7 +776,7 @@ LoraPlan plan_lora(int64_t T, int64_t n, int64_t r, int64_t K) {
     pl.splits = (int)ceil_div(K, pl.k_split);
     pl.order_at = 256 + (pl.listed ? (size_t)round_up(sizeof(Item) * pl.items, 256) : 0);
     pl.low_at = pl.order_at + (pl.listed ? (size_t)round_up(4 * T, 256) : 0);
-    pl.bytes = pl.low_at + (size_t)round_up(4 * pl.splits * T * round_up(r, 16), 256);
+    pl.bytes = pl.low_at + (size_t)round_up(4 * pl.splits * T * padded_rank(r), 256);
     return pl;
 }
 
@@ -774,6 +808,16 @@ const void* up_kernel(bool wide, bool vec_b, bool vec_y) {
     if (!vec_b) return vec_y ? (const void*)lora_up_kernel<F16, RW, MT, CU, 2, false, true> : (const void*)lora_up_kernel<F16, RW, MT, CU, 2, false, false>;
     if (wide) return vec_y ? (const void*)lora_up_kernel<F16, RW, MT, CU, 4, true, true> : (const void*)lora_up_kernel<F16, RW, MT, CU, 4, true, false>;
     return vec_y ? (const void*)lora_up_kernel<F16, RW, MT, CU, 2, true, true> : (const void*)lora_up_kernel<F16, RW, MT, CU, 2, true, false>;
+}
+
+template <bool F16, int KS>
+const void* up_ring_kernel_of(bool exact) { return exact ? (const void*)lora_up_ring_kernel<F16, KS, true> : (const void*)lora_up_ring_kernel<F16, KS, false>; }
+template <bool F16>
+const void* up_ring_kernel(int64_t r) {
+    if (r <= 16) return up_ring_kernel_of<F16, 1>(r == 16);
+    if (r <= 32) return up_ring_kernel_of<F16, 2>(r == 32);
+    if (r <= 64) return up_ring_kernel_of<F16, 4>(r == 64);
+    return up_ring_kernel_of<F16, 8>(r % 32 == 0);
 }
 
 nvfp4_status check_sizes(const char* fn, int64_t T, int64_t n, int64_t r, int64_t K, int64_t N) {
@@ -823,7 +867,7 @@ extern "C" nvfp4_status nvfp4_lora_add(const void* y, int64_t y_stride, const vo
     p.x = (const uint16_t*)x; p.a = (const uint16_t*)A; p.b = (const uint16_t*)B; p.y = (const uint16_t*)y;
     p.adapters = adapters; p.scales = scales; p.out = (uint16_t*)out;
     p.T = T; p.K = K; p.N = N; p.x_stride = x_stride; p.y_stride = y_stride;
-    p.n = (int)num_adapters; p.r = (int)r; p.rp = (int)round_up(r, 16);
+    p.n = (int)num_adapters; p.r = (int)r; p.rp = (int)padded_rank(r);
     p.splits = pl.splits; p.k_split = pl.k_split; p.rows_item = pl.rows_item; p.copy_rest = out != y;
     p.num_items = (int32_t*)w; p.items = (Item*)(w + 256); p.order = (int32_t*)(w + pl.order_at); p.low = (float*)(w + pl.low_at);
     cudaStream_t s = (cudaStream_t)stream;
@@ -848,18 +892,18 @@ extern "C" nvfp4_status nvfp4_lora_add(const void* y, int64_t y_stride, const vo
     const bool up_ring = pl.rows_item == 64 && vec_y && vec_b && r % 8 == 0 && r <= 128 && aligned(B, 16);
     const void* kernel;
     if (up_ring) {
-        kernel = wide ? (f16 ? (const void*)lora_up_ring_kernel<true, 4> : (const void*)lora_up_ring_kernel<false, 4>)
-                      : (f16 ? (const void*)lora_up_ring_kernel<true, 2> : (const void*)lora_up_ring_kernel<false, 2>);
+        kernel = f16 ? up_ring_kernel<true>(r) : up_ring_kernel<false>(r);
     } else {
         kernel = pl.rows_item == 16 ? (f16 ? up_kernel<true, 1, 1, 2>(wide, vec_b, vec_y) : up_kernel<false, 1, 1, 2>(wide, vec_b, vec_y))
                                     : (f16 ? up_kernel<true, 2, 2, 1>(wide, vec_b, vec_y) : up_kernel<false, 2, 2, 1>(wide, vec_b, vec_y));
     }
-    // Columns of a block: as many steps of its warps as leave four blocks an SM, so that the sums over
-    // splits are not read too often.
+    // Columns of a block: as many steps of its warps as leave one wave of blocks (three an SM fit; of few rows
+    // six), so that an item's sums over the splits are not read more often than that needs.
     const int step = pl.rows_item == 16 ? 256 : 64;
-    int64_t cols = step;
-    while (cols < N && (ceil_div(N, 2 * cols) * pl.items >= 4 * (int64_t)sm_count() || ceil_div(N, cols) > 65535)) cols *= 2;
-    int cols_block = (int)cols;
+    const int64_t waves = (pl.rows_item == 16 ? 6 : 3) * (int64_t)sm_count();
+    const int64_t blocks = std::min<int64_t>(std::max<int64_t>(1, waves / pl.items), 65535);        // of an item
+    int cols_block = (int)round_up(ceil_div(N, blocks), step);
+    const int64_t cols = cols_block;
     const size_t smem = (size_t)pl.rows_item * (p.rp / 2 + 4) * 8 + (up_ring ? (size_t)kUpStages * 64 * (128 + 2 * r) : 0);
     void* up_args[] = {&p, &cols_block};
     return launch_kernel(kernel, dim3((unsigned)pl.items, (unsigned)ceil_div(N, cols)), dim3(kLoraThreads), smem, 1, up_args, s, fn);
