@@ -27,7 +27,8 @@ constexpr int kSampleWarps = kSampleThreads / 32;
 constexpr int kBins = 1024;                // of the histogram
 constexpr int kList = 1024;                // values sorted at most
 constexpr int kMaxCluster = 8;
-constexpr int kStages = 4;                 // steps of a warp in flight or in use
+constexpr int kStages = 4;                 // steps of a warp in flight or in use, of rows that are not held
+constexpr int64_t kHeldBytes = 86 * 1024;  // of a block's logits that stay in shared memory, with another block beside it
 constexpr int kOneLog2 = 43;               // a weight of one is 2^43: 2^20 of them sum inside 63 bits
 constexpr int64_t kMaxVocabulary = 1 << 20;
 
@@ -206,7 +207,6 @@ struct Row {
     static constexpr int kSize = TYPE == kTypeF32 ? 4 : 2;
     static constexpr int kPieces = kSize / 2, kPer = 8 / kPieces;
     static constexpr int kStageBytes = 512 * kPieces;
-    static constexpr int kRingBytes = kSampleWarps * kStages * kStageBytes;
     const uint8_t* base;
     int first, end;                        // virtual elements that are the row's
 
@@ -265,32 +265,58 @@ struct Row {
             }
         }
     }
+    // This lane's eight of a step, from its warp's stage `s` in shared memory.
+    __device__ __forceinline__ static void fetch(uint32_t at, int s, float (&l)[8]) {
+        uint4 v[kPieces];
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[k].x), "=r"(v[k].y), "=r"(v[k].z), "=r"(v[k].w)
+                         : "r"(at + s * kStageBytes + k * 512) : "memory");
+        widen(v, l);
+    }
+    __device__ __forceinline__ void stage(int at, int j1, uint32_t to, int s) const {
+        if (at < j1)
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k) copy(index(at, k * kPer), to + s * kStageBytes + k * 512);
+    }
     // f(eight logits, the step's first element) over the elements j0 to j1 (multiples of 256 after j0, or the
-    // row's end) of a warp, three steps ahead of it on their way.  A lane reads what it copied.
-    template <class F>
-    __device__ __forceinline__ void each(int j0, int j1, uint32_t ring, F f) const {
-        ring += (threadIdx.x >> 5) * kStages * kStageBytes + (threadIdx.x & 31) * 16;
-        const auto stage = [&](int at, int s) {
-            if (at < j1)
+    // row's end) of a warp, whose stages begin at `at`.  A lane reads what it copied.  HELD: the warp's part has
+    // a stage for every step, so it is copied once (`first`) and stays; else three steps are on their way
+    // ahead of f, every time.
+    template <bool HELD, class F>
+    __device__ __forceinline__ void each(int j0, int j1, uint32_t at, bool first, F f) const {
+        if (HELD) {
+            const int half = (j1 - j0) / 512 * 256 + j0;
+            if (first) {
+                for (int j = j0; j < half; j += 256) stage(j, j1, at, (j - j0) >> 8);
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                for (int j = half; j < j1; j += 256) stage(j, j1, at, (j - j0) >> 8);
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+            }
+            int s = 0;
+            for (int j = j0; j < j1; j += 256, ++s) {
+                if (first && j == half) asm volatile("cp.async.wait_group 0;" ::: "memory");
+                float l[8];
+                fetch(at, s, l);
+                f(l, j);
+            }
+            return;
+        }
 #pragma unroll
-                for (int k = 0; k < kPieces; ++k) copy(index(at, k * kPer), ring + s * kStageBytes + k * 512);
+        for (int s = 0; s < kStages - 1; ++s) {
+            stage(j0 + s * 256, j1, at, s);
             asm volatile("cp.async.commit_group;" ::: "memory");
-        };
-#pragma unroll
-        for (int s = 0; s < kStages - 1; ++s) stage(j0 + s * 256, s);
+        }
         int s = 0;
-        for (int at = j0; at < j1; at += 256) {
+        for (int j = j0; j < j1; j += 256) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-            uint4 v[kPieces];
-#pragma unroll
-            for (int k = 0; k < kPieces; ++k)
-                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[k].x), "=r"(v[k].y), "=r"(v[k].z), "=r"(v[k].w)
-                             : "r"(ring + s * kStageBytes + k * 512) : "memory");
             float l[8];
-            widen(v, l);
-            stage(at + (kStages - 1) * 256, (s + kStages - 1) % kStages);
+            fetch(at, s, l);
+            stage(j + (kStages - 1) * 256, j1, at, (s + kStages - 1) % kStages);
+            asm volatile("cp.async.commit_group;" ::: "memory");
             s = (s + 1) % kStages;
-            f(l, at);
+            f(l, j);
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
@@ -309,8 +335,10 @@ struct Cut {
 struct Shared {
     uint2 table[512];
     uint32_t count[kBins], lo[kBins], hi[kBins];
-    uint64_t pairs[kList];                 // logits with their indices, of a row with few candidates
-    uint32_t list[2][kList];               // values of a bin, as keys: of this block; of the whole row
+    union {
+        uint64_t pairs[kList];             // logits with their indices, of a row with few candidates
+        uint32_t list[2][kList];           // values of a bin, as keys: of this block; of the whole row
+    };
     uint32_t listed, paired, few[kMaxCluster];
     uint64_t scan[2][kSampleWarps];
     uint64_t found[4];
@@ -432,11 +460,11 @@ struct Reached {
     uint64_t here, before;
 };
 
-template <int TYPE, class SCALE>
+template <int TYPE, bool HELD, class SCALE>
 struct Sampler {
     Shared& sm;
     Row<TYPE> row;
-    uint32_t ring;                         // shared address of the warps' stages
+    uint32_t stages;                       // shared address of this lane's first piece
     uint32_t rank, ranks;
     int j0, j1;                            // virtual elements of this warp
     bool large;                            // more than 2^16 of a block
@@ -445,7 +473,7 @@ struct Sampler {
     // f(eight logits, their largest, the step's first element) over this warp's elements.
     template <class F>
     __device__ __forceinline__ void each(F f) const {
-        row.each(j0, j1, ring, [&](float (&l)[8], int j) { f(l, scale.tidy(Row<TYPE>::largest(l)), j); });
+        row.template each<HELD>(j0, j1, stages, false, [&](float (&l)[8], int j) { f(l, scale.tidy(Row<TYPE>::largest(l)), j); });
     }
     __device__ __forceinline__ void tidy(float (&l)[8]) const {
 #pragma unroll
@@ -903,11 +931,10 @@ struct Sampler {
     }
 };
 
-template <int TYPE>
+template <int TYPE, bool HELD>
 __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleParams p) {
-    extern __shared__ __align__(16) uint8_t sm_ring[];
+    extern __shared__ __align__(16) uint8_t sm_stages[];
     __shared__ Shared sm;
-    const uint32_t ring = smem_u32(sm_ring);
     cluster_arrive();                                       // that every block of the row runs: before the first push
     const uint32_t rank = cluster_rank(), ranks = cluster_ranks();
     const int64_t b = blockIdx.x / ranks;
@@ -925,10 +952,12 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleP
     const int64_t start = ((int64_t)rank * kSampleWarps + warp) * p.chunk;
     const int j0 = (int)min(start, (int64_t)row.end), j1 = (int)min(start + p.chunk, (int64_t)row.end);
 
+    const uint32_t stages = smem_u32(sm_stages) + warp * (HELD ? p.chunk >> 8 : kStages) * Row<TYPE>::kStageBytes + lane * 16;
+
     // The largest logit, the first of equal ones.
     float best = -INFINITY;
     int best_at = INT32_MAX;
-    row.each(j0, j1, ring, [&](const float (&l)[8], int j) {
+    row.template each<HELD>(j0, j1, stages, true, [&](const float (&l)[8], int j) {
         const float m = Row<TYPE>::largest(l);
         if (m > best) {                                     // NaN is neither
             best = m;
@@ -984,14 +1013,17 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleP
     }
     NearScale near;
     if (near.set(best, temperature)) {
-        Sampler<TYPE, NearScale>{sm, row, ring, rank, ranks, j0, j1, p.chunk > 65536 / kSampleWarps, near}.draw(p, b, best, most, top_k, top_p, min_p);
+        Sampler<TYPE, HELD, NearScale>{sm, row, stages, rank, ranks, j0, j1, p.chunk > 65536 / kSampleWarps, near}.draw(p, b, best, most, top_k, top_p, min_p);
     } else {
         FarScale far;
         far.set(best, temperature);
-        const Sampler<TYPE, FarScale> s{sm, row, ring, rank, ranks, j0, j1, p.chunk > 65536 / kSampleWarps, far};
-        Sampler<TYPE, FarScale>::draw_far(s, p, b, best, most, top_k, top_p, min_p);
+        const Sampler<TYPE, HELD, FarScale> s{sm, row, stages, rank, ranks, j0, j1, p.chunk > 65536 / kSampleWarps, far};
+        Sampler<TYPE, HELD, FarScale>::draw_far(s, p, b, best, most, top_k, top_p, min_p);
     }
 }
+
+template <int TYPE>
+const void* sample_kernel_of(bool held) { return held ? (const void*)sample_kernel<TYPE, true> : (const void*)sample_kernel<TYPE, false>; }
 
 }  // namespace
 }  // namespace nvfp4
@@ -1021,15 +1053,21 @@ extern "C" nvfp4_status nvfp4_sample(const void* logits, int64_t row_stride, int
     if (overlaps(t, lp)) return fail(NVFP4_ERR_INVALID_ARG, "%s: logprobs overlap tokens", fn);
     if (!device_status_ptr()) return fail(NVFP4_ERR_CUDA, "%s: no CUDA device", fn);
     // Blocks of a row: enough of them for every SM, none with less than 4096 logits, or more than 65536
-    // where that can be.
+    // where that can be; more, where each block's part then stays in shared memory: it is read from memory once.
     const auto chunk = [&](unsigned ranks) { return round_up(ceil_div(ceil_div(V + 7, ranks), kSampleWarps), 256); };
+    const auto bytes = [&](unsigned ranks) { return chunk(ranks) * kSampleWarps * size; };
     unsigned ranks = 1;
     while (ranks < kMaxCluster && ((B * ranks < sm_count() && V / (2 * ranks) >= 4096) || chunk(ranks) > 65536 / kSampleWarps)) ranks *= 2;
+    unsigned more = ranks;
+    while (more < kMaxCluster && bytes(more) > kHeldBytes) ++more;
+    const bool held = bytes(more) <= kHeldBytes;
+    if (held) ranks = more;
     SampleParams p{};
     p.logits = logits; p.stride = row_stride; p.u = u; p.how = *how; p.tokens = tokens; p.logprobs = logprobs;
     p.V = (int)V; p.chunk = (int)chunk(ranks);
-    const void* kernel = type == NVFP4_LOGITS_BF16 ? (const void*)sample_kernel<kTypeBf16>
-                       : type == NVFP4_LOGITS_F16 ? (const void*)sample_kernel<kTypeF16> : (const void*)sample_kernel<kTypeF32>;
+    const void* kernel = type == NVFP4_LOGITS_BF16 ? sample_kernel_of<kTypeBf16>(held)
+                       : type == NVFP4_LOGITS_F16 ? sample_kernel_of<kTypeF16>(held) : sample_kernel_of<kTypeF32>(held);
+    const size_t smem = held ? (size_t)bytes(ranks) : (size_t)kSampleWarps * kStages * 256 * size;
     void* args[] = {&p};
-    return launch_kernel(kernel, dim3((unsigned)(B * ranks)), dim3(kSampleThreads), type == NVFP4_LOGITS_F32 ? Row<kTypeF32>::kRingBytes : Row<kTypeBf16>::kRingBytes, ranks, args, (cudaStream_t)stream, fn);
+    return launch_kernel(kernel, dim3((unsigned)(B * ranks)), dim3(kSampleThreads), smem, ranks, args, (cudaStream_t)stream, fn);
 }
