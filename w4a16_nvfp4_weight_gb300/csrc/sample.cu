@@ -334,7 +334,8 @@ struct Cut {
 
 struct Shared {
     uint2 table[512];
-    uint32_t count[kBins], lo[kBins], hi[kBins];
+    uint32_t count[kBins];
+    alignas(8) uint32_t lo[kBins], hi[kBins];
     union {
         uint64_t pairs[kList];             // logits with their indices, of a row with few candidates
         uint32_t list[2][kList];           // values of a bin, as keys: of this block; of the whole row
@@ -423,28 +424,47 @@ __device__ __forceinline__ uint64_t block_below(uint64_t v, uint64_t (&sm)[kSamp
     return x + below;
 }
 
-// `size` (a power of two, at most 2 * kSampleThreads) values from the largest down, in place; up to
-// 64 by one warp, the others skip it.
+// n <= kList values from the largest down, in place, by the whole block.  Up to 256 by counting what goes before
+// each (100 values 0.4 us where exchanges took 2.7; 512 would take 5), more by exchanges; room for kList,
+// zeros are the least.
 template <class T>
-__device__ __forceinline__ void sort_down(T* v, int size) {
-    const int i = threadIdx.x;
-    const bool small = size <= 64;
-    if (!small || i < 32)
-        for (int k = 2; k <= size; k *= 2)
-            for (int s = k / 2; s > 0; s /= 2) {
-                if (i < size / 2) {
-                    const int a = 2 * i - (i & (s - 1)), b = a + s;
-                    const T x = v[a], y = v[b];
-                    if ((x < y) == ((a & k) == 0)) {
-                        v[a] = y;
-                        v[b] = x;
-                    }
+__device__ __forceinline__ void sort_down(T* v, int n) {
+    const int tid = threadIdx.x;
+    if (n <= kSampleThreads / 2) {
+        int each_log2 = 4;                                  // threads of a value: at most 16
+        while (kSampleThreads >> each_log2 < n) --each_log2;
+        const int i = tid >> each_log2, each = 1 << each_log2;
+        const T mine = i < n ? v[i] : T(0);
+        int before = 0;
+        for (int j = tid & (each - 1); j < n; j += each) {
+            const T x = v[j];
+            before += x > mine || (x == mine && j < i);
+        }
+        for (int o = each >> 1; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+        __syncthreads();
+        if (i < n && (tid & (each - 1)) == 0) v[before] = mine;
+        __syncthreads();
+        return;
+    }
+    const int size = n <= kSampleThreads ? kSampleThreads : kList;
+    for (int i = n + tid; i < size; i += kSampleThreads) v[i] = 0;
+    __syncthreads();
+    for (int k = 2; k <= size; k *= 2)
+        for (int s = k / 2; s > 0; s /= 2) {
+            const int a = 2 * tid - (tid & (s - 1)), b = a + s;
+            if (a < size) {
+                const T x = v[a], y = v[b];
+                if ((x < y) == ((a & k) == 0)) {
+                    v[a] = y;
+                    v[b] = x;
                 }
-                // A warp's pairs lie in 64 values of its own up to 32 apart.
-                if (small || (s <= 32 && (s > 1 || k < 64))) __syncwarp();
-                else __syncthreads();
             }
+            // A warp's pairs lie in 64 values of its own up to 32 apart.
+            if (s <= 32 && (s > 1 || k < 64)) __syncwarp();
+            else __syncthreads();
+        }
 }
+static_assert(kList == 2 * kSampleThreads, "a pair a thread");
 
 constexpr int kOwnBins = kBins / kSampleThreads;           // bins of a thread when they are summed
 
@@ -658,12 +678,8 @@ struct Sampler {
             for (uint32_t i = threadIdx.x; i < held[r]; i += kSampleThreads) sm.list[1][from + i] = remote_u32(&sm.list[0][i], r);
             from += held[r];
         }
-        uint32_t size = 2;
-        while (size < n) size *= 2;
-        for (uint32_t i = n + threadIdx.x; i < size; i += kSampleThreads) sm.list[1][i] = 0;      // below every key
         __syncthreads();
-        sort_down(sm.list[1], (int)size);
-        __syncthreads();
+        sort_down(sm.list[1], (int)n);
         // The value where the target is reached, then what lies above it.
         const uint32_t i = threadIdx.x * 2;
         const auto weight_of = [&](uint32_t k) { return scale.weight(key_value(k), sm.table).w; };
@@ -693,21 +709,27 @@ struct Sampler {
     // The row's logits up to the bin `last`, which the top_k largest are among, as the candidates of the
     // first block; false where they are more than it sorts.
     __device__ __forceinline__ bool collect(int last) {
+        uint64_t* mine = (uint64_t*)sm.lo;                  // lo and hi: this block's, before they go to the first one
+        static_assert(sizeof(sm.lo) + sizeof(sm.hi) == sizeof(sm.pairs), "as many");
         if (threadIdx.x == 0) sm.listed = 0;
         __syncthreads();
         each([&](float (&l)[8], float most, int j) {
             if (scale.bin(most) > last) return;             // bins rise as logits fall
             tidy(l);
-#pragma unroll 1
+#pragma unroll
             for (int i = 0; i < 8; ++i)
                 if (scale.bin(l[i]) <= last && scale.counts(l[i])) {
-                    atomicAdd(&sm.listed, 1u);
-                    const uint32_t at = remote_add(&sm.paired, 0, 1);
-                    if (at < kList) push_u64(&sm.pairs[at], 0, (uint64_t)order_key(l[i]) << 32 | (uint32_t)~(Row<TYPE>::index(j, i) - row.first));
+                    const uint32_t at = atomicAdd(&sm.listed, 1u);
+                    if (at < kList) mine[at] = (uint64_t)order_key(l[i]) << 32 | (uint32_t)~(Row<TYPE>::index(j, i) - row.first);
                 }
         });
         __syncthreads();
-        if (threadIdx.x < ranks) push_u32(&sm.few[rank], threadIdx.x, sm.listed);
+        const uint32_t m = sm.listed;
+        if (threadIdx.x < ranks) push_u32(&sm.few[rank], threadIdx.x, m);
+        if (threadIdx.x == 0) sm.found[0] = remote_add(&sm.paired, 0, m);
+        __syncthreads();
+        const uint32_t to = (uint32_t)sm.found[0];
+        for (uint32_t i = threadIdx.x; i < m && to + i < kList; i += kSampleThreads) push_u64(&sm.pairs[to + i], 0, mine[i]);
         cluster_sync();
         uint32_t n = 0;
         for (uint32_t r = 0; r < ranks; ++r) n += sm.few[r];
@@ -717,36 +739,19 @@ struct Sampler {
     __device__ __forceinline__ void draw_of_few(const SampleParams& p, int64_t b, float best, int top_k, float top_p, float min_p) {
         if (rank != 0) return;
         const uint32_t n = sm.paired;
-        uint32_t size = 2;
-        while (size < n) size *= 2;
-        const bool small = size <= 64;                      // one warp does it all
-        if (small && threadIdx.x >= 32) return;
-        const auto sync = [&] {
-            if (small) __syncwarp();
-            else __syncthreads();
-        };
-        const auto below = [&](uint64_t v, uint64_t* all) {
-            if (!small) return block_below(v, sm.scan[0], all);
-            const uint64_t x = warp_below(v, threadIdx.x);
-            *all = __shfl_sync(0xffffffffu, x + v, 31);
-            return x;
-        };
-        for (uint32_t i = n + threadIdx.x; i < size; i += small ? 32 : kSampleThreads) sm.pairs[i] = 0;
-        sync();
-        sort_down(sm.pairs, (int)size);
-        sync();
+        sort_down(sm.pairs, (int)n);
         const uint32_t i = threadIdx.x * 2;
         uint64_t w[2] = {0, 0}, all;
         float l[2] = {0.f, 0.f};
-        if (i < size) {
+        if (i < n) {
             l[0] = key_value((uint32_t)(sm.pairs[i] >> 32));
-            l[1] = key_value((uint32_t)(sm.pairs[i + 1] >> 32));
+            l[1] = i + 1 < n ? key_value((uint32_t)(sm.pairs[i + 1] >> 32)) : l[0];
             Weight x[2];
             scale.weights(l[0], l[1], sm.table, x[0], x[1]);
             for (uint32_t k = 0; k < 2; ++k) w[k] = i + k < min(n, (uint32_t)top_k) ? x[k].units() : 0;
         }
         if (top_p < 1.f) {
-            uint64_t m = below(w[0] + w[1], &all);
+            uint64_t m = block_below(w[0] + w[1], sm.scan[0], &all);
             const uint64_t target = max(part_of(top_p, all, true), (uint64_t)1);
             for (uint32_t k = 0; k < 2; ++k) {              // what begins at or behind the target is not kept
                 const uint64_t here = w[k];
@@ -755,20 +760,18 @@ struct Sampler {
             }
         }
         const uint64_t least = least_weight(min_p, best);
-        sync();
         for (uint32_t k = 0; k < 2; ++k)
-            if (i < size) {
+            if (i + k < n) {
                 if (w[k] < least && l[k] != best) w[k] = 0;
                 // By index: the largest first, and its complement in order.  Weights have 44 bits, indices 20.
                 sm.pairs[i + k] = (uint64_t)(0xfffffu & (uint32_t)sm.pairs[i + k]) << 44 | w[k];
             }
-        sync();
-        sort_down(sm.pairs, (int)size);
-        sync();
+        __syncthreads();
+        sort_down(sm.pairs, (int)n);
         constexpr uint64_t kWeightBits = (1ull << 44) - 1;
-        w[0] = i < size ? sm.pairs[i] & kWeightBits : 0;
-        w[1] = i < size ? sm.pairs[i + 1] & kWeightBits : 0;
-        uint64_t m = below(w[0] + w[1], &all);
+        w[0] = i < n ? sm.pairs[i] & kWeightBits : 0;
+        w[1] = i + 1 < n ? sm.pairs[i + 1] & kWeightBits : 0;
+        uint64_t m = block_below(w[0] + w[1], sm.scan[0], &all);
         const float u = p.u[b];
         const uint64_t target = u < 1.f ? part_of(u, all, false) : all - 1;
         for (uint32_t k = 0; k < 2; ++k) {
