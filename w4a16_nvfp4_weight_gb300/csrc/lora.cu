@@ -447,6 +447,7 @@ __device__ __forceinline__ void sum_splits(const LoraParams& p, const int32_t* o
 }
 
 constexpr int kUpStages = 3;
+constexpr int kFewBlocks = 5;              // of the up kernel of 16 rows, on an SM
 
 // One item's 64 rows of A x times B, and y, over a range of N: stages of 64 columns of B and y through a
 // ring in shared memory (with loads to registers a step ahead, 8192 rows, 4096 columns, rank 64: 75 us).
@@ -467,8 +468,7 @@ __global__ void __launch_bounds__(kLoraThreads, 3) lora_up_ring_kernel(const Lor
     uint8_t* sm_b = sm_y + kUpStages * kYBytes;             // [kUpStages][kStep][r]
     uint32_t* sm_hi = (uint32_t*)(sm_b + kUpStages * b_bytes);      // [kRows][pitch] halves of A x
     uint32_t* sm_lo = sm_hi + kRows * pitch;
-    pdl_wait_previous();
-    pdl_launch_dependents();
+    if (p.n == 0) pdl_wait_previous();                      // else the down kernel has, for all but its own sums
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
     int adapter, rows;
     if (!item.find(p, blockIdx.x, &adapter, &rows) || (adapter < 0 && !p.copy_rest)) return;
@@ -513,6 +513,8 @@ __global__ void __launch_bounds__(kLoraThreads, 3) lora_up_ring_kernel(const Lor
     };
 #pragma unroll
     for (int s = 0; s < kUpStages - 1; ++s) stage(n_begin + s * kStep, s);
+    pdl_wait_previous();
+    pdl_launch_dependents();
     if (steps) sum_splits<F16>(p, item.row, adapter, rows, kRows, pitch, sm_hi, sm_lo, sm_scale);
     __syncthreads();
     const uint32_t *hi0 = sm_hi + (row_warp * 32 + g) * pitch + q * KP, *lo0 = sm_lo + (row_warp * 32 + g) * pitch + q * KP;
@@ -612,9 +614,10 @@ __global__ void __launch_bounds__(kLoraThreads, 3) lora_up_ring_kernel(const Lor
 // One item's rows of A x times B, and y, over a range of N.  A warp takes MT * 16 rows and CU * 32 columns
 // of a step, whose y it asks for first; tile j of four holds columns 8 (c / 2) + 2 j + c % 2, so that a
 // lane's eight outputs of a row lie side by side.  A lane takes KP words of a row of B: four k for
-// each 16, or (KP = 4) eight for each 32.
+// each 16, or (KP = 4) eight for each 32.  The first step's y and B are asked for while the down kernel
+// still runs, each further one's a step ahead (64 rows of 28672 columns, rank 16: 17.8 us without).
 template <bool F16, int RW, int MT, int CU, int KP, bool VEC_B, bool VEC_Y>
-__global__ void __launch_bounds__(kLoraThreads) lora_up_kernel(const LoraParams p, const int cols_block) {
+__global__ void __launch_bounds__(kLoraThreads, MT == 1 ? kFewBlocks : 1) lora_up_kernel(const LoraParams p, const int cols_block) {
     constexpr int kRows = 16 * MT * RW, kColWarps = kLoraThreads / 32 / RW;
     extern __shared__ __align__(16) uint8_t sm_up[];
     __shared__ ItemRows<kRows> item;
@@ -622,17 +625,13 @@ __global__ void __launch_bounds__(kLoraThreads) lora_up_kernel(const LoraParams 
     const int pitch = p.rp / 2 + 4;                         // words of two values
     uint32_t* sm_hi = (uint32_t*)sm_up;                     // [kRows][pitch] halves of A x
     uint32_t* sm_lo = sm_hi + kRows * pitch;
-    pdl_wait_previous();
-    pdl_launch_dependents();
+    if (p.n == 0) pdl_wait_previous();                      // else the down kernel has, for all but its own sums
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
     int adapter, rows;
     if (!item.find(p, blockIdx.x, &adapter, &rows) || (adapter < 0 && !p.copy_rest)) return;
     const int64_t n_begin = (int64_t)blockIdx.y * cols_block, n_end = min(n_begin + cols_block, p.N);
     const int steps = adapter < 0 ? 0 : p.rp / (8 * KP);
-    if (steps) sum_splits<F16>(p, item.row, adapter, rows, kRows, pitch, sm_hi, sm_lo, sm_scale);
-    __syncthreads();
     const int row_warp = warp % RW, col_warp = warp / RW;
-    if (row_warp * MT * 16 >= rows) return;
     bool held[MT][2];
     const uint16_t* y[MT][2];
     uint16_t* out[MT][2];
@@ -648,11 +647,6 @@ __global__ void __launch_bounds__(kLoraThreads) lora_up_kernel(const LoraParams 
         }
     const uint16_t* b = p.b + (int64_t)max(adapter, 0) * p.N * p.r + q * 2 * KP;
     const uint32_t *hi0 = sm_hi + (row_warp * MT * 16 + g) * pitch + q * KP, *lo0 = sm_lo + (row_warp * MT * 16 + g) * pitch + q * KP;
-    float scale[MT][2];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) scale[m][h] = steps ? sm_scale[(row_warp * MT + m) * 16 + h * 8 + g] : 0.f;
     const int r = p.r, first = 8 * (g >> 1) + (g & 1);
     // y of the step at n0.  `whole`: all of its columns are there.
     const auto ask = [&](int64_t n0, bool whole, uint4 (&v)[CU][MT][2]) {
@@ -666,39 +660,62 @@ __global__ void __launch_bounds__(kLoraThreads) lora_up_kernel(const LoraParams 
                     if (held[m][h]) v[u][m][h] = eight<VEC_Y>(y[m][h] + n0 + u * 32, whole ? 8 : n_end - n0 - u * 32 - q * 8);
                 }
     };
+    // B of the step at n0, its k from `st` on.
+    const auto ask_b = [&](int64_t n0, bool whole, int st, uint32_t (&v)[CU][4][KP]) {
+        const uint16_t* bn = b + (n0 + first) * r + st * 8 * KP;
+        const int left = r - st * 8 * KP - q * 2 * KP;
+        if (whole) {
+#pragma unroll
+            for (int u = 0; u < CU; ++u)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) part<KP, VEC_B>(bn + (u * 32 + 2 * j) * r, left, v[u][j]);
+        } else {
+#pragma unroll
+            for (int u = 0; u < CU; ++u)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) part<KP, VEC_B>(bn + (u * 32 + 2 * j) * r, n0 + first + u * 32 + 2 * j < n_end ? left : 0, v[u][j]);
+        }
+    };
     constexpr int kStep = 32 * CU;
     uint4 next[CU][MT][2];
+    uint32_t b_next[CU][4][KP];                             // a step's first k, asked for with its y
     int64_t n0 = n_begin + col_warp * kStep;
-    if (n0 < n_end) ask(n0, n0 + kStep <= n_end, next);
+    if (n0 < n_end) {
+        ask(n0, n0 + kStep <= n_end, next);
+        if (steps) ask_b(n0, n0 + kStep <= n_end, 0, b_next);
+    }
+    pdl_wait_previous();
+    pdl_launch_dependents();
+    if (steps) sum_splits<F16>(p, item.row, adapter, rows, kRows, pitch, sm_hi, sm_lo, sm_scale);
+    __syncthreads();
+    float scale[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) scale[m][h] = steps ? sm_scale[(row_warp * MT + m) * 16 + h * 8 + g] : 0.f;
     for (; n0 < n_end; n0 += kColWarps * kStep) {
         const bool whole = n0 + kStep <= n_end;
         uint4 now[CU][MT][2];
+        uint32_t bv[CU][4][KP];
 #pragma unroll
-        for (int u = 0; u < CU; ++u)
+        for (int u = 0; u < CU; ++u) {
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) now[u][m][h] = next[u][m][h];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int k = 0; k < KP; ++k) bv[u][j][k] = b_next[u][j][k];
+        }
         const int64_t n1 = n0 + kColWarps * kStep;
-        if (n1 < n_end) ask(n1, n1 + kStep <= n_end, next);
+        if (n1 < n_end) {
+            ask(n1, n1 + kStep <= n_end, next);
+            if (steps) ask_b(n1, n1 + kStep <= n_end, 0, b_next);
+        }
         float acc[CU][MT][4][4] = {};
-        const uint16_t* bn = b + (n0 + first) * r;
-#pragma unroll 2
         for (int st = 0; st < steps; ++st) {
-            uint32_t bv[CU][4][KP];
-            const int left = r - st * 8 * KP - q * 2 * KP;
-            if (whole) {
-#pragma unroll
-                for (int u = 0; u < CU; ++u)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) part<KP, VEC_B>(bn + (u * 32 + 2 * j) * r + st * 8 * KP, left, bv[u][j]);
-            } else {
-#pragma unroll
-                for (int u = 0; u < CU; ++u)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        part<KP, VEC_B>(bn + (u * 32 + 2 * j) * r + st * 8 * KP, n0 + first + u * 32 + 2 * j < n_end ? left : 0, bv[u][j]);
-            }
+            if (st) ask_b(n0, whole, st, bv);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 const int at = m * 16 * pitch + st * 4 * KP, at8 = at + 8 * pitch;
@@ -894,12 +911,12 @@ extern "C" nvfp4_status nvfp4_lora_add(const void* y, int64_t y_stride, const vo
     if (up_ring) {
         kernel = f16 ? up_ring_kernel<true>(r) : up_ring_kernel<false>(r);
     } else {
-        kernel = pl.rows_item == 16 ? (f16 ? up_kernel<true, 1, 1, 2>(wide, vec_b, vec_y) : up_kernel<false, 1, 1, 2>(wide, vec_b, vec_y))
+        kernel = pl.rows_item == 16 ? (f16 ? up_kernel<true, 1, 1, 1>(wide, vec_b, vec_y) : up_kernel<false, 1, 1, 1>(wide, vec_b, vec_y))
                                     : (f16 ? up_kernel<true, 2, 2, 1>(wide, vec_b, vec_y) : up_kernel<false, 2, 2, 1>(wide, vec_b, vec_y));
     }
     // Columns of a block: as many steps of its warps as leave one wave of blocks (three an SM fit; of few rows
     // six), so that an item's sums over the splits are not read more often than that needs.
-    const int step = pl.rows_item == 16 ? 256 : 64;
+    const int step = pl.rows_item == 16 ? 128 : 64;
     const int64_t waves = (pl.rows_item == 16 ? 6 : 3) * (int64_t)sm_count();
     const int64_t blocks = std::min<int64_t>(std::max<int64_t>(1, waves / pl.items), 65535);        // of an item
     int cols_block = (int)round_up(ceil_div(N, blocks), step);
