@@ -341,6 +341,7 @@ struct Shared {
         uint32_t list[2][kList];           // values of a bin, as keys: of this block; of the whole row
     };
     uint32_t listed, paired, few[kMaxCluster];
+    uint32_t key_range[2];                 // least and largest key of a bin
     uint64_t scan[2][kSampleWarps];
     uint64_t found[4];
     float best[kMaxCluster];               // pushed here by every block of the row, as the next ones
@@ -611,40 +612,51 @@ struct Sampler {
         return r;
     }
 
-    // Counts, or sums of w, of one bin's logits whose keys begin with the `bits` bits `known`, by their next
-    // `take` bits, the largest first.
-    __device__ __forceinline__ void digits(int bin, uint32_t known, uint32_t bits, uint32_t take, bool by_mass, Bins& sum) {
+    // Keys of a type of 16 bits end in bits that go by the sign alone.
+    static constexpr int kDrop = TYPE == kTypeF32 ? 0 : TYPE == kTypeF16 ? 13 : 16;
+    __device__ __forceinline__ static uint32_t short_key(float l) { return order_key(l) >> kDrop; }
+    __device__ __forceinline__ static float short_value(uint32_t k) {
+        const uint32_t key = k << kDrop;
+        return key_value(key & 0x80000000u ? key : key | ((1u << kDrop) - 1));
+    }
+    // Counts, or sums of w, of one bin's logits by their keys' distance below `top`, up to `range`, in steps
+    // of 2^shift.
+    __device__ __forceinline__ void digits(int bin, uint32_t top, uint32_t range, int shift, bool by_mass, Bins& sum) {
         clear();
         each([&](float (&l)[8], float most, int) {
             if (scale.bin(most) > bin) return;
             tidy(l);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const uint32_t k = order_key(l[i]);
-                if (!scale.counts(l[i]) || scale.bin(l[i]) != bin || (bits && k >> (32 - bits) != known)) continue;
-                const int d = (int)((1u << take) - 1 - ((k >> (32 - bits - take)) & ((1u << take) - 1)));
-                if (by_mass) add(d, scale.weight(l[i], sm.table).w);
-                else atomicAdd(&sm.count[d], 1u);
+                const uint32_t d = top - short_key(l[i]);
+                if (!scale.counts(l[i]) || scale.bin(l[i]) != bin || d > range) continue;
+                if (by_mass) add((int)(d >> shift), scale.weight(l[i], sm.table).w);
+                else atomicAdd(&sm.count[d >> shift], 1u);
             }
         });
         cluster_sync();
         if (by_mass) read_sums(sum);
         else read(sm.count, sum);
     }
-    // The cut in a bin of more values than are sorted: key bits, 10, 10, 10 and 2 of them.
-    __device__ __noinline__ static Cut cut_by_digits(Sampler s, int bin, bool by_mass, uint64_t want) {
-        uint32_t known = 0;
-        for (uint32_t bits = 0; bits < 32;) {
-            const uint32_t take = min(32 - bits, 10u);
+    // The cut in a bin of more values than are sorted, their keys within `range` below `top`: 1024 parts of
+    // that, then of one part; one round does for logits of 16 bits.
+    __device__ __noinline__ static Cut cut_by_digits(Sampler s, int bin, uint32_t top, uint32_t range, bool by_mass, uint64_t want) {
+        for (int shift = 32;;) {
+            shift = min(shift, range < kBins ? 0 : 22 - __clz(range));       // shorter every round: it ends
             Bins sum;
             uint64_t all;
-            s.digits(bin, known, bits, take, by_mass, sum);
+            s.digits(bin, top, range, shift, by_mass, sum);
             const Reached r = s.reach(sum, want, &all);
+            if (r.bin < 0) return ended(s, top, by_mass, want);             // never: the bin holds what is wanted
             want -= r.before;
-            known = (known << take) | ((1u << take) - 1 - (uint32_t)r.bin);
-            bits += take;
+            top -= (uint32_t)r.bin << shift;
+            range = min(range - ((uint32_t)r.bin << shift), (1u << shift) - 1);
+            if (shift == 0) return ended(s, top, by_mass, want);
         }
-        const float value = key_value(known);
+    }
+    // All that is left has this key.
+    __device__ __forceinline__ static Cut ended(const Sampler& s, uint32_t key, bool by_mass, uint64_t want) {
+        const float value = short_value(key);
         const uint32_t each = by_mass ? s.scale.weight(value, s.sm.table).w : 1;
         return Cut{value, (uint32_t)((want + each - 1) / each)};
     }
@@ -653,25 +665,49 @@ struct Sampler {
     // down reaches `want`.
     __device__ __noinline__ static Cut cut_in(Sampler s, int bin, bool by_mass, uint64_t want) { return s.cut(bin, by_mass, want); }
     __device__ __forceinline__ Cut cut(int bin, bool by_mass, uint64_t want) {
-        if (threadIdx.x == 0) sm.listed = 0;
+        if (threadIdx.x == 0) {
+            sm.listed = 0;
+            sm.key_range[0] = ~0u;
+            sm.key_range[1] = 0;
+        }
         __syncthreads();
+        uint32_t least = ~0u, top = 0;
         each([&](float (&l)[8], float most, int) {
             if (scale.bin(most) > bin) return;              // bins rise as logits fall
             tidy(l);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 if (scale.bin(l[i]) != bin || !scale.counts(l[i])) continue;
-                const uint32_t at = atomicAdd(&sm.listed, 1u);
+                const uint32_t at = atomicAdd(&sm.listed, 1u), k = short_key(l[i]);
+                least = min(least, k);
+                top = max(top, k);
                 if (at < kList) sm.list[0][at] = order_key(l[i]);
             }
         });
+        least = __reduce_min_sync(0xffffffffu, least);
+        top = __reduce_max_sync(0xffffffffu, top);
+        if ((threadIdx.x & 31) == 0 && least <= top) {
+            atomicMin(&sm.key_range[0], least);
+            atomicMax(&sm.key_range[1], top);
+        }
         cluster_sync();
-        uint32_t held[kMaxCluster], n = 0;
+        uint32_t held[kMaxCluster], low[kMaxCluster], high[kMaxCluster], n = 0;
 #pragma unroll
-        for (uint32_t r = 0; r < kMaxCluster; ++r) held[r] = r < ranks ? remote_u32(&sm.listed, r) : 0;
+        for (uint32_t r = 0; r < kMaxCluster; ++r) {
+            held[r] = r < ranks ? remote_u32(&sm.listed, r) : 0;
+            low[r] = r < ranks ? remote_u32(&sm.key_range[0], r) : ~0u;
+            high[r] = r < ranks ? remote_u32(&sm.key_range[1], r) : 0;
+        }
+        least = ~0u;
+        top = 0;
 #pragma unroll
-        for (uint32_t r = 0; r < kMaxCluster; ++r) n += held[r];
-        if (n > kList) return cut_by_digits(*this, bin, by_mass, want);
+        for (uint32_t r = 0; r < kMaxCluster; ++r) {
+            n += held[r];
+            least = min(least, low[r]);
+            top = max(top, high[r]);
+        }
+        if (least == top) return ended(*this, top, by_mass, want);
+        if (n > kList) return cut_by_digits(*this, bin, top, top - least, by_mass, want);
         uint32_t from = 0;
 #pragma unroll
         for (uint32_t r = 0; r < kMaxCluster; ++r) {
@@ -893,17 +929,50 @@ struct Sampler {
         }
         // The warp that holds the running mass's passage goes through its values again.
         if (target < before || target >= before + with_ties(mass, seen, ties)) return;
-        constexpr int kPer = Row<TYPE>::kPer;
-        for (int at = j0; at < j1; at += 32 * kPer) {       // in index order: a piece a lane
-            const uint4 v[2] = {row.load(at + lane * kPer), make_uint4(0, 0, 0, 0)};
-            float l[8];
-            uint64_t w[kPer], m = 0;
-            uint32_t n = 0;
-            Row<TYPE>::widen(*(const uint4(*)[Row<TYPE>::kPieces])v, l);
+        // First the step of 256, then the lane and the element.
+        constexpr int kPer = Row<TYPE>::kPer, kPieces = Row<TYPE>::kPieces;
+        float l[8];
+        uint64_t w[8];
+        int at = j0;
+        for (int step = 0; at < j1; at += 256, ++step) {
+            if (HELD) {
+                Row<TYPE>::fetch(stages, step, l);
+            } else {
+                uint4 v[kPieces];
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                l[i] = scale.tidy(l[i]);
-                w[i] = l[i] > cut.value ? kept_weight(l[i]) : 0;
+                for (int k = 0; k < kPieces; ++k) v[k] = row.load(Row<TYPE>::index(at, k * kPer));
+                Row<TYPE>::widen(v, l);
+            }
+            tidy(l);
+            uint64_t m = 0;
+            uint32_t n = 0;
+            if (__any_sync(0xffffffffu, Row<TYPE>::largest(l) >= cut.value)) {
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    Weight x[2];
+                    scale.weights(l[i], l[i + 1], sm.table, x[0], x[1]);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        w[i + k] = l[i + k] > cut.value ? kept(l[i + k], x[k].units()) : 0;
+                        m += w[i + k];
+                        n += l[i + k] == cut.value;
+                    }
+                }
+                m = warp_sum(m);
+                n = warp_sum(n);
+            }
+            const uint64_t here = with_ties(m, seen, n);
+            if (target < before + here) break;
+            before += here;
+            seen += n;
+        }
+        if (at >= j1) return;                               // never: the warp's mass reaches the target
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {
+            uint64_t m = 0;
+            uint32_t n = 0;
+#pragma unroll
+            for (int i = k * kPer; i < (k + 1) * kPer; ++i) {
                 m += w[i];
                 n += l[i] == cut.value;
             }
@@ -912,10 +981,10 @@ struct Sampler {
             uint64_t sum = before + warp_below(mine, lane);
             if (target >= sum && target < sum + mine) {
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) {
+                for (int i = k * kPer; i < (k + 1) * kPer; ++i) {
                     const uint64_t here = l[i] == cut.value ? (tie++ < cut.ties ? tie_weight : 0) : w[i];
                     if (target >= sum && target < sum + here) {
-                        p.tokens[b] = at + lane * kPer + i - row.first;
+                        p.tokens[b] = Row<TYPE>::index(at, i) - row.first;
                         if (p.logprobs) p.logprobs[b] = log_share(l[i], here, whole);
                     }
                     sum += here;
