@@ -386,12 +386,13 @@ __device__ __forceinline__ void part(const uint16_t* p, int left, uint32_t (&w)[
     }
 }
 
-// A x of an item's rows, the splits' sums in order, as two 16-bit halves in shared memory: four rows a warp at
-// a time, eight lanes each.  FP16 holds them times the power of two that puts a row's largest below 2,
-// which the end takes back.
+// s A x of an item's rows, the splits' sums in order, as two 16-bit halves in shared memory: four rows a warp at
+// a time, eight lanes each.  FP16 holds them divided by a power of two (`sm_up`) that puts a row's largest
+// below 2: the products are added to y over that, and the end takes it back.  BF16 needs none.
 template <bool F16>
 __device__ __forceinline__ void sum_splits(const LoraParams& p, const int32_t* order, int adapter, int rows, int all, int pitch, uint32_t* sm_hi,
-                                           uint32_t* sm_lo, float* sm_scale) {
+                                           uint32_t* sm_lo, float* sm_up) {
+    const float s = p.scales ? p.scales[adapter] : 1.f;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int row = warp * 4 + (lane >> 3); row < all; row += kLoraThreads / 8) {
         const bool held = row < rows;
@@ -410,7 +411,7 @@ __device__ __forceinline__ void sum_splits(const LoraParams& p, const int32_t* o
                     v.w += u.w;
                 }
             }
-            return v;
+            return make_float4(v.x * s, v.y * s, v.z * s, v.w * s);
         };
         float down = 1.f, up = 1.f;
         if (F16) {
@@ -428,7 +429,7 @@ __device__ __forceinline__ void sum_splits(const LoraParams& p, const int32_t* o
                 down = __uint_as_float(0x7f000000u - e);            // 2^-exponent
             }
         }
-        if ((lane & 7) == 0) sm_scale[row] = up * (p.scales ? p.scales[adapter] : 1.f);
+        if (F16 && (lane & 7) == 0) sm_up[row] = up;
         const auto halves = [&](float a, float b, uint32_t* hi, uint32_t* lo) {
             *hi = f32_to_act2<F16>(a, b);
             const float2 back = act2_to_f32<F16>(*hi);
@@ -461,7 +462,7 @@ __global__ void __launch_bounds__(kLoraThreads, 3) lora_up_ring_kernel(const Lor
     constexpr bool kHeld = KS <= 4;
     extern __shared__ __align__(128) uint8_t sm_up[];
     __shared__ ItemRows<kRows> item;
-    __shared__ float sm_scale[kRows];
+    __shared__ float sm_power[kRows];
     const int pitch = p.rp / 2 + 4;                         // words of two values
     const int b_bytes = kStep * p.r * 2;
     uint8_t* sm_y = sm_up;                                  // [kUpStages][kLoraThreads][4] pieces of 16 bytes
@@ -515,7 +516,7 @@ __global__ void __launch_bounds__(kLoraThreads, 3) lora_up_ring_kernel(const Lor
     for (int s = 0; s < kUpStages - 1; ++s) stage(n_begin + s * kStep, s);
     pdl_wait_previous();
     pdl_launch_dependents();
-    if (steps) sum_splits<F16>(p, item.row, adapter, rows, kRows, pitch, sm_hi, sm_lo, sm_scale);
+    if (steps) sum_splits<F16>(p, item.row, adapter, rows, kRows, pitch, sm_hi, sm_lo, sm_power);
     __syncthreads();
     const uint32_t *hi0 = sm_hi + (row_warp * 32 + g) * pitch + q * KP, *lo0 = sm_lo + (row_warp * 32 + g) * pitch + q * KP;
     // Halves of A x of a lane's rows: words w and w + 1 of step st are the k of one product.
@@ -540,11 +541,15 @@ __global__ void __launch_bounds__(kLoraThreads, 3) lora_up_ring_kernel(const Lor
                 low_words(hi0, m, st, kept[0][m][st][0], kept[0][m][st][1]);
                 low_words(lo0, m, st, kept[1][m][st][0], kept[1][m][st][1]);
             }
-    float scale[2][2];
+    float up[2][2], down[2][2];                             // FP16: of sum_splits, and its reciprocal
+    if (F16)
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) scale[m][h] = steps ? sm_scale[(row_warp * 2 + m) * 16 + h * 8 + g] : 0.f;
+            for (int h = 0; h < 2; ++h) {
+                up[m][h] = steps ? sm_power[(row_warp * 2 + m) * 16 + h * 8 + g] : 1.f;
+                down[m][h] = __uint_as_float(0x7f000000u - __float_as_uint(up[m][h]));
+            }
     const int first = col_warp * 32 + 8 * (g >> 1) + (g & 1), odd = (g & 1) * turn * 16;     // of a row's pieces: 64 bytes on, or back
     int s = 0;
     for (int64_t n0 = n_begin; n0 < n_end; n0 += kStep) {
@@ -552,7 +557,22 @@ __global__ void __launch_bounds__(kLoraThreads, 3) lora_up_ring_kernel(const Lor
         __syncthreads();                                    // this stage is there, and the last one is read
         stage(n0 + (kUpStages - 1) * kStep, (s + kUpStages - 1) % kUpStages);
         const uint8_t* bs = sm_b + s * b_bytes + first * p.r * 2;
-        float acc[2][4][4] = {};
+        // The products are added to y.
+        float acc[2][4][4];
+        uint4 yv[2][2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                yv[m][h] = *(const uint4*)(sm_y + s * kYBytes + ((m * 2 + h) * kLoraThreads + tid) * 16);
+                const uint32_t w[4] = {yv[m][h].x, yv[m][h].y, yv[m][h].z, yv[m][h].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 u = act2_to_f32<F16>(w[j]);
+                    acc[m][j][2 * h] = F16 ? u.x * down[m][h] : u.x;
+                    acc[m][j][2 * h + 1] = F16 ? u.y * down[m][h] : u.y;
+                }
+            }
         const auto products = [&](int st, const auto& words) {
             const bool in = EXACT || st * 8 * KP + q * 2 * KP < p.r;
             const int at_b = (st * 8 * KP + q * 2 * KP) * 2 ^ odd;
@@ -596,14 +616,12 @@ __global__ void __launch_bounds__(kLoraThreads, 3) lora_up_ring_kernel(const Lor
             for (int i = 0; i < 4; ++i) {
                 const int m = i >> 1, h = i & 1;
                 if (!held[m][h]) continue;
-                const uint4 v = *(const uint4*)(sm_y + s * kYBytes + (i * kLoraThreads + tid) * 16);
-                uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                uint32_t w[4] = {yv[m][h].x, yv[m][h].y, yv[m][h].z, yv[m][h].w};      // without an adapter: as it is
                 if (steps)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 u = act2_to_f32<F16>(w[j]);
-                        w[j] = f32_to_act2<F16>(fmaf(scale[m][h], acc[m][j][2 * h], u.x), fmaf(scale[m][h], acc[m][j][2 * h + 1], u.y));
-                    }
+                    for (int j = 0; j < 4; ++j)
+                        w[j] = F16 ? f32_to_act2<F16>(acc[m][j][2 * h] * up[m][h], acc[m][j][2 * h + 1] * up[m][h])
+                                   : f32_to_act2<F16>(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
                 *(uint4*)(out[m][h] + n0) = make_uint4(w[0], w[1], w[2], w[3]);
             }
         s = (s + 1) % kUpStages;
@@ -621,7 +639,7 @@ __global__ void __launch_bounds__(kLoraThreads, MT == 1 ? kFewBlocks : 1) lora_u
     constexpr int kRows = 16 * MT * RW, kColWarps = kLoraThreads / 32 / RW;
     extern __shared__ __align__(16) uint8_t sm_up[];
     __shared__ ItemRows<kRows> item;
-    __shared__ float sm_scale[kRows];
+    __shared__ float sm_power[kRows];
     const int pitch = p.rp / 2 + 4;                         // words of two values
     uint32_t* sm_hi = (uint32_t*)sm_up;                     // [kRows][pitch] halves of A x
     uint32_t* sm_lo = sm_hi + kRows * pitch;
@@ -686,13 +704,17 @@ __global__ void __launch_bounds__(kLoraThreads, MT == 1 ? kFewBlocks : 1) lora_u
     }
     pdl_wait_previous();
     pdl_launch_dependents();
-    if (steps) sum_splits<F16>(p, item.row, adapter, rows, kRows, pitch, sm_hi, sm_lo, sm_scale);
+    if (steps) sum_splits<F16>(p, item.row, adapter, rows, kRows, pitch, sm_hi, sm_lo, sm_power);
     __syncthreads();
-    float scale[MT][2];
+    float up[MT][2], down[MT][2];                           // FP16: of sum_splits, and its reciprocal
+    if (F16)
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) scale[m][h] = steps ? sm_scale[(row_warp * MT + m) * 16 + h * 8 + g] : 0.f;
+            for (int h = 0; h < 2; ++h) {
+                up[m][h] = steps ? sm_power[(row_warp * MT + m) * 16 + h * 8 + g] : 1.f;
+                down[m][h] = __uint_as_float(0x7f000000u - __float_as_uint(up[m][h]));
+            }
     for (; n0 < n_end; n0 += kColWarps * kStep) {
         const bool whole = n0 + kStep <= n_end;
         uint4 now[CU][MT][2];
@@ -713,7 +735,21 @@ __global__ void __launch_bounds__(kLoraThreads, MT == 1 ? kFewBlocks : 1) lora_u
             ask(n1, n1 + kStep <= n_end, next);
             if (steps) ask_b(n1, n1 + kStep <= n_end, 0, b_next);
         }
-        float acc[CU][MT][4][4] = {};
+        float acc[CU][MT][4][4];                            // the products are added to y
+#pragma unroll
+        for (int u = 0; u < CU; ++u)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t w[4] = {now[u][m][h].x, now[u][m][h].y, now[u][m][h].z, now[u][m][h].w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 v = act2_to_f32<F16>(w[j]);
+                        acc[u][m][j][2 * h] = F16 ? v.x * down[m][h] : v.x;
+                        acc[u][m][j][2 * h + 1] = F16 ? v.y * down[m][h] : v.y;
+                    }
+                }
         for (int st = 0; st < steps; ++st) {
             if (st) ask_b(n0, whole, st, bv);
 #pragma unroll
@@ -752,10 +788,9 @@ __global__ void __launch_bounds__(kLoraThreads, MT == 1 ? kFewBlocks : 1) lora_u
                     uint32_t w[4] = {now[u][m][h].x, now[u][m][h].y, now[u][m][h].z, now[u][m][h].w};
                     if (steps)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float2 v = act2_to_f32<F16>(w[j]);
-                            w[j] = f32_to_act2<F16>(fmaf(scale[m][h], acc[u][m][j][2 * h], v.x), fmaf(scale[m][h], acc[u][m][j][2 * h + 1], v.y));
-                        }
+                        for (int j = 0; j < 4; ++j)
+                            w[j] = F16 ? f32_to_act2<F16>(acc[u][m][j][2 * h] * up[m][h], acc[u][m][j][2 * h + 1] * up[m][h])
+                                       : f32_to_act2<F16>(acc[u][m][j][2 * h], acc[u][m][j][2 * h + 1]);
                     uint16_t* to = out[m][h] + n0 + u * 32;
                     if (VEC_Y) {
                         *(uint4*)to = make_uint4(w[0], w[1], w[2], w[3]);
