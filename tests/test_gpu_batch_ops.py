@@ -451,6 +451,19 @@ def test_sample_settings_of_each_row(B, V, act):
                  r.choice([1.0, 0.3, 0.9, 0.97], B), r.choice([0.0, 0.0, 0.03, 0.2], B))
 
 
+@pytest.mark.parametrize("B,V,act", [(2, 1 << 20, "bf16"), (1, 1 << 20, "f32"), (2, 400003, "f32"), (1, 300001, "f16"), (160, 70001, "f32")])
+def test_sample_large_rows(B, V, act):
+    """Rows that do not stay in shared memory, blocks of more than 2^16 logits, many rows of several blocks."""
+    for i, (kind, how) in enumerate([("flat", dict(top_p=0.9)), ("normal", dict(top_k=3000, top_p=0.5)), ("ties", dict(top_p=0.7)),
+                                     ("peaked", dict(top_k=50, top_p=0.9)), ("flat", dict()), ("flat", dict(top_k=V // 2))]):
+        _check_draws(_logits(B, V, kind, act, i)[:3 if B > 3 else B], torch.rand(min(B, 3), generator=_gen(i), device="cuda"), **how)
+        if B > 3:
+            l, u = _logits(B, V, kind, act, i), torch.rand(B, generator=_gen(i), device="cuda")
+            many = nv.sample(l, u, **how)
+            _check_draws(l[B - 2:], u[B - 2:], **how)
+            assert torch.equal(many[B - 2:], nv.sample(l[B - 2:], u[B - 2:], **how))
+
+
 def test_sample_ends_of_the_random_numbers():
     l = _logits(6, 3001, "peaked", "bf16", 1)
     l[:, 0] = float("-inf")
@@ -570,6 +583,34 @@ def test_sample_frequencies():
     l = torch.log(torch.tensor([0.1, 0.4, 0.2, 0.3], device="cuda")).expand(2000, 4)
     u = (torch.arange(2000, device="cuda") + 0.5) / 2000
     assert torch.bincount(nv.sample(l, u)).tolist() == [200, 800, 400, 600]
+
+
+def test_calls_on_two_streams_at_once():
+    """The same calls on two streams, whose kernels may run side by side, give what one stream gives."""
+    l = _logits(20, 50001, "normal", "bf16", 3)
+    u = torch.rand(20, generator=_gen(3), device="cuda")
+    y, x, a, b, ids, s = _lora_case(300, 512, 264, 24, 5, "bf16", 8)
+    r = np.random.default_rng(2)
+    lengths, new = r.integers(0, 60, 300), r.integers(0, 9, 300)
+    table, stack = _pool(r, lengths, 8, 12, 400)
+    args = [_i32(v) for v in (lengths, new, table, stack, [400])]
+
+    def all_of_it():
+        t = nv.extend_tables(args[0], args[1], args[2].clone(), args[3], args[4], 8, 3000, row_tables=True)
+        return [nv.sample(l, u, 0.9, 0, 0.9), nv.sample(l, u, 0.9, 40), nv.lora_add(y, x, a, b, ids, scales=s), t["slots"], t["row_tables"]]
+
+    want = all_of_it()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(20):
+        for k, stream in enumerate(streams):
+            with torch.cuda.stream(stream):
+                got[k].append(all_of_it())
+    torch.cuda.synchronize()
+    for outs in got:
+        for out in outs:
+            assert all(torch.equal(p, q) for p, q in zip(out, want))
 
 
 def test_a_batch_step_runs_together():

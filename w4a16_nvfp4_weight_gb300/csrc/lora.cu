@@ -3,14 +3,16 @@
 // x, y, A and B are 16-bit; A x and its sums are held in 32 bits and meet B as two 16-bit halves
 // (2^-16 of a value for BF16, 2^-21 for FP16 or better), so the output is rounded once.
 //
-// Three launches.  Rows are grouped by adapter into items of up to 16 or 64 rows of one
-// adapter (rows of a request need not lie side by side).  The down kernel multiplies
-// an item's rows with A, the long axis K split over blocks and warps; the up kernel adds
-// the splits' sums in their order (no atomics: the same bits every time), multiplies with
-// B and adds y.  Both products are mma.sync m16n8k16: at rank r they do r flop for each
-// byte of x or y that they read or write, far below what would need tcgen05, and the
-// operands go straight from memory to registers: an order of k that is the same for both operands
-// lets a thread load 16 bytes of each row, and an order of the columns 16 bytes of y.
+// Rows are grouped by adapter into items of up to 16 or 64 rows of one adapter (rows of a
+// request need not lie side by side): by every block for itself, or of more than 128 rows by
+// one block ahead.  The down kernels multiply an item's rows with A, the long axis K split
+// over blocks and warps; the up kernels add the splits' sums in their order (no atomics: the
+// same bits every time), multiply with B onto y.  Both products are mma.sync m16n8k16: at
+// rank r they do r flop for each byte of x or y that they read or write, far below what would
+// need tcgen05.  An order of k that is the same for both operands lets a lane load 16 bytes of each row, and
+// an order of the columns 16 bytes of y.
+// Few rows are bound by latency (1 x 4096 x 4096, rank 16, 4.9 us; 64 x 4096 x 28672 20.9, 2.0
+// TB/s), many by memory and the products (8192 x 4096 x 4096, rank 64, 65.5 us, 3.1 TB/s).
 #include <algorithm>
 
 #include "common.cuh"
@@ -633,7 +635,8 @@ __global__ void __launch_bounds__(kLoraThreads, 3) lora_up_ring_kernel(const Lor
 // of a step, whose y it asks for first; tile j of four holds columns 8 (c / 2) + 2 j + c % 2, so that a
 // lane's eight outputs of a row lie side by side.  A lane takes KP words of a row of B: four k for
 // each 16, or (KP = 4) eight for each 32.  The first step's y and B are asked for while the down kernel
-// still runs, each further one's a step ahead (64 rows of 28672 columns, rank 16: 17.8 us without).
+// still runs, each further one's a step ahead (64 rows of 4096 and 28672 columns,
+// rank 16: 22.8 us without, 20.9 with, for both kernels).
 template <bool F16, int RW, int MT, int CU, int KP, bool VEC_B, bool VEC_Y>
 __global__ void __launch_bounds__(kLoraThreads, MT == 1 ? kFewBlocks : 1) lora_up_kernel(const LoraParams p, const int cols_block) {
     constexpr int kRows = 16 * MT * RW, kColWarps = kLoraThreads / 32 / RW;

@@ -7,10 +7,22 @@
 // A draw is a comparison of sums of up to a few hundred thousand weights with a random
 // threshold: with 32-bit sums one draw in a hundred would fall on the wrong side of a
 // border, another one for another order of the sums.  So weights are whole numbers of
-// 2^-43 (of the largest weight), right to about 2^-32 of their value, and sums of them
-// are exact in 64 bits, in any order and by any block.  No sorting: a histogram over
-// the distance to the largest logit finds the bin in which top_k or top_p ends, and
-// only that bin's values are sorted.
+// 2^-43 (of the largest weight), right to about 2^-31 of their value, and sums of them
+// are exact in 64 bits, in any order and by any block.
+//
+// A cluster of one to eight blocks has a row, which stays in shared memory where it fits, so it is read
+// once.  No sort of the row:
+//  - top_k: each lane's largest logit is counted in a bin by its distance from the row's
+//    largest; the bin in which that count reaches top_k has the k-th largest logit in it or
+//    above, and the few logits from there up go to one block, which sorts and draws.
+//  - top_p: every weight is added to its bin's mass; the values of the one bin in which the
+//    running mass reaches top_p are sorted (or, where too many, divided by their keys).
+//  - the draw: masses of warps, of blocks and of the row; the warp whose part holds the
+//    target finds the step, the lane and the element.
+// Bound by latency for few rows (1 x 151936 with top_k and top_p 10.4 us: the load, four meetings
+// of the cluster, two sorts), by instructions for many: an exact weight takes about 30, a mass
+// two additions in shared memory (256 x 100003 logits of 32 bits by top_p 149 us, 0.7 TB/s;
+// by temperature alone 82, by top_k 67).
 #include <algorithm>
 
 #include "common.cuh"
@@ -32,7 +44,7 @@ constexpr int64_t kHeldBytes = 86 * 1024;  // of a block's logits that stay in s
 constexpr int kOneLog2 = 43;               // a weight of one is 2^43: 2^20 of them sum inside 63 bits
 constexpr int64_t kMaxVocabulary = 1 << 20;
 
-// 2^30 * 2^(j / 512), from the series of exp.
+// 2^30 * 2^(j / 512), from the series of exp: a step of the table leaves three terms for the rest.
 struct Exp2Table {
     uint32_t v[512];
     constexpr Exp2Table() : v() {

@@ -8,8 +8,9 @@
 // numbers throughout, so nothing depends on the order of anything.
 //
 // Bound by latency: a chain of loads (lengths, table or stack), two sums over the
-// block and a search, a few microseconds against bytes that take a tenth of one.  So
-// every block sums all requests for itself, and one launch does everything.
+// block and a search, against bytes that take a tenth of a microsecond (64 requests by a token 3.7
+// us, 16384 rows of 48 prompts 6.3, 1000 requests of which 600 end 4.5).  So every block sums all
+// requests for itself, and one launch does everything.
 #include <algorithm>
 
 #include "common.cuh"
@@ -54,7 +55,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sm, int64_t* t
 }
 
 // Pages of n tokens, 0 <= n < 2^31: by 32 bits, which n + page - 1 does not leave (64 took 13.9 us of
-// 64 requests' extension where this takes 4.1).
+// 64 requests' extension where this takes 3.7).
 __device__ __forceinline__ int pages_of(int n, int page) { return (int)((uint32_t)(n + (uint32_t)page - 1u) / (uint32_t)page); }
 
 struct ExtendParams {
