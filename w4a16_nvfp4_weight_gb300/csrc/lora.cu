@@ -452,14 +452,16 @@ __device__ __forceinline__ void sum_splits(const LoraParams& p, const int32_t* o
 constexpr int kUpStages = 3;
 constexpr int kFewBlocks = 5;              // of the up kernel of 16 rows, on an SM
 
-// One item's 64 rows of A x times B, and y, over a range of N: stages of 64 columns of B and y through a
-// ring in shared memory (with loads to registers a step ahead, 8192 rows, 4096 columns, rank 64: 75 us).
-// Two warps by two: 32 rows and 32 columns each.  Tile j of four holds columns 8 (c / 2) + 2 j + c % 2, so
-// that a lane's eight outputs of a row lie side by side: the 16 bytes of y that it copies itself.  KS: 16s
-// of the rank, or 8 for any number of them.  EXACT: it is a multiple of a step's k.
-template <bool F16, int KS, bool EXACT>
-__global__ void __launch_bounds__(kLoraThreads, 3) lora_up_ring_kernel(const LoraParams p, const int cols_block) {
-    constexpr int kRows = 64, kStep = 64, kYBytes = kRows * kStep * 2;
+// One item's rows of A x times B, and y, over a range of N: stages of columns of B and y through a ring in
+// shared memory (with loads to registers a step ahead, 8192 rows, 4096 columns, rank 64: 75 us for the
+// 43 here; 64 rows, 28672 columns, rank 16: 20.9 with the down kernel).  RW warps by 4 / RW: MT * 16 rows
+// and 32 columns each; items of 64 rows are two by two warps of 32, of 16 rows one by four.  Tile j of
+// four holds columns 8 (c / 2) + 2 j + c % 2, so that a lane's eight outputs of a row lie side by side: the
+// 16 bytes of y that it copies itself.  KS: 16s of the rank, or 8 for any number of them.  EXACT: it is
+// a multiple of a step's k.
+template <bool F16, int RW, int MT, int KS, bool EXACT>
+__global__ void __launch_bounds__(kLoraThreads, RW == 2 ? 3 : kFewBlocks) lora_up_ring_kernel(const LoraParams p, const int cols_block) {
+    constexpr int kRows = 16 * MT * RW, kStep = 32 * (kLoraThreads / 32 / RW), kYBytes = kLoraThreads * MT * 2 * 16;
     constexpr int KP = KS == 1 ? 2 : 4;
     constexpr bool kHeld = KS <= 4;
     extern __shared__ __align__(128) uint8_t sm_up[];
@@ -467,7 +469,7 @@ __global__ void __launch_bounds__(kLoraThreads, 3) lora_up_ring_kernel(const Lor
     __shared__ float sm_power[kRows];
     const int pitch = p.rp / 2 + 4;                         // words of two values
     const int b_bytes = kStep * p.r * 2;
-    uint8_t* sm_y = sm_up;                                  // [kUpStages][kLoraThreads][4] pieces of 16 bytes
+    uint8_t* sm_y = sm_up;                                  // [kUpStages][2 * MT][kLoraThreads] pieces of 16 bytes
     uint8_t* sm_b = sm_y + kUpStages * kYBytes;             // [kUpStages][kStep][r]
     uint32_t* sm_hi = (uint32_t*)(sm_b + kUpStages * b_bytes);      // [kRows][pitch] halves of A x
     uint32_t* sm_lo = sm_hi + kRows * pitch;
@@ -477,15 +479,15 @@ __global__ void __launch_bounds__(kLoraThreads, 3) lora_up_ring_kernel(const Lor
     if (!item.find(p, blockIdx.x, &adapter, &rows) || (adapter < 0 && !p.copy_rest)) return;
     const int64_t n_begin = (int64_t)blockIdx.y * cols_block, n_end = min(n_begin + cols_block, p.N);
     const int steps = adapter < 0 ? 0 : p.rp / (8 * KP);
-    const int row_warp = warp & 1, col_warp = warp >> 1;
-    bool held[2][2];
-    const uint16_t* y[2][2];
-    uint16_t* out[2][2];
+    const int row_warp = warp % RW, col_warp = warp / RW;
+    bool held[MT][2];
+    const uint16_t* y[MT][2];
+    uint16_t* out[MT][2];
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int row = (row_warp * 2 + m) * 16 + h * 8 + g;
+            const int row = (row_warp * MT + m) * 16 + h * 8 + g;
             held[m][h] = row < rows;
             const int64_t t = held[m][h] ? item.row[row] : 0;
             y[m][h] = p.y + t * p.y_stride + col_warp * 32 + q * 8;
@@ -499,7 +501,7 @@ __global__ void __launch_bounds__(kLoraThreads, 3) lora_up_ring_kernel(const Lor
         const int64_t left = n_end - n0;
         if (left > 0) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 2 * MT; ++i)
                 if (held[i >> 1][i & 1] && left > col_warp * 32 + q * 8)
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(y0 + s * kYBytes + i * kLoraThreads * 16),
                                  "l"(y[i >> 1][i & 1] + n0) : "memory");
@@ -520,7 +522,7 @@ __global__ void __launch_bounds__(kLoraThreads, 3) lora_up_ring_kernel(const Lor
     pdl_launch_dependents();
     if (steps) sum_splits<F16>(p, item.row, adapter, rows, kRows, pitch, sm_hi, sm_lo, sm_power);
     __syncthreads();
-    const uint32_t *hi0 = sm_hi + (row_warp * 32 + g) * pitch + q * KP, *lo0 = sm_lo + (row_warp * 32 + g) * pitch + q * KP;
+    const uint32_t *hi0 = sm_hi + (row_warp * MT * 16 + g) * pitch + q * KP, *lo0 = sm_lo + (row_warp * MT * 16 + g) * pitch + q * KP;
     // Halves of A x of a lane's rows: words w and w + 1 of step st are the k of one product.
     const auto low_words = [&](const uint32_t* from, int m, int st, uint32_t (&w0)[KP], uint32_t (&w1)[KP]) {
         const int at = m * 16 * pitch + st * 4 * KP, at8 = at + 8 * pitch;
@@ -534,22 +536,22 @@ __global__ void __launch_bounds__(kLoraThreads, 3) lora_up_ring_kernel(const Lor
     };
     // They are the same for all columns: up to rank 64 they stay in registers.
     constexpr int kHeldSteps = kHeld ? KS * 2 / KP : 1;
-    uint32_t kept[2][2][kHeldSteps][2][KP];                 // [half][m][step][row or row + 8]
+    uint32_t kept[2][MT][kHeldSteps][2][KP];                 // [half][m][step][row or row + 8]
     if (kHeld && steps)
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int st = 0; st < kHeldSteps; ++st) {
                 low_words(hi0, m, st, kept[0][m][st][0], kept[0][m][st][1]);
                 low_words(lo0, m, st, kept[1][m][st][0], kept[1][m][st][1]);
             }
-    float up[2][2], down[2][2];                             // FP16: of sum_splits, and its reciprocal
+    float up[MT][2], down[MT][2];                             // FP16: of sum_splits, and its reciprocal
     if (F16)
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                up[m][h] = steps ? sm_power[(row_warp * 2 + m) * 16 + h * 8 + g] : 1.f;
+                up[m][h] = steps ? sm_power[(row_warp * MT + m) * 16 + h * 8 + g] : 1.f;
                 down[m][h] = __uint_as_float(0x7f000000u - __float_as_uint(up[m][h]));
             }
     const int first = col_warp * 32 + 8 * (g >> 1) + (g & 1), odd = (g & 1) * turn * 16;     // of a row's pieces: 64 bytes on, or back
@@ -560,10 +562,10 @@ __global__ void __launch_bounds__(kLoraThreads, 3) lora_up_ring_kernel(const Lor
         stage(n0 + (kUpStages - 1) * kStep, (s + kUpStages - 1) % kUpStages);
         const uint8_t* bs = sm_b + s * b_bytes + first * p.r * 2;
         // The products are added to y.
-        float acc[2][4][4];
-        uint4 yv[2][2];
+        float acc[MT][4][4];
+        uint4 yv[MT][2];
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 yv[m][h] = *(const uint4*)(sm_y + s * kYBytes + ((m * 2 + h) * kLoraThreads + tid) * 16);
@@ -587,7 +589,7 @@ __global__ void __launch_bounds__(kLoraThreads, 3) lora_up_ring_kernel(const Lor
 #pragma unroll
             for (int half = 0; half < 2; ++half)
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
+                for (int m = 0; m < MT; ++m) {
                     uint32_t w0[KP], w1[KP];
                     words(half, m, w0, w1);
 #pragma unroll
@@ -615,7 +617,7 @@ __global__ void __launch_bounds__(kLoraThreads, 3) lora_up_ring_kernel(const Lor
         }
         if (n_end - n0 > col_warp * 32 + q * 8)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 2 * MT; ++i) {
                 const int m = i >> 1, h = i & 1;
                 if (!held[m][h]) continue;
                 uint32_t w[4] = {yv[m][h].x, yv[m][h].y, yv[m][h].z, yv[m][h].w};      // without an adapter: as it is
@@ -865,14 +867,16 @@ const void* up_kernel(bool wide, bool vec_b, bool vec_y) {
     return vec_y ? (const void*)lora_up_kernel<F16, RW, MT, CU, 2, true, true> : (const void*)lora_up_kernel<F16, RW, MT, CU, 2, true, false>;
 }
 
-template <bool F16, int KS>
-const void* up_ring_kernel_of(bool exact) { return exact ? (const void*)lora_up_ring_kernel<F16, KS, true> : (const void*)lora_up_ring_kernel<F16, KS, false>; }
-template <bool F16>
+template <bool F16, int RW, int KS>
+const void* up_ring_kernel_of(bool exact) {
+    return exact ? (const void*)lora_up_ring_kernel<F16, RW, RW, KS, true> : (const void*)lora_up_ring_kernel<F16, RW, RW, KS, false>;
+}
+template <bool F16, int RW>
 const void* up_ring_kernel(int64_t r) {
-    if (r <= 16) return up_ring_kernel_of<F16, 1>(r == 16);
-    if (r <= 32) return up_ring_kernel_of<F16, 2>(r == 32);
-    if (r <= 64) return up_ring_kernel_of<F16, 4>(r == 64);
-    return up_ring_kernel_of<F16, 8>(r % 32 == 0);
+    if (r <= 16) return up_ring_kernel_of<F16, RW, 1>(r == 16);
+    if (r <= 32) return up_ring_kernel_of<F16, RW, 2>(r == 32);
+    if (r <= 64) return up_ring_kernel_of<F16, RW, 4>(r == 64);
+    return up_ring_kernel_of<F16, RW, 8>(r % 32 == 0);
 }
 
 nvfp4_status check_sizes(const char* fn, int64_t T, int64_t n, int64_t r, int64_t K, int64_t N) {
@@ -943,23 +947,26 @@ extern "C" nvfp4_status nvfp4_lora_add(const void* y, int64_t y_stride, const vo
         const size_t smem = ring ? kRingStages * (64 + 8 * pl.nt) * 128 : 0;
         if (nvfp4_status st = launch_kernel(kernel, grid, dim3(kLoraThreads), smem, 1, args, s, fn)) return st;
     }
-    // The ring of a large rank does not leave room for two blocks an SM, so it goes up to 128 (rank 256: 147 KB).
-    const bool up_ring = pl.rows_item == 64 && vec_y && vec_b && r % 8 == 0 && r <= 128 && aligned(B, 16);
+    // Stages of 64 or 128 columns of B and y: as far as two blocks an SM have room for them (rank 256: 147 KB
+    // for 64 rows).
+    const int step = pl.rows_item == 16 ? 128 : 64;
+    const size_t halves = (size_t)pl.rows_item * (p.rp / 2 + 4) * 8, stage = (size_t)kLoraThreads * (pl.rows_item == 16 ? 32 : 64) + (size_t)step * 2 * r;
+    const bool up_ring = vec_y && vec_b && r % 8 == 0 && aligned(B, 16) && halves + kUpStages * stage <= 110 * 1024;
     const void* kernel;
     if (up_ring) {
-        kernel = f16 ? up_ring_kernel<true>(r) : up_ring_kernel<false>(r);
+        kernel = pl.rows_item == 16 ? (f16 ? up_ring_kernel<true, 1>(r) : up_ring_kernel<false, 1>(r))
+                                    : (f16 ? up_ring_kernel<true, 2>(r) : up_ring_kernel<false, 2>(r));
     } else {
         kernel = pl.rows_item == 16 ? (f16 ? up_kernel<true, 1, 1, 1>(wide, vec_b, vec_y) : up_kernel<false, 1, 1, 1>(wide, vec_b, vec_y))
                                     : (f16 ? up_kernel<true, 2, 2, 1>(wide, vec_b, vec_y) : up_kernel<false, 2, 2, 1>(wide, vec_b, vec_y));
     }
     // Columns of a block: as many steps of its warps as leave one wave of blocks (three an SM fit; of few rows
     // six), so that an item's sums over the splits are not read more often than that needs.
-    const int step = pl.rows_item == 16 ? 128 : 64;
     const int64_t waves = (pl.rows_item == 16 ? 6 : 3) * (int64_t)sm_count();
     const int64_t blocks = std::min<int64_t>(std::max<int64_t>(1, waves / pl.items), 65535);        // of an item
     int cols_block = (int)round_up(ceil_div(N, blocks), step);
     const int64_t cols = cols_block;
-    const size_t smem = (size_t)pl.rows_item * (p.rp / 2 + 4) * 8 + (up_ring ? (size_t)kUpStages * 64 * (128 + 2 * r) : 0);
+    const size_t smem = halves + (up_ring ? kUpStages * stage : 0);
     void* up_args[] = {&p, &cols_block};
     return launch_kernel(kernel, dim3((unsigned)pl.items, (unsigned)ceil_div(N, cols)), dim3(kLoraThreads), smem, 1, up_args, s, fn);
 }
