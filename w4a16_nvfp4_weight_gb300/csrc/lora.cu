@@ -11,7 +11,7 @@
 // rank r they do r flop for each byte of x or y that they read or write, far below what would
 // need tcgen05.  An order of k that is the same for both operands lets a lane load 16 bytes of each row, and
 // an order of the columns 16 bytes of y.
-// Few rows are bound by latency (1 x 4096 x 4096, rank 16, 4.9 us; 64 x 4096 x 28672 20.9, 2.0
+// Few rows are bound by latency (1 x 4096 x 4096, rank 16, 5.1 us; 64 x 4096 x 28672 16.7, 2.5
 // TB/s), many by memory and the products (8192 x 4096 x 4096, rank 64, 65.5 us, 3.1 TB/s).
 #include <algorithm>
 
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(1024) lora_group_kernel(const LoraParams p) {
 template <int ROWS>
 struct ItemRows {
     int32_t row[ROWS];
-    int32_t ids[kSelfRows];
+    alignas(16) int32_t ids[kSelfRows];
     int32_t warp_starts[kLoraThreads / 32];
     int32_t adapter, first;
 
@@ -167,7 +167,11 @@ struct ItemRows {
         if (tid == 0) first = -1;
         __syncthreads();
         int rank = 0;
-        for (int t = 0; t < (int)p.T; ++t) rank += t < tid && ids[t] == id;
+#pragma unroll 4
+        for (int t = 0; t < (int)p.T; t += 4) {             // what follows the last row is no adapter's
+            const int4 v = *(const int4*)(ids + t);
+            rank += (t < tid && v.x == id) + (t + 1 < tid && v.y == id) + (t + 2 < tid && v.z == id) + (t + 3 < tid && v.w == id);
+        }
         const bool starts = id >= (p.copy_rest ? -1 : 0) && rank % ROWS == 0;
         const uint32_t mine = __ballot_sync(0xffffffffu, starts);
         if ((tid & 31) == 0) warp_starts[tid >> 5] = __popc(mine);
@@ -454,7 +458,8 @@ constexpr int kFewBlocks = 5;              // of the up kernel of 16 rows, on an
 
 // One item's rows of A x times B, and y, over a range of N: stages of columns of B and y through a ring in
 // shared memory (with loads to registers a step ahead, 8192 rows, 4096 columns, rank 64: 75 us for the
-// 43 here; 64 rows, 28672 columns, rank 16: 20.9 with the down kernel).  RW warps by 4 / RW: MT * 16 rows
+// 43 here; 64 rows, 28672 columns, rank 16: 20.9 for the 16.7
+// here, with the down kernel).  RW warps by 4 / RW: MT * 16 rows
 // and 32 columns each; items of 64 rows are two by two warps of 32, of 16 rows one by four.  Tile j of
 // four holds columns 8 (c / 2) + 2 j + c % 2, so that a lane's eight outputs of a row lie side by side: the
 // 16 bytes of y that it copies itself.  KS: 16s of the rank, or 8 for any number of them.  EXACT: it is
@@ -568,7 +573,9 @@ __global__ void __launch_bounds__(kLoraThreads, RW == 2 ? 3 : kFewBlocks) lora_u
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                yv[m][h] = *(const uint4*)(sm_y + s * kYBytes + ((m * 2 + h) * kLoraThreads + tid) * 16);
+                yv[m][h] = make_uint4(0, 0, 0, 0);
+                if (MT > 1 || h * 8 < rows)                 // of few rows the second eight are often not there
+                    yv[m][h] = *(const uint4*)(sm_y + s * kYBytes + ((m * 2 + h) * kLoraThreads + tid) * 16);
                 const uint32_t w[4] = {yv[m][h].x, yv[m][h].y, yv[m][h].z, yv[m][h].w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -638,7 +645,8 @@ __global__ void __launch_bounds__(kLoraThreads, RW == 2 ? 3 : kFewBlocks) lora_u
 // lane's eight outputs of a row lie side by side.  A lane takes KP words of a row of B: four k for
 // each 16, or (KP = 4) eight for each 32.  The first step's y and B are asked for while the down kernel
 // still runs, each further one's a step ahead (64 rows of 4096 and 28672 columns,
-// rank 16: 22.8 us without, 20.9 with, for both kernels).
+// rank 16: 22.8 us without, 20.9 with, for both kernels).  For what the ring does not take: rows of B or y
+// off 16-byte boundaries, ranks that are no multiple of 8 or beyond its room.
 template <bool F16, int RW, int MT, int CU, int KP, bool VEC_B, bool VEC_Y>
 __global__ void __launch_bounds__(kLoraThreads, MT == 1 ? kFewBlocks : 1) lora_up_kernel(const LoraParams p, const int cols_block) {
     constexpr int kRows = 16 * MT * RW, kColWarps = kLoraThreads / 32 / RW;
@@ -960,9 +968,10 @@ extern "C" nvfp4_status nvfp4_lora_add(const void* y, int64_t y_stride, const vo
         kernel = pl.rows_item == 16 ? (f16 ? up_kernel<true, 1, 1, 1>(wide, vec_b, vec_y) : up_kernel<false, 1, 1, 1>(wide, vec_b, vec_y))
                                     : (f16 ? up_kernel<true, 2, 2, 1>(wide, vec_b, vec_y) : up_kernel<false, 2, 2, 1>(wide, vec_b, vec_y));
     }
-    // Columns of a block: as many steps of its warps as leave one wave of blocks (three an SM fit; of few rows
-    // six), so that an item's sums over the splits are not read more often than that needs.
-    const int64_t waves = (pl.rows_item == 16 ? 6 : 3) * (int64_t)sm_count();
+    // Columns of a block: as many steps of its warps as leave one wave of blocks, so that an item's sums over
+    // the splits are not read more often than that needs.  Three an SM fit of 64 rows; of few rows nine for each item
+    // that there may be, of which fewer are (64 x 4096 x 28672: 16.7 us, six 18.9, twelve 18.1).
+    const int64_t waves = (pl.rows_item == 16 ? 9 : 3) * (int64_t)sm_count();
     const int64_t blocks = std::min<int64_t>(std::max<int64_t>(1, waves / pl.items), 65535);        // of an item
     int cols_block = (int)round_up(ceil_div(N, blocks), step);
     const int64_t cols = cols_block;
