@@ -251,10 +251,9 @@ __global__ void __launch_bounds__(kLoraThreads) lora_down_kernel(const LoraParam
                 const uint32_t lo[4] = {xv[u][m][0].x, xv[u][m][1].x, xv[u][m][0].y, xv[u][m][1].y};
                 const uint32_t hi[4] = {xv[u][m][0].z, xv[u][m][1].z, xv[u][m][0].w, xv[u][m][1].w};
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    mma_16816<F16>(acc[m][j], lo, av[u][j].x, av[u][j].y);
-                    mma_16816<F16>(acc[m][j], hi, av[u][j].z, av[u][j].w);
-                }
+                for (int j = 0; j < NT; ++j) mma_16816<F16>(acc[m][j], lo, av[u][j].x, av[u][j].y);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) mma_16816<F16>(acc[m][j], hi, av[u][j].z, av[u][j].w);
             }
     }
 #pragma unroll
@@ -341,16 +340,21 @@ __global__ void __launch_bounds__(kLoraThreads) lora_down_ring_kernel(const Lora
         for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int h = 0; h < 2; ++h) xv[m][h] = *(const uint4*)(at + ((row_warp * 2 + m) * 16 + h * 8) * 128);
+        uint4 av[NT];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const uint4 av = *(const uint4*)(at + (kRows + j * 8) * 128);
+        for (int j = 0; j < NT; ++j) av[j] = *(const uint4*)(at + (kRows + j * 8) * 128);
+        // Both products of a sum are far apart: one waits for the other.
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const uint32_t lo[4] = {xv[m][0].x, xv[m][1].x, xv[m][0].y, xv[m][1].y};
-                const uint32_t hi[4] = {xv[m][0].z, xv[m][1].z, xv[m][0].w, xv[m][1].w};
-                mma_16816<F16>(acc[m][j], lo, av.x, av.y);
-                mma_16816<F16>(acc[m][j], hi, av.z, av.w);
-            }
+        for (int m = 0; m < 2; ++m) {
+            const uint32_t lo[4] = {xv[m][0].x, xv[m][1].x, xv[m][0].y, xv[m][1].y};
+#pragma unroll
+            for (int j = 0; j < NT; ++j) mma_16816<F16>(acc[m][j], lo, av[j].x, av[j].y);
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            const uint32_t hi[4] = {xv[m][0].z, xv[m][1].z, xv[m][0].w, xv[m][1].w};
+#pragma unroll
+            for (int j = 0; j < NT; ++j) mma_16816<F16>(acc[m][j], hi, av[j].z, av[j].w);
         }
         s = (s + 1) % kRingStages;
     }
@@ -594,18 +598,20 @@ __global__ void __launch_bounds__(kLoraThreads, RW == 2 ? 3 : kFewBlocks) lora_u
                 else *(uint2*)bv[j] = in ? *(const uint2*)(bs + 2 * j * p.r * 2 + at_b) : make_uint2(0, 0);
             }
 #pragma unroll
-            for (int half = 0; half < 2; ++half)
+            for (int half = 0; half < 2; ++half) {
+                uint32_t w0[MT][KP], w1[MT][KP];
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    uint32_t w0[KP], w1[KP];
-                    words(half, m, w0, w1);
+                for (int m = 0; m < MT; ++m) words(half, m, w0[m], w1[m]);
+                // Products of one sum as far apart as they go: one waits for the other.
 #pragma unroll
-                    for (int k = 0; k < KP; k += 2) {
-                        const uint32_t a[4] = {w0[k], w1[k], w0[k + 1], w1[k + 1]};
+                for (int k = 0; k < KP; k += 2)
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        const uint32_t a[4] = {w0[m][k], w1[m][k], w0[m][k + 1], w1[m][k + 1]};
 #pragma unroll
                         for (int j = 0; j < 4; ++j) mma_16816<F16>(acc[m][j], a, bv[j][k], bv[j][k + 1]);
                     }
-                }
+            }
         };
         if (kHeld) {
             if (steps)
