@@ -666,6 +666,34 @@ struct Sampler {
             if (shift == 0) return ended(s, top, by_mass, want);
         }
     }
+    // The same of the n keys in the row's list, by every block for itself: no other reads its histogram any more.
+    __device__ __forceinline__ Cut cut_of_list(uint32_t n, uint32_t top, uint32_t range, bool by_mass, uint64_t want) {
+        for (int shift = 32;;) {
+            shift = min(shift, range < kBins ? 0 : 22 - __clz(range));
+            for (int i = threadIdx.x; i < kBins; i += kSampleThreads) sm.count[i] = sm.lo[i] = sm.hi[i] = 0;
+            __syncthreads();
+            for (uint32_t i = threadIdx.x; i < n; i += kSampleThreads) {
+                const uint32_t k = sm.list[1][i], d = top - (k >> kDrop);
+                if (d > range) continue;
+                if (by_mass) add((int)(d >> shift), scale.weight(key_value(k), sm.table).w);
+                else atomicAdd(&sm.count[d >> shift], 1u);
+            }
+            __syncthreads();
+            Bins sum;
+#pragma unroll
+            for (int k = 0; k < kOwnBins; ++k) {
+                const int at = threadIdx.x * kOwnBins + k;
+                sum[k] = by_mass ? ((uint64_t)sm.hi[at] << (large ? 32 : 16)) + sm.lo[at] : sm.count[at];
+            }
+            uint64_t all;
+            const Reached r = reach(sum, want, &all);
+            if (r.bin < 0) return ended(*this, top, by_mass, want);         // never: the list holds what is wanted
+            want -= r.before;
+            top -= (uint32_t)r.bin << shift;
+            range = min(range - ((uint32_t)r.bin << shift), (1u << shift) - 1);
+            if (shift == 0) return ended(*this, top, by_mass, want);
+        }
+    }
     // All that is left has this key.
     __device__ __forceinline__ static Cut ended(const Sampler& s, uint32_t key, bool by_mass, uint64_t want) {
         const float value = short_value(key);
@@ -727,31 +755,7 @@ struct Sampler {
             from += held[r];
         }
         __syncthreads();
-        sort_down(sm.list[1], (int)n);
-        // The value where the target is reached, then what lies above it.
-        const uint32_t i = threadIdx.x * 2;
-        const auto weight_of = [&](uint32_t k) { return scale.weight(key_value(k), sm.table).w; };
-        uint64_t w[2] = {0, 0}, all;
-        for (uint32_t k = 0; k < 2; ++k)
-            if (i + k < n) w[k] = by_mass ? weight_of(sm.list[1][i + k]) : 1;
-        const uint64_t m = block_below(w[0] + w[1], sm.scan[0], &all);
-        for (uint32_t k = 0; k < 2; ++k) {
-            const uint64_t ahead = m + (k ? w[0] : 0);
-            if (ahead < want && want <= ahead + w[k]) sm.found[0] = sm.list[1][i + k];
-        }
-        __syncthreads();
-        const uint32_t key = (uint32_t)sm.found[0];
-        for (uint32_t k = 0; k < 2; ++k) {                  // its first place in the list
-            const uint32_t at = i + k;
-            if (at < n && sm.list[1][at] == key && (at == 0 || sm.list[1][at - 1] != key)) {
-                sm.found[1] = m + (k ? w[0] : 0);
-                sm.found[2] = w[k];
-            }
-        }
-        __syncthreads();
-        const uint64_t above = sm.found[1], each = sm.found[2];
-        __syncthreads();
-        return Cut{key_value(key), (uint32_t)((want - above + each - 1) / each)};
+        return cut_of_list(n, top, top - least, by_mass, want);
     }
 
     // The row's logits up to the bin `last`, which the top_k largest are among, as the candidates of the
