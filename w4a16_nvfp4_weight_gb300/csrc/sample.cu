@@ -16,13 +16,13 @@
 //    largest; the bin in which that count reaches top_k has the k-th largest logit in it or
 //    above, and the few logits from there up go to one block, which sorts and draws.
 //  - top_p: every weight is added to its bin's mass; the values of the one bin in which the
-//    running mass reaches top_p are sorted (or, where too many, divided by their keys).
+//    running mass reaches top_p are divided by their keys, as a list or, where too many, in place.
 //  - the draw: masses of warps, of blocks and of the row; the warp whose part holds the
 //    target finds the step, the lane and the element.
 // Bound by latency for few rows (1 x 151936 with top_k and top_p 10.4 us: the load, four meetings
 // of the cluster, two sorts), by instructions for many: an exact weight takes about 30, a mass
-// two additions in shared memory (256 x 100003 logits of 32 bits by top_p 149 us, 0.7 TB/s;
-// by temperature alone 82, by top_k 67).
+// two additions in shared memory (256 x 100003 logits of 32 bits by top_p 146 us, 0.7 TB/s;
+// by temperature alone 81, by top_k 67).
 #include <algorithm>
 
 #include "common.cuh"
@@ -37,7 +37,7 @@ namespace {
 constexpr int kSampleThreads = 512;
 constexpr int kSampleWarps = kSampleThreads / 32;
 constexpr int kBins = 1024;                // of the histogram
-constexpr int kList = 1024;                // values sorted at most
+constexpr int kList = 1024;                // values of a list at most
 constexpr int kMaxCluster = 8;
 constexpr int kStages = 4;                 // steps of a warp in flight or in use, of rows that are not held
 constexpr int64_t kHeldBytes = 86 * 1024;  // of a block's logits that stay in shared memory, with another block beside it
@@ -650,7 +650,7 @@ struct Sampler {
         if (by_mass) read_sums(sum);
         else read(sm.count, sum);
     }
-    // The cut in a bin of more values than are sorted, their keys within `range` below `top`: 1024 parts of
+    // The cut in a bin of more values than a list has, their keys within `range` below `top`: 1024 parts of
     // that, then of one part; one round does for logits of 16 bits.
     __device__ __noinline__ static Cut cut_by_digits(Sampler s, int bin, uint32_t top, uint32_t range, bool by_mass, uint64_t want) {
         for (int shift = 32;;) {
@@ -759,7 +759,7 @@ struct Sampler {
     }
 
     // The row's logits up to the bin `last`, which the top_k largest are among, as the candidates of the
-    // first block; false where they are more than it sorts.
+    // first block; false where they are more than a list has.
     __device__ __forceinline__ bool collect(int last) {
         uint64_t* mine = (uint64_t*)sm.lo;                  // lo and hi: this block's, before they go to the first one
         static_assert(sizeof(sm.lo) + sizeof(sm.hi) == sizeof(sm.pairs), "as many");
