@@ -354,8 +354,8 @@ struct Shared {
     };
     uint32_t listed, paired, few[kMaxCluster];
     uint32_t key_range[2];                 // least and largest key of a bin
-    uint64_t scan[2][kSampleWarps];
-    uint64_t found[4];
+    uint64_t scan[kSampleWarps];
+    uint64_t found[3];
     float best[kMaxCluster];               // pushed here by every block of the row, as the next ones
     int best_at[kMaxCluster];
     uint64_t mass[kMaxCluster];
@@ -608,7 +608,7 @@ struct Sampler {
 #pragma unroll
         for (int k = 0; k < kOwnBins; ++k) mine += v[k];
         if (threadIdx.x == 0) sm.found[0] = ~0ull;
-        uint64_t sum = block_below(mine, sm.scan[0], all);
+        uint64_t sum = block_below(mine, sm.scan, all);
 #pragma unroll
         for (int k = 0; k < kOwnBins; ++k) {
             if (sum < target && target <= sum + v[k]) {
@@ -803,7 +803,7 @@ struct Sampler {
             for (uint32_t k = 0; k < 2; ++k) w[k] = i + k < min(n, (uint32_t)top_k) ? x[k].units() : 0;
         }
         if (top_p < 1.f) {
-            uint64_t m = block_below(w[0] + w[1], sm.scan[0], &all);
+            uint64_t m = block_below(w[0] + w[1], sm.scan, &all);
             const uint64_t target = max(part_of(top_p, all, true), (uint64_t)1);
             for (uint32_t k = 0; k < 2; ++k) {              // what begins at or behind the target is not kept
                 const uint64_t here = w[k];
@@ -823,7 +823,7 @@ struct Sampler {
         constexpr uint64_t kWeightBits = (1ull << 44) - 1;
         w[0] = i < n ? sm.pairs[i] & kWeightBits : 0;
         w[1] = i + 1 < n ? sm.pairs[i + 1] & kWeightBits : 0;
-        uint64_t m = block_below(w[0] + w[1], sm.scan[0], &all);
+        uint64_t m = block_below(w[0] + w[1], sm.scan, &all);
         const float u = p.u[b];
         const uint64_t target = u < 1.f ? part_of(u, all, false) : all - 1;
         for (uint32_t k = 0; k < 2; ++k) {
@@ -862,7 +862,7 @@ struct Sampler {
         }
         if (by_p) {
             weigh_bins(cut, bins);
-            block_below(bins[0] + bins[1], sm.scan[0], &all);
+            block_below(bins[0] + bins[1], sm.scan, &all);
             const uint64_t target = max(part_of(top_p, all, true), (uint64_t)1);
             const Reached r = reach(bins, target, &all);
             // From units to w, up: as much as makes a bin's units reach it.
@@ -1150,6 +1150,9 @@ extern "C" nvfp4_status nvfp4_sample(const void* logits, int64_t row_stride, int
     while (more < kMaxCluster && bytes(more) > kHeldBytes) ++more;
     const bool held = bytes(more) <= kHeldBytes;
     if (held) ranks = more;
+    // No block without logits: a share is whole steps of its warps, so fewer often hold all (16 rows of 32768 by top-p
+    // 19.5 us with eight blocks a row, 16.1 with the five that have some).
+    ranks = (unsigned)ceil_div(V + 7, chunk(ranks) * kSampleWarps);
     SampleParams p{};
     p.logits = logits; p.stride = row_stride; p.u = u; p.how = *how; p.tokens = tokens; p.logprobs = logprobs;
     p.V = (int)V; p.chunk = (int)chunk(ranks);
