@@ -647,8 +647,8 @@ typedef struct {
  *  how           host; its arrays are device arrays of B values.
  *  tokens        device int64 [B].
  *  logprobs      device FP32 [B] or NULL: log of the token's share of the kept mass.
- * Weights are whole numbers of 2^-43, right to about 2^-32 of their value; their sums are exact,
- * so the result does not depend on how the work is split.
+ * Weights are whole numbers of 2^-43, before that rounding right to 2^-29.9 of their value (2^-31.7 in
+ * the mean square); their sums are exact, so the result does not depend on how the work is split.
  */
 nvfp4_status nvfp4_sample(const void* logits, int64_t row_stride, int type, int64_t B, int64_t V, const float* u,
                           const nvfp4_sampling* how, int64_t* tokens, float* logprobs, void* stream);

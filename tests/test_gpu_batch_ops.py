@@ -1,8 +1,8 @@
 """Page tables, adapters and the draw of tokens against the 64-bit oracle.
 
 Tolerances.  Tables, slots and tokens are whole numbers: equal.  (A token could differ
-where a random number lies within the weights' error, 2^-32, of a border of the running
-sum: for all rows here together a chance below 10^-4.)  A log-probability takes four
+where a random number lies within the error of a running sum of n weights, 2^-31.7 / sqrt(n)
+of it, of one of its n borders: for all rows here together a chance of about 10^-4.)  A log-probability takes four
 roundings of numbers up to its own size plus log V, each at most 2^-23 of them: 2^-21.
 An adapter's output is rounded once, u |ref| (u: BF16 2^-8, FP16 2^-11, with 2^-25
 below FP16's normals); before it, two sums of at most K and 256 products in 32 bits

@@ -7,7 +7,7 @@
 // A draw is a comparison of sums of up to a few hundred thousand weights with a random
 // threshold: with 32-bit sums one draw in a hundred would fall on the wrong side of a
 // border, another one for another order of the sums.  So weights are whole numbers of
-// 2^-43 (of the largest weight), right to about 2^-31 of their value, and sums of them
+// 2^-43 (of the largest weight), before that rounding right to 2^-29.9 of their value (2^-31.7 in the mean square), and sums of them
 // are exact in 64 bits, in any order and by any block.
 //
 // A cluster of one to eight blocks has a row, which stays in shared memory where it fits, so it is read
@@ -125,8 +125,9 @@ struct NearScale {
     __device__ __forceinline__ int bin(float l) const { return (kWholeBits >> 5) - (place(l) >> 5); }
     __device__ __forceinline__ float log_weight(float l) const { return fmaf(l, cl, fmaf(l, ch, -mh)) * 0.693147180559945f; }
     // 2^(l ch + l cl - mh): the nearest 512th by table, in 2^-30; the rest, below 2^-10 (and 2^-12
-    // for l cl), by three terms of exp's series, good to 2^-31 of the whole.  The rest itself is
-    // exact but for its last bit: mh plus a 512th has no rounding.
+    // for l cl), by three terms of exp's series.  The rest itself is exact but for its last bit: mh plus a
+    // 512th has no rounding.  So the table's and the product's roundings, half of 2^-30 each, are the error (2^-29.97
+    // found over eight million logits).
     __device__ __forceinline__ void weights(float la, float lb, const uint2* table, Weight& wa, Weight& wb) const {
         const F2 l = make_f2(la, lb);
         const F2 whole = fma2(l, make_f2(ch * 512.f, ch * 512.f), make_f2(kWhole - mh * 512.f, kWhole - mh * 512.f));
