@@ -372,6 +372,29 @@ def test_lora_workspace_stream_and_graph():
         _close_lora(out, y, x, a, b, ids, s, "bf16")
 
 
+@pytest.mark.parametrize("T", [5, 128, 129, 3000])
+@pytest.mark.parametrize("n", [1, 9])
+def test_lora_in_place_without_an_adapter_keeps_the_order_of_calls(T, n):
+    """In place and with no row on an adapter there is nothing to add: the call still ends behind its
+    own kernels, so its indexes may be rewritten, and its workspace used again, by what follows."""
+    y, x, a, b, ids, s = _lora_case(T, 256, 128, 16, n, "bf16", T + n, none=0.0)
+    room = torch.empty(nv.lora_workspace_size(T, n, 16, 256), dtype=torch.uint8, device="cuda")
+    none, want = torch.full_like(ids, -1), nv.lora_add(y, x, a, b, ids, scales=s)
+    _close_lora(want, y, x, a, b, ids, s, "bf16")
+    now = none.clone()
+    for _ in range(50):
+        z = y.clone()
+        now.copy_(none)
+        nv.lora_add(z, x, a, b, now, scales=s, out=z, workspace=room)
+        now.copy_(ids)
+        nv.lora_add(z, x, a, b, now, scales=s, out=z, workspace=room)
+        assert torch.equal(z, want)
+        nv.lora_add(z, x, a, b, none, scales=s, out=z, workspace=room)       # two such calls in a row, and a third kind behind them
+        nv.lora_add(z, x, a, b, none, scales=s, out=z, workspace=room)
+        nv.lora_add(y, x, a, b, ids, scales=s, out=z, workspace=room)
+        assert torch.equal(z, want)
+
+
 def test_lora_beside_an_nvfp4_projection():
     """gemm and lora_add as a layer would use them, against the dense product of both."""
     from w4a16_nvfp4_weight_gb300 import synth

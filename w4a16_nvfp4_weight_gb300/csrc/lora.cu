@@ -485,7 +485,10 @@ __global__ void __launch_bounds__(kLoraThreads, RW == 2 ? 3 : kFewBlocks) lora_u
     if (p.n == 0) pdl_wait_previous();                      // else the down kernel has, for all but its own sums
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
     int adapter, rows;
-    if (!item.find(p, blockIdx.x, &adapter, &rows) || (adapter < 0 && !p.copy_rest)) return;
+    if (!item.find(p, blockIdx.x, &adapter, &rows) || (adapter < 0 && !p.copy_rest)) {
+        pdl_wait_previous();                                // as below: this grid ends behind the down kernel, whatever its items
+        return;
+    }
     const int64_t n_begin = (int64_t)blockIdx.y * cols_block, n_end = min(n_begin + cols_block, p.N);
     const int steps = adapter < 0 ? 0 : p.rp / (8 * KP);
     const int row_warp = warp % RW, col_warp = warp / RW;
@@ -665,7 +668,10 @@ __global__ void __launch_bounds__(kLoraThreads, MT == 1 ? kFewBlocks : 1) lora_u
     if (p.n == 0) pdl_wait_previous();                      // else the down kernel has, for all but its own sums
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
     int adapter, rows;
-    if (!item.find(p, blockIdx.x, &adapter, &rows) || (adapter < 0 && !p.copy_rest)) return;
+    if (!item.find(p, blockIdx.x, &adapter, &rows) || (adapter < 0 && !p.copy_rest)) {
+        pdl_wait_previous();                                // as below: this grid ends behind the down kernel, whatever its items
+        return;
+    }
     const int64_t n_begin = (int64_t)blockIdx.y * cols_block, n_end = min(n_begin + cols_block, p.N);
     const int steps = adapter < 0 ? 0 : p.rp / (8 * KP);
     const int row_warp = warp % RW, col_warp = warp / RW;
