@@ -598,7 +598,8 @@ nvfp4_status nvfp4_trim_tables(const int32_t* lengths, const int32_t* keep, int6
  * Low-rank adapters of many requests at once, beside a projection that all share:
  *     out_t = RN(y_t + scales[a] * B[a] (A[a] x_t)),  a = adapters[t];  a < 0: out_t = y_t.
  * The rows of an adapter need not lie side by side.  A x is held in 32 bits and meets B as two
- * 16-bit halves, so the one rounding is that of the output.
+ * 16-bit halves: BF16 to 2^-16 of a value of A x, FP16 to 2^-22 of it or 2^-39 of the row's largest,
+ * whichever is more.  The sums with y have 32 bits, and the output is rounded to its type.
  *  y, x          device BF16 (FP16 with f16 = 1) [T, N] and [T, K], rows y_stride / x_stride
  *                elements apart; any alignment (16-byte rows run on vector loads).
  *  A, B          device [num_adapters, r, K] and [num_adapters, N, r], the same type, dense.  An

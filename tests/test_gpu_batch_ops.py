@@ -337,6 +337,60 @@ def test_lora_infinite_and_large_values_stay_in_their_rows(act, T):
     _close_lora(nv.lora_add(y, big, a3, b, ids, scales=s3), y, big, a3, b, ids, s3, act)
 
 
+# Halves of FP16 leave a component off by 2^-22 of it or 2^-39 of its row's largest (11 bits each: 2^-11 of 2^-11; the last
+# bit is 2^-24 and the largest at least 2^14, rounded by half of that bit), those of BF16 by 2^-16; then as above.  y goes
+# through the accumulators of at most 12 products (two for each 16 of a rank of up to 96), each off by at most 2^-23 of it.
+@pytest.mark.parametrize("apart", [3, 14, 20, 24, 30])
+@pytest.mark.parametrize("T,N,rank", [(1, 64, 16), (20, 33, 2), (150, 64, 8), (150, 31, 24), (200, 40, 72), (200, 64, 64)])
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+def test_lora_small_components_beside_large_ones(apart, T, N, rank, act):
+    """Every second column of B is zero at the row's largest component, as where the adapters of q, k
+    and v are one block-diagonal matrix: the output there is that of components far smaller."""
+    K, g, half = 64, _gen(apart), apart // 2
+    x, a, b = (torch.zeros(s, device="cuda") for s in ((T, K), (1, rank, K), (1, N, rank)))
+    uniform = lambda *s: 1 + torch.rand(s, generator=g, device="cuda")
+    x[:, 0], x[:, 1] = 2.0 ** (half // 2) * uniform(T), 2.0 ** -((apart - half) // 2) * uniform(T)
+    a[0, 0, 0], a[0, 1:, 1] = 2.0 ** (half - half // 2) * 1.5, 2.0 ** -(apart - half - (apart - half) // 2) * uniform(rank - 1)
+    b[0] = torch.randn(N, rank, generator=g, device="cuda")
+    b[0, ::2, 0] = 0
+    y = torch.randn(T, N, generator=g, device="cuda") * 2.0 ** -9
+    x, a, b, y = (t.to(DT[act]) for t in (x, a, b, y))
+    ids, s = _i32(np.zeros(T)), torch.full((1,), 2.0 ** -half, device="cuda")
+    for scale in (s, s * 2.0 ** half):
+        got = nv.lora_add(y, x, a, b, ids, scales=scale).double().cpu().numpy()
+        f = lambda t: t.double().cpu().numpy()
+        ref, mag = batch.lora(f(y), f(x), f(a), f(b), ids.tolist(), f(scale))
+        low = np.abs(f(x) @ f(a)[0].T) * f(scale)[0]
+        halves = 2.0 ** -16 * mag if act == "bf16" else 2.0 ** -22 * mag + 2.0 ** -39 * low.max(1)[:, None] * np.abs(f(b)[0]).sum(1)
+        ref[np.abs(ref) > float(torch.finfo(DT[act]).max)] = np.inf
+        lim = U[act] * np.abs(ref) + (K + 256) * 2.0 ** -24 * mag + halves + 12 * 2.0 ** -23 * np.abs(f(y)) + TINY[act]
+        near = np.abs(got[:, ::2] - ref[:, ::2]) <= lim[:, ::2]
+        assert near.all(), np.abs(got[:, ::2] - ref[:, ::2]).max()
+        finite = np.isfinite(ref)
+        assert np.all(np.abs(got[finite] - ref[finite]) <= lim[finite])
+
+
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+@pytest.mark.parametrize("T,N,rank", [(3, 64, 16), (20, 33, 2), (200, 64, 64), (200, 31, 24)])
+def test_lora_keeps_y_beside_the_largest_and_smallest_products(act, T, N, rank):
+    """s A x next to either end of 32 bits: where B is zero the output is y itself."""
+    g = _gen(2)
+    x, a = torch.zeros(T, 32, device="cuda"), torch.zeros(1, rank, 32, device="cuda")
+    x[:, 3], a[0, :, 3] = 1, torch.rand(rank, generator=g, device="cuda") * 0.5
+    a[0, 0, 3] = 1
+    b = torch.randn(1, N, rank, generator=g, device="cuda")
+    b[0, ::3] = 0
+    y = torch.randn(T, N, generator=g, device="cuda")
+    x, a, b, y = (t.to(DT[act]) for t in (x, a, b, y))
+    for s in (1.5 * 2.0 ** 127, 2.0 ** 127, 2.0 ** 126, 2.0 ** 100, 2.0 ** -59, 2.0 ** -60, 2.0 ** -61, 2.0 ** -100, 2.0 ** -126, 0.0):
+        got = nv.lora_add(y, x, a, b, _i32(np.zeros(T)), scales=torch.full((1,), s, device="cuda"))
+        assert torch.equal(got[:, ::3], y[:, ::3]), s
+        if s < 2.0 ** -50:
+            assert torch.equal(got, y), s
+        elif act == "f16":
+            assert bool((got.isinf() | (torch.arange(N, device="cuda") % 3 == 0)).all()), s
+
+
 def test_lora_zero_padded_ranks_and_adapters_of_one_matrix():
     y, x, a, b, ids, s = _lora_case(40, 128, 64, 32, 3, "bf16", 4)
     a[:, 20:] = 0

@@ -1,7 +1,7 @@
 // Low-rank adapters of many requests at once, beside a projection that all share:
 //     out_t = RN(y_t + s_a B_a (A_a x_t)),  a = adapters[t]  (a < 0: out_t = y_t).
-// x, y, A and B are 16-bit; A x and its sums are held in 32 bits and meet B as two 16-bit halves
-// (2^-16 of a value for BF16, 2^-21 for FP16 or better), so the output is rounded once.
+// x, y, A and B are 16-bit; A x and its sums are held in 32 bits and meet B as two 16-bit halves, right
+// to 2^-16 of a value for BF16, for FP16 to 2^-22 of it or 2^-39 of the row's largest, whichever is more.
 //
 // Rows are grouped by adapter into items of up to 16 or 64 rows of one adapter (rows of a
 // request need not lie side by side): by every block for itself, or of more than 128 rows by
@@ -398,7 +398,9 @@ __device__ __forceinline__ void part(const uint16_t* p, int left, uint32_t (&w)[
 
 // s A x of an item's rows, the splits' sums in order, as two 16-bit halves in shared memory: four rows a warp at
 // a time, eight lanes each.  FP16 holds them divided by a power of two (`sm_up`) that puts a row's largest
-// below 2: the products are added to y over that, and the end takes it back.  BF16 needs none.
+// into [2^14, 2^15), the top of its range: the halves' last bit is then 2^-24 of an absolute 1, so what is 2^17 times
+// smaller than the largest still has 22 bits, and B may be zero at the large ones (with the largest in [1, 2) a value 2^14
+// times smaller was off by 2^-11).  The products are added to y over that power, and the end takes it back.  BF16 needs none.
 template <bool F16>
 __device__ __forceinline__ void sum_splits(const LoraParams& p, const int32_t* order, int adapter, int rows, int all, int pitch, uint32_t* sm_hi,
                                            uint32_t* sm_lo, float* sm_up) {
@@ -425,19 +427,22 @@ __device__ __forceinline__ void sum_splits(const LoraParams& p, const int32_t* o
         };
         float down = 1.f, up = 1.f;
         if (F16) {
-            float most = 0.f;
+            float most = 0.f;                               // of what is finite
+            const auto meet = [&](float x) { most = fmaxf(most, fabsf(x) < INFINITY ? fabsf(x) : 0.f); };
             for (int c = (lane & 7) * 4; c < p.rp; c += 32) {
                 const float4 v = sum(c);
-                most = fmaxf(most, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+                meet(v.x);
+                meet(v.y);
+                meet(v.z);
+                meet(v.w);
             }
             __syncwarp();
 #pragma unroll
             for (int o = 4; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-            if (most > 0x1p-100f && most < INFINITY) {
-                const uint32_t e = __float_as_uint(most) & 0x7f800000u;
-                up = __uint_as_float(e);
-                down = __uint_as_float(0x7f000000u - e);            // 2^-exponent
-            }
+            // From 2^-60 on (less is nothing beside 2^-25, the half of FP16's smallest): either power is a normal number.
+            const uint32_t e = max(__float_as_uint(most) & 0x7f800000u, (127u - 60u) << 23) - (14u << 23);
+            up = __uint_as_float(e);
+            down = __uint_as_float(0x7f000000u - e);                // 1 / up
         }
         if (F16 && (lane & 7) == 0) sm_up[row] = up;
         const auto halves = [&](float a, float b, uint32_t* hi, uint32_t* lo) {
