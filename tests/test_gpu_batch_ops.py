@@ -337,6 +337,31 @@ def test_lora_infinite_and_large_values_stay_in_their_rows(act, T):
     _close_lora(nv.lora_add(y, big, a3, b, ids, scales=s3), y, big, a3, b, ids, s3, act)
 
 
+@pytest.mark.parametrize("rank", [1, 3, 8, 16, 20, 24, 40, 64, 72, 130])
+@pytest.mark.parametrize("T,N,K", [(1, 64, 64), (40, 33, 40), (200, 72, 300), (200, 31, 33)])
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+def test_lora_infinities_are_those_of_the_formula(act, T, N, K, rank):
+    """An infinite x meets the rank's own columns alone: infinite of the product's sign, NaN where
+    signs meet, and finite in the other rows."""
+    y, x, a, b, ids, s = _lora_case(T, K, N, rank, 1, act, rank, none=0.0)
+    a, b = a.abs() + 0.25, b.abs() + 0.25                                    # one sign, none zero
+    b[0, 1::3] *= -1
+    if rank > 1:
+        b[0, 2::3, rank - 1] *= -1                                           # both
+    x[0, K // 2] = float("inf")
+    if T > 1:
+        x[T // 2, 0], x[T - 1, K - 1] = float("-inf"), float("inf")
+        x[T - 1, 0], x[T - 2] = float("-inf"), 0                             # NaN; nothing
+    f = lambda t: t.double().cpu().numpy()
+    got = nv.lora_add(y, x, a, b, ids, scales=s)
+    with np.errstate(all="ignore"):
+        ref = f(y) + f(s)[0] * (f(x) @ f(a)[0].T @ f(b)[0].T)
+    got = f(got)
+    assert np.isinf(ref[0, :2]).all() and np.isnan(ref[0, 2::3]).all() == (rank > 1) and np.isfinite(ref[1:T // 2]).all()
+    assert np.array_equal(np.isnan(got), np.isnan(ref)) and np.array_equal(np.isinf(got), np.isinf(ref))
+    assert np.array_equal(np.sign(got[np.isinf(ref)]), np.sign(ref[np.isinf(ref)]))
+
+
 # Halves of FP16 leave a component off by 2^-22 of it or 2^-39 of its row's largest (11 bits each: 2^-11 of 2^-11; the last
 # bit is 2^-24 and the largest at least 2^14, rounded by half of that bit), those of BF16 by 2^-16; then as above.  y goes
 # through the accumulators of at most 12 products (two for each 16 of a rank of up to 96), each off by at most 2^-23 of it.

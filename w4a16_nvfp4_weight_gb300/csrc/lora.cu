@@ -410,9 +410,9 @@ __device__ __forceinline__ void sum_splits(const LoraParams& p, const int32_t* o
         const bool held = row < rows;
         const float* low = p.low + (int64_t)(held ? order[row] : 0) * p.rp;
         const int64_t apart = p.T * p.rp;
-        const auto sum = [&](int c) {                   // of four
+        const auto sum = [&](int c) {                   // of four; behind r zeros, where x or s is infinite, too
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (held && c < p.rp) {
+            if (held && c < p.r) {
                 const float* at = low + c;
 #pragma unroll 4
                 for (int sp = 0; sp < p.splits; ++sp, at += apart) {
@@ -422,8 +422,12 @@ __device__ __forceinline__ void sum_splits(const LoraParams& p, const int32_t* o
                     v.z += u.z;
                     v.w += u.w;
                 }
+                v.x *= s;
+                v.y = c + 1 < p.r ? v.y * s : 0.f;
+                v.z = c + 2 < p.r ? v.z * s : 0.f;
+                v.w = c + 3 < p.r ? v.w * s : 0.f;
             }
-            return make_float4(v.x * s, v.y * s, v.z * s, v.w * s);
+            return v;
         };
         float down = 1.f, up = 1.f;
         if (F16) {
