@@ -451,6 +451,18 @@ def test_lora_workspace_stream_and_graph():
         _close_lora(out, y, x, a, b, ids, s, "bf16")
 
 
+@pytest.mark.parametrize("rank", [1, 4, 7, 8, 9, 17, 33, 65])
+@pytest.mark.parametrize("T,N", [(3, 40), (200, 33), (200, 64)])
+def test_lora_reads_no_sums_that_it_has_not_made(T, N, rank):
+    """Whatever lies in the columns behind the rank, which nothing is multiplied for."""
+    y, x, a, b, ids, s = _lora_case(T, 264, N, rank, 1, "f16", rank)
+    room = torch.full((nv.lora_workspace_size(T, 1, rank, 264),), 255, dtype=torch.uint8, device="cuda")     # NaN
+    got = nv.lora_add(y, x, a, b, ids, scales=s, workspace=room)
+    _close_lora(got, y, x, a, b, ids, s, "f16")
+    room.zero_()
+    assert torch.equal(nv.lora_add(y, x, a, b, ids, scales=s, workspace=room), got)
+
+
 @pytest.mark.parametrize("T", [5, 128, 129, 3000])
 @pytest.mark.parametrize("n", [1, 9])
 def test_lora_in_place_without_an_adapter_keeps_the_order_of_calls(T, n):

@@ -972,7 +972,7 @@ extern "C" nvfp4_status nvfp4_lora_add(const void* y, int64_t y_stride, const vo
         const bool ring = vec_x && pl.rows_item == 64;
         const void* kernel = ring ? (f16 ? ring_kernel<true>(pl.nt) : ring_kernel<false>(pl.nt))
                                   : (f16 ? down_kernel<true>(pl.rows_item, pl.nt, vec_x) : down_kernel<false>(pl.rows_item, pl.nt, vec_x));
-        const dim3 grid((unsigned)pl.items, (unsigned)pl.splits, (unsigned)ceil_div(p.rp, pl.nt * 8));
+        const dim3 grid((unsigned)pl.items, (unsigned)pl.splits, (unsigned)ceil_div(r, pl.nt * 8));
         const size_t smem = ring ? kRingStages * (64 + 8 * pl.nt) * 128 : 0;
         if (nvfp4_status st = launch_kernel(kernel, grid, dim3(kLoraThreads), smem, 1, args, s, fn)) return st;
     }
