@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(kLoraThreads, RW == 2 ? 3 : kFewBlocks) lora_u
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
     int adapter, rows;
     if (!item.find(p, blockIdx.x, &adapter, &rows) || (adapter < 0 && !p.copy_rest)) {
-        pdl_wait_previous();                                // as below: this grid ends behind the down kernel, whatever its items
+        if (blockIdx.x == 0 && blockIdx.y == 0) pdl_wait_previous();        // the grid ends behind the down kernel, whatever its items
         return;
     }
     const int64_t n_begin = (int64_t)blockIdx.y * cols_block, n_end = min(n_begin + cols_block, p.N);
@@ -678,7 +678,7 @@ __global__ void __launch_bounds__(kLoraThreads, MT == 1 ? kFewBlocks : 1) lora_u
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
     int adapter, rows;
     if (!item.find(p, blockIdx.x, &adapter, &rows) || (adapter < 0 && !p.copy_rest)) {
-        pdl_wait_previous();                                // as below: this grid ends behind the down kernel, whatever its items
+        if (blockIdx.x == 0 && blockIdx.y == 0) pdl_wait_previous();        // the grid ends behind the down kernel, whatever its items
         return;
     }
     const int64_t n_begin = (int64_t)blockIdx.y * cols_block, n_end = min(n_begin + cols_block, p.N);
