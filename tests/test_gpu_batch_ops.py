@@ -10,11 +10,15 @@ move it by at most (K + 256) 2^-24 of |s| |B| (|A| |x|), and A x as two 16-bit h
 2^-16 of that.
 """
 
+import ctypes
+import threading
+
 import numpy as np
 import pytest
 import torch
 
 import w4a16_nvfp4_weight_gb300 as nv
+from w4a16_nvfp4_weight_gb300 import _lib as _lib_module
 from oracle import batch
 from tests import gpu_util as gu
 
@@ -725,6 +729,43 @@ def test_calls_on_two_streams_at_once():
     for outs in got:
         for out in outs:
             assert all(torch.equal(p, q) for p, q in zip(out, want))
+
+
+def test_calls_of_other_sizes_from_other_threads(lib):
+    """The C ABI from four host threads at once (ctypes holds no lock over a call), each with sizes for which
+    the same kernels take another amount of shared memory: no launch fails, and all give what one thread gives."""
+    P = lambda t: ctypes.c_void_p(t.data_ptr())
+    how = _lib_module.Sampling(temperature_all=1.0, top_p_all=0.9)
+
+    def draws(V):
+        l, u = _logits(2, V, "normal", "f32", V), torch.rand(2, generator=_gen(V), device="cuda")
+        return nv.sample(l, u, top_p=float(np.float32(0.9))), lambda out, stream: lib.nvfp4_sample(
+            P(l), V, 2, 2, V, P(u), ctypes.byref(how), P(out), None, stream)
+
+    def adapters(n, rank):
+        y, x, a, b, ids, s = _lora_case(2000, 64, 64, rank, n, "bf16", n)
+        room = torch.empty(nv.lora_workspace_size(2000, n, rank, 64), dtype=torch.uint8, device="cuda")
+        return nv.lora_add(y, x, a, b, ids, scales=s), lambda out, stream: lib.nvfp4_lora_add(
+            P(y), 64, P(x), 64, P(a), P(b), P(s), P(ids), 2000, n, rank, 64, 64, 0, P(out), P(room), room.numel(), stream)
+
+    calls = [draws(9000), draws(100003), adapters(1100, 4), adapters(4000, 4)]
+    torch.cuda.synchronize()
+    failed, wrong = [0] * 4, [0] * 4
+
+    def run(k):
+        want, call = calls[k]
+        stream, out = torch.cuda.Stream(), torch.empty_like(want)
+        for _ in range(1500):
+            failed[k] += call(out, ctypes.c_void_p(stream.cuda_stream)) != 0
+        stream.synchronize()
+        wrong[k] = not torch.equal(out, want)
+
+    threads = [threading.Thread(target=run, args=(k,)) for k in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert failed == [0] * 4 and not any(wrong), (failed, wrong)
 
 
 def test_a_batch_step_runs_together():

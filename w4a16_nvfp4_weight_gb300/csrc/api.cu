@@ -11,6 +11,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <mutex>
+#include <unordered_map>
 
 #include "common.cuh"
 #include "gemm_decode.cuh"
@@ -25,6 +26,7 @@ constexpr int kMaxDevices = 64;
 int* g_status_ptr[kMaxDevices] = {};
 int g_sm_count[kMaxDevices] = {};
 std::mutex g_mu;
+std::unordered_map<const void*, size_t> g_smem[kMaxDevices];      // allowed so far, of each kernel
 }  // namespace
 
 void set_error(const char* fmt, ...) {
@@ -69,6 +71,19 @@ int sm_count() {
         g_sm_count[dev] = n;
     }
     return g_sm_count[dev];
+}
+
+nvfp4_status allow_smem(const void* kernel, size_t bytes, const char* what) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return check_cuda(e, what);
+    if (dev < 0 || dev >= kMaxDevices) return fail(NVFP4_ERR_CUDA, "%s: device %d", what, dev);
+    std::lock_guard<std::mutex> lock(g_mu);
+    size_t& most = g_smem[dev][kernel];
+    if (bytes <= most) return NVFP4_OK;
+    if (nvfp4_status st = check_cuda(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes), what)) return st;
+    most = bytes;
+    return NVFP4_OK;
 }
 
 // Split-K plan of the decode kernel for an M x N x K problem.

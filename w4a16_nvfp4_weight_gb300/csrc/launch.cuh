@@ -9,7 +9,7 @@ namespace nvfp4 {
 inline nvfp4_status launch_kernel(const void* kernel, dim3 grid, dim3 block, size_t smem, unsigned cluster, void** args,
                                   cudaStream_t stream, const char* fn) {
     if (smem > 8 * 1024)                                    // with what the kernel declares, past 48 KB
-        if (nvfp4_status st = check_cuda(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem), fn)) return st;
+        if (nvfp4_status st = allow_smem(kernel, smem, fn)) return st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
