@@ -4,6 +4,9 @@ global scales, and the AWQ scale finalization max over experts of max(w3, w1).
 Streaming (few rows per expert) and tile (many rows per expert) paths, BF16 and
 FP16 activations."""
 
+import ctypes
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -93,6 +96,54 @@ def test_shards_with_a_shared_global_match_the_fused_layer_bitwise(T):
     fused, _ = _run(c, _stack(fc1, 2 * I, H), _stack(fc2, H, I), "bf16", "swiglu", False, awq=False)
     split, _ = _run(c, _stack(shards, I, H), _stack(fc2, H, I), "bf16", "swiglu", True, awq=False)
     assert np.array_equal(fused, split)
+
+
+@pytest.mark.parametrize("T,E,topk,H,I", [(1, 8, 2, 256, 256), (7, 4, 2, 256, 256), (64, 16, 4, 256, 128)])
+def test_fused_and_shard_layers_from_several_threads(lib, T, E, topk, H, I):
+    """The same kernels with one table and with two (another amount of shared memory), and routings of few and of
+    many experts, by the C ABI from host threads at once: no launch fails, and each gives what it gives alone."""
+    c, fc1, fc2 = _case(T, E, topk, H, I, seed=3 + T, kind="gated")
+    shards = [w for p, s, d in fc1 for w in ((p[:I], s[:I], d), (p[I:], s[I:], d))]
+    x, logits = gu.bits_to_tensor(c.x_bits, "bf16"), torch.from_numpy(np.ascontiguousarray(c.logits)).cuda()
+    fused, split, down = _stack(fc1, 2 * I, H), _stack(shards, I, H), _stack(fc2, H, I)
+    P = lambda t: ctypes.c_void_p(t.data_ptr())
+    need = nv.moe_workspace_size(T, E, topk, H, I)
+    rooms = []
+
+    def layer(weights, is_split, stream, out):
+        rooms.append(torch.empty(need, dtype=torch.uint8, device="cuda"))
+        return lib.nvfp4_w4a16_moe_grouped_ex, (P(x), P(logits), P(weights), P(down), None, T, E, topk, H, I, 0, is_split, 0, P(out), None, None, None,
+                                                None, P(rooms[-1]), need, stream)
+
+    def route(E, stream, out):
+        tables = [torch.randn(300, E, device="cuda"), torch.empty(600, dtype=torch.int32, device="cuda"), torch.empty(600, device="cuda"),
+                  torch.empty(600, dtype=torch.int32, device="cuda"), torch.zeros(E + 1, dtype=torch.int32, device="cuda")]
+        rooms.append(tables)
+        return lib.nvfp4_moe_route, (P(tables[0]), 300, E, 2, P(tables[1]), P(tables[2]), P(out), P(tables[3]), P(tables[4]), stream)
+
+    kinds = [lambda *a: layer(fused, 0, *a), lambda *a: layer(split, 1, *a), lambda *a: route(8, *a), lambda *a: route(256, *a)] * 2
+    streams = [torch.cuda.Stream() for _ in kinds]
+    outs = [torch.empty(T, H, dtype=torch.bfloat16, device="cuda") if k % 4 < 2 else torch.empty(600, dtype=torch.int32, device="cuda") for k in range(8)]
+    calls = [kind(ctypes.c_void_p(st.cuda_stream), out) for kind, st, out in zip(kinds, streams, outs)]
+    torch.cuda.synchronize()
+    assert all(fn(*args) == 0 for fn, args in calls)
+    torch.cuda.synchronize()
+    want, failed = [o.clone() for o in outs], [0] * 8
+    torch.cuda.synchronize()
+
+    def run(k):
+        fn, args = calls[k]
+        for _ in range(2000):
+            failed[k] += fn(*args) != 0
+
+    threads = [threading.Thread(target=run, args=(k,)) for k in range(8)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert failed == [0] * 8 and all(torch.equal(g, w) for g, w in zip(outs, want))
+    gu.check_device_status()
 
 
 @pytest.mark.parametrize("act", ["bf16", "f16"])

@@ -1232,9 +1232,7 @@ size_t moe_lin_smem(int MT, bool gated, bool shards) {
 template <int MT, bool GATED, bool F16, bool AWQ>
 nvfp4_status launch_moe_linear_typed(const MoeLinParams& p, unsigned gx, unsigned max_items, cudaStream_t s) {
     const size_t smem = moe_lin_smem(MT, GATED, GATED && p.half_stride != 0);
-    cudaError_t e = cudaFuncSetAttribute(moe_linear_kernel<MT, GATED, F16, AWQ>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return check_cuda(e, "MoE linear: shared memory attribute");
+    if (nvfp4_status st = allow_smem((const void*)moe_linear_kernel<MT, GATED, F16, AWQ>, smem, "MoE linear: shared memory attribute")) return st;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(gx, (unsigned)p.splits, max_items);
     cfg.blockDim = dim3(kThreads, 1, 1);
@@ -1249,7 +1247,7 @@ nvfp4_status launch_moe_linear_typed(const MoeLinParams& p, unsigned gx, unsigne
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, moe_linear_kernel<MT, GATED, F16, AWQ>, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, moe_linear_kernel<MT, GATED, F16, AWQ>, p);
     return check_cuda(e, GATED ? "MoE FC1: launch" : "MoE FC2: launch");
 }
 
@@ -1262,8 +1260,7 @@ int persist_ctas_per_sm(size_t smem) {
     const int k = smem > persist_smem(MT, GATED, false) ? 1 : 0;      // with gate/up shards
     std::call_once(once[k], [&] {
         int n = 0;
-        if (cudaFuncSetAttribute(moe_persist_kernel<MT, GATED, F16, AWQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)smem) == cudaSuccess &&
+        if (allow_smem((const void*)moe_persist_kernel<MT, GATED, F16, AWQ>, smem, "MoE persistent linear: shared memory attribute") == NVFP4_OK &&
             cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, moe_persist_kernel<MT, GATED, F16, AWQ>, kThreads,
                                                           smem) == cudaSuccess)
             cache[k] = n;
@@ -1274,9 +1271,8 @@ int persist_ctas_per_sm(size_t smem) {
 template <int MT, bool GATED, bool F16, bool AWQ>
 nvfp4_status launch_moe_persist_typed(const MoeLinParams& p, int ncg, int64_t max_units, int early, cudaStream_t s) {
     const size_t smem = persist_smem(MT, GATED, GATED && p.half_stride != 0);
-    cudaError_t e = cudaFuncSetAttribute(moe_persist_kernel<MT, GATED, F16, AWQ>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return check_cuda(e, "MoE persistent linear: shared memory attribute");
+    if (nvfp4_status st = allow_smem((const void*)moe_persist_kernel<MT, GATED, F16, AWQ>, smem, "MoE persistent linear: shared memory attribute"))
+        return st;
     const int per_sm = std::max(1, persist_ctas_per_sm<MT, GATED, F16, AWQ>(smem));
     const int64_t grid = std::min<int64_t>(max_units, (int64_t)per_sm * sm_count());
     return launch_chained(moe_persist_kernel<MT, GATED, F16, AWQ>, dim3((unsigned)std::max<int64_t>(grid, 1)),
@@ -1311,9 +1307,9 @@ nvfp4_status launch_moe_linear(const MoeLinParams& p, unsigned gx, unsigned max_
 template <bool GATED, bool F16, bool AWQ, int ONE>
 nvfp4_status launch_moe_one_typed(const MoeLinParams& p, unsigned gx, cudaStream_t s) {
     const size_t smem = moe_lin_smem(1, GATED, GATED && p.half_stride != 0);
-    cudaError_t e = cudaFuncSetAttribute(moe_linear_kernel<1, GATED, F16, AWQ, ONE>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return check_cuda(e, "MoE single token: shared memory attribute");
+    if (nvfp4_status st = allow_smem((const void*)moe_linear_kernel<1, GATED, F16, AWQ, ONE>, smem, "MoE single token: shared memory attribute"))
+        return st;
+    cudaError_t e;
     const unsigned ys = (unsigned)p.splits;
     const unsigned zs = ONE == 2 ? (unsigned)p.topk : 1u;
     if (ys * zs > 8) {             // clusters of up to 16 CTAs are not portable: opt in
@@ -1436,8 +1432,7 @@ nvfp4_status launch_routing(const float* router_logits, int64_t T, int E, int to
     st = launch_chained(route_kernel, dim3((unsigned)ceil_div(T, 8)), dim3(256), 0, s, "MoE route: launch",
                         router_logits, T, E, topk, idx, wts);
     if (st != NVFP4_OK) return st;
-    cudaError_t ce = cudaFuncSetAttribute(permute_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)psmem);
-    if ((st = check_cuda(ce, "MoE permute: shared memory attribute")) != NVFP4_OK) return st;
+    if ((st = allow_smem((const void*)permute_kernel, psmem, "MoE permute: shared memory attribute")) != NVFP4_OK) return st;
     return launch_chained(permute_kernel, dim3(1), dim3(kPermThreads), psmem, s, "MoE permute: launch",
                           (const int32_t*)idx, T, topk, E, tok, wc, offsets, perm, inv, items, n_items, tail_rows,
                           tail_base);
