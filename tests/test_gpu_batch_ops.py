@@ -288,6 +288,41 @@ def test_lora(T, K, N, rank, n, act, runs):
     assert nv.lora_add(z, x, a, b, ids, scales=s, out=z) is not None and torch.equal(z, got)
 
 
+# T >= 64 (n + 1): items of 64 rows, here with remainders.  K and N with and without vector loads, ranks below, between
+# and at the tiles' sizes, up to beyond the room of the ring.
+@pytest.mark.parametrize("rank", [1, 3, 8, 12, 20, 32, 64, 72, 100, 128, 192, 200, 256])
+@pytest.mark.parametrize("T,K,N,n", [(129, 64, 72, 1), (200, 300, 264, 2), (333, 520, 33, 3), (450, 33, 128, 1), (260, 1032, 257, 1)])
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+def test_lora_items_of_64_rows(T, K, N, n, rank, act):
+    for wide, runs in ((0, True), (1, False), (8, False)):
+        y, x, a, b, ids, s = _lora_case(T, K, N, rank, n, act, T + rank + wide, runs=runs, wide=wide)
+        got = nv.lora_add(y, x, a, b, ids, scales=s)
+        _close_lora(got, y, x, a, b, ids, s, act)
+        z = torch.full((T + 1, N), 7.0, dtype=DT[act], device="cuda")
+        nv.lora_add(y, x, a, b, ids, scales=s, out=z[:T])
+        assert torch.equal(z[:T], got) and bool((z[T] == 7).all())
+
+
+@pytest.mark.parametrize("off", [1, 2, 4])
+@pytest.mark.parametrize("T,rank", [(40, 16), (200, 16), (200, 24), (200, 128)])
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+def test_lora_tensors_off_16_byte_boundaries(act, T, rank, off):
+    """x, y, A and B, each by itself, begin 2, 4 or 8 bytes past a boundary."""
+    y, x, a, b, ids, s = _lora_case(T, 128, 64, rank, 1, act, off)
+    want = nv.lora_add(y, x, a, b, ids, scales=s)
+    _close_lora(want, y, x, a, b, ids, s, act)
+
+    def moved(t):
+        room = torch.empty(t.numel() + off, dtype=t.dtype, device="cuda")
+        room[off:].copy_(t.reshape(-1))
+        return room[off:].view(t.shape)
+
+    for k in range(4):
+        args = [y, x, a, b]
+        args[k] = moved(args[k])
+        _close_lora(nv.lora_add(*args, ids, scales=s), y, x, a, b, ids, s, act)
+
+
 @pytest.mark.parametrize("act", ["bf16", "f16"])
 @pytest.mark.parametrize("wide", [1, 8, 72])
 def test_lora_strided_rows_and_no_scales(act, wide):
