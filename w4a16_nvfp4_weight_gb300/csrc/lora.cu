@@ -467,6 +467,7 @@ __device__ __forceinline__ void sum_splits(const LoraParams& p, const int32_t* o
 }
 
 constexpr int kUpStages = 3;
+constexpr int kUpRingRank = 128;           // where a row of B is a multiple of 128 bytes it is 128 or 256 (`turn`)
 constexpr int kFewBlocks = 5;              // of the up kernel of 16 rows, on an SM
 
 // One item's rows of A x times B, and y, over a range of N: stages of columns of B and y through a ring in
@@ -516,7 +517,8 @@ __global__ void __launch_bounds__(kLoraThreads, RW == 2 ? 3 : kFewBlocks) lora_u
         }
     const uint16_t* b = p.b + (int64_t)max(adapter, 0) * p.N * p.r;
     const uint32_t y0 = smem_u32(sm_y) + tid * 16, b0 = smem_u32(sm_b);
-    // Rows of 128 bytes and their multiples: the four pieces of a lane group lie in the halves of 128 bytes by turns.
+    // Rows of 128 and of 256 bytes: the four pieces of a lane group lie in the halves of 128 bytes by turns, which
+    // go by the row's last bit (bit 3 or 4 of a piece's number).
     const int turn = p.r % 64 == 0 ? 4 : 0, row_bit = p.r == 128 ? 4 : 3, pieces = p.r / 8;
     const auto stage = [&](int64_t n0, int s) {
         const int64_t left = n_end - n0;
@@ -980,7 +982,7 @@ extern "C" nvfp4_status nvfp4_lora_add(const void* y, int64_t y_stride, const vo
     // for 64 rows).
     const int step = pl.rows_item == 16 ? 128 : 64;
     const size_t halves = (size_t)pl.rows_item * (p.rp / 2 + 4) * 8, stage = (size_t)kLoraThreads * (pl.rows_item == 16 ? 32 : 64) + (size_t)step * 2 * r;
-    const bool up_ring = vec_y && vec_b && r % 8 == 0 && aligned(B, 16) && halves + kUpStages * stage <= 110 * 1024;
+    const bool up_ring = vec_y && vec_b && r % 8 == 0 && r <= kUpRingRank && aligned(B, 16) && halves + kUpStages * stage <= 110 * 1024;
     const void* kernel;
     if (up_ring) {
         kernel = pl.rows_item == 16 ? (f16 ? up_ring_kernel<true, 1>(r) : up_ring_kernel<false, 1>(r))
