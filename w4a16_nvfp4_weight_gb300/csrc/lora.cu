@@ -660,14 +660,14 @@ __global__ void __launch_bounds__(kLoraThreads, RW == 2 ? 3 : kFewBlocks) lora_u
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// One item's rows of A x times B, and y, over a range of N.  A warp takes MT * 16 rows and CU * 32 columns
+// One item's rows of A x times B, and y, over a range of N.  A warp takes MT * 16 rows and 32 columns
 // of a step, whose y it asks for first; tile j of four holds columns 8 (c / 2) + 2 j + c % 2, so that a
 // lane's eight outputs of a row lie side by side.  A lane takes KP words of a row of B: four k for
 // each 16, or (KP = 4) eight for each 32.  The first step's y and B are asked for while the down kernel
 // still runs, each further one's a step ahead (64 rows of 4096 and 28672 columns,
 // rank 16: 22.8 us without, 20.9 with, for both kernels).  For what the ring does not take: rows of B or y
 // off 16-byte boundaries, ranks that are no multiple of 8 or beyond its room.
-template <bool F16, int RW, int MT, int CU, int KP, bool VEC_B, bool VEC_Y>
+template <bool F16, int RW, int MT, int KP, bool VEC_B, bool VEC_Y>
 __global__ void __launch_bounds__(kLoraThreads, MT == 1 ? kFewBlocks : 1) lora_up_kernel(const LoraParams p, const int cols_block) {
     constexpr int kRows = 16 * MT * RW, kColWarps = kLoraThreads / 32 / RW;
     extern __shared__ __align__(16) uint8_t sm_up[];
@@ -703,36 +703,30 @@ __global__ void __launch_bounds__(kLoraThreads, MT == 1 ? kFewBlocks : 1) lora_u
     const uint32_t *hi0 = sm_hi + (row_warp * MT * 16 + g) * pitch + q * KP, *lo0 = sm_lo + (row_warp * MT * 16 + g) * pitch + q * KP;
     const int r = p.r, first = 8 * (g >> 1) + (g & 1);
     // y of the step at n0.  `whole`: all of its columns are there.
-    const auto ask = [&](int64_t n0, bool whole, uint4 (&v)[CU][MT][2]) {
+    const auto ask = [&](int64_t n0, bool whole, uint4 (&v)[MT][2]) {
 #pragma unroll
-        for (int u = 0; u < CU; ++u)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    v[u][m][h] = make_uint4(0, 0, 0, 0);
-                    if (held[m][h]) v[u][m][h] = eight<VEC_Y>(y[m][h] + n0 + u * 32, whole ? 8 : n_end - n0 - u * 32 - q * 8);
-                }
+            for (int h = 0; h < 2; ++h) {
+                v[m][h] = make_uint4(0, 0, 0, 0);
+                if (held[m][h]) v[m][h] = eight<VEC_Y>(y[m][h] + n0, whole ? 8 : n_end - n0 - q * 8);
+            }
     };
     // B of the step at n0, its k from `st` on.
-    const auto ask_b = [&](int64_t n0, bool whole, int st, uint32_t (&v)[CU][4][KP]) {
+    const auto ask_b = [&](int64_t n0, bool whole, int st, uint32_t (&v)[4][KP]) {
         const uint16_t* bn = b + (n0 + first) * r + st * 8 * KP;
         const int left = r - st * 8 * KP - q * 2 * KP;
         if (whole) {
 #pragma unroll
-            for (int u = 0; u < CU; ++u)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) part<KP, VEC_B>(bn + (u * 32 + 2 * j) * r, left, v[u][j]);
+            for (int j = 0; j < 4; ++j) part<KP, VEC_B>(bn + 2 * j * r, left, v[j]);
         } else {
 #pragma unroll
-            for (int u = 0; u < CU; ++u)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) part<KP, VEC_B>(bn + (u * 32 + 2 * j) * r, n0 + first + u * 32 + 2 * j < n_end ? left : 0, v[u][j]);
+            for (int j = 0; j < 4; ++j) part<KP, VEC_B>(bn + 2 * j * r, n0 + first + 2 * j < n_end ? left : 0, v[j]);
         }
     };
-    constexpr int kStep = 32 * CU;
-    uint4 next[CU][MT][2];
-    uint32_t b_next[CU][4][KP];                             // a step's first k, asked for with its y
+    constexpr int kStep = 32;
+    uint4 next[MT][2];
+    uint32_t b_next[4][KP];                             // a step's first k, asked for with its y
     int64_t n0 = n_begin + col_warp * kStep;
     if (n0 < n_end) {
         ask(n0, n0 + kStep <= n_end, next);
@@ -753,39 +747,34 @@ __global__ void __launch_bounds__(kLoraThreads, MT == 1 ? kFewBlocks : 1) lora_u
             }
     for (; n0 < n_end; n0 += kColWarps * kStep) {
         const bool whole = n0 + kStep <= n_end;
-        uint4 now[CU][MT][2];
-        uint32_t bv[CU][4][KP];
+        uint4 now[MT][2];
+        uint32_t bv[4][KP];
 #pragma unroll
-        for (int u = 0; u < CU; ++u) {
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int h = 0; h < 2; ++h) now[m][h] = next[m][h];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) now[u][m][h] = next[u][m][h];
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int k = 0; k < KP; ++k) bv[u][j][k] = b_next[u][j][k];
-        }
+            for (int k = 0; k < KP; ++k) bv[j][k] = b_next[j][k];
         const int64_t n1 = n0 + kColWarps * kStep;
         if (n1 < n_end) {
             ask(n1, n1 + kStep <= n_end, next);
             if (steps) ask_b(n1, n1 + kStep <= n_end, 0, b_next);
         }
-        float acc[CU][MT][4][4];                            // the products are added to y
+        float acc[MT][4][4];                                // the products are added to y
 #pragma unroll
-        for (int u = 0; u < CU; ++u)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t w[4] = {now[m][h].x, now[m][h].y, now[m][h].z, now[m][h].w};
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t w[4] = {now[u][m][h].x, now[u][m][h].y, now[u][m][h].z, now[u][m][h].w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 v = act2_to_f32<F16>(w[j]);
-                        acc[u][m][j][2 * h] = F16 ? v.x * down[m][h] : v.x;
-                        acc[u][m][j][2 * h + 1] = F16 ? v.y * down[m][h] : v.y;
-                    }
+                for (int j = 0; j < 4; ++j) {
+                    const float2 v = act2_to_f32<F16>(w[j]);
+                    acc[m][j][2 * h] = F16 ? v.x * down[m][h] : v.x;
+                    acc[m][j][2 * h + 1] = F16 ? v.y * down[m][h] : v.y;
                 }
+            }
         for (int st = 0; st < steps; ++st) {
             if (st) ask_b(n0, whole, st, bv);
 #pragma unroll
@@ -803,40 +792,35 @@ __global__ void __launch_bounds__(kLoraThreads, MT == 1 ? kFewBlocks : 1) lora_u
                 for (int k = 0; k < KP; k += 2) {
                     const uint32_t hi[4] = {h0[k], h1[k], h0[k + 1], h1[k + 1]}, lo[4] = {l0[k], l1[k], l0[k + 1], l1[k + 1]};
 #pragma unroll
-                    for (int u = 0; u < CU; ++u)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            mma_16816<F16>(acc[u][m][j], hi, bv[u][j][k], bv[u][j][k + 1]);
-                            mma_16816<F16>(acc[u][m][j], lo, bv[u][j][k], bv[u][j][k + 1]);
-                        }
+                    for (int j = 0; j < 4; ++j) {
+                        mma_16816<F16>(acc[m][j], hi, bv[j][k], bv[j][k + 1]);
+                        mma_16816<F16>(acc[m][j], lo, bv[j][k], bv[j][k + 1]);
+                    }
                 }
             }
         }
+        const int64_t left = n_end - n0 - q * 8;
+        if (left <= 0) continue;
 #pragma unroll
-        for (int u = 0; u < CU; ++u) {
-            const int64_t left = n_end - n0 - u * 32 - q * 8;
-            if (left <= 0) continue;
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int h = 0; h < 2; ++h) {
+                if (!held[m][h]) continue;
+                uint32_t w[4] = {now[m][h].x, now[m][h].y, now[m][h].z, now[m][h].w};
+                if (steps)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (!held[m][h]) continue;
-                    uint32_t w[4] = {now[u][m][h].x, now[u][m][h].y, now[u][m][h].z, now[u][m][h].w};
-                    if (steps)
+                    for (int j = 0; j < 4; ++j)
+                        w[j] = F16 ? f32_to_act2<F16>(acc[m][j][2 * h] * up[m][h], acc[m][j][2 * h + 1] * up[m][h])
+                                   : f32_to_act2<F16>(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
+                uint16_t* to = out[m][h] + n0;
+                if (VEC_Y) {
+                    *(uint4*)to = make_uint4(w[0], w[1], w[2], w[3]);
+                } else {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            w[j] = F16 ? f32_to_act2<F16>(acc[u][m][j][2 * h] * up[m][h], acc[u][m][j][2 * h + 1] * up[m][h])
-                                       : f32_to_act2<F16>(acc[u][m][j][2 * h], acc[u][m][j][2 * h + 1]);
-                    uint16_t* to = out[m][h] + n0 + u * 32;
-                    if (VEC_Y) {
-                        *(uint4*)to = make_uint4(w[0], w[1], w[2], w[3]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (i < left) to[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
-                    }
+                    for (int i = 0; i < 8; ++i)
+                        if (i < left) to[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
                 }
-        }
+            }
     }
 }
 
@@ -891,11 +875,11 @@ const void* ring_kernel(int nt) {
 }
 
 // wide: B in 16-byte pieces of eight k.  (Without vector loads there is one form of each.)
-template <bool F16, int RW, int MT, int CU>
+template <bool F16, int RW, int MT>
 const void* up_kernel(bool wide, bool vec_b, bool vec_y) {
-    if (!vec_b) return vec_y ? (const void*)lora_up_kernel<F16, RW, MT, CU, 2, false, true> : (const void*)lora_up_kernel<F16, RW, MT, CU, 2, false, false>;
-    if (wide) return vec_y ? (const void*)lora_up_kernel<F16, RW, MT, CU, 4, true, true> : (const void*)lora_up_kernel<F16, RW, MT, CU, 4, true, false>;
-    return vec_y ? (const void*)lora_up_kernel<F16, RW, MT, CU, 2, true, true> : (const void*)lora_up_kernel<F16, RW, MT, CU, 2, true, false>;
+    if (!vec_b) return vec_y ? (const void*)lora_up_kernel<F16, RW, MT, 2, false, true> : (const void*)lora_up_kernel<F16, RW, MT, 2, false, false>;
+    if (wide) return vec_y ? (const void*)lora_up_kernel<F16, RW, MT, 4, true, true> : (const void*)lora_up_kernel<F16, RW, MT, 4, true, false>;
+    return vec_y ? (const void*)lora_up_kernel<F16, RW, MT, 2, true, true> : (const void*)lora_up_kernel<F16, RW, MT, 2, true, false>;
 }
 
 template <bool F16, int RW, int KS>
@@ -988,8 +972,8 @@ extern "C" nvfp4_status nvfp4_lora_add(const void* y, int64_t y_stride, const vo
         kernel = pl.rows_item == 16 ? (f16 ? up_ring_kernel<true, 1>(r) : up_ring_kernel<false, 1>(r))
                                     : (f16 ? up_ring_kernel<true, 2>(r) : up_ring_kernel<false, 2>(r));
     } else {
-        kernel = pl.rows_item == 16 ? (f16 ? up_kernel<true, 1, 1, 1>(wide, vec_b, vec_y) : up_kernel<false, 1, 1, 1>(wide, vec_b, vec_y))
-                                    : (f16 ? up_kernel<true, 2, 2, 1>(wide, vec_b, vec_y) : up_kernel<false, 2, 2, 1>(wide, vec_b, vec_y));
+        kernel = pl.rows_item == 16 ? (f16 ? up_kernel<true, 1, 1>(wide, vec_b, vec_y) : up_kernel<false, 1, 1>(wide, vec_b, vec_y))
+                                    : (f16 ? up_kernel<true, 2, 2>(wide, vec_b, vec_y) : up_kernel<false, 2, 2>(wide, vec_b, vec_y));
     }
     // Columns of a block: as many steps of its warps as leave one wave of blocks, so that an item's sums over
     // the splits are not read more often than that needs.  Three an SM fit of 64 rows; of few rows nine for each item

@@ -441,17 +441,16 @@ __device__ __forceinline__ uint64_t block_below(uint64_t v, uint64_t (&sm)[kSamp
 // n <= kList values from the largest down, in place, by the whole block.  Up to 256 by counting what goes before
 // each (100 values 0.4 us where exchanges took 2.7; 512 would take 5), more by exchanges; room for kList,
 // zeros are the least.
-template <class T>
-__device__ __forceinline__ void sort_down(T* v, int n) {
+__device__ __forceinline__ void sort_down(uint64_t* v, int n) {
     const int tid = threadIdx.x;
     if (n <= kSampleThreads / 2) {
         int each_log2 = 4;                                  // threads of a value: at most 16
         while (kSampleThreads >> each_log2 < n) --each_log2;
         const int i = tid >> each_log2, each = 1 << each_log2;
-        const T mine = i < n ? v[i] : T(0);
+        const uint64_t mine = i < n ? v[i] : 0;
         int before = 0;
         for (int j = tid & (each - 1); j < n; j += each) {
-            const T x = v[j];
+            const uint64_t x = v[j];
             before += x > mine || (x == mine && j < i);
         }
         for (int o = each >> 1; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
@@ -467,7 +466,7 @@ __device__ __forceinline__ void sort_down(T* v, int n) {
         for (int s = k / 2; s > 0; s /= 2) {
             const int a = 2 * tid - (tid & (s - 1)), b = a + s;
             if (a < size) {
-                const T x = v[a], y = v[b];
+                const uint64_t x = v[a], y = v[b];
                 if ((x < y) == ((a & k) == 0)) {
                     v[a] = y;
                     v[b] = x;
