@@ -70,17 +70,19 @@ class Model:
 
 
 def prefill(model, batch, cache, prompts, u):
-    """The prompts (lists of tokens) as one batch of rows; the first token of each request."""
+    """The prompts (lists of tokens) as one batch of rows; the first token of each request (-1: no
+    prompt, or no room for it)."""
     new = torch.tensor([len(p) for p in prompts], dtype=torch.int32, device="cuda")
     tokens = torch.tensor([t for p in prompts for t in p], device="cuda")
     t = batch.extend(new, tokens.numel(), row_tables=True)
     logits = model.logits(tokens, batch.adapters[t["request"].long()], t["positions"], t["slots"], t["row_tables"], t["row_lengths"], cache)
-    last = logits[(t["starts"][1:] - 1).long()]
-    return nv.sample(last, u, **batch.how)
+    last = logits[(t["starts"][1:] - 1).clamp(min=0).long()]
+    return torch.where(batch.lengths > 0, nv.sample(last, u, **batch.how), -1)
 
 
 def step(model, batch, cache, tokens, u, end_token):
-    """One token of every request that has not ended; the next ones (-1: ended)."""
+    """One token of every request that has not ended; the next ones (-1: ended, by the end token
+    or because there was no page left for it)."""
     running = tokens >= 0
     t = batch.extend(running.int(), tokens.numel())
     # rows of the requests that run come first; the rest of them store and attend to nothing
@@ -91,6 +93,7 @@ def step(model, batch, cache, tokens, u, end_token):
     logits = model.logits(torch.where(valid, tokens[row], -1), torch.where(valid, batch.adapters[row], -1), t["positions"], t["slots"],
                           batch.table[row], lengths, cache)
     drawn = nv.sample(logits, u, **{k: v[row] for k, v in batch.how.items()})
+    drawn = torch.where(t["slots"] >= 0, drawn, end_token)   # without room: its token went nowhere
     out = tokens.new_full((tokens.numel() + 1,), -1)         # the last: for rows behind the running requests'
     out.scatter_(0, torch.where(valid, row, tokens.numel()), drawn)
     out = torch.where(running, out[:-1], -1)
