@@ -976,13 +976,17 @@ extern "C" nvfp4_status nvfp4_lora_add(const void* y, int64_t y_stride, const vo
                                     : (f16 ? up_kernel<true, 2, 2>(wide, vec_b, vec_y) : up_kernel<false, 2, 2>(wide, vec_b, vec_y));
     }
     // Columns of a block: as many steps of its warps as leave one wave of blocks, so that an item's sums over
-    // the splits are not read more often than that needs.  Three an SM fit of 64 rows; of few rows nine for each item
-    // that there may be, of which fewer are (64 x 4096 x 28672: 16.7 us, six 18.9, twelve 18.1).
-    const int64_t waves = (pl.rows_item == 16 ? 9 : 3) * (int64_t)sm_count();
+    // the splits are not read more often than that needs.  Of 64 rows three an SM fit by their registers, two
+    // by the shared memory of ranks beyond 64 (4096 x 4096 x 4096, rank 128: 76 us, with three counted 94; rank 80 67 and 79;
+    // 2048 x 5120 x 5120, rank 96, 53.4 and 52.8).  Of few rows nine for each item that there may be, of which fewer are (six / nine /
+    // twelve: 64 x 4096 x 28672, rank 16, 32 adapters 17.5 / 15.9 / 18.2 us, 16 x 4096 x 28672 8.4 / 7.7 / 9.8, 300 x 4096 x
+    // 4096 12.0 / 12.1 / 13.5, 64 x 4096 x 4096 8.5 / 9.4 / 9.4, 1000 x 4096 x 8192, rank 32, 33.7 / 35.1 / 34.7).
+    const size_t smem = halves + (up_ring ? kUpStages * stage : 0);
+    const int64_t fit = std::min<int64_t>(3, (227 * 1024) / (int64_t)(smem + 2 * 1024));       // with what is static, and reserved
+    const int64_t waves = (pl.rows_item == 16 ? 9 : fit) * sm_count();
     const int64_t blocks = std::min<int64_t>(std::max<int64_t>(1, waves / pl.items), 65535);        // of an item
     int cols_block = (int)round_up(ceil_div(N, blocks), step);
     const int64_t cols = cols_block;
-    const size_t smem = halves + (up_ring ? kUpStages * stage : 0);
     void* up_args[] = {&p, &cols_block};
     return launch_kernel(kernel, dim3((unsigned)pl.items, (unsigned)ceil_div(N, cols)), dim3(kLoraThreads), smem, 1, up_args, s, fn);
 }
