@@ -732,6 +732,24 @@ def test_sample_does_not_depend_on_the_split():
         assert one[0] == many[i] and lp1[0] == lp[i]
 
 
+# The logarithm has one unit in the last place, the sum behind it half of one: 1.5 * 2^-23 of the result, whose weights
+# are right to 2^-29.9 each.  Shares below 2^-19 or so may come from places instead: two fused products and one by ln 2
+# (2^-24 of at most the result each, 2^-25 ln 2's own), a logarithm and a conversion (2^-23 of it, 2^-24), the difference.
+@pytest.mark.parametrize("kind", ["normal", "peaked", "flat"])
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("how", [dict(), dict(temperature=0.6, top_k=20), dict(top_p=0.9), dict(temperature=1.5, top_k=50, top_p=0.95)])
+def test_sample_log_probabilities_to_their_last_bits(kind, act, how):
+    B, V = 400, 1500
+    l, u = _logits(B, V, kind, act, 5), torch.rand(B, generator=_gen(5), device="cuda")
+    tokens, logprob = nv.sample(l, u, return_logprob=True, **how)
+    l, u, tokens, logprob = l.double().cpu().numpy(), u.double().cpu().numpy(), tokens.tolist(), logprob.double().tolist()
+    f32 = {k: float(np.float32(v)) if isinstance(v, float) else v for k, v in how.items()}
+    for i in range(B):
+        t, lp = batch.draw(l[i], u[i], f32.get("temperature", 1.0), f32.get("top_k", 0), f32.get("top_p", 1.0))
+        lim = 1.5 * 2.0 ** -23 * abs(lp) + 2.0 ** -28 if lp > -13 else 4.5 * 2.0 ** -24 * abs(lp) + 2.0 ** -24
+        assert tokens[i] == t and abs(logprob[i] - lp) <= lim, (i, lp, logprob[i] - lp)
+
+
 def test_sample_frequencies():
     l = torch.log(torch.tensor([0.1, 0.4, 0.2, 0.3], device="cuda")).expand(2000, 4)
     u = (torch.arange(2000, device="cuda") + 0.5) / 2000

@@ -210,6 +210,14 @@ __device__ __forceinline__ uint64_t part_of(float f, uint64_t s, bool up) {
     return q + (up && rest != 0);
 }
 
+// a / b, and what is missing from it: 0 <= a <= b < 2^63.
+__device__ __forceinline__ float2 ratio(uint64_t a, uint64_t b) {
+    const float ah = (float)a, bh = (float)b;
+    const float al = (float)(int64_t)(a - (uint64_t)ah), bl = (float)(int64_t)(b - (uint64_t)bh);
+    const float q = __fdiv_rn(ah, bh);
+    return make_float2(q, __fdiv_rn(fmaf(-q, bh, ah) + fmaf(-q, bl, al), bh));
+}
+
 enum { kTypeBf16, kTypeF16, kTypeF32 };
 
 // The row's virtual elements, in 16-byte pieces: element 0 is on a boundary of eight elements.  A warp
@@ -1011,10 +1019,17 @@ struct Sampler {
         }
     }
 
-    // log(w / whole): near one by what is missing, from 2^24 units on by the quotient, else by the place.
+    // log(w / whole): near one by what is missing, from 2^24 units on by the quotient, else by the place.  Quotients
+    // with what their roundings leave, so that the logarithm's own rounding is the error.
     __device__ __forceinline__ float log_share(float l, uint64_t w, uint64_t whole) const {
-        if (w > whole / 2) return log1pf(-((float)(whole - w) / (float)whole));
-        if (w >= 1u << 24) return logf((float)w / (float)whole);
+        if (w > whole / 2) {
+            const float2 x = ratio(whole - w, whole);
+            return log1pf(-x.x) - x.y / (1.f - x.x);
+        }
+        if (w >= 1u << 24) {
+            const float2 x = ratio(w, whole);
+            return logf(x.x) + x.y / x.x;
+        }
         return scale.log_weight(l) - logf((float)whole * (1.f / (float)(1ull << kOneLog2)));
     }
 };
