@@ -1,7 +1,7 @@
 """One call of each profiled case of the operators between the linears, a 256 MB fill
 before it; layer_operators.md has the commands that profile it.
 
-    python profiles/layer_operators.py
+    python profiles/layer_operators.py [CASE ...]
 """
 
 import os
@@ -17,11 +17,11 @@ CASES = ("norm prefill 8192x8192", "norm8 4096x5120 g128", "write prompt 4096 3-
          "attend 16x4096 e4m3", "attend 48x3001 window", "attend 64x16384")
 
 
-def main():
+def main(names):
     operators.own = True
     listed = {c["name"]: c for c in operators.listed()}
     fill = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
-    for name in CASES:
+    for name in names:
         case = dict(listed[name])
         if name == "attend 64x16384":
             case["B"] = 16                                   # a quarter of its memory
@@ -32,4 +32,4 @@ def main():
 
 
 if __name__ == "__main__":
-    main()
+    main(sys.argv[1:] or CASES)
