@@ -611,6 +611,8 @@ nvfp4_status nvfp4_trim_tables(const int32_t* lengths, const int32_t* keep, int6
  *                it is refused.
  *  workspace     device, >= nvfp4_lora_workspace(...) bytes, 256-byte aligned.  Contents on
  *                entry do not matter.
+ * An infinite x (or A) gives what the formula gives; B has to be finite: an infinity there meets both halves, and
+ * is NaN where one of them is zero.
  * r is at most 256, num_adapters at most 4096.  T == 0 or N == 0 launches nothing.  Repeated
  * calls on the same inputs give the same bits.
  */
@@ -649,7 +651,11 @@ typedef struct {
  *  tokens        device int64 [B].
  *  logprobs      device FP32 [B] or NULL: log of the token's share of the kept mass.
  * Weights are whole numbers of 2^-43, before that rounding right to 2^-29.9 of their value (2^-31.7 in
- * the mean square); their sums are exact, so the result does not depend on how the work is split.
+ * the mean square); their sums are exact, so the order of the work does not matter, and the blocks that a row
+ * gets do not either, but in one place: with top_k and top_p both set, top_p is cut by sums of rounded weights
+ * where few logits may be among the top_k, and by sums rounded for each sixteenth of a factor of two where
+ * many may, which goes by the blocks, too.  The two lie within 2^-32 of each other: a row whose top_p ends that
+ * near a border can keep one token more or less beside other rows.  The same call gives the same tokens.
  */
 nvfp4_status nvfp4_sample(const void* logits, int64_t row_stride, int type, int64_t B, int64_t V, const float* u,
                           const nvfp4_sampling* how, int64_t* tokens, float* logprobs, void* stream);

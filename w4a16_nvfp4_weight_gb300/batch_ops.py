@@ -64,7 +64,8 @@ def lora_add(y, x, a, b, adapters, scales=None, out=None, workspace=None):
     x [T, K] that they share (BF16 or FP16, rows with any stride; views of a fused
     projection will do).  ``a`` [adapters, r, K] and ``b`` [adapters, N, r] have their
     type, ``scales`` is float32 [adapters] or None (1); r at most 256, smaller ranks padded
-    with zeros.  Rounded once, to the type of y.  ``out`` may be y where that is
+    with zeros.  a @ x is held in 32 bits and meets b as two halves of the type; the sums are
+    rounded once, to the type of y.  b has to be finite.  ``out`` may be y where that is
     contiguous.  An index that is not below the number of adapters counts as none, and
     device_status() then reports 8."""
     return _ops.lora_add(y, x, a, b, adapters, scales, out, workspace)

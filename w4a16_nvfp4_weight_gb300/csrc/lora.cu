@@ -11,8 +11,8 @@
 // rank r they do r flop for each byte of x or y that they read or write, far below what would
 // need tcgen05.  An order of k that is the same for both operands lets a lane load 16 bytes of each row, and
 // an order of the columns 16 bytes of y.
-// Few rows are bound by latency (1 x 4096 x 4096, rank 16, 5.1 us; 64 x 4096 x 28672 16.7, 2.5
-// TB/s), many by memory and the products (8192 x 4096 x 4096, rank 64, 65.5 us, 3.1 TB/s).
+// Few rows are bound by latency (1 x 4096 x 4096, rank 16, 4.7 us; 64 x 4096 x 28672 16.5, 2.5
+// TB/s), many by memory and the products (8192 x 4096 x 4096, rank 64, 65.7 us, 3.1 TB/s).
 #include <algorithm>
 
 #include "common.cuh"
@@ -472,7 +472,7 @@ constexpr int kFewBlocks = 5;              // of the up kernel of 16 rows, on an
 
 // One item's rows of A x times B, and y, over a range of N: stages of columns of B and y through a ring in
 // shared memory (with loads to registers a step ahead, 8192 rows, 4096 columns, rank 64: 75 us for the
-// 43 here; 64 rows, 28672 columns, rank 16: 20.9 for the 16.7
+// 43 here; 64 rows, 28672 columns, rank 16: 20.9 for the 16.5
 // here, with the down kernel).  RW warps by 4 / RW: MT * 16 rows
 // and 32 columns each; items of 64 rows are two by two warps of 32, of 16 rows one by four.  Tile j of
 // four holds columns 8 (c / 2) + 2 j + c % 2, so that a lane's eight outputs of a row lie side by side: the

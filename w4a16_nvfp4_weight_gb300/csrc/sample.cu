@@ -8,7 +8,8 @@
 // threshold: with 32-bit sums one draw in a hundred would fall on the wrong side of a
 // border, another one for another order of the sums.  So weights are whole numbers of
 // 2^-43 (of the largest weight), before that rounding right to 2^-29.9 of their value (2^-31.7 in the mean square), and sums of them
-// are exact in 64 bits, in any order and by any block.
+// are exact in 64 bits, in any order and by any block.  (top_p among many candidates of top_k is cut by sums rounded for
+// each bin instead of each weight: within 2^-32 of the mass of what few candidates are cut by.)
 //
 // A cluster of one to eight blocks has a row, which stays in shared memory where it fits, so it is read
 // once.  No sort of the row:
@@ -20,9 +21,9 @@
 //  - the draw: masses of warps, of blocks and of the row; the warp whose part holds the
 //    target finds the step, the lane and the element.
 // Bound by latency for few rows (1 x 151936 with top_k and top_p 10.4 us: the load, four meetings
-// of the cluster, two sorts), by instructions for many: an exact weight takes about 30, a mass
-// two additions in shared memory (256 x 100003 logits of 32 bits by top_p 146 us, 0.7 TB/s;
-// by temperature alone 81, by top_k 67).
+// of the cluster, two sorts; greedy 3.0), by instructions for many (256 x 100003 logits of 32 bits: by top_p 92
+// a logit, two additions in shared memory among them, 146 us, 0.7 TB/s; by temperature alone 49 and
+// 81 us, by top_k 35 and 68; greedy rows 37 us).
 #include <algorithm>
 
 #include "common.cuh"

@@ -8,8 +8,8 @@
 // numbers throughout, so nothing depends on the order of anything.
 //
 // Bound by latency: a chain of loads (lengths, table or stack), two sums over the
-// block and a search, against bytes that take a tenth of a microsecond (64 requests by a token 3.7
-// us, 16384 rows of 48 prompts 6.3, 1000 requests of which 600 end 4.5).  So every block sums all
+// block and a search, against bytes that take a tenth of a microsecond (64 requests by a token 3.5
+// us, 16384 rows of 48 prompts 6.1, 1000 requests of which 600 end 4.2).  So every block sums all
 // requests for itself, and one launch does everything.
 #include <algorithm>
 
