@@ -16,6 +16,7 @@
 #include "common.cuh"
 #include "gemm_decode.cuh"
 #include "gemm_tc.cuh"
+#include "launch.cuh"
 
 namespace nvfp4 {
 

@@ -166,11 +166,6 @@ int* device_status_ptr();
 // Multiprocessor count of the current device (cached per device).
 int sm_count();
 
-// Lets `kernel` take `bytes` of dynamic shared memory on the current device.  The limit is
-// the kernel's, not the call's: it only ever rises, so that calls of other sizes, from other
-// threads, do not take it away between this and the launch.
-nvfp4_status allow_smem(const void* kernel, size_t bytes, const char* what);
-
 // The dense GEMM behind nvfp4_w4a16_gemm / nvfp4_w4a16_gemm_f16 (argument
 // checks, then the decode or the tile kernel), for layers built from it.
 nvfp4_status run_dense_gemm(const void* X, const void* repacked, const void* pre_quant_scale, int64_t M,

@@ -1,10 +1,15 @@
-// One launch, with clusters where asked, that may begin while the kernel before it
-// in the stream ends (the kernels wait for it themselves, pdl_wait_previous).
+// Shared memory limits of kernels, and one launch, with clusters where asked, that may begin while the
+// kernel before it in the stream ends (the kernels wait for it themselves, pdl_wait_previous).
 #pragma once
 
 #include "common.cuh"
 
 namespace nvfp4 {
+
+// Lets `kernel` take `bytes` of dynamic shared memory on the current device.  The limit is
+// the kernel's, not the call's: it only ever rises, so that calls of other sizes, from other
+// threads, do not take it away between this and the launch.
+nvfp4_status allow_smem(const void* kernel, size_t bytes, const char* what);
 
 inline nvfp4_status launch_kernel(const void* kernel, dim3 grid, dim3 block, size_t smem, unsigned cluster, void** args,
                                   cudaStream_t stream, const char* fn) {

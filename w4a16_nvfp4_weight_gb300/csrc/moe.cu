@@ -41,6 +41,7 @@
 #include "common.cuh"
 #include "gemm_decode.cuh"
 #include "gemm_tc.cuh"
+#include "launch.cuh"
 #include "ptx.cuh"
 #include "stream_mma.cuh"
 
